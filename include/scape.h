@@ -434,6 +434,147 @@ int scape_profile_enable(scape_ctx* ctx, int32_t enable);
  * milliseconds (ms[SCAPE_PHASE_COUNT]) and the number of steps recorded. */
 int scape_profile_read(scape_ctx* ctx, double* ms, int64_t* steps);
 
+/*
+ * ----------------------------------------------------------------------------
+ * Losses of the training step around the optimizer: what makes the logits'
+ * gradients that become the gradients scape_step takes.  None of these needs a
+ * context; they hold no state and allocate nothing.  A call that needs device
+ * scratch takes it as `workspace` (16-byte aligned, at least the bytes its
+ * _workspace query says, contents arbitrary before and after); calls that may
+ * overlap, on two streams or in two graphs, need workspaces of their own.
+ * Every call can be captured into a HIP graph (its launches clear and copy
+ * nothing by memset or memcpy), and repeated calls on equal inputs give equal
+ * bits.
+ *
+ * Logits are matrices of one of three types, `rows` rows of `cols` elements
+ * that lie `ld` >= cols elements apart.  A matrix needs no more than its
+ * element's alignment; rows on 16-byte boundaries, and a gradient with the
+ * logits' own alignment, are read and written fastest.  Sums are held in fp32
+ * or more, and each output is rounded once, to its own type.
+ */
+#define SCAPE_DTYPE_F32 0
+#define SCAPE_DTYPE_BF16 1
+#define SCAPE_DTYPE_F16 2
+#define SCAPE_ROW_MAX_COLS 262144  /* columns of a row (2^18)            */
+#define SCAPE_TOPK_MAX_K 1024
+#define SCAPE_DISTILL_MAX_K 1024
+#define SCAPE_BALANCE_MAX_EXPERTS 1024
+
+/*
+ * The k largest entries of each row, largest first, equal values (-0 and +0
+ * are equal) by the lower column - the tie rule of scape_mask_build - and the
+ * row's log-sum-exp lse[r] = log sum_c exp(scale * z[r][c]) where lse is not
+ * NULL.  A teacher's records for scape_distill_forward (k values, k columns
+ * and one lse in the place of a vocabulary of logits), or a router's choice of
+ * experts for scape_balance_forward.
+ *   val[rows*k]  in z's type, a zero as +0; idx[rows*k] columns.  An entry of
+ *   -inf is none: the slots that no entry is left for hold -inf and -1.  NaN
+ *   counts as larger than every number (val is then NaN).  lse is -inf for a
+ *   row of -inf, and NaN where the row holds NaN or +inf.
+ * 1 <= k <= min(cols, SCAPE_TOPK_MAX_K); scale > 0; rows = 0 enqueues nothing.
+ * The workspace is 0 bytes unless few or long rows are split.
+ * Errors: INVALID_ARG, ALIGN, SHAPE (limits, ld < cols, workspace too small),
+ * HIP.
+ */
+int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t k, float scale,
+                    void* val, int32_t* idx, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+int scape_topk_rows_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes);
+
+/* A teacher's top logits, k slots for each row of the student's logits: val
+ * and idx [rows*k] as scape_topk_rows writes them (val of any of the three
+ * types), lse [rows] or NULL.  A slot whose column is outside [0, cols) is
+ * empty; of slots with the same column the first counts. */
+typedef struct scape_teacher {
+    const void* val;
+    int32_t dtype;
+    const int32_t* idx;
+    const float* lse;
+    int32_t k;
+} scape_teacher;
+
+/*
+ * Distillation from a teacher's top logits.  Per row, with s = scale (1 over
+ * the temperature), p = softmax(s * z) over all columns, and the row's entries
+ * (t_j, i_j):
+ *   teacher->lse given: q_j = exp(s * t_j - lse), and what the teacher holds
+ *     outside the entries, q_T = max(0, 1 - sum_j q_j), is compared with what
+ *     the student holds there, p_T (lse at the same scale);
+ *   teacher->lse NULL:  q = softmax of s * t_j over the entries, q_T = 0.
+ *   KL = sum_j q_j * (log q_j - log p_{i_j}) + q_T * (log q_T - log p_T)
+ *   loss[r]       = weight[r] * KL           (weight NULL: 1)
+ *   stats[2r]     = log sum_c exp(s * z[r][c])
+ *   stats[2r + 1] = log p_T, -inf if the student holds nothing outside
+ *   dz            = d(sum of loss)/dz, where dz is not NULL: the gradient of
+ *     this call's own loss, in the same pass, for a program whose weights
+ *     already hold every factor (1/tokens, loss scale).
+ * A row with weight 0, or without entries, is not read: loss, stats and
+ * gradient are 0.  So are loss and gradient of a row whose logits are all
+ * -inf.  Where the student holds nothing outside the entries the q_T term is
+ * left out.  An entry with q_j > 0 at a column of -inf makes the loss +inf.  A
+ * row that is read and holds NaN or +inf gives NaN.
+ * Arguments: z as above, read only; loss fp32 [rows]; stats fp32 [2*rows],
+ * needed also where no backward call follows; dz of z's type, rows ld_dz >=
+ * cols elements apart, columns past cols untouched, may be z itself (then
+ * ld_dz = ld; any other overlap is not allowed).
+ * 1 <= k <= SCAPE_DISTILL_MAX_K; cols <= SCAPE_ROW_MAX_COLS.
+ * Errors: as scape_topk_rows.
+ */
+int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                          const scape_teacher* teacher, float scale, const float* weight, float* loss, float* stats,
+                          void* dz, int64_t ld_dz, void* workspace, int64_t workspace_bytes, void* stream);
+int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes);
+
+/* The gradient alone, from the statistics of a forward call on the same z,
+ * teacher and scale: dz = dloss[r] * weight[r] * dKL/dz (either NULL: 1).  A
+ * row whose factor is 0 is not read and gets 0.  Needs no workspace.
+ * Errors: as scape_topk_rows. */
+int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                           const scape_teacher* teacher, float scale, const float* weight, const float* stats,
+                           const float* dloss, void* dz, int64_t ld_dz, void* stream);
+
+/*
+ * A router's balance loss.  Tokens lie in segments (sequences, or one for the
+ * whole batch): segment i is tokens offsets[i] .. offsets[i+1]-1 (int32
+ * [segments+1], ascending, within 0..tokens; NULL: one segment of all).  A
+ * token counts if its mask byte is not 0 (mask NULL: all do); the scores of a
+ * token over its E = experts logits are
+ *   SCAPE_SCORE_SOFTMAX: p = softmax(logits)
+ *   SCAPE_SCORE_SIGMOID: p_e = s_e / sum_j s_j, s = sigmoid(logits)
+ * and p = 0 for a token whose logits are all -inf.  Per segment:
+ *   counts[i*E + e] valid tokens' choices of e (idx [tokens*k], as
+ *                   scape_topk_rows writes it; outside [0, E): no choice)
+ *   psum[i*E + e]   the sum of p_e over valid tokens
+ *   n_tok[i]        valid tokens
+ *   loss[i]         alpha * E / (k * n^2) * sum_e counts_e * psum_e, which is
+ *                   alpha * sum_e (E * counts_e / (k n)) * (psum_e / n); 0 if n = 0
+ * loss may be NULL: a data-parallel program adds counts, psum and n_tok over
+ * its workers and then calls scape_balance_loss for the loss of them all.
+ * Errors: as scape_topk_rows.
+ */
+#define SCAPE_SCORE_SOFTMAX 0
+#define SCAPE_SCORE_SIGMOID 1
+int scape_balance_forward(const void* logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t ld,
+                          const int32_t* idx, int32_t k, const int32_t* offsets, int32_t segments,
+                          const uint8_t* mask, int32_t score, float alpha, int32_t* counts, float* psum,
+                          int32_t* n_tok, float* loss, void* workspace, int64_t workspace_bytes, void* stream);
+int scape_balance_workspace(int64_t tokens, int32_t experts, int32_t segments, int64_t* bytes);
+
+/* loss[segments] from counts, psum and n_tok, as in scape_balance_forward. */
+int scape_balance_loss(const int32_t* counts, const float* psum, const int32_t* n_tok, int32_t segments,
+                       int32_t experts, int32_t k, float alpha, float* loss, void* stream);
+
+/* dlogits = sum over segments of dloss[i] * d loss[i] / d logits (dloss NULL:
+ * 1), with counts and n_tok as given: this worker's own, or the sums over all
+ * workers.  The counts carry no gradient.  Rows of tokens that do not count
+ * get 0; rows outside every segment are left as they were.  dlogits has the
+ * logits' type, rows ld_d >= experts apart, and may be the logits themselves
+ * (then ld_d = ld).
+ * Errors: as scape_topk_rows. */
+int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k,
+                           const int32_t* offsets, int32_t segments, const uint8_t* mask, int32_t score, float alpha,
+                           const int32_t* counts, const int32_t* n_tok, const float* dloss, void* dlogits,
+                           int64_t ld_d, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

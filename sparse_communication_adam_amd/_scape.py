@@ -45,6 +45,11 @@ class _Config(ctypes.Structure):
                 ("weight_decay", ctypes.c_float), ("keep_num", ctypes.c_uint32), ("keep_den", ctypes.c_uint32)]
 
 
+class _Teacher(ctypes.Structure):
+    _fields_ = [("val", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("idx", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("k", ctypes.c_int32)]
+
+
 class _Mask(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("block_prefix", ctypes.c_void_p)]
 
@@ -56,7 +61,8 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() (hipcc, gfx950)")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-        cfgp, maskp = ctypes.POINTER(_Config), ctypes.POINTER(_Mask)
+        f32 = ctypes.c_float
+        cfgp, maskp, teachp = ctypes.POINTER(_Config), ctypes.POINTER(_Mask), ctypes.POINTER(_Teacher)
         sig = {
             "scape_version": [vp, vp],
             "scape_layout": [cfgp, vp, vp, vp, vp, vp],
@@ -84,6 +90,16 @@ def lib() -> ctypes.CDLL:
             "scape_profile_read": [vp, vp, vp],
             "scape_copy_probe": [vp, vp, ctypes.c_uint64, vp],
             "scape_stream_probe": [vp, vp, i32, vp, vp, i32, ctypes.c_uint64, vp],
+            "scape_topk_rows": [vp, i32, i64, i64, i64, i32, f32, vp, vp, vp, vp, i64, vp],
+            "scape_topk_rows_workspace": [i32, i64, i64, i32, vp],
+            "scape_distill_forward": [vp, i32, i64, i64, i64, teachp, f32, vp, vp, vp, vp, i64, vp, i64, vp],
+            "scape_distill_workspace": [i32, i64, i64, i32, vp],
+            "scape_distill_backward": [vp, i32, i64, i64, i64, teachp, f32, vp, vp, vp, vp, i64, vp],
+            "scape_balance_forward": [vp, i32, i64, i32, i64, vp, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp, vp, i64,
+                                      vp],
+            "scape_balance_workspace": [i64, i32, i32, vp],
+            "scape_balance_loss": [vp, vp, vp, i32, i32, i32, f32, vp, vp],
+            "scape_balance_backward": [vp, i32, i64, i32, i64, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp, i64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -536,3 +552,241 @@ def scape_profile_read(ctx: Context):
     steps = ctypes.c_int64()
     _check(lib().scape_profile_read(ctx.handle, ms, ctypes.byref(steps)))
     return dict(zip(PHASES, list(ms))), steps.value
+
+
+# ----------------------------------------------------------------------------
+# losses: row top-k, distillation from a teacher's top logits, router balance.
+# No context; outputs and workspaces are the caller's tensors.
+
+
+def _dtype_id(dtype) -> int:
+    import torch
+    ids = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if dtype not in ids:
+        raise TypeError(f"logits must be float32, bfloat16 or float16 (got {dtype})")
+    return ids[dtype]
+
+
+def _matrix(t, name: str, like=None):
+    """(pointer, dtype id, rows, cols, ld) of a 2-D tensor whose rows are
+    contiguous; `like`: the tensor whose dtype and shape it must have.  The
+    device is checked by _on_device."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {t.dim()})")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name} must have the logits' dtype and shape ({like.dtype}, {tuple(like.shape)})")
+    did = _dtype_id(t.dtype)
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride {t.stride(1)} between columns)")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows of {cols} columns overlap (stride {ld})")
+    return t.data_ptr(), did, rows, cols, ld
+
+
+def _array(t, dtype, numel: int, name: str, optional: bool = False):
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be a torch tensor")
+    _shape(t, dtype, numel, name)
+    return t.data_ptr()
+
+
+def _on_device(**tensors) -> None:
+    """Every tensor on the current GPU: a launch goes there, whatever device
+    its pointers belong to."""
+    import torch
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU (got {t.device})")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device} but cuda:{torch.cuda.current_device()} is the current device")
+
+
+def _workspace(t, need: int):
+    import torch
+    if t is None:
+        if need:
+            raise ValueError(f"this call needs a workspace of {need} bytes")
+        return None, 0
+    _shape(t, (torch.uint8, torch.int8), need, "workspace")
+    return t.data_ptr(), t.numel()
+
+
+def scape_topk_rows_workspace_bytes(z, k: int) -> int:
+    """Bytes of workspace scape_topk_rows needs for this tensor's shape."""
+    _, did, rows, cols, _ = _matrix(z, "z")
+    b = ctypes.c_int64()
+    _check(lib().scape_topk_rows_workspace(did, rows, cols, int(k), ctypes.byref(b)))
+    return b.value
+
+
+def scape_topk_rows(z, k: int, val, idx, lse=None, scale: float = 1.0, workspace=None, stream=None) -> None:
+    """The k largest entries of each row of z (2-D, rows contiguous) into val
+    (z's dtype) and idx (int32), both rows*k elements, and the row's
+    log-sum-exp of scale*z into lse (fp32) where given."""
+    import torch
+    zp, did, rows, cols, ld = _matrix(z, "z")
+    need = scape_topk_rows_workspace_bytes(z, k)
+    vp = _array(val, z.dtype, rows * k, "val")
+    ip = _array(idx, torch.int32, rows * k, "idx")
+    lp = _array(lse, torch.float32, rows, "lse", optional=True)
+    wp, wb = _workspace(workspace, need)
+    _on_device(z=z, val=val, idx=idx, lse=lse, workspace=workspace)
+    _check(lib().scape_topk_rows(zp, did, rows, cols, ld, int(k), float(scale), vp, ip, lp, wp, wb, _stream(stream)))
+
+
+def _teacher(t_val, t_idx, t_lse, rows: int) -> _Teacher:
+    import torch
+    for t, name in ((t_val, "t_val"), (t_idx, "t_idx")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+    if t_val.dim() != 2 or t_val.shape != t_idx.shape or t_val.shape[0] != rows:
+        raise ValueError(f"t_val and t_idx must both be [{rows}, k] (got {tuple(t_val.shape)}, {tuple(t_idx.shape)})")
+    k = t_val.shape[1]
+    vp = _array(t_val, (torch.float32, torch.bfloat16, torch.float16), rows * k, "t_val")
+    ip = _array(t_idx, torch.int32, rows * k, "t_idx")
+    lp = _array(t_lse, torch.float32, rows, "t_lse", optional=True)
+    return _Teacher(vp, _dtype_id(t_val.dtype), ip, lp, k)
+
+
+def scape_distill_workspace_bytes(z, k: int, grad: bool = False) -> int:
+    """Bytes of workspace scape_distill_forward needs for this tensor's shape
+    (with or without the gradient)."""
+    _, did, rows, cols, _ = _matrix(z, "z")
+    b = ctypes.c_int64()
+    _check(lib().scape_distill_workspace(did, rows, cols, int(k), ctypes.byref(b)))
+    return b.value
+
+
+def scape_distill_forward(z, t_val, t_idx, loss, stats, t_lse=None, scale: float = 1.0, weight=None, dz=None,
+                          workspace=None, stream=None) -> None:
+    """Distillation loss of the logits z [rows, cols] from a teacher's top
+    logits t_val, t_idx [rows, k]: with t_lse the teacher's mass outside the
+    entries is matched as one more class, without it the teacher is
+    renormalised over them.  loss fp32 [rows], stats fp32 [rows, 2]; dz (z's
+    dtype and shape, may be z) also takes the gradient of loss.sum().  For
+    autograd: z.backward(dz) on the logits' graph."""
+    import torch
+    zp, did, rows, cols, ld = _matrix(z, "z")
+    t = _teacher(t_val, t_idx, t_lse, rows)
+    dp, ld_dz = None, 0
+    if dz is not None:
+        dp, _, _, _, ld_dz = _matrix(dz, "dz", like=z)
+    wt = _array(weight, torch.float32, rows, "weight", optional=True)
+    lp = _array(loss, torch.float32, rows, "loss")
+    sp = _array(stats, torch.float32, 2 * rows, "stats")
+    wp, wb = _workspace(workspace, scape_distill_workspace_bytes(z, t.k, grad=dz is not None))
+    _on_device(z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, loss=loss, stats=stats, dz=dz,
+               workspace=workspace)
+    _check(lib().scape_distill_forward(zp, did, rows, cols, ld, ctypes.byref(t), float(scale), wt, lp, sp, dp, ld_dz,
+                                       wp, wb, _stream(stream)))
+
+
+def scape_distill_backward(z, t_val, t_idx, stats, dz, t_lse=None, scale: float = 1.0, weight=None, dloss=None,
+                           stream=None) -> None:
+    """dz = dloss * weight * dKL/dz per row, from the stats of a forward call
+    on the same z, teacher and scale.  dz may be z."""
+    import torch
+    zp, did, rows, cols, ld = _matrix(z, "z")
+    t = _teacher(t_val, t_idx, t_lse, rows)
+    dp, _, _, _, ld_dz = _matrix(dz, "dz", like=z)
+    wt = _array(weight, torch.float32, rows, "weight", optional=True)
+    sp = _array(stats, torch.float32, 2 * rows, "stats")
+    gp = _array(dloss, torch.float32, rows, "dloss", optional=True)
+    _on_device(z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, stats=stats, dloss=dloss, dz=dz)
+    _check(lib().scape_distill_backward(zp, did, rows, cols, ld, ctypes.byref(t), float(scale), wt, sp, gp, dp, ld_dz,
+                                        _stream(stream)))
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)} (got {score!r})")
+    return SCORES[score]
+
+
+def _segments(offsets) -> int:
+    import torch
+    if offsets is None:
+        return 1
+    _shape(offsets, torch.int32, 2, "offsets")
+    return offsets.numel() - 1
+
+
+def scape_balance_workspace_bytes(logits, segments: int = 1) -> int:
+    """Bytes of workspace scape_balance_forward needs for this tensor's shape."""
+    _, _, tokens, experts, _ = _matrix(logits, "logits")
+    b = ctypes.c_int64()
+    _check(lib().scape_balance_workspace(tokens, experts, int(segments), ctypes.byref(b)))
+    return b.value
+
+
+def scape_balance_forward(logits, idx, counts, psum, n_tok, loss=None, alpha: float = 1.0, offsets=None, mask=None,
+                          score: str = "softmax", workspace=None, stream=None) -> None:
+    """Per segment: the experts' counts (int32 [segments, experts]), the sums
+    of their scores psum (fp32), the valid tokens n_tok (int32) and the
+    balance loss (fp32) of router logits [tokens, experts] and choices idx
+    (int32 [tokens, k]).  offsets: int32 [segments + 1], or one segment of all
+    tokens; mask: uint8 or bool [tokens]."""
+    import torch
+    zp, did, tokens, experts, ld = _matrix(logits, "logits")
+    segs = _segments(offsets)
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.shape[0] != tokens:
+        raise ValueError(f"idx must be a tensor of [{tokens}, k]")
+    k = idx.shape[1]
+    ip = _array(idx, torch.int32, tokens * k, "idx")
+    op = _array(offsets, torch.int32, segs + 1, "offsets", optional=True)
+    mp = _array(mask, (torch.uint8, torch.bool), tokens, "mask", optional=True)
+    cp = _array(counts, torch.int32, segs * experts, "counts")
+    pp = _array(psum, torch.float32, segs * experts, "psum")
+    np_ = _array(n_tok, torch.int32, segs, "n_tok")
+    lp = _array(loss, torch.float32, segs, "loss", optional=True)
+    wp, wb = _workspace(workspace, scape_balance_workspace_bytes(logits, segs))
+    _on_device(logits=logits, idx=idx, offsets=offsets, mask=mask, counts=counts, psum=psum, n_tok=n_tok, loss=loss,
+               workspace=workspace)
+    _check(lib().scape_balance_forward(zp, did, tokens, experts, ld, ip, k, op, segs, mp, _score(score), float(alpha),
+                                       cp, pp, np_, lp, wp, wb, _stream(stream)))
+
+
+def scape_balance_loss(counts, psum, n_tok, loss, k: int, alpha: float = 1.0, stream=None) -> None:
+    """The loss of counts and psum [segments, experts] and n_tok [segments],
+    for instance their sums over data-parallel workers."""
+    import torch
+    if not isinstance(counts, torch.Tensor) or counts.dim() != 2:
+        raise ValueError("counts must be a tensor of [segments, experts]")
+    segs, experts = counts.shape
+    cp = _array(counts, torch.int32, segs * experts, "counts")
+    pp = _array(psum, torch.float32, segs * experts, "psum")
+    np_ = _array(n_tok, torch.int32, segs, "n_tok")
+    lp = _array(loss, torch.float32, segs, "loss")
+    _on_device(counts=counts, psum=psum, n_tok=n_tok, loss=loss)
+    _check(lib().scape_balance_loss(cp, pp, np_, segs, experts, int(k), float(alpha), lp, _stream(stream)))
+
+
+def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha: float = 1.0, offsets=None, mask=None,
+                           score: str = "softmax", stream=None) -> None:
+    """dlogits (the logits' dtype and shape, may be the logits) from counts
+    and n_tok (this worker's, or their sums over workers) and dloss
+    [segments] (None: 1).  Rows outside every segment are left as they were."""
+    import torch
+    zp, did, tokens, experts, ld = _matrix(logits, "logits")
+    dp, _, _, _, ld_d = _matrix(dlogits, "dlogits", like=logits)
+    segs = _segments(offsets)
+    op = _array(offsets, torch.int32, segs + 1, "offsets", optional=True)
+    mp = _array(mask, (torch.uint8, torch.bool), tokens, "mask", optional=True)
+    cp = _array(counts, torch.int32, segs * experts, "counts")
+    np_ = _array(n_tok, torch.int32, segs, "n_tok")
+    gp = _array(dloss, torch.float32, segs, "dloss", optional=True)
+    _on_device(logits=logits, counts=counts, n_tok=n_tok, dloss=dloss, dlogits=dlogits, offsets=offsets, mask=mask)
+    _check(lib().scape_balance_backward(zp, did, tokens, experts, ld, int(k), op, segs, mp, _score(score),
+                                        float(alpha), cp, np_, gp, dp, ld_d, _stream(stream)))

@@ -1,0 +1,348 @@
+// k_balance.hip - a router's balance loss and per-expert counts, with the
+// gradient of its logits, for gfx950.
+//
+// Token t has a score p_te for each of E experts: softmax of its logits, or
+// their sigmoids s_te over the sum of them.  Over a segment's n valid tokens,
+// c_e selections and P_e = sum_t p_te:
+//   loss      = alpha E / (k n^2) sum_e c_e P_e
+//   d/dl_te   = G p_te (c_e - sum_j p_tj c_j) [(1 - s_te) for sigmoids]
+//   G         = dloss alpha E / (k n^2)
+// The counts do not depend on the logits' values (a choice has no gradient).
+//
+// A group of lanes holds a token's logits, each lane 16-byte granules of it,
+// so a wave reads a run of tokens as one contiguous piece and the sums over
+// experts stay inside the group.  What bounds the kernels is the read of the
+// logits (and the write of the gradient).  Sums over tokens are held in
+// float32 inside a workgroup's run and in float64 across runs, in a fixed
+// order.
+#include "loss_device.h"
+
+namespace scape {
+
+constexpr int kBalanceWaves = kBalanceThreads / 64;
+
+struct Run {
+    int32_t seg, t0, t1;  // tokens [t0, t1) of segment seg
+};
+
+// Offsets are read clamped to the tokens there are: a wrong one gives wrong
+// sums but no access outside.
+__device__ __forceinline__ int32_t offset_at(const BalanceArgs& a, int32_t s) {
+    if (!a.offsets) return s == 0 ? 0 : (int32_t)a.in.rows;
+    const int32_t o = a.offsets[s];
+    return o < 0 ? 0 : (o > (int32_t)a.in.rows ? (int32_t)a.in.rows : o);
+}
+__device__ __forceinline__ int32_t first_slot(const BalanceArgs& a, int32_t s) { return offset_at(a, s) / a.run + s; }
+
+__device__ __forceinline__ Run run_of(const BalanceArgs& a, int32_t slot) {
+    int32_t lo = 0, hi = a.segments;  // the last segment that starts at or before the slot
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) / 2;
+        if (first_slot(a, mid) <= slot)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int64_t t0 = offset_at(a, lo) + (int64_t)(slot - first_slot(a, lo)) * a.run;
+    const int64_t end = offset_at(a, lo + 1), t1 = t0 + a.run;
+    if (slot < first_slot(a, lo) || t0 >= end) return Run{lo, 0, 0};
+    return Run{lo, (int32_t)t0, (int32_t)(t1 < end ? t1 : end)};
+}
+
+// A token's logits in a group of lanes: lane l has granules l, l + kLanes, ...
+template <class T, int kLanes, int kGran, bool kVec>
+__device__ __forceinline__ void load_token(const BalanceArgs& a, int64_t t, bool live, uint32_t l,
+                                           float (&x)[kGran * T::kN]) {
+    using raw = typename T::raw;
+    const raw* z = static_cast<const raw*>(a.in.z) + (live ? t : 0) * a.in.ld;
+    const int32_t n = live ? (int32_t)a.in.cols : 0;
+#pragma unroll
+    for (int c = 0; c < kGran; ++c) {
+        const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
+        gran g = {0u, 0u, 0u, 0u};
+        if (kVec && e0 + T::kN <= n) {
+            g = *reinterpret_cast<const gran*>(z + e0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) T::set(g, j, e0 + j < n ? z[e0 + j] : (raw)T::kNegInfBits);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kN; ++j) x[c * T::kN + j] = T::up(g, j);
+    }
+}
+
+// p[i] <- the scores; slope[i] <- 1 - s_te for sigmoids.  A token whose
+// logits are all -inf scores 0 everywhere.
+template <int kLanes, int kV, bool kSlope>
+__device__ __forceinline__ void scores(int32_t score, float (&p)[kV], float (&slope)[kV]) {
+    float sum = 0.0f;
+    if (score == SCAPE_SCORE_SOFTMAX) {
+        float m = p[0];
+#pragma unroll
+        for (int i = 1; i < kV; ++i) m = fmaxf(m, p[i]);
+        m = group_reduce<OpMaxF, kLanes>(m);
+        if (m == kNegInf) m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            p[i] = fast_exp2((p[i] - m) * kLog2e);
+            sum += p[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const float e = fast_exp2(-p[i] * kLog2e);  // inf for -inf: a score of 0
+            p[i] = 1.0f / (1.0f + e);
+            if constexpr (kSlope) slope[i] = 1.0f / (1.0f + 1.0f / e);
+            sum += p[i];
+        }
+    }
+    sum = group_reduce<OpSumF, kLanes>(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) p[i] *= inv;
+}
+
+template <class T, int kLanes, int kGran, bool kVec>
+__global__ __launch_bounds__(kBalanceThreads) void k_balance_runs(BalanceArgs a) {
+    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBalanceWaves * kTokens;
+    __shared__ float part[kBalanceWaves][SCAPE_BALANCE_MAX_EXPERTS];
+    __shared__ int32_t hist[SCAPE_BALANCE_MAX_EXPERTS];
+    __shared__ int32_t s_tok;
+    const uint32_t tid = threadIdx.x, lane = lane_id(), wave = tid / 64, l = lane % kLanes;
+    const int32_t E = (int32_t)a.in.cols;
+    const Run r = run_of(a, (int32_t)blockIdx.x);
+    if (r.t0 >= r.t1) return;
+    for (int32_t e = (int32_t)tid; e < E; e += kBalanceThreads) hist[e] = 0;
+    if (tid == 0) s_tok = 0;
+    __syncthreads();
+
+    float acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+    uint32_t tokens = 0;
+    for (int32_t b = r.t0; b < r.t1; b += kStep) {
+        const int32_t t = b + (int32_t)(wave * kTokens + lane / kLanes);
+        const bool live = t < r.t1 && (!a.mask || a.mask[t] != 0);
+        float p[kV], none[kV];
+        load_token<T, kLanes, kGran, kVec>(a, t, live, l, p);
+        scores<kLanes, kV, false>(a.score, p, none);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] += live ? p[i] : 0.0f;
+        tokens += live && l == 0 ? 1u : 0u;
+    }
+    // the wave's groups, then the waves
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int d = kLanes; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d, 64);
+    if (lane < kLanes) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int32_t e = (int32_t)(l + (i / T::kN) * kLanes) * T::kN + i % T::kN;
+            if (e < E) part[wave][e] = acc[i];
+        }
+    }
+    tokens = wave_sum(tokens);
+    if (lane == 0) atomicAdd(&s_tok, (int32_t)tokens);
+    const int64_t c0 = (int64_t)r.t0 * a.k;
+    const uint32_t choices = (uint32_t)((int64_t)(r.t1 - r.t0) * a.k);
+    for (uint32_t f = tid; f < choices; f += kBalanceThreads) {
+        const int32_t e = a.idx[c0 + f];
+        if (e >= 0 && e < E && (!a.mask || a.mask[r.t0 + (int32_t)(f / (uint32_t)a.k)] != 0)) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    const int64_t o = (int64_t)blockIdx.x * E;
+    for (int32_t e = (int32_t)tid; e < E; e += kBalanceThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBalanceWaves; ++w) s += part[w][e];
+        a.part_psum[o + e] = s;
+        a.part_counts[o + e] = hist[e];
+    }
+    if (tid == 0) a.part_tok[blockIdx.x] = s_tok;
+}
+
+__device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t E, int32_t k, float alpha) {
+    if (n <= 0) return 0.0f;
+    return (float)((double)alpha * E / ((double)k * n * n) * dot);
+}
+
+// One workgroup a segment: the sums over its runs, and the loss.
+__global__ __launch_bounds__(kBalanceThreads) void k_balance_finish(BalanceArgs a) {
+    __shared__ double ps[kBalanceThreads];
+    __shared__ int32_t cs[kBalanceThreads];
+    __shared__ double wd[kBalanceWaves];
+    __shared__ int32_t s_tok;
+    const int32_t tid = (int32_t)threadIdx.x, E = (int32_t)a.in.cols, s = (int32_t)blockIdx.x;
+    const int32_t len = offset_at(a, s + 1) - offset_at(a, s);
+    const int32_t base = first_slot(a, s);
+    int32_t runs = len > 0 ? (len + a.run - 1) / a.run : 0;
+    if (runs > a.slots - base) runs = a.slots - base;
+    if (tid == 0) s_tok = 0;
+    __syncthreads();
+    int32_t tok = 0;
+    for (int32_t c = tid; c < runs; c += kBalanceThreads) tok += a.part_tok[base + c];
+    if (tok) atomicAdd(&s_tok, tok);
+    const int32_t wide = E < kBalanceThreads ? E : kBalanceThreads, deep = kBalanceThreads / wide;
+    const int32_t col = tid % wide, d = tid / wide;
+    double dot = 0.0;
+    for (int32_t e0 = 0; e0 < E; e0 += wide) {
+        const int32_t e = e0 + col;
+        double p = 0.0;
+        int32_t n = 0;
+        if (e < E && d < deep)
+            for (int32_t c = d; c < runs; c += deep) {
+                const int64_t o = (int64_t)(base + c) * E + e;
+                p += (double)a.part_psum[o];
+                n += a.part_counts[o];
+            }
+        ps[tid] = p;
+        cs[tid] = n;
+        __syncthreads();
+        if (d == 0 && e < E) {
+            for (int32_t i = 1; i < deep; ++i) {
+                p += ps[i * wide + col];
+                n += cs[i * wide + col];
+            }
+            a.counts[(int64_t)s * E + e] = n;
+            a.psum[(int64_t)s * E + e] = (float)p;
+            dot += (double)n * p;
+        }
+        __syncthreads();
+    }
+    dot = wave_sum_f64(dot);
+    if ((tid & 63) == 0) wd[tid / 64] = dot;
+    __syncthreads();
+    if (tid == 0) {
+        a.n_tok[s] = s_tok;
+        double t = 0.0;
+        for (int w = 0; w < kBalanceWaves; ++w) t += wd[w];
+        if (a.loss) a.loss[s] = balance_loss_of(t, s_tok, E, a.k, a.alpha);
+    }
+}
+
+__global__ __launch_bounds__(kBlock) void k_balance_loss(const int32_t* counts, const float* psum,
+                                                         const int32_t* n_tok, int32_t E, int32_t k, float alpha,
+                                                         float* loss) {
+    __shared__ double wd[kWaves];
+    const int64_t o = (int64_t)blockIdx.x * E;
+    double dot = 0.0;
+    for (int32_t e = (int32_t)threadIdx.x; e < E; e += kBlock) dot += (double)counts[o + e] * (double)psum[o + e];
+    dot = wave_sum_f64(dot);
+    if ((threadIdx.x & 63) == 0) wd[threadIdx.x / 64] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < kWaves; ++w) t += wd[w];
+        loss[blockIdx.x] = balance_loss_of(t, n_tok[blockIdx.x], E, k, alpha);
+    }
+}
+
+template <class T, int kLanes, int kGran, bool kVec>
+__global__ __launch_bounds__(kBalanceThreads) void k_balance_grad(BalanceArgs a) {
+    using raw = typename T::raw;
+    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBalanceWaves * kTokens;
+    const uint32_t lane = lane_id(), wave = threadIdx.x / 64, l = lane % kLanes;
+    const int32_t E = (int32_t)a.in.cols;
+    const Run r = run_of(a, (int32_t)blockIdx.x);
+    if (r.t0 >= r.t1) return;
+    float c[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        const int32_t e = (int32_t)(l + (i / T::kN) * kLanes) * T::kN + i % T::kN;
+        c[i] = e < E ? (float)a.counts[(int64_t)r.seg * E + e] : 0.0f;
+    }
+    const int32_t n = a.n_tok[r.seg];
+    const float up = a.dloss ? a.dloss[r.seg] : 1.0f;
+    const float G = n > 0 ? (float)((double)up * (double)a.alpha * E / ((double)a.k * n * n)) : 0.0f;
+    for (int32_t b = r.t0; b < r.t1; b += kStep) {
+        const int32_t t = b + (int32_t)(wave * kTokens + lane / kLanes);
+        const bool there = t < r.t1, live = there && (!a.mask || a.mask[t] != 0);
+        float p[kV], slope[kV];
+        load_token<T, kLanes, kGran, kVec>(a, t, live, l, p);
+        scores<kLanes, kV, true>(a.score, p, slope);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) dot += p[i] * c[i];
+        dot = group_reduce<OpSumF, kLanes>(dot);
+        if (!there) continue;
+        raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
+#pragma unroll
+        for (int q = 0; q < kGran; ++q) {
+            const int32_t e0 = (int32_t)(l + q * kLanes) * T::kN;
+            float v[T::kN];
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) {
+                const int i = q * T::kN + j;
+                v[j] = live ? G * p[i] * (c[i] - dot) : 0.0f;
+                if (a.score != SCAPE_SCORE_SOFTMAX && live) v[j] *= slope[i];
+            }
+            if (kVec && e0 + T::kN <= E) {
+                *reinterpret_cast<gran*>(dz + e0) = T::down(v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < T::kN; ++j)
+                    if (e0 + j < E) dz[e0 + j] = T::down1(v[j]);
+            }
+        }
+    }
+}
+
+template <class T, int kLanes, int kGran, bool kVec>
+static void runs_or_grad(hipStream_t s, const BalanceArgs& a) {
+    if (a.dz)
+        hipLaunchKernelGGL((k_balance_grad<T, kLanes, kGran, kVec>), dim3((uint32_t)a.slots), dim3(kBalanceThreads), 0,
+                           s, a);
+    else
+        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kVec>), dim3((uint32_t)a.slots), dim3(kBalanceThreads), 0,
+                           s, a);
+}
+
+template <class T, bool kVec>
+static void balance_lanes(hipStream_t s, const BalanceArgs& a) {
+    const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a token
+    if (g <= 4) runs_or_grad<T, 4, 1, kVec>(s, a);
+    else if (g <= 16) runs_or_grad<T, 16, 1, kVec>(s, a);
+    else if (g <= 32) runs_or_grad<T, 32, 1, kVec>(s, a);
+    else if (g <= 64) runs_or_grad<T, 64, 1, kVec>(s, a);
+    else if (g <= 128) runs_or_grad<T, 64, 2, kVec>(s, a);
+    else runs_or_grad<T, 64, 4, kVec>(s, a);
+}
+
+template <class T>
+static hipError_t balance_typed(hipStream_t s, const BalanceArgs& a) {
+    const size_t b = sizeof(typename T::raw);
+    bool vec = (uintptr_t)a.in.z % 16 == 0 && a.in.ld * b % 16 == 0;
+    if (a.dz) vec = vec && (uintptr_t)a.dz % 16 == 0 && a.ld_dz * b % 16 == 0;
+    if (vec)
+        balance_lanes<T, true>(s, a);
+    else
+        balance_lanes<T, false>(s, a);
+    return hipGetLastError();
+}
+
+static hipError_t balance_any(hipStream_t s, const BalanceArgs& a) {
+    if (a.in.dtype == SCAPE_DTYPE_F32) return balance_typed<F32>(s, a);
+    if (a.in.dtype == SCAPE_DTYPE_BF16) return balance_typed<BF16>(s, a);
+    return balance_typed<F16>(s, a);
+}
+
+hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a) {
+    if (a.in.rows > 0) {
+        const hipError_t e = balance_any(s, a);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(k_balance_finish, dim3((uint32_t)a.segments), dim3(kBalanceThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_loss(hipStream_t s, const int32_t* counts, const float* psum, const int32_t* n_tok,
+                               int32_t segments, int32_t experts, int32_t k, float alpha, float* loss) {
+    hipLaunchKernelGGL(k_balance_loss, dim3((uint32_t)segments), dim3(kBlock), 0, s, counts, psum, n_tok, experts, k,
+                       alpha, loss);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a) { return balance_any(s, a); }
+
+}  // namespace scape

@@ -1,0 +1,435 @@
+// k_topk.hip - the k largest entries of each row of a logit matrix, in order
+// (larger value first, equal values by the lower column), and the row's
+// log-sum-exp: the per-layer mask's tie rule on rows.  For gfx950.
+//
+// An entry's rank is one unsigned 64-bit number, (ordered value bits) << 32 |
+// ~column, so no two entries of a row are equal and the result does not
+// depend on the order in which candidates are found.
+//
+// Each kernel reads a row once, so what bounds it is the read of the logits.
+//  - k_topk_small: rows of up to 1024 columns (a router's experts), a group
+//    of lanes per row.
+//  - k_topk_rows: longer rows, a workgroup per row or part of one, the row in
+//    registers.
+//  - k_topk_merge: joins the parts of a split row.
+#include <float.h>
+
+#include "loss_device.h"
+
+namespace scape {
+
+// Unsigned order of floats: -inf < ... < -0 = +0 < ... < +inf < NaN.
+__device__ __forceinline__ uint32_t order_key(float f) {
+    uint32_t b = __float_as_uint(f + 0.0f);  // -0 becomes +0
+    if (f != f) return 0xFFFFFFFFu;
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order_key(-inf): no entry
+
+// Entry `r` of the row's result.
+template <class T>
+__device__ __forceinline__ void write_entry(const TopkArgs& a, int64_t row, int32_t r, uint64_t comp) {
+    const int64_t o = row * a.k + r;
+    const bool none = comp == 0;
+    const float v = none ? kNegInf : key_value((uint32_t)(comp >> 32));
+    static_cast<typename T::raw*>(a.val)[o] = T::down1(v);  // exact: v came from this type
+    a.idx[o] = none ? -1 : (int32_t)~(uint32_t)comp;
+}
+
+// log-sum-exp from sum = sum 2^(x - ref) in the base-2 domain.  The
+// reference is a float that the exponents were taken against exactly, so it
+// adds no error; only the last step rounds.
+__device__ __forceinline__ float lse_of(float ref, double sum) { return (float)(((double)ref + log2(sum)) * kLn2); }
+
+// ---------------------------------------------------------------------------
+// Long rows
+
+// Ranks the n candidates in list (n <= kTopkList, all different) and hands
+// the first k, in order, to emit(r, composite); slots past n get 0.
+template <class Emit>
+__device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
+    const uint32_t tid = threadIdx.x;
+    if (n <= kRowThreads) {
+        // each thread counts the candidates above its own
+        if (tid < n) {
+            const uint64_t mine = list[tid];
+            uint32_t r = 0;
+            for (uint32_t j = 0; j < n; ++j) r += list[j] > mine ? 1u : 0u;
+            if (r < (uint32_t)k) emit((int32_t)r, mine);
+        }
+    } else {
+        uint32_t p = kRowThreads * 2;
+        while (p < n) p <<= 1;
+        for (uint32_t i = n + tid; i < p; i += kRowThreads) list[i] = 0;
+        for (uint32_t size = 2; size <= p; size <<= 1)
+            for (uint32_t d = size >> 1; d > 0; d >>= 1) {
+                __syncthreads();
+                for (uint32_t t = tid; t < p / 2; t += kRowThreads) {
+                    const uint32_t i = 2 * t - (t & (d - 1)), j = i + d;
+                    const uint64_t x = list[i], y = list[j];
+                    if ((x < y) == ((i & size) == 0)) {
+                        list[i] = y;
+                        list[j] = x;
+                    }
+                }
+            }
+        __syncthreads();
+        for (uint32_t i = tid; i < (uint32_t)k && i < n; i += kRowThreads) emit((int32_t)i, list[i]);
+    }
+    for (uint32_t i = n + tid; i < (uint32_t)k; i += kRowThreads) emit((int32_t)i, 0ull);
+}
+
+// A workgroup takes `per` granules of a row into registers (kGran a thread at
+// most) and makes the row's k largest, or its part's, from them.
+//
+// Candidates: the k-th largest of the threads' maxima is at most the k-th
+// largest entry, and for k well below the number of threads only a few more
+// than k entries reach it.  Where they are more than the list holds (ties, or
+// k too large), the exact threshold comes from a radix selection that reads
+// the row again, from the caches, for each 8-bit digit.
+template <class T, int kGran>
+__global__ __launch_bounds__(kRowThreads) void k_topk_rows(TopkArgs a) {
+    __shared__ uint64_t list[kTopkList];
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t tmax[kRowThreads];
+    __shared__ float wmax[kRowWaves], wsum[kRowWaves];
+    __shared__ uint32_t s_n, s_bin, s_need, s_tau;
+    using raw = typename T::raw;
+    const uint32_t tid = threadIdx.x, wave = tid / 64;
+    const int64_t row = blockIdx.x / (uint32_t)a.splits;
+    const int32_t sp = (int32_t)(blockIdx.x % (uint32_t)a.splits);
+    const raw* z = static_cast<const raw*>(a.in.z) + row * a.in.ld;
+    const int lead = row_lead<T>(z);
+    const int32_t total = (int32_t)((lead + a.in.cols + T::kN - 1) / T::kN);
+    const int32_t g0 = sp * a.per;
+    const int32_t cnt = min(a.per, total - g0);  // may be <= 0 in the last split
+    const int64_t n = a.in.cols;
+    const int32_t k = a.k;
+
+    gran g[kGran];
+#pragma unroll
+    for (int c = 0; c < kGran; ++c) {
+        const int32_t gi = (int32_t)tid + c * kRowThreads;
+        // a granule outside the part lies at element n: nothing is read and all is -inf
+        const int64_t e0 = gi < cnt ? (int64_t)(g0 + gi) * T::kN - lead : n;
+        if (c * kRowThreads < cnt || c == 0) g[c] = load_granule<T>(z, e0, n);
+    }
+    if (tid == 0) s_n = 0;
+
+    // the threads' maxima (NaN left out)
+    float m = kNegInf;
+#pragma unroll
+    for (int c = 0; c < kGran; ++c)
+        if (c * kRowThreads < cnt || c == 0) {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) m = fmaxf(m, T::up(g[c], j));
+        }
+    tmax[tid] = order_key(m) >> 16;
+    const float wm = group_reduce<OpMaxF, 64>(m);
+    if ((tid & 63) == 0) wmax[wave] = wm;
+    __syncthreads();
+    float bm = wmax[0];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) bm = fmaxf(bm, wmax[w]);
+
+    // wave 0: the k-th largest of the maxima, to the top 16 bits of its key
+    if (wave == 0) {
+        uint32_t mk[kRowWaves];
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) mk[w] = tmax[w * 64 + tid];
+        uint32_t t = 0;
+        for (int b = 15; b >= 0; --b) {
+            const uint32_t x = t | (1u << b);
+            uint32_t count = 0;
+#pragma unroll
+            for (int w = 0; w < kRowWaves; ++w) count += (uint32_t)__popcll(wave_ballot(mk[w] >= x));
+            if (count >= (uint32_t)k) t = x;
+        }
+        if (tid == 0) s_tau = t;
+    }
+    // everyone: the sum against the maximum
+    const float ref = bm == kNegInf ? 0.0f : bm * a.c2;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kGran; ++c)
+        if (c * kRowThreads < cnt || c == 0) {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) sum += fast_exp2(__builtin_fmaf(T::up(g[c], j), a.c2, -ref));
+        }
+    const float ws = group_reduce<OpSumF, 64>(sum);
+    if ((tid & 63) == 0) wsum[wave] = ws;
+    __syncthreads();
+
+    // candidates: entries not below the threshold, which is finite (so -inf
+    // is never one, and NaN, which compares false, always is)
+    const float tau = fmaxf(key_value(s_tau << 16), -FLT_MAX);
+#pragma unroll
+    for (int c = 0; c < kGran; ++c)
+        if (c * kRowThreads < cnt || c == 0) {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) {
+                const float f = T::up(g[c], j);
+                if (!(f < tau)) {
+                    const uint32_t e = (uint32_t)((g0 + (int32_t)tid + c * kRowThreads) * T::kN - lead + j);
+                    const uint32_t at = atomicAdd(&s_n, 1u);
+                    if (at < kTopkList) list[at] = ((uint64_t)order_key(f) << 32) | (uint32_t)~e;
+                }
+            }
+        }
+    __syncthreads();
+    uint32_t found = s_n;
+    if (found > kTopkList) {
+        // radix selection over 8-bit digits of the composite, largest first
+        uint64_t prefix = 0;
+        uint32_t need = (uint32_t)k;
+        int shift = 56;
+        for (;; shift -= 8) {
+            if (shift == 24) {  // ~column >> 24 is 0xFF: columns are below 2^24
+                prefix = (prefix << 8) | 0xFFu;
+                continue;
+            }
+            for (uint32_t i = tid; i < 256; i += kRowThreads) hist[i] = 0;
+            __syncthreads();
+            for (int32_t g1 = 0; g1 < cnt; g1 += kRowThreads) {
+                const int32_t gi = g1 + (int32_t)tid;
+                const int64_t e0 = gi < cnt ? (int64_t)(g0 + gi) * T::kN - lead : n;
+                const gran x = load_granule<T>(z, e0, n);
+#pragma unroll
+                for (int j = 0; j < T::kN; ++j) {
+                    const float f = T::up(x, j);
+                    const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)(e0 + j);
+                    const bool in = f != kNegInf && (shift == 56 || (comp >> (shift + 8)) == prefix);
+                    hist_add_wave(hist, (uint32_t)(comp >> shift) & 255u, in);
+                }
+            }
+            __syncthreads();
+            if (wave == 0) {
+                // bins from the top, four a lane: the one that holds the need-th
+                uint32_t h[4], own = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own += h[i] = hist[255 - (4 * tid + i)];
+                const uint32_t upto = wave_inclusive_scan(own);
+                const uint64_t reach = wave_ballot(upto >= need);
+                // at least kTopkList entries are there, more than k
+                if (tid == (uint32_t)__builtin_ctzll(reach)) {
+                    uint32_t above = upto - own;
+                    uint32_t i = 0;
+#pragma unroll
+                    for (uint32_t u = 0; u < 3; ++u)
+                        if (i == u && above + h[u] < need) {
+                            above += h[u];
+                            i = u + 1;
+                        }
+                    s_bin = 255 - (4 * tid + i);
+                    s_need = need - above;
+                }
+            }
+            __syncthreads();
+            prefix = (prefix << 8) | s_bin;
+            need = s_need;
+            if ((uint32_t)k - need + hist[s_bin] <= kTopkList || shift == 0) break;
+            __syncthreads();
+        }
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        for (int32_t gi = (int32_t)tid; gi < cnt; gi += kRowThreads) {
+            const int64_t e0 = (int64_t)(g0 + gi) * T::kN - lead;
+            const gran x = load_granule<T>(z, e0, n);
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) {
+                const float f = T::up(x, j);
+                const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)(e0 + j);
+                if (f != kNegInf && (comp >> shift) >= prefix) list[atomicAdd(&s_n, 1u)] = comp;
+            }
+        }
+        __syncthreads();
+        found = s_n;
+    }
+
+    if (a.splits == 1) {
+        emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
+    } else {
+        uint64_t* out = a.cand + (row * a.splits + sp) * k;
+        emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { out[r] = comp; });
+    }
+    if (tid == 0) {
+        double sum64 = 0.0;
+        for (int w = 0; w < kRowWaves; ++w) sum64 += (double)wsum[w];
+        if (a.splits > 1)
+            a.part[row * a.splits + sp] = make_float2(ref, (float)sum64);
+        else if (a.lse)
+            a.lse[row] = lse_of(ref, sum64);
+    }
+}
+
+// The parts' candidates are sorted lists; an entry's rank in the row is its
+// place in its own list plus, for each other list, the number of entries
+// above it (a binary search).
+constexpr int kMergeLds = 4096;
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
+    __shared__ uint64_t lds[kMergeLds];
+    __shared__ uint32_t s_n;
+    const uint32_t tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const uint32_t k = (uint32_t)a.k, all = (uint32_t)a.splits * k;
+    const uint64_t* cand = a.cand + row * all;
+    if (tid == 0) s_n = 0;
+    if (all <= kMergeLds) {
+        for (uint32_t i = tid; i < all; i += kRowThreads) lds[i] = cand[i];
+        cand = lds;
+    }
+    __syncthreads();
+    uint32_t mine = 0;
+    for (uint32_t i = tid; i < all; i += kRowThreads) {
+        const uint64_t x = cand[i];
+        if (x == 0) continue;
+        ++mine;
+        const uint32_t own = i / k;
+        uint32_t r = i - own * k;
+        for (uint32_t s = 0; s < (uint32_t)a.splits && r < k; ++s) {
+            if (s == own) continue;
+            const uint64_t* l = cand + s * k;
+            uint32_t lo = 0, hi = k;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (l[mid] > x)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            r += lo;
+        }
+        if (r < k) write_entry<T>(a, row, (int32_t)r, x);
+    }
+    if (mine) atomicAdd(&s_n, mine);
+    __syncthreads();
+    for (uint32_t i = s_n + tid; i < k; i += kRowThreads) write_entry<T>(a, row, (int32_t)i, 0ull);
+    if (tid == 0 && a.lse) {
+        const float2* p = a.part + row * a.splits;
+        float ref = kNegInf;
+        for (int s = 0; s < a.splits; ++s)
+            if (p[s].y != 0.0f) ref = fmaxf(ref, p[s].x);
+        if (ref == kNegInf) ref = 0.0f;
+        double sum = 0.0;
+        for (int s = 0; s < a.splits; ++s)
+            if (p[s].y != 0.0f) sum += (double)p[s].y * exp2((double)p[s].x - (double)ref);
+        a.lse[row] = lse_of(ref, sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Short rows: kLanes lanes a row, kGran granules a lane; lane l holds the
+// granules l, l + kLanes, ...  (vec: rows on 16-byte boundaries; otherwise
+// element by element).  k rounds take the largest key of the group, and of
+// equal keys the lowest column, out of the lane that holds it.
+template <class T, int kLanes, int kGran, bool kVec>
+__global__ __launch_bounds__(kBlock) void k_topk_small(TopkArgs a) {
+    using raw = typename T::raw;
+    constexpr int kRowsPerWave = 64 / kLanes, kV = kGran * T::kN;
+    const uint32_t lane = lane_id(), l = lane % kLanes;
+    const int64_t row = ((int64_t)blockIdx.x * kWaves + threadIdx.x / 64) * kRowsPerWave + lane / kLanes;
+    const bool live = row < a.in.rows;
+    const raw* z = static_cast<const raw*>(a.in.z) + (live ? row : 0) * a.in.ld;
+    const int32_t n = live ? (int32_t)a.in.cols : 0;
+    uint32_t key[kV];
+    float x[kV];
+#pragma unroll
+    for (int c = 0; c < kGran; ++c) {
+        const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
+        gran g = {0u, 0u, 0u, 0u};
+        if (kVec && e0 + T::kN <= n) {
+            g = *reinterpret_cast<const gran*>(z + e0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) T::set(g, j, e0 + j < n ? z[e0 + j] : (raw)T::kNegInfBits);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kN; ++j) {
+            x[c * T::kN + j] = T::up(g, j);
+            key[c * T::kN + j] = order_key(x[c * T::kN + j]);
+        }
+    }
+    if (a.lse) {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < kV; ++i) m = fmaxf(m, x[i]);
+        m = group_reduce<OpMaxF, kLanes>(m);
+        const float ref = m == kNegInf ? 0.0f : m * a.c2;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sum += fast_exp2(__builtin_fmaf(x[i], a.c2, -ref));
+        sum = group_reduce<OpSumF, kLanes>(sum);
+        if (l == 0 && live) a.lse[row] = lse_of(ref, (double)sum);
+    }
+    for (int32_t r = 0; r < a.k; ++r) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int i = 1; i < kV; ++i) m = key[i] > m ? key[i] : m;
+        const uint32_t top = group_reduce<OpMaxU, kLanes>(m);
+        // the lowest column of those that hold it: granules lie in turn over
+        // the lanes, so by granule first, then by lane
+        uint32_t col = 0xFFFFFFFFu;
+        int slot = 0;
+#pragma unroll
+        for (int i = kV - 1; i >= 0; --i)
+            if (key[i] == top) {
+                col = (l + (uint32_t)(i / T::kN) * kLanes) * T::kN + (uint32_t)(i % T::kN);
+                slot = i;
+            }
+        const uint32_t first = ~group_reduce<OpMaxU, kLanes>(~col);
+        if (col == first) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (i == slot) key[i] = 0;
+            // 0 and -inf: no entry is left
+            if (live) write_entry<T>(a, row, r, top <= kKeyNegInf ? 0ull : ((uint64_t)top << 32) | (uint32_t)~first);
+        }
+    }
+}
+
+template <class T, int kLanes, int kGran>
+static void topk_small(hipStream_t s, const TopkArgs& a, bool vec) {
+    constexpr int rows = kWaves * (64 / kLanes);
+    const dim3 grid((uint32_t)((a.in.rows + rows - 1) / rows));
+    if (vec)
+        hipLaunchKernelGGL((k_topk_small<T, kLanes, kGran, true>), grid, dim3(kBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_topk_small<T, kLanes, kGran, false>), grid, dim3(kBlock), 0, s, a);
+}
+
+template <class T>
+static hipError_t topk_typed(hipStream_t s, const TopkArgs& a) {
+    if (topk_small(a.in.cols, a.k)) {
+        const bool vec = (uintptr_t)a.in.z % 16 == 0 && a.in.ld * sizeof(typename T::raw) % 16 == 0;
+        const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a row
+        if (g <= 4) topk_small<T, 4, 1>(s, a, vec);
+        else if (g <= 16) topk_small<T, 16, 1>(s, a, vec);
+        else if (g <= 64) topk_small<T, 64, 1>(s, a, vec);
+        else if (g <= 128) topk_small<T, 64, 2>(s, a, vec);
+        else topk_small<T, 64, 4>(s, a, vec);
+        return hipGetLastError();
+    }
+    const dim3 grid((uint32_t)(a.in.rows * a.splits));
+    const int32_t each = (a.per + kRowThreads - 1) / kRowThreads;
+    if (each <= 4) hipLaunchKernelGGL((k_topk_rows<T, 4>), grid, dim3(kRowThreads), 0, s, a);
+    else if (each <= 8) hipLaunchKernelGGL((k_topk_rows<T, 8>), grid, dim3(kRowThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_topk_rows<T, kRowGranules>), grid, dim3(kRowThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL((k_topk_merge<T>), dim3((uint32_t)a.in.rows), dim3(kRowThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_topk(hipStream_t s, const TopkArgs& a) {
+    if (a.in.dtype == SCAPE_DTYPE_F32) return topk_typed<F32>(s, a);
+    if (a.in.dtype == SCAPE_DTYPE_BF16) return topk_typed<BF16>(s, a);
+    return topk_typed<F16>(s, a);
+}
+
+}  // namespace scape

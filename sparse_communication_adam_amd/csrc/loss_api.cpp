@@ -1,0 +1,391 @@
+// loss_api.cpp - host side of the loss operators of include/scape.h: row
+// top-k, distillation from a teacher's top logits, router balance loss.
+// Arguments are validated here, before anything is launched; the operators
+// hold no state and allocate nothing.
+#include "loss_internal.h"
+
+#include <cmath>
+
+using namespace scape;
+
+namespace scape {
+
+// A row is split where it does not fit a workgroup's registers, and where
+// there are fewer rows than it takes to fill the 256 CUs: up to kFill
+// workgroups in all, none with less than a granule for every thread.
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols) {
+    constexpr int64_t kFill = 512;
+    const int64_t g = row_granules(dtype, cols);
+    const int64_t need = (g + kRowCapacity - 1) / kRowCapacity;
+    int64_t want = rows > 0 ? kFill / rows : 1;
+    if (want > g / kRowThreads) want = g / kRowThreads;
+    const int64_t n = want > need ? want : need;
+    const int64_t per = (g + n - 1) / n;
+    return RowSplit{(int32_t)((g + per - 1) / per), (int32_t)per};
+}
+
+}  // namespace scape
+
+namespace {
+
+constexpr size_t kWorkspaceAlign = 16;
+// A launch's threads are counted in 32 bits.
+constexpr int64_t kMaxRowBlocks = (int64_t(1) << 32) / kRowThreads - 1;
+constexpr int64_t kMaxSmallRows = int64_t(1) << 25;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxSegments = int64_t(1) << 22;
+constexpr int64_t kMaxElements = int64_t(1) << 46;  // rows * ld: far beyond memory, far below 2^63
+
+bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int check_dtype(int32_t dtype, const char* name) {
+    if (dtype != SCAPE_DTYPE_F32 && dtype != SCAPE_DTYPE_BF16 && dtype != SCAPE_DTYPE_F16)
+        return fail(SCAPE_ERR_INVALID_ARG, "%s: unknown type %d", name, dtype);
+    return SCAPE_OK;
+}
+
+// A matrix argument: its pointer may be NULL only where it holds no row.
+int check_matrix(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const char* name) {
+    if (rows > 0 && !p) return fail(SCAPE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!is_aligned(p, dtype_size(dtype))) return fail(SCAPE_ERR_ALIGN, "%s must be aligned to its element", name);
+    if (ld < cols) return fail(SCAPE_ERR_SHAPE, "%s: rows of %lld columns are %lld elements apart", name, (long long)cols,
+                               (long long)ld);
+    if (ld > kMaxElements || rows * (double)ld > (double)kMaxElements)
+        return fail(SCAPE_ERR_SHAPE, "%s is too large", name);
+    return SCAPE_OK;
+}
+
+int check_array(const void* p, size_t align, const char* name) {
+    if (!p) return fail(SCAPE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!is_aligned(p, align)) return fail(SCAPE_ERR_ALIGN, "%s must be %zu-byte aligned", name, align);
+    return SCAPE_OK;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (need == 0) return SCAPE_OK;
+    if (!ws) return fail(SCAPE_ERR_INVALID_ARG, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (have < need)
+        return fail(SCAPE_ERR_SHAPE, "workspace has %lld bytes, needs %lld", (long long)have, (long long)need);
+    if (!is_aligned(ws, kWorkspaceAlign)) return fail(SCAPE_ERR_ALIGN, "workspace must be %zu-byte aligned", kWorkspaceAlign);
+    return SCAPE_OK;
+}
+
+int check_scale(float scale) {
+    if (!(scale > 0.0f) || !std::isfinite(scale))
+        return fail(SCAPE_ERR_INVALID_ARG, "scale must be positive and finite");
+    return SCAPE_OK;
+}
+
+// Shapes of the row operators.
+int check_rows(int64_t rows, int64_t cols, int32_t k, int32_t max_k) {
+    if (rows < 0 || cols < 1) return fail(SCAPE_ERR_SHAPE, "rows must be >= 0 and cols >= 1");
+    if (cols > SCAPE_ROW_MAX_COLS)
+        return fail(SCAPE_ERR_SHAPE, "%lld columns exceed the maximum of %d", (long long)cols, SCAPE_ROW_MAX_COLS);
+    if (k < 1 || k > max_k) return fail(SCAPE_ERR_SHAPE, "k must be in 1..%d (got %d)", max_k, k);
+    return SCAPE_OK;
+}
+int check_blocks(int64_t rows, const RowSplit& sp) {
+    if (rows > kMaxRowBlocks / sp.splits) return fail(SCAPE_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
+    return SCAPE_OK;
+}
+
+float base2(float scale) { return (float)((double)scale * 1.44269504088896340736); }
+
+int topk_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* sp) {
+    int rc;
+    if ((rc = check_dtype(dtype, "z"))) return rc;
+    if ((rc = check_rows(rows, cols, k, SCAPE_TOPK_MAX_K))) return rc;
+    if (k > cols) return fail(SCAPE_ERR_SHAPE, "k = %d exceeds the row's %lld columns", k, (long long)cols);
+    *sp = RowSplit{1, 0};
+    if (topk_small(cols, k)) {
+        if (rows > kMaxSmallRows) return fail(SCAPE_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
+        return SCAPE_OK;
+    }
+    *sp = row_split(dtype, rows, cols);
+    return check_blocks(rows, *sp);
+}
+int64_t topk_bytes(int64_t rows, int32_t k, const RowSplit& sp) {
+    return sp.splits > 1 ? rows * sp.splits * ((int64_t)k * 8 + 8) : 0;
+}
+
+int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* sp) {
+    int rc;
+    if ((rc = check_dtype(dtype, "z"))) return rc;
+    if ((rc = check_rows(rows, cols, k, SCAPE_DISTILL_MAX_K))) return rc;
+    *sp = row_split(dtype, rows, cols);
+    return check_blocks(rows, *sp);
+}
+int64_t distill_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }
+
+int check_teacher(const scape_teacher* t, int64_t rows) {
+    if (!t) return fail(SCAPE_ERR_INVALID_ARG, "teacher is NULL");
+    int rc;
+    if ((rc = check_dtype(t->dtype, "teacher->val"))) return rc;
+    if (rows == 0) return SCAPE_OK;
+    if ((rc = check_array(t->val, dtype_size(t->dtype), "teacher->val"))) return rc;
+    if ((rc = check_array(t->idx, 4, "teacher->idx"))) return rc;
+    if (t->lse && !is_aligned(t->lse, 4)) return fail(SCAPE_ERR_ALIGN, "teacher->lse must be 4-byte aligned");
+    return SCAPE_OK;
+}
+
+int check_optional(const void* p, const char* name) {
+    if (p && !is_aligned(p, 4)) return fail(SCAPE_ERR_ALIGN, "%s must be 4-byte aligned", name);
+    return SCAPE_OK;
+}
+
+// Tokens of a run: whole steps of a workgroup, and about kRuns runs in all.
+// The forward pass joins its runs in one workgroup a segment, so it takes
+// fewer.
+int32_t balance_run(int64_t tokens, int64_t runs) {
+    constexpr int64_t kStep = 128;
+    int64_t r = (tokens + runs - 1) / runs;
+    r = (r + kStep - 1) / kStep * kStep;
+    return (int32_t)(r < kStep ? kStep : r);
+}
+constexpr int64_t kForwardRuns = 512, kBackwardRuns = 2048;
+
+int balance_shape(int32_t dtype, int64_t tokens, int32_t experts, int32_t segments) {
+    int rc;
+    if ((rc = check_dtype(dtype, "logits"))) return rc;
+    if (tokens < 0 || tokens > kMaxTokens) return fail(SCAPE_ERR_SHAPE, "tokens must be in 0..2^30");
+    if (experts < 1 || experts > SCAPE_BALANCE_MAX_EXPERTS)
+        return fail(SCAPE_ERR_SHAPE, "experts must be in 1..%d (got %d)", SCAPE_BALANCE_MAX_EXPERTS, experts);
+    if (segments < 1 || segments > kMaxSegments) return fail(SCAPE_ERR_SHAPE, "segments must be in 1..2^22");
+    return SCAPE_OK;
+}
+int check_choices(int64_t tokens, int32_t experts, int32_t k) {
+    if (k < 1 || k > experts) return fail(SCAPE_ERR_SHAPE, "k must be in 1..experts (got %d)", k);
+    if (tokens * k > INT32_MAX) return fail(SCAPE_ERR_SHAPE, "more than 2^31 - 1 choices");
+    return SCAPE_OK;
+}
+int check_alpha(float alpha) {
+    if (!std::isfinite(alpha)) return fail(SCAPE_ERR_INVALID_ARG, "alpha must be finite");
+    return SCAPE_OK;
+}
+int check_router(int32_t score, const int32_t* offsets, int32_t segments) {
+    if (score != SCAPE_SCORE_SOFTMAX && score != SCAPE_SCORE_SIGMOID)
+        return fail(SCAPE_ERR_INVALID_ARG, "unknown score %d", score);
+    if (!offsets && segments != 1) return fail(SCAPE_ERR_INVALID_ARG, "%d segments need offsets", segments);
+    return check_optional(offsets, "offsets");
+}
+int64_t balance_bytes(int64_t tokens, int32_t experts, int32_t segments) {
+    const int64_t slots = tokens / balance_run(tokens, kForwardRuns) + segments;
+    return slots * (8 * (int64_t)experts + 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+int scape_topk_rows_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    RowSplit sp;
+    if (int rc = topk_shape(dtype, rows, cols, k, &sp)) return rc;
+    *bytes = topk_bytes(rows, k, sp);
+    return SCAPE_OK;
+}
+
+int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t k, float scale,
+                    void* val, int32_t* idx, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+    RowSplit sp;
+    int rc;
+    if ((rc = topk_shape(dtype, rows, cols, k, &sp))) return rc;
+    if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if (rows == 0) return SCAPE_OK;
+    if ((rc = check_array(val, dtype_size(dtype), "val"))) return rc;
+    if ((rc = check_array(idx, 4, "idx"))) return rc;
+    if ((rc = check_optional(lse, "lse"))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, topk_bytes(rows, k, sp)))) return rc;
+    TopkArgs a{};
+    a.in = Logits{z, dtype, rows, cols, ld};
+    a.k = k;
+    a.c2 = base2(scale);
+    a.val = val;
+    a.idx = idx;
+    a.lse = lse;
+    a.splits = sp.splits;
+    a.per = sp.per;
+    a.cand = static_cast<uint64_t*>(workspace);
+    a.part = reinterpret_cast<float2*>(static_cast<uint64_t*>(workspace) + (sp.splits > 1 ? rows * sp.splits * k : 0));
+    const hipError_t e = launch_topk((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "row top-k");
+}
+
+int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    RowSplit sp;
+    if (int rc = distill_shape(dtype, rows, cols, k, &sp)) return rc;
+    *bytes = distill_bytes(rows, sp);
+    return SCAPE_OK;
+}
+
+int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                          const scape_teacher* teacher, float scale, const float* weight, float* loss, float* stats,
+                          void* dz, int64_t ld_dz, void* workspace, int64_t workspace_bytes, void* stream) {
+    RowSplit sp;
+    int rc;
+    if ((rc = check_teacher(teacher, rows))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, &sp))) return rc;
+    if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if (dz && (rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;
+    if (dz == z && dz && ld_dz != ld) return fail(SCAPE_ERR_SHAPE, "dz over z needs z's row distance");
+    if (rows == 0) return SCAPE_OK;
+    if ((rc = check_optional(weight, "weight"))) return rc;
+    if ((rc = check_array(loss, 4, "loss"))) return rc;
+    if ((rc = check_array(stats, 4, "stats"))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, distill_bytes(rows, sp)))) return rc;
+    DistillArgs a{};
+    a.in = Logits{z, dtype, rows, cols, ld};
+    a.t_val = teacher->val;
+    a.t_dtype = teacher->dtype;
+    a.t_idx = teacher->idx;
+    a.t_lse = teacher->lse;
+    a.k = teacher->k;
+    a.scale = scale;
+    a.c2 = base2(scale);
+    a.weight = weight;
+    a.loss = loss;
+    a.stats = stats;
+    a.dz = dz;
+    a.ld_dz = ld_dz;
+    a.part = static_cast<float2*>(workspace);
+    a.splits = sp.splits;
+    a.per = sp.per;
+    const hipError_t e = launch_distill_forward((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "distillation loss");
+}
+
+int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                           const scape_teacher* teacher, float scale, const float* weight, const float* stats,
+                           const float* dloss, void* dz, int64_t ld_dz, void* stream) {
+    RowSplit sp;
+    int rc;
+    if ((rc = check_teacher(teacher, rows))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, &sp))) return rc;
+    if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if ((rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;
+    if (dz == z && dz && ld_dz != ld) return fail(SCAPE_ERR_SHAPE, "dz over z needs z's row distance");
+    if (rows == 0) return SCAPE_OK;
+    if ((rc = check_optional(weight, "weight"))) return rc;
+    if ((rc = check_array(stats, 4, "stats"))) return rc;
+    if ((rc = check_optional(dloss, "dloss"))) return rc;
+    DistillArgs a{};
+    a.in = Logits{z, dtype, rows, cols, ld};
+    a.t_val = teacher->val;
+    a.t_dtype = teacher->dtype;
+    a.t_idx = teacher->idx;
+    a.t_lse = teacher->lse;
+    a.k = teacher->k;
+    a.scale = scale;
+    a.c2 = base2(scale);
+    a.weight = weight;
+    a.dloss = dloss;
+    a.stats = const_cast<float*>(stats);  // read only in this launch
+    a.dz = dz;
+    a.ld_dz = ld_dz;
+    a.splits = sp.splits;
+    a.per = sp.per;
+    const hipError_t e = launch_distill_backward((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "distillation gradient");
+}
+
+int scape_balance_workspace(int64_t tokens, int32_t experts, int32_t segments, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    if (int rc = balance_shape(SCAPE_DTYPE_F32, tokens, experts, segments)) return rc;
+    *bytes = balance_bytes(tokens, experts, segments);
+    return SCAPE_OK;
+}
+
+int scape_balance_forward(const void* logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t ld,
+                          const int32_t* idx, int32_t k, const int32_t* offsets, int32_t segments,
+                          const uint8_t* mask, int32_t score, float alpha, int32_t* counts, float* psum,
+                          int32_t* n_tok, float* loss, void* workspace, int64_t workspace_bytes, void* stream) {
+    int rc;
+    if ((rc = balance_shape(dtype, tokens, experts, segments))) return rc;
+    if ((rc = check_choices(tokens, experts, k))) return rc;
+    if ((rc = check_matrix(logits, dtype, tokens, experts, ld, "logits"))) return rc;
+    if ((rc = check_router(score, offsets, segments))) return rc;
+    if ((rc = check_alpha(alpha))) return rc;
+    if (tokens > 0 && (rc = check_array(idx, 4, "idx"))) return rc;
+    if ((rc = check_array(counts, 4, "counts"))) return rc;
+    if ((rc = check_array(psum, 4, "psum"))) return rc;
+    if ((rc = check_array(n_tok, 4, "n_tok"))) return rc;
+    if ((rc = check_optional(loss, "loss"))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, balance_bytes(tokens, experts, segments)))) return rc;
+    BalanceArgs a{};
+    a.in = Logits{logits, dtype, tokens, experts, ld};
+    a.idx = idx;
+    a.k = k;
+    a.offsets = offsets;
+    a.segments = segments;
+    a.mask = mask;
+    a.score = score;
+    a.alpha = alpha;
+    a.counts = counts;
+    a.psum = psum;
+    a.n_tok = n_tok;
+    a.loss = loss;
+    a.run = balance_run(tokens, kForwardRuns);
+    a.slots = (int32_t)(tokens / a.run + segments);
+    const int64_t cells = (int64_t)a.slots * experts;
+    a.part_psum = static_cast<float*>(workspace);
+    a.part_counts = static_cast<int32_t*>(workspace) + cells;
+    a.part_tok = static_cast<int32_t*>(workspace) + 2 * cells;
+    const hipError_t e = launch_balance_forward((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance loss");
+}
+
+int scape_balance_loss(const int32_t* counts, const float* psum, const int32_t* n_tok, int32_t segments,
+                       int32_t experts, int32_t k, float alpha, float* loss, void* stream) {
+    int rc;
+    if ((rc = balance_shape(SCAPE_DTYPE_F32, 0, experts, segments))) return rc;
+    if ((rc = check_choices(0, experts, k))) return rc;
+    if ((rc = check_alpha(alpha))) return rc;
+    if ((rc = check_array(counts, 4, "counts"))) return rc;
+    if ((rc = check_array(psum, 4, "psum"))) return rc;
+    if ((rc = check_array(n_tok, 4, "n_tok"))) return rc;
+    if ((rc = check_array(loss, 4, "loss"))) return rc;
+    const hipError_t e = launch_balance_loss((hipStream_t)stream, counts, psum, n_tok, segments, experts, k, alpha, loss);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance loss");
+}
+
+int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k,
+                           const int32_t* offsets, int32_t segments, const uint8_t* mask, int32_t score, float alpha,
+                           const int32_t* counts, const int32_t* n_tok, const float* dloss, void* dlogits,
+                           int64_t ld_d, void* stream) {
+    int rc;
+    if ((rc = balance_shape(dtype, tokens, experts, segments))) return rc;
+    if ((rc = check_choices(tokens, experts, k))) return rc;
+    if ((rc = check_matrix(logits, dtype, tokens, experts, ld, "logits"))) return rc;
+    if ((rc = check_matrix(dlogits, dtype, tokens, experts, ld_d, "dlogits"))) return rc;
+    if (dlogits == logits && dlogits && ld_d != ld)
+        return fail(SCAPE_ERR_SHAPE, "dlogits over logits needs the logits' row distance");
+    if ((rc = check_router(score, offsets, segments))) return rc;
+    if ((rc = check_alpha(alpha))) return rc;
+    if (tokens == 0) return SCAPE_OK;
+    if ((rc = check_array(counts, 4, "counts"))) return rc;
+    if ((rc = check_array(n_tok, 4, "n_tok"))) return rc;
+    if ((rc = check_optional(dloss, "dloss"))) return rc;
+    BalanceArgs a{};
+    a.in = Logits{logits, dtype, tokens, experts, ld};
+    a.k = k;
+    a.offsets = offsets;
+    a.segments = segments;
+    a.mask = mask;
+    a.score = score;
+    a.alpha = alpha;
+    a.counts = const_cast<int32_t*>(counts);  // read only in this launch
+    a.n_tok = const_cast<int32_t*>(n_tok);
+    a.dloss = dloss;
+    a.dz = dlogits;
+    a.ld_dz = ld_d;
+    a.run = balance_run(tokens, kBackwardRuns);
+    a.slots = (int32_t)(tokens / a.run + segments);
+    const hipError_t e = launch_balance_backward((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance gradient");
+}
+
+}  // extern "C"

@@ -1,0 +1,117 @@
+// loss_internal.h - types shared by the host side of the loss operators
+// (loss_api.cpp) and their kernels (k_topk.hip, k_distill.hip,
+// k_balance.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "scape.h"
+
+namespace scape {
+
+// Errors and checks shared with scape_api.cpp.
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int hip_fail(hipError_t e, const char* what);
+
+// A matrix of logits: rows of `cols` elements, `ld` elements apart.
+struct Logits {
+    const void* z;
+    int32_t dtype;
+    int64_t rows, cols, ld;
+};
+inline int dtype_size(int32_t dtype) { return dtype == SCAPE_DTYPE_F32 ? 4 : 2; }
+
+// ---------------------------------------------------------------------------
+// Row kernels: a workgroup of kRowThreads threads holds a run of a row's
+// granules in registers, at most kRowGranules a thread; a longer row, or one
+// of few rows, is split over several workgroups.
+constexpr int kRowThreads = 512;
+constexpr int kRowWaves = kRowThreads / 64;
+constexpr int kRowGranules = 16;
+constexpr int64_t kRowCapacity = (int64_t)kRowThreads * kRowGranules;
+
+// Granules a row of `cols` elements can touch, whatever its alignment.
+inline int64_t row_granules(int32_t dtype, int64_t cols) {
+    const int n = 16 / dtype_size(dtype);
+    return (cols + n - 1 + n - 1) / n;
+}
+
+// Workgroups a row is split over.
+struct RowSplit {
+    int32_t splits;
+    int32_t per;  // granules of each split (the last one may have fewer)
+};
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols);
+
+// ---- k_topk.hip
+constexpr int kTopkList = 2048;       // candidates a workgroup sorts in LDS (>= SCAPE_TOPK_MAX_K)
+constexpr int kTopkSmallCols = 1024;  // rows that a wave or part of one holds
+constexpr int kTopkSmallK = 32;
+inline bool topk_small(int64_t cols, int32_t k) { return cols <= kTopkSmallCols && k <= kTopkSmallK; }
+struct TopkArgs {
+    Logits in;
+    int32_t k;
+    float c2;  // scale * log2(e)
+    void* val;
+    int32_t* idx;
+    float* lse;       // or NULL
+    uint64_t* cand;   // splits > 1: [rows][splits][k] candidates, then
+    float2* part;     // [rows][splits] (reference, sum)
+    int32_t splits, per;
+};
+hipError_t launch_topk(hipStream_t s, const TopkArgs& a);
+
+// ---- k_distill.hip
+struct DistillArgs {
+    Logits in;
+    const void* t_val;
+    int32_t t_dtype;
+    const int32_t* t_idx;
+    const float* t_lse;  // or NULL: renormalised over the entries
+    int32_t k;
+    float scale, c2;     // c2 = scale * log2(e)
+    const float* weight; // or NULL
+    const float* dloss;  // backward only, or NULL
+    float* loss;
+    float* stats;        // [rows][2]
+    void* dz;            // or NULL
+    int64_t ld_dz;
+    float2* part;        // splits > 1: [rows][splits] (reference, sum)
+    int32_t splits, per;
+};
+hipError_t launch_distill_forward(hipStream_t s, const DistillArgs& a);
+hipError_t launch_distill_backward(hipStream_t s, const DistillArgs& a);
+
+// ---- k_balance.hip
+constexpr int kBalanceThreads = 512;
+// The tokens of a segment are cut into runs of `run` tokens, one workgroup
+// each.  Segment s's runs start at slot offsets[s] / run + s: no two segments
+// share a slot, and tokens / run + segments slots hold them all.
+struct BalanceArgs {
+    Logits in;             // rows: tokens, cols: experts
+    const int32_t* idx;    // [tokens][k]
+    int32_t k;
+    const int32_t* offsets;  // [segments + 1], or NULL: one segment of all tokens
+    int32_t segments;
+    const uint8_t* mask;   // [tokens], or NULL
+    int32_t score;
+    float alpha;
+    int32_t* counts;       // [segments][experts]
+    float* psum;           // [segments][experts]
+    int32_t* n_tok;        // [segments]
+    float* loss;           // [segments], or NULL
+    const float* dloss;    // backward only: [segments], or NULL
+    void* dz;
+    int64_t ld_dz;
+    int32_t run, slots;
+    float* part_psum;      // [slots][experts]
+    int32_t* part_counts;  // [slots][experts]
+    int32_t* part_tok;     // [slots]
+};
+hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a);
+hipError_t launch_balance_loss(hipStream_t s, const int32_t* counts, const float* psum, const int32_t* n_tok,
+                               int32_t segments, int32_t experts, int32_t k, float alpha, float* loss);
+hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a);
+
+}  // namespace scape

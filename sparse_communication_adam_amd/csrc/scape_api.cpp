@@ -10,13 +10,17 @@
 #include <string>
 #include <vector>
 
+#include "loss_internal.h"
 #include "scape_internal.h"
 
 using namespace scape;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+// Used by loss_api.cpp too.
+namespace scape {
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -31,6 +35,10 @@ int fail(int code, const char* fmt, ...) {
 int hip_fail(hipError_t e, const char* what) {
     return fail(SCAPE_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
+
+}  // namespace scape
+
+namespace {
 
 #define SCAPE_HIP(call, what)                      \
     do {                                           \
