@@ -343,6 +343,8 @@ def _own(s):
         sc.scape_balance_forward(s["z"], s["idx"], s["counts"], s["psum"], s["n_tok"], s["loss"], alpha=s["alpha"],
                                  offsets=s["offsets"], mask=s["mask"], score=c["score"], workspace=ws)
         return dict(counts=s["counts"], psum=s["psum"], n_tok=s["n_tok"], loss=s["loss"])
+    if not s["counts"].is_contiguous():
+        s["counts"] = s["counts"].contiguous()  # as the forward call writes them
     sc.scape_balance_backward(s["z"], s["counts"], s["n_tok"], s["dloss"], s["dz"], k=c["k"], alpha=s["alpha"],
                               offsets=s["offsets"], mask=s["mask"], score=c["score"])
     return dict(dz=s["dz"])
