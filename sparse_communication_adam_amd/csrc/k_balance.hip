@@ -20,6 +20,7 @@
 namespace scape {
 
 constexpr int kBalanceWaves = kBalanceThreads / 64;
+static_assert(SCAPE_BALANCE_MAX_EXPERTS <= 1024, "a thread for each expert in k_balance_finish");
 
 struct Run {
     int32_t seg, t0, t1;  // tokens [t0, t1) of segment seg
@@ -34,72 +35,82 @@ __device__ __forceinline__ int32_t offset_at(const BalanceArgs& a, int32_t s) {
 }
 __device__ __forceinline__ int32_t first_slot(const BalanceArgs& a, int32_t s) { return offset_at(a, s) / a.run + s; }
 
+// The run of a slot: the last segment that starts at or before it, found by a
+// whole wave, 64 segments (or strides of segments) a step.
 __device__ __forceinline__ Run run_of(const BalanceArgs& a, int32_t slot) {
-    int32_t lo = 0, hi = a.segments;  // the last segment that starts at or before the slot
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) / 2;
-        if (first_slot(a, mid) <= slot)
-            lo = mid;
-        else
-            hi = mid;
+    int32_t lo = 0;
+    if (a.offsets) {
+        for (int32_t n = a.segments; n > 1;) {
+            const int32_t step = (n + 63) / 64, s = lo + (int32_t)lane_id() * step;
+            const int32_t at = s < lo + n ? first_slot(a, s) : 0x7FFFFFFF;
+            const int32_t below = (int32_t)__popcll(wave_ballot(at <= slot));
+            const int32_t k = below > 0 ? below - 1 : 0;
+            lo += k * step;
+            n -= k * step;
+            n = n < step ? n : step;
+        }
     }
-    const int64_t t0 = offset_at(a, lo) + (int64_t)(slot - first_slot(a, lo)) * a.run;
+    const int32_t f = first_slot(a, lo);
+    const int64_t t0 = offset_at(a, lo) + (int64_t)(slot - f) * a.run;
     const int64_t end = offset_at(a, lo + 1), t1 = t0 + a.run;
-    if (slot < first_slot(a, lo) || t0 >= end) return Run{lo, 0, 0};
+    if (slot < f || t0 >= end) return Run{lo, 0, 0};
     return Run{lo, (int32_t)t0, (int32_t)(t1 < end ? t1 : end)};
 }
 
-// A token's logits in a group of lanes: lane l has granules l, l + kLanes, ...
+// A token's logits in a group of lanes: lane l has granules l, l + kLanes,
+// ...; past the last expert, and of tokens that do not count, -inf.
 template <class T, int kLanes, int kGran, bool kVec>
-__device__ __forceinline__ void load_token(const BalanceArgs& a, int64_t t, bool live, uint32_t l,
-                                           float (&x)[kGran * T::kN]) {
+__device__ __forceinline__ void load_token(const BalanceArgs& a, int64_t t, bool live, uint32_t l, gran (&g)[kGran]) {
     using raw = typename T::raw;
     const raw* z = static_cast<const raw*>(a.in.z) + (live ? t : 0) * a.in.ld;
     const int32_t n = live ? (int32_t)a.in.cols : 0;
 #pragma unroll
     for (int c = 0; c < kGran; ++c) {
         const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
-        gran g = {0u, 0u, 0u, 0u};
+        g[c] = no_entries<T>();
         if (kVec && e0 + T::kN <= n) {
-            g = *reinterpret_cast<const gran*>(z + e0);
+            g[c] = *reinterpret_cast<const gran*>(z + e0);
         } else {
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) T::set(g, j, e0 + j < n ? z[e0 + j] : (raw)T::kNegInfBits);
+            for (int j = 0; j < T::kN; ++j)
+                if (e0 + j < n) T::set(g[c], j, z[e0 + j]);
         }
-#pragma unroll
-        for (int j = 0; j < T::kN; ++j) x[c * T::kN + j] = T::up(g, j);
     }
 }
 
-// p[i] <- the scores; slope[i] <- 1 - s_te for sigmoids.  A token whose
-// logits are all -inf scores 0 everywhere.
-template <int kLanes, int kV, bool kSlope>
-__device__ __forceinline__ void scores(int32_t score, float (&p)[kV], float (&slope)[kV]) {
+// A token's scores, not yet divided by their sum: w[i], and 1 / sum.  A token
+// whose logits are all -inf has 0 for both.  For sigmoids grad[i] is
+// s (1 - s), the slope of the score.  v_exp_f32 and v_rcp_f32 are good to a
+// step of float32.
+template <class T, int kLanes, int kGran, bool kGrad>
+__device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], float (&w)[kGran * T::kN],
+                                        float (&grad)[kGran * T::kN]) {
     float sum = 0.0f;
     if (score == SCAPE_SCORE_SOFTMAX) {
-        float m = p[0];
+        float m = granule_max<T>(g[0]);
 #pragma unroll
-        for (int i = 1; i < kV; ++i) m = fmaxf(m, p[i]);
+        for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(g[c]));
         m = group_reduce<OpMaxF, kLanes>(m);
-        if (m == kNegInf) m = 0.0f;
+        // the reference is a float that all exponents are taken against
+        // exactly, and it cancels in the division
+        const float ref = m == kNegInf ? 0.0f : m * kLog2e;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            p[i] = fast_exp2((p[i] - m) * kLog2e);
-            sum += p[i];
+        for (int i = 0; i < kGran * T::kN; ++i) {
+            w[i] = fast_exp2(__builtin_fmaf(T::up(g[i / T::kN], i % T::kN), kLog2e, -ref));
+            if constexpr (kGrad) grad[i] = w[i];
+            sum += w[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float e = fast_exp2(-p[i] * kLog2e);  // inf for -inf: a score of 0
-            p[i] = 1.0f / (1.0f + e);
-            if constexpr (kSlope) slope[i] = 1.0f / (1.0f + 1.0f / e);
-            sum += p[i];
+        for (int i = 0; i < kGran * T::kN; ++i) {
+            const float e = fast_exp2(T::up(g[i / T::kN], i % T::kN) * -kLog2e);  // inf for -inf: a score of 0
+            w[i] = __builtin_amdgcn_rcpf(1.0f + e);
+            if constexpr (kGrad) grad[i] = e < 1e30f ? w[i] * (e * w[i]) : w[i];
+            sum += w[i];
         }
     }
     sum = group_reduce<OpSumF, kLanes>(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) p[i] *= inv;
+    return sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 }
 
 template <class T, int kLanes, int kGran, bool kVec>
@@ -120,15 +131,23 @@ __global__ __launch_bounds__(kBalanceThreads) void k_balance_runs(BalanceArgs a)
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
     uint32_t tokens = 0;
+    // the next token's logits are on their way while this one's are worked on
+    const int32_t mine = (int32_t)(wave * kTokens + lane / kLanes);
+    auto counts = [&](int32_t t) { return t < r.t1 && (!a.mask || a.mask[t] != 0); };
+    bool live = counts(r.t0 + mine);
+    gran g[kGran], next[kGran];
+    load_token<T, kLanes, kGran, kVec>(a, r.t0 + mine, live, l, g);
     for (int32_t b = r.t0; b < r.t1; b += kStep) {
-        const int32_t t = b + (int32_t)(wave * kTokens + lane / kLanes);
-        const bool live = t < r.t1 && (!a.mask || a.mask[t] != 0);
-        float p[kV], none[kV];
-        load_token<T, kLanes, kGran, kVec>(a, t, live, l, p);
-        scores<kLanes, kV, false>(a.score, p, none);
+        const bool live1 = counts(b + kStep + mine);
+        load_token<T, kLanes, kGran, kVec>(a, b + kStep + mine, live1, l, next);
+        float w[kV], none[kV];
+        const float inv = scores<T, kLanes, kGran, false>(a.score, g, w, none);  // a token that does not count: 0
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] += live ? p[i] : 0.0f;
+        for (int i = 0; i < kV; ++i) acc[i] = __builtin_fmaf(w[i], inv, acc[i]);
         tokens += live && l == 0 ? 1u : 0u;
+        live = live1;
+#pragma unroll
+        for (int c = 0; c < kGran; ++c) g[c] = next[c];
     }
     // the wave's groups, then the waves
 #pragma unroll
@@ -167,11 +186,14 @@ __device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t 
     return (float)((double)alpha * E / ((double)k * n * n) * dot);
 }
 
-// One workgroup a segment: the sums over its runs, and the loss.
-__global__ __launch_bounds__(kBalanceThreads) void k_balance_finish(BalanceArgs a) {
-    __shared__ double ps[kBalanceThreads];
-    __shared__ int32_t cs[kBalanceThreads];
-    __shared__ double wd[kBalanceWaves];
+// One workgroup a segment: the sums over its runs, and the loss.  A column's
+// runs are dealt out over as many threads as there are columns to spare, eight
+// loads of each in flight, and joined in order.
+constexpr int kFinishThreads = 1024;
+__global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a) {
+    __shared__ double ps[kFinishThreads];
+    __shared__ int32_t cs[kFinishThreads];
+    __shared__ double wd[kFinishThreads / 64];
     __shared__ int32_t s_tok;
     const int32_t tid = (int32_t)threadIdx.x, E = (int32_t)a.in.cols, s = (int32_t)blockIdx.x;
     const int32_t len = offset_at(a, s + 1) - offset_at(a, s);
@@ -181,34 +203,43 @@ __global__ __launch_bounds__(kBalanceThreads) void k_balance_finish(BalanceArgs 
     if (tid == 0) s_tok = 0;
     __syncthreads();
     int32_t tok = 0;
-    for (int32_t c = tid; c < runs; c += kBalanceThreads) tok += a.part_tok[base + c];
+    for (int32_t c = tid; c < runs; c += kFinishThreads) tok += a.part_tok[base + c];
     if (tok) atomicAdd(&s_tok, tok);
-    const int32_t wide = E < kBalanceThreads ? E : kBalanceThreads, deep = kBalanceThreads / wide;
-    const int32_t col = tid % wide, d = tid / wide;
-    double dot = 0.0;
-    for (int32_t e0 = 0; e0 < E; e0 += wide) {
-        const int32_t e = e0 + col;
-        double p = 0.0;
-        int32_t n = 0;
-        if (e < E && d < deep)
-            for (int32_t c = d; c < runs; c += deep) {
-                const int64_t o = (int64_t)(base + c) * E + e;
-                p += (double)a.part_psum[o];
-                n += a.part_counts[o];
+    const int32_t deep = kFinishThreads / E;  // E <= kFinishThreads
+    const int32_t e = tid % E, d = tid / E;
+    double p = 0.0, dot = 0.0;
+    int32_t n = 0;
+    if (d < deep) {
+        constexpr int kBatch = 8;
+        for (int32_t c0 = d; c0 < runs; c0 += deep * kBatch) {
+            float x[kBatch];
+            int32_t y[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int32_t c = c0 + i * deep;
+                const int64_t o = (int64_t)(base + (c < runs ? c : c0)) * E + e;
+                x[i] = a.part_psum[o];
+                y[i] = a.part_counts[o];
             }
-        ps[tid] = p;
-        cs[tid] = n;
-        __syncthreads();
-        if (d == 0 && e < E) {
-            for (int32_t i = 1; i < deep; ++i) {
-                p += ps[i * wide + col];
-                n += cs[i * wide + col];
-            }
-            a.counts[(int64_t)s * E + e] = n;
-            a.psum[(int64_t)s * E + e] = (float)p;
-            dot += (double)n * p;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (c0 + i * deep < runs) {
+                    p += (double)x[i];
+                    n += y[i];
+                }
         }
-        __syncthreads();
+    }
+    ps[tid] = p;
+    cs[tid] = n;
+    __syncthreads();
+    if (d == 0) {
+        for (int32_t i = 1; i < deep; ++i) {
+            p += ps[i * E + e];
+            n += cs[i * E + e];
+        }
+        a.counts[(int64_t)s * E + e] = n;
+        a.psum[(int64_t)s * E + e] = (float)p;
+        dot = (double)n * p;
     }
     dot = wave_sum_f64(dot);
     if ((tid & 63) == 0) wd[tid / 64] = dot;
@@ -216,7 +247,7 @@ __global__ __launch_bounds__(kBalanceThreads) void k_balance_finish(BalanceArgs 
     if (tid == 0) {
         a.n_tok[s] = s_tok;
         double t = 0.0;
-        for (int w = 0; w < kBalanceWaves; ++w) t += wd[w];
+        for (int w = 0; w < kFinishThreads / 64; ++w) t += wd[w];
         if (a.loss) a.loss[s] = balance_loss_of(t, s_tok, E, a.k, a.alpha);
     }
 }
@@ -255,36 +286,45 @@ __global__ __launch_bounds__(kBalanceThreads) void k_balance_grad(BalanceArgs a)
     const int32_t n = a.n_tok[r.seg];
     const float up = a.dloss ? a.dloss[r.seg] : 1.0f;
     const float G = n > 0 ? (float)((double)up * (double)a.alpha * E / ((double)a.k * n * n)) : 0.0f;
+    const int32_t mine = (int32_t)(wave * kTokens + lane / kLanes);
+    auto counts = [&](int32_t t) { return t < r.t1 && (!a.mask || a.mask[t] != 0); };
+    bool live = counts(r.t0 + mine);
+    gran g[kGran], next[kGran];
+    load_token<T, kLanes, kGran, kVec>(a, r.t0 + mine, live, l, g);
     for (int32_t b = r.t0; b < r.t1; b += kStep) {
-        const int32_t t = b + (int32_t)(wave * kTokens + lane / kLanes);
-        const bool there = t < r.t1, live = there && (!a.mask || a.mask[t] != 0);
-        float p[kV], slope[kV];
-        load_token<T, kLanes, kGran, kVec>(a, t, live, l, p);
-        scores<kLanes, kV, true>(a.score, p, slope);
+        const int32_t t = b + mine;
+        const bool live1 = counts(t + kStep);
+        load_token<T, kLanes, kGran, kVec>(a, t + kStep, live1, l, next);
+        float w[kV], grad[kV];
+        const float inv = scores<T, kLanes, kGran, true>(a.score, g, w, grad);
         float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) dot += p[i] * c[i];
-        dot = group_reduce<OpSumF, kLanes>(dot);
-        if (!there) continue;
-        raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
+        for (int i = 0; i < kV; ++i) dot = __builtin_fmaf(w[i], c[i], dot);
+        dot = group_reduce<OpSumF, kLanes>(dot) * inv;
+        const float up1 = G * inv;
+        if (t < r.t1) {
+            raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
 #pragma unroll
-        for (int q = 0; q < kGran; ++q) {
-            const int32_t e0 = (int32_t)(l + q * kLanes) * T::kN;
-            float v[T::kN];
+            for (int q = 0; q < kGran; ++q) {
+                const int32_t e0 = (int32_t)(l + q * kLanes) * T::kN;
+                float v[T::kN];
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) {
-                const int i = q * T::kN + j;
-                v[j] = live ? G * p[i] * (c[i] - dot) : 0.0f;
-                if (a.score != SCAPE_SCORE_SOFTMAX && live) v[j] *= slope[i];
-            }
-            if (kVec && e0 + T::kN <= E) {
-                *reinterpret_cast<gran*>(dz + e0) = T::down(v);
-            } else {
+                for (int j = 0; j < T::kN; ++j) {
+                    const int i = q * T::kN + j;
+                    v[j] = live ? up1 * grad[i] * (c[i] - dot) : 0.0f;
+                }
+                if (kVec && e0 + T::kN <= E) {
+                    *reinterpret_cast<gran*>(dz + e0) = T::down(v);
+                } else {
 #pragma unroll
-                for (int j = 0; j < T::kN; ++j)
-                    if (e0 + j < E) dz[e0 + j] = T::down1(v[j]);
+                    for (int j = 0; j < T::kN; ++j)
+                        if (e0 + j < E) dz[e0 + j] = T::down1(v[j]);
+                }
             }
         }
+        live = live1;
+#pragma unroll
+        for (int q = 0; q < kGran; ++q) g[q] = next[q];
     }
 }
 
@@ -305,8 +345,8 @@ static void balance_lanes(hipStream_t s, const BalanceArgs& a) {
     else if (g <= 16) runs_or_grad<T, 16, 1, kVec>(s, a);
     else if (g <= 32) runs_or_grad<T, 32, 1, kVec>(s, a);
     else if (g <= 64) runs_or_grad<T, 64, 1, kVec>(s, a);
-    else if (g <= 128) runs_or_grad<T, 64, 2, kVec>(s, a);
-    else runs_or_grad<T, 64, 4, kVec>(s, a);
+    else if (T::kN == 8 || g <= 128) runs_or_grad<T, 64, 2, kVec>(s, a);
+    else if constexpr (T::kN == 4) runs_or_grad<T, 64, 4, kVec>(s, a);
 }
 
 template <class T>
@@ -332,7 +372,7 @@ hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a) {
         const hipError_t e = balance_any(s, a);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_balance_finish, dim3((uint32_t)a.segments), dim3(kBalanceThreads), 0, s, a);
+    hipLaunchKernelGGL(k_balance_finish, dim3((uint32_t)a.segments), dim3(kFinishThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -58,6 +58,7 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
         if (tid < n) {
             const uint64_t mine = list[tid];
             uint32_t r = 0;
+#pragma unroll 4
             for (uint32_t j = 0; j < n; ++j) r += list[j] > mine ? 1u : 0u;
             if (r < (uint32_t)k) emit((int32_t)r, mine);
         }
@@ -88,53 +89,56 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
 //
 // Candidates: the k-th largest of the threads' maxima is at most the k-th
 // largest entry, and for k well below the number of threads only a few more
-// than k entries reach it.  Where they are more than the list holds (ties, or
-// k too large), the exact threshold comes from a radix selection that reads
-// the row again, from the caches, for each 8-bit digit.
+// than k entries reach it.  Granules whose maximum reaches it are copied to
+// LDS and gone through there, so a thread with such a granule does not hold
+// up its wave.  Where there are more than the lists hold (ties, or k near the
+// number of threads), the exact threshold comes from a radix selection that
+// reads the row again, from the caches, for each 8-bit digit.
+constexpr int kTopkHits = 768;  // granules
 template <class T, int kGran>
-__global__ __launch_bounds__(kRowThreads) void k_topk_rows(TopkArgs a) {
+__global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(TopkArgs a) {
     __shared__ uint64_t list[kTopkList];
+    __shared__ gran hit[kTopkHits];
+    __shared__ int32_t hit_at[kTopkHits];
     __shared__ uint32_t hist[256];
     __shared__ uint32_t tmax[kRowThreads];
     __shared__ float wmax[kRowWaves], wsum[kRowWaves];
-    __shared__ uint32_t s_n, s_bin, s_need, s_tau;
+    __shared__ uint32_t s_n, s_hits, s_bin, s_need, s_tau;
     using raw = typename T::raw;
-    const uint32_t tid = threadIdx.x, wave = tid / 64;
+    const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const int64_t row = blockIdx.x / (uint32_t)a.splits;
     const int32_t sp = (int32_t)(blockIdx.x % (uint32_t)a.splits);
     const raw* z = static_cast<const raw*>(a.in.z) + row * a.in.ld;
-    const int lead = row_lead<T>(z);
-    const int32_t total = (int32_t)((lead + a.in.cols + T::kN - 1) / T::kN);
+    const int32_t n = (int32_t)a.in.cols, k = a.k;
+    const RowShape sh = row_shape<T>(z, n);
     const int32_t g0 = sp * a.per;
-    const int32_t cnt = min(a.per, total - g0);  // may be <= 0 in the last split
-    const int64_t n = a.in.cols;
-    const int32_t k = a.k;
+    const int32_t cnt = min(a.per, sh.granules - g0);  // may be <= 0 in the last split
+    const gran* body = reinterpret_cast<const gran*>(z + sh.head) + g0;
+    const int32_t first = sh.head + g0 * T::kN;  // column of granule 0's first element
 
     gran g[kGran];
 #pragma unroll
     for (int c = 0; c < kGran; ++c) {
-        const int32_t gi = (int32_t)tid + c * kRowThreads;
-        // a granule outside the part lies at element n: nothing is read and all is -inf
-        const int64_t e0 = gi < cnt ? (int64_t)(g0 + gi) * T::kN - lead : n;
-        if (c * kRowThreads < cnt || c == 0) g[c] = load_granule<T>(z, e0, n);
+        const int32_t i = tid + c * kRowThreads;
+        g[c] = no_entries<T>();
+        if (i < cnt) g[c] = body[i];
     }
-    if (tid == 0) s_n = 0;
+    const int32_t lone = lone_element(sh, n, sp == 0, sp == a.splits - 1);
+    const float lx = lone >= 0 ? T::up1(z[lone]) : kNegInf;
+    if (tid == 0) s_n = s_hits = 0;
 
-    // the threads' maxima (NaN left out)
-    float m = kNegInf;
+    float gm[kGran], m = lx;
 #pragma unroll
-    for (int c = 0; c < kGran; ++c)
-        if (c * kRowThreads < cnt || c == 0) {
-#pragma unroll
-            for (int j = 0; j < T::kN; ++j) m = fmaxf(m, T::up(g[c], j));
-        }
+    for (int c = 0; c < kGran; ++c) {
+        gm[c] = granule_max<T>(g[c]);
+        m = max_nan(m, gm[c]);
+    }
     tmax[tid] = order_key(m) >> 16;
-    const float wm = group_reduce<OpMaxF, 64>(m);
-    if ((tid & 63) == 0) wmax[wave] = wm;
+    m = group_reduce<OpMaxF, 64>(m);
+    if ((tid & 63) == 0) wmax[wave] = m;
     __syncthreads();
-    float bm = wmax[0];
 #pragma unroll
-    for (int w = 1; w < kRowWaves; ++w) bm = fmaxf(bm, wmax[w]);
+    for (int w = 0; w < kRowWaves; ++w) m = max_nan(m, wmax[w]);
 
     // wave 0: the k-th largest of the maxima, to the top 16 bits of its key
     if (wave == 0) {
@@ -151,80 +155,97 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_rows(TopkArgs a) {
         }
         if (tid == 0) s_tau = t;
     }
-    // everyone: the sum against the maximum
-    const float ref = bm == kNegInf ? 0.0f : bm * a.c2;
-    float sum = 0.0f;
+    // everyone: the sum against the maximum (two chains, for the adders)
+    const float ref = m == kNegInf ? 0.0f : m * a.c2;
+    float sum = fast_exp2(__builtin_fmaf(lx, a.c2, -ref)), sum1 = 0.0f;
 #pragma unroll
     for (int c = 0; c < kGran; ++c)
-        if (c * kRowThreads < cnt || c == 0) {
+        if (c * kRowThreads < cnt) {
+            forget_unpacked(g[c]);
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) sum += fast_exp2(__builtin_fmaf(T::up(g[c], j), a.c2, -ref));
+            for (int j = 0; j < T::kN; j += 2) {
+                sum += fast_exp2(__builtin_fmaf(T::up(g[c], j), a.c2, -ref));
+                sum1 += fast_exp2(__builtin_fmaf(T::up(g[c], j + 1), a.c2, -ref));
+            }
         }
-    const float ws = group_reduce<OpSumF, 64>(sum);
-    if ((tid & 63) == 0) wsum[wave] = ws;
+    sum = group_reduce<OpSumF, 64>(sum + sum1);
+    if ((tid & 63) == 0) wsum[wave] = sum;
     __syncthreads();
 
     // candidates: entries not below the threshold, which is finite (so -inf
     // is never one, and NaN, which compares false, always is)
     const float tau = fmaxf(key_value(s_tau << 16), -FLT_MAX);
+    auto take = [&](float f, int32_t col) {
+        if (!(f < tau)) {
+            const uint32_t at = atomicAdd(&s_n, 1u);
+            if (at < kTopkList) list[at] = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)col;
+        }
+    };
+    take(lx, lone);
 #pragma unroll
     for (int c = 0; c < kGran; ++c)
-        if (c * kRowThreads < cnt || c == 0) {
-#pragma unroll
-            for (int j = 0; j < T::kN; ++j) {
-                const float f = T::up(g[c], j);
-                if (!(f < tau)) {
-                    const uint32_t e = (uint32_t)((g0 + (int32_t)tid + c * kRowThreads) * T::kN - lead + j);
-                    const uint32_t at = atomicAdd(&s_n, 1u);
-                    if (at < kTopkList) list[at] = ((uint64_t)order_key(f) << 32) | (uint32_t)~e;
-                }
+        if (!(gm[c] < tau)) {
+            const uint32_t at = atomicAdd(&s_hits, 1u);
+            if (at < kTopkHits) {
+                hit[at] = g[c];
+                hit_at[at] = first + (tid + c * kRowThreads) * T::kN;
             }
         }
     __syncthreads();
+    const uint32_t hits = s_hits;
+    if (hits <= kTopkHits) {
+        const raw* elems = reinterpret_cast<const raw*>(hit);
+        for (uint32_t i = (uint32_t)tid; i < hits * T::kN; i += kRowThreads)
+            take(T::up1(elems[i]), hit_at[i / T::kN] + (int32_t)(i % T::kN));
+        __syncthreads();
+    }
     uint32_t found = s_n;
-    if (found > kTopkList) {
-        // radix selection over 8-bit digits of the composite, largest first
+    if (hits > kTopkHits || found > kTopkList) {
+        // radix selection over 8-bit digits of the composite, largest first;
+        // every part of the row by its granules, then the lone elements
+        auto each = [&](auto f) {
+            for (int32_t i0 = 0; i0 < cnt; i0 += kRowThreads) {
+                const int32_t i = i0 + tid;
+                const gran x = i < cnt ? body[i] : no_entries<T>();
+#pragma unroll
+                for (int j = 0; j < T::kN; ++j) f(T::up(x, j), first + i * T::kN + j);
+            }
+            f(lx, lone);
+        };
         uint64_t prefix = 0;
         uint32_t need = (uint32_t)k;
         int shift = 56;
+        __syncthreads();
         for (;; shift -= 8) {
             if (shift == 24) {  // ~column >> 24 is 0xFF: columns are below 2^24
                 prefix = (prefix << 8) | 0xFFu;
                 continue;
             }
-            for (uint32_t i = tid; i < 256; i += kRowThreads) hist[i] = 0;
+            for (int32_t i = tid; i < 256; i += kRowThreads) hist[i] = 0;
             __syncthreads();
-            for (int32_t g1 = 0; g1 < cnt; g1 += kRowThreads) {
-                const int32_t gi = g1 + (int32_t)tid;
-                const int64_t e0 = gi < cnt ? (int64_t)(g0 + gi) * T::kN - lead : n;
-                const gran x = load_granule<T>(z, e0, n);
-#pragma unroll
-                for (int j = 0; j < T::kN; ++j) {
-                    const float f = T::up(x, j);
-                    const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)(e0 + j);
-                    const bool in = f != kNegInf && (shift == 56 || (comp >> (shift + 8)) == prefix);
-                    hist_add_wave(hist, (uint32_t)(comp >> shift) & 255u, in);
-                }
-            }
+            each([&](float f, int32_t col) {
+                const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)col;
+                const bool in = f != kNegInf && (shift == 56 || (comp >> (shift + 8)) == prefix);
+                hist_add_wave(hist, (uint32_t)(comp >> shift) & 255u, in);
+            });
             __syncthreads();
             if (wave == 0) {
-                // bins from the top, four a lane: the one that holds the need-th
+                // bins from the top, four a lane: the one that holds the
+                // need-th, or the lowest where there are fewer
                 uint32_t h[4], own = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) own += h[i] = hist[255 - (4 * tid + i)];
                 const uint32_t upto = wave_inclusive_scan(own);
                 const uint64_t reach = wave_ballot(upto >= need);
-                // at least kTopkList entries are there, more than k
-                if (tid == (uint32_t)__builtin_ctzll(reach)) {
-                    uint32_t above = upto - own;
-                    uint32_t i = 0;
+                if (tid == (reach ? (int)__builtin_ctzll(reach) : 63)) {
+                    uint32_t above = upto - own, i = 0;
 #pragma unroll
                     for (uint32_t u = 0; u < 3; ++u)
                         if (i == u && above + h[u] < need) {
                             above += h[u];
                             i = u + 1;
                         }
-                    s_bin = 255 - (4 * tid + i);
+                    s_bin = 255 - (4 * (uint32_t)tid + i);
                     s_need = need - above;
                 }
             }
@@ -237,16 +258,10 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_rows(TopkArgs a) {
         __syncthreads();
         if (tid == 0) s_n = 0;
         __syncthreads();
-        for (int32_t gi = (int32_t)tid; gi < cnt; gi += kRowThreads) {
-            const int64_t e0 = (int64_t)(g0 + gi) * T::kN - lead;
-            const gran x = load_granule<T>(z, e0, n);
-#pragma unroll
-            for (int j = 0; j < T::kN; ++j) {
-                const float f = T::up(x, j);
-                const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)(e0 + j);
-                if (f != kNegInf && (comp >> shift) >= prefix) list[atomicAdd(&s_n, 1u)] = comp;
-            }
-        }
+        each([&](float f, int32_t col) {
+            const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)col;
+            if (f != kNegInf && (comp >> shift) >= prefix) list[atomicAdd(&s_n, 1u)] = comp;
+        });
         __syncthreads();
         found = s_n;
     }
@@ -257,48 +272,77 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_rows(TopkArgs a) {
         uint64_t* out = a.cand + (row * a.splits + sp) * k;
         emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { out[r] = comp; });
     }
-    if (tid == 0) {
-        double sum64 = 0.0;
-        for (int w = 0; w < kRowWaves; ++w) sum64 += (double)wsum[w];
+    if (tid == kRowThreads - 1) {
+        float total = wsum[0];
+        for (int w = 1; w < kRowWaves; ++w) total += wsum[w];
         if (a.splits > 1)
-            a.part[row * a.splits + sp] = make_float2(ref, (float)sum64);
+            a.part[row * a.splits + sp] = make_float2(ref, total);
         else if (a.lse)
-            a.lse[row] = lse_of(ref, sum64);
+            a.lse[row] = lse_of(ref, (double)total);
     }
 }
 
-// The parts' candidates are sorted lists; an entry's rank in the row is its
-// place in its own list plus, for each other list, the number of entries
-// above it (a binary search).
-constexpr int kMergeLds = 4096;
+// Joins a row's parts.  Each part's candidates are sorted, so of the first
+// ceil(k / splits) of every part at least k are in the row: only entries that
+// reach the smallest of those can be among the row's k largest.
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
-    __shared__ uint64_t lds[kMergeLds];
+    __shared__ uint64_t list[kTopkList];
+    __shared__ uint64_t s_low;
     __shared__ uint32_t s_n;
-    const uint32_t tid = threadIdx.x;
+    const int32_t tid = (int32_t)threadIdx.x;
     const int64_t row = blockIdx.x;
     const uint32_t k = (uint32_t)a.k, all = (uint32_t)a.splits * k;
     const uint64_t* cand = a.cand + row * all;
-    if (tid == 0) s_n = 0;
-    if (all <= kMergeLds) {
-        for (uint32_t i = tid; i < all; i += kRowThreads) lds[i] = cand[i];
-        cand = lds;
+    if (tid < 64) {
+        const uint32_t at = (k + (uint32_t)a.splits - 1) / (uint32_t)a.splits - 1;
+        uint64_t low = ~0ull;
+        if (tid < a.splits) low = cand[(uint32_t)tid * k + at];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint64_t o = __shfl_xor((unsigned long long)low, d, 64);
+            low = o < low ? o : low;
+        }
+        if (tid == 0) {
+            s_low = low;
+            s_n = 0;
+        }
+    } else if (tid < 128 && a.lse) {
+        float2 p = make_float2(0.0f, 0.0f);
+        if (tid - 64 < a.splits) p = a.part[row * a.splits + (tid - 64)];
+        float ref = group_reduce<OpMaxF, 64>(p.y != 0.0f ? p.x : kNegInf);
+        if (ref == kNegInf) ref = 0.0f;
+        const double sum = wave_sum_f64(p.y != 0.0f ? (double)p.y * exp2((double)p.x - (double)ref) : 0.0);
+        if (tid == 64) a.lse[row] = lse_of(ref, sum);
     }
     __syncthreads();
-    uint32_t mine = 0;
-    for (uint32_t i = tid; i < all; i += kRowThreads) {
+    const uint64_t low = s_low;
+    for (uint32_t i = (uint32_t)tid; i < all; i += kRowThreads) {
+        const uint64_t x = cand[i];
+        if (x >= low && x != 0) {
+            const uint32_t at = atomicAdd(&s_n, 1u);
+            if (at < kTopkList) list[at] = x;
+        }
+    }
+    __syncthreads();
+    const uint32_t found = s_n;
+    if (found <= kTopkList) {
+        emit_sorted(list, found, a.k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
+        return;
+    }
+    // too many (one part holds most of them): an entry's rank is its place in
+    // its own part plus, by binary search, the entries above it in the others
+    for (uint32_t i = (uint32_t)tid; i < all; i += kRowThreads) {
         const uint64_t x = cand[i];
         if (x == 0) continue;
-        ++mine;
         const uint32_t own = i / k;
         uint32_t r = i - own * k;
         for (uint32_t s = 0; s < (uint32_t)a.splits && r < k; ++s) {
             if (s == own) continue;
-            const uint64_t* l = cand + s * k;
             uint32_t lo = 0, hi = k;
             while (lo < hi) {
                 const uint32_t mid = (lo + hi) / 2;
-                if (l[mid] > x)
+                if (cand[s * k + mid] > x)
                     lo = mid + 1;
                 else
                     hi = mid;
@@ -306,20 +350,6 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
             r += lo;
         }
         if (r < k) write_entry<T>(a, row, (int32_t)r, x);
-    }
-    if (mine) atomicAdd(&s_n, mine);
-    __syncthreads();
-    for (uint32_t i = s_n + tid; i < k; i += kRowThreads) write_entry<T>(a, row, (int32_t)i, 0ull);
-    if (tid == 0 && a.lse) {
-        const float2* p = a.part + row * a.splits;
-        float ref = kNegInf;
-        for (int s = 0; s < a.splits; ++s)
-            if (p[s].y != 0.0f) ref = fmaxf(ref, p[s].x);
-        if (ref == kNegInf) ref = 0.0f;
-        double sum = 0.0;
-        for (int s = 0; s < a.splits; ++s)
-            if (p[s].y != 0.0f) sum += (double)p[s].y * exp2((double)p[s].x - (double)ref);
-        a.lse[row] = lse_of(ref, sum);
     }
 }
 
@@ -411,8 +441,8 @@ static hipError_t topk_typed(hipStream_t s, const TopkArgs& a) {
         if (g <= 4) topk_small<T, 4, 1>(s, a, vec);
         else if (g <= 16) topk_small<T, 16, 1>(s, a, vec);
         else if (g <= 64) topk_small<T, 64, 1>(s, a, vec);
-        else if (g <= 128) topk_small<T, 64, 2>(s, a, vec);
-        else topk_small<T, 64, 4>(s, a, vec);
+        else if (T::kN == 8 || g <= 128) topk_small<T, 64, 2>(s, a, vec);
+        else if constexpr (T::kN == 4) topk_small<T, 64, 4>(s, a, vec);
         return hipGetLastError();
     }
     const dim3 grid((uint32_t)(a.in.rows * a.splits));

@@ -19,6 +19,7 @@ RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols) {
     const int64_t need = (g + kRowCapacity - 1) / kRowCapacity;
     int64_t want = rows > 0 ? kFill / rows : 1;
     if (want > g / kRowThreads) want = g / kRowThreads;
+    if (want > kMaxSplits) want = kMaxSplits;
     const int64_t n = want > need ? want : need;
     const int64_t per = (g + n - 1) / n;
     return RowSplit{(int32_t)((g + per - 1) / per), (int32_t)per};

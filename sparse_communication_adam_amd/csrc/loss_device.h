@@ -81,41 +81,62 @@ __device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t 
     return dtype == SCAPE_DTYPE_BF16 ? BF16::up1(r) : F16::up1(r);
 }
 
-// A row starts anywhere, its granules lie on 16-byte boundaries: element e of
-// the row is element (e + lead) % N of granule (e + lead) / N.  Only the first
-// and the last granule can reach past the row; those are read and written
-// element by element, so nothing outside the row is touched.
+// A row starts anywhere; its granules lie on 16-byte boundaries.  The `head`
+// elements before the first boundary and the `tail` elements after the last
+// whole granule are fewer than a granule each, and are taken one a thread
+// beside the granules, so nothing outside the row is touched.  Granule i
+// holds elements head + i N ...
+struct RowShape {
+    int32_t head, granules, tail;
+};
 template <class T>
-__device__ __forceinline__ int row_lead(const void* row) {
-    return (int)(((uintptr_t)row & 15u) / sizeof(typename T::raw));
+__device__ __forceinline__ RowShape row_shape(const void* row, int32_t n) {
+    RowShape r;
+    r.head = (int32_t)(((16u - ((uint32_t)(uintptr_t)row & 15u)) & 15u) / sizeof(typename T::raw));
+    if (r.head > n) r.head = n;
+    r.granules = (n - r.head) / T::kN;
+    r.tail = n - r.head - r.granules * T::kN;
+    return r;
+}
+// The element a thread takes beside its granules in the first or the last
+// part of a row, or -1.
+__device__ __forceinline__ int32_t lone_element(const RowShape& r, int32_t n, bool first, bool last) {
+    const int32_t tid = (int32_t)threadIdx.x;
+    if (first && tid < r.head) return tid;
+    if (last && tid >= 64 && tid - 64 < r.tail) return n - r.tail + tid - 64;
+    return -1;
 }
 
+// 16 bytes to an address of any alignment: one store (the target's memory
+// mode takes them; the compiler picks the instruction).
+typedef uint32_t loose_gran __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ void store_loose(void* p, const gran& g) { *static_cast<loose_gran*>(p) = g; }
+
 template <class T>
-__device__ __forceinline__ gran load_granule(const typename T::raw* row, int64_t e0, int64_t n) {
-    if (e0 >= 0 && e0 + T::kN <= n) return *reinterpret_cast<const gran*>(row + e0);
-    gran g = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < T::kN; ++j) {
-        const int64_t e = e0 + j;
-        T::set(g, j, (e >= 0 && e < n) ? row[e] : (typename T::raw)T::kNegInfBits);
-    }
-    return g;
+__device__ __forceinline__ gran no_entries() {  // a granule of -inf
+    return T::kN == 4 ? gran{T::kNegInfBits, T::kNegInfBits, T::kNegInfBits, T::kNegInfBits}
+                      : gran{T::kNegInfBits * 0x10001u, T::kNegInfBits * 0x10001u, T::kNegInfBits * 0x10001u,
+                             T::kNegInfBits * 0x10001u};
 }
 
-// vec: the destination row has the source row's lead.
+// Between two passes over registers: the compiler would keep a first pass's
+// unpacked 16-bit elements, two registers for one, for the second, and spill.
+__device__ __forceinline__ void forget_unpacked(gran& g) { asm volatile("" : "+v"(g)); }
+// A thread's index anew, so that the addresses made from it in one pass are
+// not kept for the next.
+__device__ __forceinline__ int32_t again(int32_t tid) {
+    asm volatile("" : "+v"(tid));
+    return tid;
+}
+
+// The larger of two, NaN if either is: v_maximum3_f32 takes three at once.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 template <class T>
-__device__ __forceinline__ void store_granule(typename T::raw* row, int64_t e0, int64_t n, bool vec, const gran& g) {
-    if (vec && e0 >= 0 && e0 + T::kN <= n) {
-        *reinterpret_cast<gran*>(row + e0) = g;
-        return;
-    }
+__device__ __forceinline__ float granule_max(const gran& g) {
+    float m = T::up(g, 0);
 #pragma unroll
-    for (int j = 0; j < T::kN; ++j) {
-        const int64_t e = e0 + j;
-        if (e >= 0 && e < n)
-            row[e] = sizeof(typename T::raw) == 4 ? (typename T::raw)g[j & 3]
-                                                  : (typename T::raw)((j & 1) ? g[(j >> 1) & 3] >> 16 : g[(j >> 1) & 3]);
-    }
+    for (int j = 1; j < T::kN; ++j) m = max_nan(m, T::up(g, j));
+    return m;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
@@ -131,7 +152,7 @@ __device__ __forceinline__ uint32_t dpp32(uint32_t x) {
 }
 
 struct OpMaxF {
-    static __device__ __forceinline__ float f(float a, float b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ float f(float a, float b) { return max_nan(a, b); }
 };
 struct OpSumF {
     static __device__ __forceinline__ float f(float a, float b) { return a + b; }
@@ -166,10 +187,51 @@ __device__ __forceinline__ V group_reduce(V x) {
     return x;
 }
 
-__device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+template <int kCtrl>
+__device__ __forceinline__ double dpp64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)dpp32<kCtrl>((uint32_t)u) | (uint64_t)dpp32<kCtrl>((uint32_t)(u >> 32)) << 32);
+}
+
+// Sum over eight values that each group of eight lanes holds alike: the
+// workgroup's waves' partial sums, read by lane % 8.
+__device__ __forceinline__ double sum8_f64(double x) {
+    x += dpp64<0xB1>(x);
+    x += dpp64<0x4E>(x);
+    x += dpp64<0x141>(x);
     return x;
 }
+
+__device__ __forceinline__ double wave_sum_f64(double x) {
+    x = sum8_f64(x);
+    x += dpp64<0x140>(x);
+    {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+        x = __builtin_bit_cast(double, (uint64_t)(uint32_t)lo[0] | (uint64_t)(uint32_t)hi[0] << 32) +
+            __builtin_bit_cast(double, (uint64_t)(uint32_t)lo[1] | (uint64_t)(uint32_t)hi[1] << 32);
+    }
+    {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+        x = __builtin_bit_cast(double, (uint64_t)(uint32_t)lo[0] | (uint64_t)(uint32_t)hi[0] << 32) +
+            __builtin_bit_cast(double, (uint64_t)(uint32_t)lo[1] | (uint64_t)(uint32_t)hi[1] << 32);
+    }
+    return x;
+}
+
+// x of one lane (a constant) in every lane.
+__device__ __forceinline__ double from_lane(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane) |
+                                          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane)
+                                              << 32);
+}
+
+// Registers a row kernel may use, as waves per SIMD: two or three workgroups
+// of kRowThreads on a CU, so that one's loads run under another's arithmetic.
+constexpr int row_waves(int granules) { return granules <= 4 ? 8 : granules <= 8 ? 6 : 4; }
 
 }  // namespace scape

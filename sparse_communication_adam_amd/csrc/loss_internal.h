@@ -30,6 +30,8 @@ constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kRowGranules = 16;
 constexpr int64_t kRowCapacity = (int64_t)kRowThreads * kRowGranules;
+constexpr int kMaxSplits = 64;  // a lane of the joining wave for each part
+static_assert((SCAPE_ROW_MAX_COLS / 4 + 2) / kRowCapacity < kMaxSplits, "the longest row fits");
 
 // Granules a row of `cols` elements can touch, whatever its alignment.
 inline int64_t row_granules(int32_t dtype, int64_t cols) {
