@@ -559,64 +559,91 @@ def scape_profile_read(ctx: Context):
 # No context; outputs and workspaces are the caller's tensors.
 
 
+# These calls are short (a router's loss takes a few microseconds on the GPU),
+# so their argument checks are made with one cheap query each.
+
+_TORCH = None
+_FLOATS = None
+
+
+def _torch():
+    global _TORCH, _FLOATS
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+        _FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _TORCH
+
+
 def _dtype_id(dtype) -> int:
-    import torch
-    ids = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if dtype not in ids:
+    did = _FLOATS.get(dtype)
+    if did is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16 (got {dtype})")
-    return ids[dtype]
+    return did
 
 
 def _matrix(t, name: str, like=None):
     """(pointer, dtype id, rows, cols, ld) of a 2-D tensor whose rows are
-    contiguous; `like`: the tensor whose dtype and shape it must have.  The
-    device is checked by _on_device."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    contiguous; `like`: the tensor whose dtype and shape it must have."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions (got {t.dim()})")
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape):
         raise ValueError(f"{name} must have the logits' dtype and shape ({like.dtype}, {tuple(like.shape)})")
     did = _dtype_id(t.dtype)
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows (stride {t.stride(1)} between columns)")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride {step} between columns)")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"{name}: rows of {cols} columns overlap (stride {ld})")
     return t.data_ptr(), did, rows, cols, ld
 
 
-def _array(t, dtype, numel: int, name: str, optional: bool = False):
+def _array(t, dtype, numel: int, name: str):
+    """Pointer of a contiguous tensor of one dtype (None: no tensor)."""
     if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} must be a torch tensor")
-    _shape(t, dtype, numel, name)
+        return None
+    if not isinstance(t, _TORCH.Tensor) or t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
+        _shape(t, dtype, numel, name)  # says which
     return t.data_ptr()
 
 
-def _on_device(**tensors) -> None:
-    """Every tensor on the current GPU: a launch goes there, whatever device
-    its pointers belong to."""
-    import torch
+def _needed(t, name: str):
+    if t is None:
+        raise TypeError(f"{name} must be a torch tensor")
+    return t
+
+
+def _launch_on(stream, **tensors) -> int:
+    """The stream to launch on, after checking that every tensor is on the
+    current GPU: a launch goes there, whatever device its pointers belong to."""
+    here = None
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.device.type != "cuda":
+        at = t.get_device()
+        if at < 0:
             raise ValueError(f"{name} must be on the GPU (got {t.device})")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device} but cuda:{torch.cuda.current_device()} is the current device")
+        if here is None:
+            here = _TORCH.cuda.current_device()
+        if at != here:
+            raise ValueError(f"{name} is on {t.device} but cuda:{here} is the current device")
+    if stream is None and here is not None:
+        return _TORCH._C._cuda_getCurrentRawStream(here)  # current_stream() takes longer than a launch
+    return _stream(stream)
 
 
-def _workspace(t, need: int):
-    import torch
+def _workspace(t, need):
+    """(pointer, bytes); the library compares the bytes with what it needs."""
     if t is None:
-        if need:
-            raise ValueError(f"this call needs a workspace of {need} bytes")
+        if (n := need()):
+            raise ValueError(f"this call needs a workspace of {n} bytes")
         return None, 0
-    _shape(t, (torch.uint8, torch.int8), need, "workspace")
+    _shape(t, (_TORCH.uint8, _TORCH.int8), None, "workspace")
     return t.data_ptr(), t.numel()
 
 
@@ -632,29 +659,25 @@ def scape_topk_rows(z, k: int, val, idx, lse=None, scale: float = 1.0, workspace
     """The k largest entries of each row of z (2-D, rows contiguous) into val
     (z's dtype) and idx (int32), both rows*k elements, and the row's
     log-sum-exp of scale*z into lse (fp32) where given."""
-    import torch
     zp, did, rows, cols, ld = _matrix(z, "z")
-    need = scape_topk_rows_workspace_bytes(z, k)
-    vp = _array(val, z.dtype, rows * k, "val")
-    ip = _array(idx, torch.int32, rows * k, "idx")
-    lp = _array(lse, torch.float32, rows, "lse", optional=True)
-    wp, wb = _workspace(workspace, need)
-    _on_device(z=z, val=val, idx=idx, lse=lse, workspace=workspace)
-    _check(lib().scape_topk_rows(zp, did, rows, cols, ld, int(k), float(scale), vp, ip, lp, wp, wb, _stream(stream)))
+    vp = _array(_needed(val, "val"), z.dtype, rows * k, "val")
+    ip = _array(_needed(idx, "idx"), _TORCH.int32, rows * k, "idx")
+    lp = _array(lse, _TORCH.float32, rows, "lse")
+    wp, wb = _workspace(workspace, lambda: scape_topk_rows_workspace_bytes(z, k))
+    st = _launch_on(stream, z=z, val=val, idx=idx, lse=lse, workspace=workspace)
+    _check(lib().scape_topk_rows(zp, did, rows, cols, ld, k, scale, vp, ip, lp, wp, wb, st))
 
 
 def _teacher(t_val, t_idx, t_lse, rows: int) -> _Teacher:
-    import torch
     for t, name in ((t_val, "t_val"), (t_idx, "t_idx")):
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _TORCH.Tensor):
             raise TypeError(f"{name} must be a torch tensor")
     if t_val.dim() != 2 or t_val.shape != t_idx.shape or t_val.shape[0] != rows:
         raise ValueError(f"t_val and t_idx must both be [{rows}, k] (got {tuple(t_val.shape)}, {tuple(t_idx.shape)})")
     k = t_val.shape[1]
-    vp = _array(t_val, (torch.float32, torch.bfloat16, torch.float16), rows * k, "t_val")
-    ip = _array(t_idx, torch.int32, rows * k, "t_idx")
-    lp = _array(t_lse, torch.float32, rows, "t_lse", optional=True)
-    return _Teacher(vp, _dtype_id(t_val.dtype), ip, lp, k)
+    did = _dtype_id(t_val.dtype)
+    return _Teacher(_array(t_val, t_val.dtype, rows * k, "t_val"), did, _array(t_idx, _TORCH.int32, rows * k, "t_idx"),
+                    _array(t_lse, _TORCH.float32, rows, "t_lse"), k)
 
 
 def scape_distill_workspace_bytes(z, k: int, grad: bool = False) -> int:
@@ -674,36 +697,34 @@ def scape_distill_forward(z, t_val, t_idx, loss, stats, t_lse=None, scale: float
     renormalised over them.  loss fp32 [rows], stats fp32 [rows, 2]; dz (z's
     dtype and shape, may be z) also takes the gradient of loss.sum().  For
     autograd: z.backward(dz) on the logits' graph."""
-    import torch
     zp, did, rows, cols, ld = _matrix(z, "z")
     t = _teacher(t_val, t_idx, t_lse, rows)
     dp, ld_dz = None, 0
     if dz is not None:
         dp, _, _, _, ld_dz = _matrix(dz, "dz", like=z)
-    wt = _array(weight, torch.float32, rows, "weight", optional=True)
-    lp = _array(loss, torch.float32, rows, "loss")
-    sp = _array(stats, torch.float32, 2 * rows, "stats")
-    wp, wb = _workspace(workspace, scape_distill_workspace_bytes(z, t.k, grad=dz is not None))
-    _on_device(z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, loss=loss, stats=stats, dz=dz,
-               workspace=workspace)
-    _check(lib().scape_distill_forward(zp, did, rows, cols, ld, ctypes.byref(t), float(scale), wt, lp, sp, dp, ld_dz,
-                                       wp, wb, _stream(stream)))
+    f32 = _TORCH.float32
+    wt = _array(weight, f32, rows, "weight")
+    lp = _array(_needed(loss, "loss"), f32, rows, "loss")
+    sp = _array(_needed(stats, "stats"), f32, 2 * rows, "stats")
+    wp, wb = _workspace(workspace, lambda: scape_distill_workspace_bytes(z, t.k, grad=dz is not None))
+    st = _launch_on(stream, z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, loss=loss, stats=stats, dz=dz,
+                    workspace=workspace)
+    _check(lib().scape_distill_forward(zp, did, rows, cols, ld, t, scale, wt, lp, sp, dp, ld_dz, wp, wb, st))
 
 
 def scape_distill_backward(z, t_val, t_idx, stats, dz, t_lse=None, scale: float = 1.0, weight=None, dloss=None,
                            stream=None) -> None:
     """dz = dloss * weight * dKL/dz per row, from the stats of a forward call
     on the same z, teacher and scale.  dz may be z."""
-    import torch
     zp, did, rows, cols, ld = _matrix(z, "z")
     t = _teacher(t_val, t_idx, t_lse, rows)
     dp, _, _, _, ld_dz = _matrix(dz, "dz", like=z)
-    wt = _array(weight, torch.float32, rows, "weight", optional=True)
-    sp = _array(stats, torch.float32, 2 * rows, "stats")
-    gp = _array(dloss, torch.float32, rows, "dloss", optional=True)
-    _on_device(z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, stats=stats, dloss=dloss, dz=dz)
-    _check(lib().scape_distill_backward(zp, did, rows, cols, ld, ctypes.byref(t), float(scale), wt, sp, gp, dp, ld_dz,
-                                        _stream(stream)))
+    f32 = _TORCH.float32
+    wt = _array(weight, f32, rows, "weight")
+    sp = _array(_needed(stats, "stats"), f32, 2 * rows, "stats")
+    gp = _array(dloss, f32, rows, "dloss")
+    st = _launch_on(stream, z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, stats=stats, dloss=dloss, dz=dz)
+    _check(lib().scape_distill_backward(zp, did, rows, cols, ld, t, scale, wt, sp, gp, dp, ld_dz, st))
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -715,12 +736,16 @@ def _score(score: str) -> int:
     return SCORES[score]
 
 
-def _segments(offsets) -> int:
-    import torch
-    if offsets is None:
-        return 1
-    _shape(offsets, torch.int32, 2, "offsets")
-    return offsets.numel() - 1
+def _router(offsets, mask, tokens: int):
+    """(offsets pointer, segments, mask pointer)"""
+    segs = 1
+    if offsets is not None:
+        _array(offsets, _TORCH.int32, 2, "offsets")
+        segs = offsets.numel() - 1
+    mp = None
+    if mask is not None:
+        mp = _array(mask, _TORCH.bool if getattr(mask, "dtype", None) is _TORCH.bool else _TORCH.uint8, tokens, "mask")
+    return (None if offsets is None else offsets.data_ptr()), segs, mp
 
 
 def scape_balance_workspace_bytes(logits, segments: int = 1) -> int:
@@ -738,39 +763,37 @@ def scape_balance_forward(logits, idx, counts, psum, n_tok, loss=None, alpha: fl
     balance loss (fp32) of router logits [tokens, experts] and choices idx
     (int32 [tokens, k]).  offsets: int32 [segments + 1], or one segment of all
     tokens; mask: uint8 or bool [tokens]."""
-    import torch
     zp, did, tokens, experts, ld = _matrix(logits, "logits")
-    segs = _segments(offsets)
-    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.shape[0] != tokens:
+    op, segs, mp = _router(offsets, mask, tokens)
+    if not isinstance(idx, _TORCH.Tensor) or idx.dim() != 2 or idx.shape[0] != tokens:
         raise ValueError(f"idx must be a tensor of [{tokens}, k]")
     k = idx.shape[1]
-    ip = _array(idx, torch.int32, tokens * k, "idx")
-    op = _array(offsets, torch.int32, segs + 1, "offsets", optional=True)
-    mp = _array(mask, (torch.uint8, torch.bool), tokens, "mask", optional=True)
-    cp = _array(counts, torch.int32, segs * experts, "counts")
-    pp = _array(psum, torch.float32, segs * experts, "psum")
-    np_ = _array(n_tok, torch.int32, segs, "n_tok")
-    lp = _array(loss, torch.float32, segs, "loss", optional=True)
-    wp, wb = _workspace(workspace, scape_balance_workspace_bytes(logits, segs))
-    _on_device(logits=logits, idx=idx, offsets=offsets, mask=mask, counts=counts, psum=psum, n_tok=n_tok, loss=loss,
-               workspace=workspace)
-    _check(lib().scape_balance_forward(zp, did, tokens, experts, ld, ip, k, op, segs, mp, _score(score), float(alpha),
-                                       cp, pp, np_, lp, wp, wb, _stream(stream)))
+    i32, f32 = _TORCH.int32, _TORCH.float32
+    ip = _array(idx, i32, tokens * k, "idx")
+    cp = _array(_needed(counts, "counts"), i32, segs * experts, "counts")
+    pp = _array(_needed(psum, "psum"), f32, segs * experts, "psum")
+    np_ = _array(_needed(n_tok, "n_tok"), i32, segs, "n_tok")
+    lp = _array(loss, f32, segs, "loss")
+    wp, wb = _workspace(workspace, lambda: scape_balance_workspace_bytes(logits, segs))
+    st = _launch_on(stream, logits=logits, idx=idx, offsets=offsets, mask=mask, counts=counts, psum=psum, n_tok=n_tok,
+                    loss=loss, workspace=workspace)
+    _check(lib().scape_balance_forward(zp, did, tokens, experts, ld, ip, k, op, segs, mp, _score(score), alpha, cp, pp,
+                                       np_, lp, wp, wb, st))
 
 
 def scape_balance_loss(counts, psum, n_tok, loss, k: int, alpha: float = 1.0, stream=None) -> None:
     """The loss of counts and psum [segments, experts] and n_tok [segments],
     for instance their sums over data-parallel workers."""
-    import torch
-    if not isinstance(counts, torch.Tensor) or counts.dim() != 2:
+    if not isinstance(counts, _torch().Tensor) or counts.dim() != 2:
         raise ValueError("counts must be a tensor of [segments, experts]")
     segs, experts = counts.shape
-    cp = _array(counts, torch.int32, segs * experts, "counts")
-    pp = _array(psum, torch.float32, segs * experts, "psum")
-    np_ = _array(n_tok, torch.int32, segs, "n_tok")
-    lp = _array(loss, torch.float32, segs, "loss")
-    _on_device(counts=counts, psum=psum, n_tok=n_tok, loss=loss)
-    _check(lib().scape_balance_loss(cp, pp, np_, segs, experts, int(k), float(alpha), lp, _stream(stream)))
+    i32, f32 = _TORCH.int32, _TORCH.float32
+    cp = _array(counts, i32, segs * experts, "counts")
+    pp = _array(_needed(psum, "psum"), f32, segs * experts, "psum")
+    np_ = _array(_needed(n_tok, "n_tok"), i32, segs, "n_tok")
+    lp = _array(_needed(loss, "loss"), f32, segs, "loss")
+    st = _launch_on(stream, counts=counts, psum=psum, n_tok=n_tok, loss=loss)
+    _check(lib().scape_balance_loss(cp, pp, np_, segs, experts, k, alpha, lp, st))
 
 
 def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha: float = 1.0, offsets=None, mask=None,
@@ -778,15 +801,14 @@ def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha:
     """dlogits (the logits' dtype and shape, may be the logits) from counts
     and n_tok (this worker's, or their sums over workers) and dloss
     [segments] (None: 1).  Rows outside every segment are left as they were."""
-    import torch
     zp, did, tokens, experts, ld = _matrix(logits, "logits")
     dp, _, _, _, ld_d = _matrix(dlogits, "dlogits", like=logits)
-    segs = _segments(offsets)
-    op = _array(offsets, torch.int32, segs + 1, "offsets", optional=True)
-    mp = _array(mask, (torch.uint8, torch.bool), tokens, "mask", optional=True)
-    cp = _array(counts, torch.int32, segs * experts, "counts")
-    np_ = _array(n_tok, torch.int32, segs, "n_tok")
-    gp = _array(dloss, torch.float32, segs, "dloss", optional=True)
-    _on_device(logits=logits, counts=counts, n_tok=n_tok, dloss=dloss, dlogits=dlogits, offsets=offsets, mask=mask)
-    _check(lib().scape_balance_backward(zp, did, tokens, experts, ld, int(k), op, segs, mp, _score(score),
-                                        float(alpha), cp, np_, gp, dp, ld_d, _stream(stream)))
+    op, segs, mp = _router(offsets, mask, tokens)
+    i32, f32 = _TORCH.int32, _TORCH.float32
+    cp = _array(_needed(counts, "counts"), i32, segs * experts, "counts")
+    np_ = _array(_needed(n_tok, "n_tok"), i32, segs, "n_tok")
+    gp = _array(dloss, f32, segs, "dloss")
+    st = _launch_on(stream, logits=logits, counts=counts, n_tok=n_tok, dloss=dloss, dlogits=dlogits, offsets=offsets,
+                    mask=mask)
+    _check(lib().scape_balance_backward(zp, did, tokens, experts, ld, k, op, segs, mp, _score(score), alpha, cp, np_,
+                                        gp, dp, ld_d, st))

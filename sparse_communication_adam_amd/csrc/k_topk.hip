@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
     __shared__ int32_t hit_at[kTopkHits];
     __shared__ uint32_t hist[256];
     __shared__ uint32_t tmax[kRowThreads];
-    __shared__ float wmax[kRowWaves], wsum[kRowWaves];
+    __shared__ float2 wsum[kRowWaves];
     __shared__ uint32_t s_n, s_hits, s_bin, s_need, s_tau;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
@@ -127,18 +127,31 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
     const float lx = lone >= 0 ? T::up1(z[lone]) : kNegInf;
     if (tid == 0) s_n = s_hits = 0;
 
+    constexpr int kBatch = kGran < 4 ? kGran : 4;
     float gm[kGran], m = lx;
+    RunningSum rs = RunningSum::none();
+    rs.add1(lx, a.c2);
 #pragma unroll
-    for (int c = 0; c < kGran; ++c) {
-        gm[c] = granule_max<T>(g[c]);
-        m = max_nan(m, gm[c]);
-    }
+    for (int c = 0; c < kGran; c += kBatch)
+        if (c * kRowThreads < cnt || c == 0) {
+            gran x[kBatch];
+            float bm = kNegInf;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                gm[c + b] = granule_max<T>(g[c + b]);
+                bm = max_nan(bm, gm[c + b]);
+                x[b] = g[c + b];
+            }
+            m = max_nan(m, bm);
+            rs.template add<T, kBatch>(x, bm, a.c2);
+        } else {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) gm[c + b] = kNegInf;
+        }
     tmax[tid] = order_key(m) >> 16;
-    m = group_reduce<OpMaxF, 64>(m);
-    if ((tid & 63) == 0) wmax[wave] = m;
+    wave_join(rs);
+    if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) m = max_nan(m, wmax[w]);
 
     // wave 0: the k-th largest of the maxima, to the top 16 bits of its key
     if (wave == 0) {
@@ -155,21 +168,6 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
         }
         if (tid == 0) s_tau = t;
     }
-    // everyone: the sum against the maximum (two chains, for the adders)
-    const float ref = m == kNegInf ? 0.0f : m * a.c2;
-    float sum = fast_exp2(__builtin_fmaf(lx, a.c2, -ref)), sum1 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kGran; ++c)
-        if (c * kRowThreads < cnt) {
-            forget_unpacked(g[c]);
-#pragma unroll
-            for (int j = 0; j < T::kN; j += 2) {
-                sum += fast_exp2(__builtin_fmaf(T::up(g[c], j), a.c2, -ref));
-                sum1 += fast_exp2(__builtin_fmaf(T::up(g[c], j + 1), a.c2, -ref));
-            }
-        }
-    sum = group_reduce<OpSumF, 64>(sum + sum1);
-    if ((tid & 63) == 0) wsum[wave] = sum;
     __syncthreads();
 
     // candidates: entries not below the threshold, which is finite (so -inf
@@ -272,13 +270,15 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
         uint64_t* out = a.cand + (row * a.splits + sp) * k;
         emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { out[r] = comp; });
     }
-    if (tid == kRowThreads - 1) {
-        float total = wsum[0];
-        for (int w = 1; w < kRowWaves; ++w) total += wsum[w];
-        if (a.splits > 1)
-            a.part[row * a.splits + sp] = make_float2(ref, total);
-        else if (a.lse)
-            a.lse[row] = lse_of(ref, (double)total);
+    if (wave == kRowWaves - 1) {
+        RunningSum r{wsum[tid & 7].x, wsum[tid & 7].y};
+        join8(r);
+        if (tid == kRowThreads - 1) {
+            if (a.splits > 1)
+                a.part[row * a.splits + sp] = make_float2(r.ref, r.sum);
+            else if (a.lse)
+                a.lse[row] = lse_of(r.ref, (double)r.sum);
+        }
     }
 }
 
@@ -308,12 +308,13 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
             s_n = 0;
         }
     } else if (tid < 128 && a.lse) {
-        float2 p = make_float2(0.0f, 0.0f);
-        if (tid - 64 < a.splits) p = a.part[row * a.splits + (tid - 64)];
-        float ref = group_reduce<OpMaxF, 64>(p.y != 0.0f ? p.x : kNegInf);
-        if (ref == kNegInf) ref = 0.0f;
-        const double sum = wave_sum_f64(p.y != 0.0f ? (double)p.y * exp2((double)p.x - (double)ref) : 0.0);
-        if (tid == 64) a.lse[row] = lse_of(ref, sum);
+        RunningSum r = RunningSum::none();
+        if (tid - 64 < a.splits) {
+            const float2 p = a.part[row * a.splits + (tid - 64)];
+            r = RunningSum{p.x, p.y};
+        }
+        wave_join(r);
+        if (tid == 64) a.lse[row] = lse_of(r.ref, (double)r.sum);
     }
     __syncthreads();
     const uint64_t low = s_low;

@@ -10,13 +10,14 @@ using namespace scape;
 
 namespace scape {
 
-// A row is split where it does not fit a workgroup's registers, and where
-// there are fewer rows than it takes to fill the 256 CUs: up to kFill
-// workgroups in all, none with less than a granule for every thread.
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols) {
+// A row is split where a kernel must hold it and it does not fit a workgroup's
+// registers, and where there are fewer rows than it takes to fill the 256 CUs:
+// up to kFill workgroups in all, none with less than a granule for every
+// thread.
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool resident) {
     constexpr int64_t kFill = 512;
     const int64_t g = row_granules(dtype, cols);
-    const int64_t need = (g + kRowCapacity - 1) / kRowCapacity;
+    const int64_t need = resident ? (g + kRowCapacity - 1) / kRowCapacity : 1;
     int64_t want = rows > 0 ? kFill / rows : 1;
     if (want > g / kRowThreads) want = g / kRowThreads;
     if (want > kMaxSplits) want = kMaxSplits;
@@ -102,7 +103,7 @@ int topk_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* s
         if (rows > kMaxSmallRows) return fail(SCAPE_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
         return SCAPE_OK;
     }
-    *sp = row_split(dtype, rows, cols);
+    *sp = row_split(dtype, rows, cols, true);
     return check_blocks(rows, *sp);
 }
 int64_t topk_bytes(int64_t rows, int32_t k, const RowSplit& sp) {
@@ -113,7 +114,7 @@ int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit
     int rc;
     if ((rc = check_dtype(dtype, "z"))) return rc;
     if ((rc = check_rows(rows, cols, k, SCAPE_DISTILL_MAX_K))) return rc;
-    *sp = row_split(dtype, rows, cols);
+    *sp = row_split(dtype, rows, cols, false);
     return check_blocks(rows, *sp);
 }
 int64_t distill_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }

@@ -141,6 +141,35 @@ __device__ __forceinline__ float granule_max(const gran& g) {
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
 
+// A running sum of 2^(c2 x) held as sum * 2^ref, ref the largest c2 x so far
+// (as a float that the exponents are then taken against exactly, so it adds
+// no error).  It follows the loads as they arrive: no pass for the maximum
+// first.  -inf adds nothing; NaN and +inf make the sum NaN.
+struct RunningSum {
+    float ref, sum;
+    static __device__ __forceinline__ RunningSum none() { return RunningSum{-3.402823466e38f, 0.0f}; }
+    // B granules whose largest element is m
+    template <class T, int B>
+    __device__ __forceinline__ void add(const gran (&g)[B], float m, float c2) {
+        const float r = fmaxf(ref, m * c2);
+        float s0 = sum * fast_exp2(ref - r), s1 = 0.0f;  // two chains, for the adders
+        ref = r;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int j = 0; j < T::kN; j += 2) {
+                s0 += fast_exp2(__builtin_fmaf(T::up(g[b], j), c2, -r));
+                s1 += fast_exp2(__builtin_fmaf(T::up(g[b], j + 1), c2, -r));
+            }
+        sum = s0 + s1;
+    }
+    __device__ __forceinline__ void add1(float x, float c2) {
+        const float r = fmaxf(ref, x * c2);
+        sum = sum * fast_exp2(ref - r) + fast_exp2(__builtin_fmaf(x, c2, -r));
+        ref = r;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Reductions.  Over a wave without LDS: quads and rows of 16 by DPP
 // permutations, then rows against rows with the gfx950 row swaps (both
@@ -153,6 +182,9 @@ __device__ __forceinline__ uint32_t dpp32(uint32_t x) {
 
 struct OpMaxF {
     static __device__ __forceinline__ float f(float a, float b) { return max_nan(a, b); }
+};
+struct OpMaxNum {  // NaN left out
+    static __device__ __forceinline__ float f(float a, float b) { return fmaxf(a, b); }
 };
 struct OpSumF {
     static __device__ __forceinline__ float f(float a, float b) { return a + b; }
@@ -228,6 +260,19 @@ __device__ __forceinline__ double from_lane(double x, int lane) {
     return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane) |
                                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane)
                                               << 32);
+}
+
+// Joins the lanes' running sums: every lane gets the wave's.
+__device__ __forceinline__ void wave_join(RunningSum& r) {
+    const float ref = group_reduce<OpMaxNum, 64>(r.ref);
+    r.sum = group_reduce<OpSumF, 64>(r.sum * fast_exp2(r.ref - ref));
+    r.ref = ref;
+}
+// Joins the sums of eight waves, that of wave l in the lanes l, l + 8, ...
+__device__ __forceinline__ void join8(RunningSum& r) {
+    const float ref = group_reduce<OpMaxNum, 8>(r.ref);
+    r.sum = group_reduce<OpSumF, 8>(r.sum * fast_exp2(r.ref - ref));
+    r.ref = ref;
 }
 
 // Registers a row kernel may use, as waves per SIMD: two or three workgroups

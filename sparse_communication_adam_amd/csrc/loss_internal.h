@@ -23,9 +23,9 @@ struct Logits {
 inline int dtype_size(int32_t dtype) { return dtype == SCAPE_DTYPE_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------------------
-// Row kernels: a workgroup of kRowThreads threads holds a run of a row's
-// granules in registers, at most kRowGranules a thread; a longer row, or one
-// of few rows, is split over several workgroups.
+// Row kernels: a workgroup of kRowThreads threads takes a row, or a part of
+// one.  A kernel that holds it in registers holds at most kRowGranules
+// granules a thread.
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kRowGranules = 16;
@@ -44,7 +44,7 @@ struct RowSplit {
     int32_t splits;
     int32_t per;  // granules of each split (the last one may have fewer)
 };
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols);
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool resident);
 
 // ---- k_topk.hip
 constexpr int kTopkList = 2048;       // candidates a workgroup sorts in LDS (>= SCAPE_TOPK_MAX_K)
