@@ -24,86 +24,124 @@
 // log p_T.  The latter is near 0 where the entries hold little of the
 // student's mass, and the gradient's tail factor (Q - q_T / p_T) p_T =
 // sum q_j p_T + q_T (p_T - 1) is then made of two small terms.
+#include <type_traits>
+
 #include "loss_device.h"
 
 namespace scape {
 
-static_assert(kRowWaves == 8, "the waves' partial sums are joined by eight lanes");
-constexpr int kEntries = SCAPE_DISTILL_MAX_K / kRowThreads;  // entries a thread
-static_assert(SCAPE_DISTILL_MAX_K % kRowThreads == 0, "entries are dealt out evenly");
-
-// The bitmap: column v is bit v + 8 - head, so that a granule's columns are a
-// byte of it, or half of one.
-inline uint32_t bitmap_words(int64_t cols) { return (uint32_t)((cols + 8 + 31) / 32); }
-template <class T>
-__device__ __forceinline__ uint32_t granule_bits(const uint32_t* bitmap, int32_t i) {
-    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bitmap);
-    return T::kN == 8 ? bytes[1 + i] : ((uint32_t)bytes[1 + (i >> 1)] >> (4 * (i & 1))) & 15u;
-}
-
-// A row's teacher entries, thread t holding entries t, t + kRowThreads, ...
-struct Entries {
-    int32_t col[kEntries];  // -1: none
-    float t[kEntries];      // the teacher's value
-    float z[kEntries];      // the student's logit
-    // kept for the gradient in float32 (the sums are over float64): each is
-    // rounded once more, a step of a float32 gradient
-    float q[kEntries];  // exp of the teacher's log-probability (against the wave's largest where its lse is not given)
-    float p[kEntries];  // 2^x_j against the wave's largest, x_j = z_j c2
+// LDS of a workgroup: a bitmap of the row's columns, then the row's k slots:
+// column (-1: no entry), teacher's value and student's logit.
+//
+// The bitmap lies as a thread's granules do, four of them (tid, tid + threads,
+// ...) in one cell: whether a thread's next four granules hold an entry is one
+// read and one test.  The lone elements beside the granules have 16 bits of
+// their own behind the cells.
+template <class T, int kThreads>
+struct Bitmap {
+    using Cell = std::conditional_t<T::kN == 8, uint32_t, uint16_t>;
+    static constexpr int kCellBits = 4 * T::kN, kCellGranules = 4 * kThreads;
+    Cell* cells;
+    RowShape sh;
+    int32_t n;
+    static __host__ __device__ int32_t cell_count(int32_t granules) {
+        return (granules + kCellGranules - 1) / kCellGranules * kThreads;
+    }
+    // for rows of at most this many granules
+    static __host__ __device__ int32_t bytes(int32_t granules) {
+        return (cell_count(granules) * (int32_t)sizeof(Cell) + 4 + 15) / 16 * 16;
+    }
+    __device__ __forceinline__ uint32_t bit_of(int32_t col) const {
+        const int32_t e = col - sh.head, i = e / T::kN;
+        if (e >= 0 && i < sh.granules) {
+            const int32_t cell = i / kCellGranules * kThreads + i % kThreads;
+            return (uint32_t)(cell * kCellBits + (i / kThreads & 3) * T::kN + e % T::kN);
+        }
+        return (uint32_t)(cell_count(sh.granules) * kCellBits + (e < 0 ? col : 8 + col - (n - sh.tail)));
+    }
+    __device__ __forceinline__ void clear() const {
+        const int32_t words = bytes(sh.granules) / 4;
+        uint32_t* w = reinterpret_cast<uint32_t*>(cells);
+        for (int32_t i = (int32_t)threadIdx.x; i < words; i += kThreads) w[i] = 0;
+    }
+    // whether it was set before
+    __device__ __forceinline__ bool set(int32_t col) const {
+        const uint32_t at = bit_of(col), bit = 1u << (at & 31u);
+        return (atomicOr(reinterpret_cast<uint32_t*>(cells) + (at >> 5), bit) & bit) != 0;
+    }
+    __device__ __forceinline__ bool has(int32_t col) const {
+        const uint32_t at = bit_of(col);
+        return (reinterpret_cast<const uint32_t*>(cells)[at >> 5] >> (at & 31u)) & 1u;
+    }
+    // Strikes the entries out of the thread's granules tid + (b + 4 c) kThreads, b < 4, c = cell_row.
+    __device__ __forceinline__ void strike(int32_t cell_row, gran (&g)[4]) const {
+        const uint32_t bits = cells[cell_row * kThreads + (int32_t)threadIdx.x];
+        if (bits) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int j = 0; j < T::kN; ++j)
+                    if (bits & (1u << (b * T::kN + j))) T::set(g[b], j, (typename T::raw)T::kNegInfBits);
+        }
+    }
 };
 
-// Reads the row's columns; one outside the row is no entry.
-__device__ __forceinline__ void read_columns(const DistillArgs& a, int64_t row, Entries& en) {
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i) {
-        const int32_t slot = (int32_t)threadIdx.x + i * kRowThreads;
-        int32_t c = -1;
-        if (slot < a.k) c = a.t_idx[row * a.k + slot];
-        en.col[i] = c >= 0 && c < (int32_t)a.in.cols ? c : -1;
-    }
+// The k slots of a row.  Slot tid's values wait in registers until the row's
+// logits have gone by; t and z hold the entry's terms q and p afterwards.
+struct Slots {
+    int32_t* col;
+    float* t;
+    float* z;
+    float t0, z0;
+};
+inline int32_t slot_bytes(int32_t k) { return 12 * k; }
+
+// Column of a slot; one outside the row is no entry.
+__device__ __forceinline__ int32_t slot_column(const DistillArgs& a, int64_t row, int32_t slot) {
+    const int32_t c = slot < a.k ? a.t_idx[row * a.k + slot] : -1;
+    return c >= 0 && c < (int32_t)a.in.cols ? c : -1;
 }
 
-// Reads the entries' values, and their logits for columns in [lo, hi).
-template <class T>
-__device__ __forceinline__ void read_values(const DistillArgs& a, int64_t row, const typename T::raw* z, int32_t lo,
-                                            int32_t hi, Entries& en) {
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i) {
-        en.t[i] = en.z[i] = 0.0f;
-        if (en.col[i] >= 0) {
-            en.t[i] = load_any(a.t_val, a.t_dtype, row * a.k + (int32_t)threadIdx.x + i * kRowThreads);
-            if (en.col[i] >= lo && en.col[i] < hi) en.z[i] = T::up1(z[en.col[i]]);
-        }
-    }
-}
-
-// Marks the entries' columns in the bitmap, which the workgroup has cleared
-// (a barrier ago).  An entry whose column a lower slot has is dropped.
-// Returns whether the row has any entry.  The bitmap is complete after it.
-__device__ __forceinline__ bool mark_columns(const DistillArgs& a, int64_t row, int32_t head, uint32_t* bitmap,
-                                             Entries& en) {
+// Reads the slots' values, logits for columns in [lo, hi) only (hi = 0: no
+// values at all), and marks the columns.  c0 is slot tid's column.  An entry
+// whose column a lower slot has is dropped.  The bitmap has been cleared, by
+// this workgroup, without a barrier since; it is complete afterwards.  Returns
+// whether the row has any entry.
+template <class T, int kThreads>
+__device__ __forceinline__ bool read_slots(const DistillArgs& a, int64_t row, const typename T::raw* z, int32_t lo,
+                                           int32_t hi, int32_t c0, const Bitmap<T, kThreads>& bitmap, Slots& s) {
+    const int32_t tid = (int32_t)threadIdx.x;
+    __syncthreads();
     uint32_t seen = 0;  // bit 0: some entry; bit 1: some column twice
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i)
-        if (en.col[i] >= 0) {
-            const uint32_t at = (uint32_t)(en.col[i] + 8 - head), bit = 1u << (at & 31u);
-            seen |= (atomicOr(&bitmap[at >> 5], bit) & bit) ? 3u : 1u;
+    s.t0 = s.z0 = 0.0f;
+    for (int32_t slot = tid; slot < a.k; slot += kThreads) {
+        const int32_t c = slot == tid ? c0 : slot_column(a, row, slot);
+        s.col[slot] = c;
+        if (c < 0) continue;
+        float t = 0.0f, x = 0.0f;
+        if (hi > 0) t = load_any(a.t_val, a.t_dtype, row * a.k + slot);
+        if (c >= lo && c < hi) x = T::up1(z[c]);
+        if (slot == tid) {
+            s.t0 = t;
+            s.z0 = x;
+        } else {
+            s.t[slot] = t;
+            s.z[slot] = x;
         }
-    const bool any = __syncthreads_or(seen != 0);
-    if (!any) return false;
-    if (__syncthreads_or((seen & 2u) != 0)) {
+        seen |= bitmap.set(c) ? 3u : 1u;
+    }
+    if (!__syncthreads_or((int)seen)) return false;
+    if (__syncthreads_or((int)(seen & 2u))) {
         // which of two threads came first is chance, so every entry looks for
         // its column in the slots below its own
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i)
-            if (en.col[i] >= 0) {
-                const int32_t slot = (int32_t)threadIdx.x + i * kRowThreads;
-                for (int32_t j = 0; j < slot; ++j)
-                    if (a.t_idx[row * a.k + j] == en.col[i]) {
-                        en.col[i] = -1;
-                        break;
-                    }
-            }
+        for (int32_t slot = tid; slot < a.k; slot += kThreads) {
+            const int32_t c = s.col[slot];
+            for (int32_t j = 0; j < slot && c >= 0; ++j)
+                if (a.t_idx[row * a.k + j] == c) {
+                    s.col[slot] = -1;
+                    break;
+                }
+        }
     }
     return true;
 }
@@ -125,32 +163,35 @@ struct WaveSums {
 };
 constexpr float kLowest = -3.402823466e38f;
 
-// kStudent: also the student's terms.  en.q and en.p are set.
-template <bool kStudent>
-__device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse, Entries& en) {
+// kStudent: also the student's terms.  Slots' t and z become q and p, for the
+// gradient, in float32: each is rounded once more, a step of a float32
+// gradient (the sums are over float64).
+template <int kThreads, bool kStudent>
+__device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse, Slots& sl) {
+    const int32_t tid = (int32_t)threadIdx.x;
     WaveSums s{0.0, 0.0, 0.0, 0.0, kLowest, a.t_lse ? 0.0f : kLowest};
-    bool some = false;
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i) {
-        en.q[i] = en.p[i] = 0.0f;
-        if (en.col[i] >= 0) {
-            some = true;
-            if (kStudent) s.mt = fmaxf(s.mt, en.z[i] * a.c2);
-            if (!a.t_lse) s.mq = fmaxf(s.mq, en.t[i] * a.scale);
-        }
+    if (tid < a.k) {
+        sl.t[tid] = sl.t0;
+        sl.z[tid] = sl.z0;
     }
+    bool some = false;
+    for (int32_t slot = tid; slot < a.k; slot += kThreads)
+        if (sl.col[slot] >= 0) {
+            some = true;
+            if (kStudent) s.mt = fmaxf(s.mt, sl.z[slot] * a.c2);
+            if (!a.t_lse) s.mq = fmaxf(s.mq, sl.t[slot] * a.scale);
+        }
     if (wave_ballot(some) == 0) return s;
     if (kStudent) s.mt = group_reduce<OpMaxNum, 64>(s.mt);
     if (!a.t_lse) s.mq = group_reduce<OpMaxNum, 64>(s.mq);
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i)
-        if (en.col[i] >= 0) {
-            const double lq = log_q(a, lse, en.t[i]) - (double)s.mq, q = exp(lq);
-            en.q[i] = (float)q;
+    for (int32_t slot = tid; slot < a.k; slot += kThreads)
+        if (sl.col[slot] >= 0) {
+            const double lq = log_q(a, lse, sl.t[slot]) - (double)s.mq, q = exp(lq);
+            sl.t[slot] = (float)q;
             s.q += q;
             if (kStudent) {
-                const double x = (double)en.z[i] * (double)a.c2, p = exp2(x - (double)s.mt);
-                en.p[i] = (float)p;
+                const double x = (double)sl.z[slot] * (double)a.c2, p = exp2(x - (double)s.mt);
+                sl.z[slot] = (float)p;
                 s.top += p;
                 if (q != 0.0) {
                     s.qt += q * lq;
@@ -172,30 +213,31 @@ struct RowResult {
     float loss;          // KL
     float stat0, stat1;  // L, log p_T
     float vref, tail;    // the tail's gradient is tail 2^(x_v - vref)
-    double p, q;         // an entry's gradient is p en.p - q en.q, for the entries of this lane's wave (lane % 8)
+    double p, q;         // an entry's gradient is p p_j - q q_j, for the entries of this lane's wave (lane % kWaves)
     bool dead;           // no student mass at all: nothing to learn
 };
 
-// A whole wave calls it; lane l brings the entries' sums of wave l % 8 and
-// the tail's running sum of the row.  The four logarithms of the row are one,
-// on four lanes.
+// A whole wave calls it; lane l brings the entries' sums of wave l % kWaves
+// and the tail's running sum of the row.  The four logarithms of the row are
+// one, on four lanes.
+template <int kWaves>
 __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const RunningSum& tail, const WaveSums& w) {
     RowResult r;
     const double t = (double)tail.sum;
     const bool has_tail = !(t == 0.0);
     const double tref = (double)tail.ref;
-    const double ref = fmax(has_tail ? tref : (double)kLowest, (double)group_reduce<OpMaxNum, 8>(w.mt));
+    const double ref = fmax(has_tail ? tref : (double)kLowest, (double)group_reduce<OpMaxNum, kWaves>(w.mt));
     const double fp = exp2((double)w.mt - ref);
-    const double top = sum8_f64(w.top * fp);
+    const double top = sum_waves_f64<kWaves>(w.top * fp);
     double fq = 1.0, qt = w.qt;
     if (!a.t_lse) {
-        const double d = (double)w.mq - (double)group_reduce<OpMaxNum, 8>(w.mq);
+        const double d = (double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq);
         fq = exp(d);
         qt += w.q != 0.0 ? w.q * d : 0.0;
     }
-    const double q = sum8_f64(w.q * fq);
-    qt = sum8_f64(qt * fq);
-    const double qx = sum8_f64(w.qx * fq);
+    const double q = sum_waves_f64<kWaves>(w.q * fq);
+    qt = sum_waves_f64<kWaves>(qt * fq);
+    const double qx = sum_waves_f64<kWaves>(w.qx * fq);
     const double far = has_tail ? exp2(tref - ref) : 0.0;  // 0 too where the tail is out of range
     const double sum = t * far + top;
     double qsum, rest = 0.0;
@@ -269,63 +311,62 @@ struct Part {
         col0 = sp == 0 ? 0 : first;
         col1 = last ? n : first + cnt * T::kN;
     }
-    __device__ __forceinline__ gran load(int32_t i) const { return i < cnt ? body[i] : no_entries<T>(); }
+    // four granules of a thread, from number base + tid on
+    template <int kThreads>
+    __device__ __forceinline__ void load(int32_t base, gran (&g)[4]) const {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int32_t i = base + (int32_t)threadIdx.x + b * kThreads;
+            g[b] = no_entries<T>();
+            if (i < cnt) g[b] = granule_at(body, i);
+        }
+    }
 };
 
-__device__ __forceinline__ void clear_bitmap(uint32_t* bitmap, int32_t n) {
-    const uint32_t words = (uint32_t)(n + 8 + 31) / 32u;
-    for (uint32_t i = threadIdx.x; i < words; i += kRowThreads) bitmap[i] = 0;
-}
-
-// Granule g, number i of the row, without the entries' columns.
-template <class T>
-__device__ __forceinline__ void strike(const uint32_t* bitmap, int32_t i, gran& g) {
-    const uint32_t b = granule_bits<T>(bitmap, i);
-    if (b) {
-#pragma unroll
-        for (int j = 0; j < T::kN; ++j)
-            if (b & (1u << j)) T::set(g, j, (typename T::raw)T::kNegInfBits);
-    }
-}
-__device__ __forceinline__ bool struck(const uint32_t* bitmap, int32_t head, int32_t col) {
-    const uint32_t at = (uint32_t)(col + 8 - head);
-    return (bitmap[at >> 5] >> (at & 31u)) & 1u;
-}
-
 // A row that is not read: zeros.
-template <class T>
+template <class T, int kThreads>
 __device__ __forceinline__ void zero_part(const Part<T>& p, typename T::raw* dz) {
-    for (int32_t i = (int32_t)threadIdx.x; i < p.cnt; i += kRowThreads)
-        store_loose(dz + p.first + i * T::kN, gran{0u, 0u, 0u, 0u});
+    for (int32_t i = (int32_t)threadIdx.x; i < p.cnt; i += kThreads)
+        store_loose(dz + p.first, i, gran{0u, 0u, 0u, 0u});
     if (p.lone >= 0) dz[p.lone] = 0;
+}
+
+template <class T, int kThreads>
+__device__ __forceinline__ void lds_layout(const DistillArgs& a, const RowShape& sh, uint8_t* lds,
+                                           Bitmap<T, kThreads>& bitmap, Slots& s) {
+    bitmap.cells = reinterpret_cast<typename Bitmap<T, kThreads>::Cell*>(lds);
+    bitmap.sh = sh;
+    bitmap.n = (int32_t)a.in.cols;
+    s.col = reinterpret_cast<int32_t*>(lds + Bitmap<T, kThreads>::bytes(sh.granules));
+    s.t = reinterpret_cast<float*>(s.col + a.k);
+    s.z = s.t + a.k;
 }
 
 // kPart: only the part's running sum of the tail, for k_distill_join.
 // Four granules a thread are worked on while the next four are on their way.
 template <class T, bool kPart>
-__global__ __launch_bounds__(kRowThreads, 8) void k_distill_loss(DistillArgs a) {
-    extern __shared__ uint32_t bitmap[];
-    __shared__ float2 wsum[kRowWaves];
-    __shared__ WaveSums wrec[kRowWaves];
-    constexpr int kBatch = 4, kStep = kBatch * kRowThreads;
+__global__ __launch_bounds__(kStreamThreads, 8) void k_distill_loss(DistillArgs a) {
+    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ float2 wsum[kNW];
+    __shared__ WaveSums wrec[kNW];
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
     const float w = a.weight ? a.weight[p.row] : 1.0f;
-    gran g[kBatch], next[kBatch];
+    Bitmap<T, kThreads> bitmap;
+    Slots slots;
+    lds_layout(a, p.sh, lds, bitmap, slots);
+    gran g[4], next[4];
     float lx = kNegInf;
-    Entries en;
     double t_lse = 0.0;
     bool alive = false;
     if (w != 0.0f) {
-        read_columns(a, p.row, en);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) g[b] = p.load(tid + b * kRowThreads);
+        const int32_t c0 = slot_column(a, p.row, tid);
+        p.template load<kThreads>(0, g);
         if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
-        read_values<T>(a, p.row, p.z, 0, kPart ? 0 : p.n, en);
         if (!kPart && a.t_lse) t_lse = (double)a.t_lse[p.row];
-        clear_bitmap(bitmap, p.n);
-        __syncthreads();
-        alive = mark_columns(a, p.row, p.sh.head, bitmap, en);
+        bitmap.clear();
+        alive = read_slots<T, kThreads>(a, p.row, p.z, 0, kPart ? 0 : p.n, c0, bitmap, slots);
     }
     if (!alive) {  // the same for the whole workgroup
         if (tid == 0) {
@@ -337,117 +378,106 @@ __global__ __launch_bounds__(kRowThreads, 8) void k_distill_loss(DistillArgs a) 
         return;
     }
     RunningSum rs = RunningSum::none();
-    if (p.lone >= 0 && !struck(bitmap, p.sh.head, p.lone)) rs.add1(lx, a.c2);
+    if (p.lone >= 0 && !bitmap.has(p.lone)) rs.add1(lx, a.c2);
     for (int32_t base = 0; base < p.cnt; base += kStep) {
-        const int32_t i = base + tid;
-        if (base + kStep < p.cnt) {
+        if (base + kStep < p.cnt) p.template load<kThreads>(base + kStep, next);
+        bitmap.strike((p.g0 + base) / kStep, g);
+        float m = granule_max<T>(g[0]);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) next[b] = p.load(i + kStep + b * kRowThreads);
-        }
-        float m = kNegInf;
+        for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(g[b]));
+        rs.template add<T, 4>(g, m, a.c2);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (i + b * kRowThreads < p.cnt) strike<T>(bitmap, p.g0 + i + b * kRowThreads, g[b]);
-            m = max_nan(m, granule_max<T>(g[b]));
-        }
-        rs.template add<T, kBatch>(g, m, a.c2);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) g[b] = next[b];
+        for (int b = 0; b < 4; ++b) g[b] = next[b];
     }
     wave_join(rs);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     if constexpr (!kPart) {
-        const WaveSums ws = entry_sums<true>(a, t_lse, en);
+        const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
     __syncthreads();
     if (wave == 0) {
-        RunningSum r{wsum[tid & 7].x, wsum[tid & 7].y};
-        join8(r);
+        RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
+        join_waves<kNW>(r);
         if constexpr (kPart) {
             if (tid == 0) a.part[p.row * a.splits + p.sp] = make_float2(r.ref, r.sum);
         } else {
-            const RowResult res = finish_row(a, r, wrec[tid & 7]);
+            const RowResult res = finish_row<kNW>(a, r, wrec[tid & (kNW - 1)]);
             if (tid == 0) write_row(a, p.row, w, res);
         }
     }
 }
 
-// Writes the entries' columns: d_j = fp en.p - fq en.q.
-template <class T>
-__device__ __forceinline__ void write_entries(const Part<T>& p, const Entries& en, float gs, double fp, double fq,
-                                              typename T::raw* dz) {
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i)
-        if (en.col[i] >= p.col0 && en.col[i] < p.col1)
-            dz[en.col[i]] = gs == 0.0f ? (typename T::raw)0
-                                       : T::down1((float)((double)gs * (fp * (double)en.p[i] - fq * (double)en.q[i])));
+// Writes the entries' columns: d_j = gs (fp p_j - fq q_j).
+template <class T, int kThreads>
+__device__ __forceinline__ void write_entries(const DistillArgs& a, const Part<T>& p, const Slots& s, float gs,
+                                              double fp, double fq, typename T::raw* dz) {
+    for (int32_t slot = (int32_t)threadIdx.x; slot < a.k; slot += kThreads) {
+        const int32_t c = s.col[slot];
+        if (c < 0 || c < p.col0 || c >= p.col1) continue;
+        const double d = (double)gs * (fp * (double)s.z[slot] - fq * (double)s.t[slot]);
+        dz[c] = gs == 0.0f ? (typename T::raw)0 : T::down1((float)d);
+    }
 }
 
 // Loss and gradient of whole rows, kGran granules a thread.
-template <class T, int kGran>
-__global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_distill_fused(DistillArgs a) {
-    extern __shared__ uint32_t bitmap[];
-    __shared__ float2 wsum[kRowWaves];
-    __shared__ WaveSums wrec[kRowWaves];
-    __shared__ double s_p[kRowWaves], s_q[kRowWaves];
+template <class T, int kThreads, int kGran>
+__global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
+    constexpr int kNW = kThreads / 64;
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ float2 wsum[kNW];
+    __shared__ WaveSums wrec[kNW];
+    __shared__ double s_p[kNW], s_q[kNW];
     __shared__ float s_vref, s_tail, s_gs;
-    constexpr int kBatch = kGran < 4 ? kGran : 4;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     const float w = a.weight ? a.weight[p.row] : 1.0f;
-    gran g[kGran];
+    Bitmap<T, kThreads> bitmap;
+    Slots slots;
+    lds_layout(a, p.sh, lds, bitmap, slots);
+    gran g[kGran / 4][4];
     float lx = kNegInf;
-    Entries en;
     double t_lse = 0.0;
     bool alive = false;
     if (w != 0.0f) {
-        read_columns(a, p.row, en);
+        const int32_t c0 = slot_column(a, p.row, tid);
 #pragma unroll
-        for (int c = 0; c < kGran; ++c) g[c] = p.load(tid + c * kRowThreads);
+        for (int c = 0; c < kGran / 4; ++c) p.template load<kThreads>(c * 4 * kThreads, g[c]);
         if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
-        read_values<T>(a, p.row, p.z, 0, p.n, en);
         if (a.t_lse) t_lse = (double)a.t_lse[p.row];
-        clear_bitmap(bitmap, p.n);
-        __syncthreads();
-        alive = mark_columns(a, p.row, p.sh.head, bitmap, en);
+        bitmap.clear();
+        alive = read_slots<T, kThreads>(a, p.row, p.z, 0, p.n, c0, bitmap, slots);
     }
     if (!alive) {  // the same for the whole workgroup
         if (tid == 0) write_no_row(a, p.row);
-        zero_part(p, dz);
+        zero_part<T, kThreads>(p, dz);
         return;
     }
     RunningSum rs = RunningSum::none();
-    if (p.lone >= 0 && !struck(bitmap, p.sh.head, p.lone)) rs.add1(lx, a.c2);
-    const int32_t tid1 = again(tid);
+    if (p.lone >= 0 && !bitmap.has(p.lone)) rs.add1(lx, a.c2);
 #pragma unroll
-    for (int c = 0; c < kGran; c += kBatch)
-        if (c * kRowThreads < p.cnt) {
-            gran x[kBatch];
-            float m = kNegInf;
+    for (int c = 0; c < kGran / 4; ++c)
+        if (c * 4 * kThreads < p.cnt) {
+            bitmap.strike(c, g[c]);
+            float m = granule_max<T>(g[c][0]);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int32_t i = tid1 + (c + b) * kRowThreads;
-                if (i < p.cnt) strike<T>(bitmap, i, g[c + b]);
-                x[b] = g[c + b];
-                m = max_nan(m, granule_max<T>(x[b]));
-            }
-            rs.template add<T, kBatch>(x, m, a.c2);
+            for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(g[c][b]));
+            rs.template add<T, 4>(g[c], m, a.c2);
         }
     wave_join(rs);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     {
-        const WaveSums ws = entry_sums<true>(a, t_lse, en);
+        const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
     __syncthreads();
     if (wave == 0) {
-        RunningSum r{wsum[tid & 7].x, wsum[tid & 7].y};
-        join8(r);
-        const RowResult res = finish_row(a, r, wrec[tid & 7]);
-        if (tid < kRowWaves) {
+        RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
+        join_waves<kNW>(r);
+        const RowResult res = finish_row<kNW>(a, r, wrec[tid & (kNW - 1)]);
+        if (tid < kNW) {
             s_p[tid] = res.p;
             s_q[tid] = res.q;
         }
@@ -464,69 +494,68 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_distill_fused
     const int32_t tid2 = again(tid);
 #pragma unroll
     for (int c = 0; c < kGran; ++c) {
-        const int32_t i = tid2 + c * kRowThreads;
-        forget_unpacked(g[c]);
+        const int32_t i = tid2 + c * kThreads;
+        gran& x = g[c / 4][c % 4];
+        forget_unpacked(x);
         if (i < p.cnt) {
             float d[T::kN];
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2(__builtin_fmaf(T::up(g[c], j), a.c2, -vref));
-            store_loose(dz + p.first + i * T::kN, T::down(d));
+            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2(__builtin_fmaf(T::up(x, j), a.c2, -vref));
+            store_loose(dz + p.first, i, T::down(d));
         }
     }
     if (p.lone >= 0) dz[p.lone] = T::down1(f * fast_exp2(__builtin_fmaf(lx, a.c2, -vref)));
     __syncthreads();  // the entries' columns are written over the tail's values
-    write_entries(p, en, s_gs, s_p[wave], s_q[wave], dz);
+    write_entries<T, kThreads>(a, p, slots, s_gs, s_p[wave], s_q[wave], dz);
 }
 
 // The gradient of a row or a part of one, from the statistics.
 template <class T>
-__global__ __launch_bounds__(kRowThreads, 8) void k_distill_grad(DistillArgs a) {
-    extern __shared__ uint32_t bitmap[];
-    __shared__ WaveSums wrec[kRowWaves];
-    __shared__ double s_p, s_q[kRowWaves];
+__global__ __launch_bounds__(kStreamThreads, 8) void k_distill_grad(DistillArgs a) {
+    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ WaveSums wrec[kNW];
+    __shared__ double s_p, s_q[kNW];
     __shared__ float s_vref, s_tail, s_gs;
-    constexpr int kBatch = 4, kStep = kBatch * kRowThreads;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     float w = a.weight ? a.weight[p.row] : 1.0f;
     if (a.dloss) w = w == 0.0f ? 0.0f : w * a.dloss[p.row];
-    gran g[kBatch], next[kBatch];
+    Bitmap<T, kThreads> bitmap;
+    Slots slots;
+    lds_layout(a, p.sh, lds, bitmap, slots);
+    gran g[4], next[4];
     float lx = kNegInf;
-    Entries en;
     double t_lse = 0.0;
     bool alive = false;
     if (w != 0.0f) {
-        read_columns(a, p.row, en);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) g[b] = p.load(tid + b * kRowThreads);
+        const int32_t c0 = slot_column(a, p.row, tid);
+        p.template load<kThreads>(0, g);
         if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
+        if (a.t_lse) t_lse = (double)a.t_lse[p.row];
+        bitmap.clear();
         // dz may be z, and other workgroups write their parts of it: only
         // this part's logits are read
-        read_values<T>(a, p.row, p.z, p.col0, p.col1, en);
-        if (a.t_lse) t_lse = (double)a.t_lse[p.row];
-        clear_bitmap(bitmap, p.n);
-        __syncthreads();
-        alive = mark_columns(a, p.row, p.sh.head, bitmap, en);
+        alive = read_slots<T, kThreads>(a, p.row, p.z, p.col0, p.col1, c0, bitmap, slots);
     }
     if (!alive) {  // the same for the whole workgroup
-        zero_part(p, dz);
+        zero_part<T, kThreads>(p, dz);
         return;
     }
+    const float l = a.stats[2 * p.row], lpt = a.stats[2 * p.row + 1];
     {
-        const WaveSums ws = entry_sums<false>(a, t_lse, en);
+        const WaveSums ws = entry_sums<kThreads, false>(a, t_lse, slots);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
-    const float l = a.stats[2 * p.row], lpt = a.stats[2 * p.row + 1];
-#pragma unroll
-    for (int i = 0; i < kEntries; ++i)
-        if (en.col[i] >= 0) en.p[i] = (float)exp((double)en.z[i] * (double)a.scale - (double)l);
+    for (int32_t slot = tid; slot < a.k; slot += kThreads)
+        slots.z[slot] = (float)exp((double)slots.z[slot] * (double)a.scale - (double)l);
     __syncthreads();
     if (wave == 0) {
-        const WaveSums r = wrec[tid & 7];
-        const double fq = a.t_lse ? 1.0 : exp((double)r.mq - (double)group_reduce<OpMaxNum, 8>(r.mq));
-        const double q = sum8_f64(r.q * fq);
+        const WaveSums r = wrec[tid & (kNW - 1)];
+        const double fq = a.t_lse ? 1.0 : exp((double)r.mq - (double)group_reduce<OpMaxNum, kNW>(r.mq));
+        const double q = sum_waves_f64<kNW>(r.q * fq);
         const double qsum = a.t_lse ? q : q == 0.0 ? 0.0 : 1.0;
         const double rest = a.t_lse && 1.0 - q > 0.0 && lpt != kNegInf ? 1.0 - q : 0.0;
         // (Q - q_T / p_T) p_v, against L, or where 1 / p_T could leave the
@@ -538,7 +567,7 @@ __global__ __launch_bounds__(kRowThreads, 8) void k_distill_grad(DistillArgs a) 
             tail = (float)(near ? c / pt : c);
             if (!near) v = (float)((double)l + (double)lpt);
         }
-        if (tid < kRowWaves) s_q[tid] = fq * (qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q);
+        if (tid < kNW) s_q[tid] = fq * (qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q);
         if (tid == 0) {
             const float gs = l == kNegInf ? 0.0f : w * a.scale;
             s_p = qsum + rest;
@@ -557,90 +586,98 @@ __global__ __launch_bounds__(kRowThreads, 8) void k_distill_grad(DistillArgs a) 
         return f * fast_exp2(e);
     };
     for (int32_t base = 0; base < p.cnt; base += kStep) {
-        const int32_t i = base + tid;
-        if (base + kStep < p.cnt) {
+        if (base + kStep < p.cnt) p.template load<kThreads>(base + kStep, next);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) next[b] = p.load(i + kStep + b * kRowThreads);
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (i + b * kRowThreads < p.cnt) {
+        for (int b = 0; b < 4; ++b) {
+            const int32_t i = base + tid + b * kThreads;
+            if (i < p.cnt) {
                 float d[T::kN];
 #pragma unroll
                 for (int j = 0; j < T::kN; ++j) d[j] = grad(T::up(g[b], j));
-                store_loose(dz + p.first + (i + b * kRowThreads) * T::kN, T::down(d));
+                store_loose(dz + p.first, i, T::down(d));
             }
+        }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) g[b] = next[b];
+        for (int b = 0; b < 4; ++b) g[b] = next[b];
     }
     if (p.lone >= 0) dz[p.lone] = T::down1(grad(lx));
     __syncthreads();  // the entries' columns are written over the tail's values
-    write_entries(p, en, s_gs, s_p, s_q[wave], dz);
+    write_entries<T, kThreads>(a, p, slots, s_gs, s_p, s_q[wave], dz);
 }
 
 // Joins the parts of a split row: the loss and the statistics.
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void k_distill_join(DistillArgs a) {
-    extern __shared__ uint32_t bitmap[];
-    __shared__ WaveSums wrec[kRowWaves];
+__global__ __launch_bounds__(kStreamThreads) void k_distill_join(DistillArgs a) {
+    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64;
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ WaveSums wrec[kNW];
     using raw = typename T::raw;
-    const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64, n = (int32_t)a.in.cols;
+    const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const int64_t row = blockIdx.x;
     const raw* z = static_cast<const raw*>(a.in.z) + row * a.in.ld;
     const float w = a.weight ? a.weight[row] : 1.0f;
-    Entries en;
+    Bitmap<T, kThreads> bitmap;
+    Slots slots;
+    lds_layout(a, row_shape<T>(z, (int32_t)a.in.cols), lds, bitmap, slots);
     double t_lse = 0.0;
     bool alive = false;
     RunningSum r = RunningSum::none();  // of lane s: part s
     if (w != 0.0f) {
-        read_columns(a, row, en);
-        read_values<T>(a, row, z, 0, n, en);
+        const int32_t c0 = slot_column(a, row, tid);
         if (a.t_lse) t_lse = (double)a.t_lse[row];
         if ((tid & 63) < a.splits) {
             const float2 p = a.part[row * a.splits + (tid & 63)];
             r = RunningSum{p.x, p.y};
         }
-        clear_bitmap(bitmap, n);
-        __syncthreads();
-        alive = mark_columns(a, row, 0, bitmap, en);
+        bitmap.clear();
+        alive = read_slots<T, kThreads>(a, row, z, 0, (int32_t)a.in.cols, c0, bitmap, slots);
     }
     if (!alive) {
         if (tid == 0) write_no_row(a, row);
         return;
     }
-    const WaveSums ws = entry_sums<true>(a, t_lse, en);
+    const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
     if ((tid & 63) == 0) wrec[wave] = ws;
     __syncthreads();
     if (wave == 0) {
         wave_join(r);
-        const RowResult res = finish_row(a, r, wrec[tid & 7]);
+        const RowResult res = finish_row<kNW>(a, r, wrec[tid & (kNW - 1)]);
         if (tid == 0) write_row(a, row, w, res);
     }
 }
 
-static size_t bitmap_bytes(const DistillArgs& a) { return bitmap_words(a.in.cols) * sizeof(uint32_t); }
+template <class T, int kThreads>
+static size_t lds_bytes(const DistillArgs& a) {
+    return (size_t)(Bitmap<T, kThreads>::bytes((int32_t)row_granules(a.in.dtype, a.in.cols)) + slot_bytes(a.k));
+}
 static dim3 parts(const DistillArgs& a) { return dim3((uint32_t)(a.in.rows * a.splits)); }
 
 template <class T>
 static hipError_t backward_typed(hipStream_t s, const DistillArgs& a) {
-    hipLaunchKernelGGL((k_distill_grad<T>), parts(a), dim3(kRowThreads), bitmap_bytes(a), s, a);
+    hipLaunchKernelGGL((k_distill_grad<T>), parts(a), dim3(kStreamThreads), (lds_bytes<T, kStreamThreads>(a)), s, a);
     return hipGetLastError();
+}
+
+template <class T, int kThreads, int kGran>
+static void fused(hipStream_t s, const DistillArgs& a) {
+    hipLaunchKernelGGL((k_distill_fused<T, kThreads, kGran>), parts(a), dim3(kThreads), (lds_bytes<T, kThreads>(a)), s,
+                       a);
 }
 
 template <class T>
 static hipError_t forward_typed(hipStream_t s, const DistillArgs& a) {
-    const size_t lds = bitmap_bytes(a);
-    const int32_t each = (a.per + kRowThreads - 1) / kRowThreads;
+    const size_t lds = lds_bytes<T, kStreamThreads>(a);
     if (a.splits > 1) {
-        hipLaunchKernelGGL((k_distill_loss<T, true>), parts(a), dim3(kRowThreads), lds, s, a);
-        hipLaunchKernelGGL((k_distill_join<T>), dim3((uint32_t)a.in.rows), dim3(kRowThreads), lds, s, a);
-    } else if (a.dz && each <= kRowGranules) {
-        if (each <= 4) hipLaunchKernelGGL((k_distill_fused<T, 4>), parts(a), dim3(kRowThreads), lds, s, a);
-        else if (each <= 8) hipLaunchKernelGGL((k_distill_fused<T, 8>), parts(a), dim3(kRowThreads), lds, s, a);
-        else hipLaunchKernelGGL((k_distill_fused<T, kRowGranules>), parts(a), dim3(kRowThreads), lds, s, a);
+        hipLaunchKernelGGL((k_distill_loss<T, true>), parts(a), dim3(kStreamThreads), lds, s, a);
+        hipLaunchKernelGGL((k_distill_join<T>), dim3((uint32_t)a.in.rows), dim3(kStreamThreads), lds, s, a);
+    } else if (a.dz && a.per <= kRowCapacity) {
+        if (a.per <= 256 * 4) fused<T, 256, 4>(s, a);
+        else if (a.per <= 256 * 8) fused<T, 256, 8>(s, a);
+        else if (a.per <= 256 * 16) fused<T, 256, 16>(s, a);
+        else fused<T, 512, 16>(s, a);
         return hipGetLastError();
     } else {
-        hipLaunchKernelGGL((k_distill_loss<T, false>), parts(a), dim3(kRowThreads), lds, s, a);
+        hipLaunchKernelGGL((k_distill_loss<T, false>), parts(a), dim3(kStreamThreads), lds, s, a);
     }
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !a.dz ? e : backward_typed<T>(s, a);

@@ -50,26 +50,26 @@ __device__ __forceinline__ float lse_of(float ref, double sum) { return (float)(
 
 // Ranks the n candidates in list (n <= kTopkList, all different) and hands
 // the first k, in order, to emit(r, composite); slots past n get 0.
-template <class Emit>
+template <int kThreads, class Emit>
 __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
     const uint32_t tid = threadIdx.x;
-    if (n <= kRowThreads) {
-        // each thread counts the candidates above its own
-        if (tid < n) {
-            const uint64_t mine = list[tid];
+    if (n <= 512) {
+        // each candidate counts those above it
+        for (uint32_t i = tid; i < n; i += kThreads) {
+            const uint64_t mine = list[i];
             uint32_t r = 0;
 #pragma unroll 4
             for (uint32_t j = 0; j < n; ++j) r += list[j] > mine ? 1u : 0u;
             if (r < (uint32_t)k) emit((int32_t)r, mine);
         }
     } else {
-        uint32_t p = kRowThreads * 2;
+        uint32_t p = 1024;
         while (p < n) p <<= 1;
-        for (uint32_t i = n + tid; i < p; i += kRowThreads) list[i] = 0;
+        for (uint32_t i = n + tid; i < p; i += kThreads) list[i] = 0;
         for (uint32_t size = 2; size <= p; size <<= 1)
             for (uint32_t d = size >> 1; d > 0; d >>= 1) {
                 __syncthreads();
-                for (uint32_t t = tid; t < p / 2; t += kRowThreads) {
+                for (uint32_t t = tid; t < p / 2; t += kThreads) {
                     const uint32_t i = 2 * t - (t & (d - 1)), j = i + d;
                     const uint64_t x = list[i], y = list[j];
                     if ((x < y) == ((i & size) == 0)) {
@@ -79,30 +79,32 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
                 }
             }
         __syncthreads();
-        for (uint32_t i = tid; i < (uint32_t)k && i < n; i += kRowThreads) emit((int32_t)i, list[i]);
+        for (uint32_t i = tid; i < (uint32_t)k && i < n; i += kThreads) emit((int32_t)i, list[i]);
     }
-    for (uint32_t i = n + tid; i < (uint32_t)k; i += kRowThreads) emit((int32_t)i, 0ull);
+    for (uint32_t i = n + tid; i < (uint32_t)k; i += kThreads) emit((int32_t)i, 0ull);
 }
 
-// A workgroup takes `per` granules of a row into registers (kGran a thread at
-// most) and makes the row's k largest, or its part's, from them.
+// A workgroup takes `per` granules of a row into registers and makes the
+// row's k largest, or its part's, from them.
 //
-// Candidates: the k-th largest of the threads' maxima is at most the k-th
-// largest entry, and for k well below the number of threads only a few more
-// than k entries reach it.  Granules whose maximum reaches it are copied to
-// LDS and gone through there, so a thread with such a granule does not hold
-// up its wave.  Where there are more than the lists hold (ties, or k near the
-// number of threads), the exact threshold comes from a radix selection that
-// reads the row again, from the caches, for each 8-bit digit.
+// Candidates: of disjoint groups of entries, two a thread, the k-th largest of
+// the groups' maxima is at most the k-th largest entry, and for k well below
+// the number of groups only a few more than k entries reach it.  Granules
+// whose maximum reaches it are copied to LDS and gone through there, so a
+// thread with such a granule does not hold up its wave.  Where there are more
+// than the lists hold (ties, or k near the number of groups), the exact
+// threshold comes from a radix selection that reads the row again, from the
+// caches, for each 8-bit digit.
 constexpr int kTopkHits = 768;  // granules
-template <class T, int kGran>
-__global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(TopkArgs a) {
+template <class T, int kThreads, int kGran>
+__global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
+    constexpr int kNW = kThreads / 64;
     __shared__ uint64_t list[kTopkList];
     __shared__ gran hit[kTopkHits];
     __shared__ int32_t hit_at[kTopkHits];
     __shared__ uint32_t hist[256];
-    __shared__ uint32_t tmax[kRowThreads];
-    __shared__ float2 wsum[kRowWaves];
+    __shared__ uint32_t gmax[2 * kThreads];
+    __shared__ float2 wsum[kNW];
     __shared__ uint32_t s_n, s_hits, s_bin, s_need, s_tau;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
@@ -119,54 +121,64 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
     gran g[kGran];
 #pragma unroll
     for (int c = 0; c < kGran; ++c) {
-        const int32_t i = tid + c * kRowThreads;
+        const int32_t i = tid + c * kThreads;
         g[c] = no_entries<T>();
-        if (i < cnt) g[c] = body[i];
+        if (i < cnt) g[c] = granule_at(body, i);
     }
     const int32_t lone = lone_element(sh, n, sp == 0, sp == a.splits - 1);
     const float lx = lone >= 0 ? T::up1(z[lone]) : kNegInf;
     if (tid == 0) s_n = s_hits = 0;
 
-    constexpr int kBatch = kGran < 4 ? kGran : 4;
-    float gm[kGran], m = lx;
+    constexpr int kBatch = 2;
+    float gm[kGran], m0 = lx, m1 = kNegInf;
     RunningSum rs = RunningSum::none();
     rs.add1(lx, a.c2);
 #pragma unroll
     for (int c = 0; c < kGran; c += kBatch)
-        if (c * kRowThreads < cnt || c == 0) {
+        if (c * kThreads < cnt || c == 0) {
             gran x[kBatch];
             float bm = kNegInf;
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                gm[c + b] = granule_max<T>(g[c + b]);
-                bm = max_nan(bm, gm[c + b]);
                 x[b] = g[c + b];
+                gm[c + b] = granule_max<T>(x[b]);
+                bm = max_nan(bm, gm[c + b]);
             }
-            m = max_nan(m, bm);
+            (c & kBatch ? m1 : m0) = max_nan(c & kBatch ? m1 : m0, bm);
             rs.template add<T, kBatch>(x, bm, a.c2);
         } else {
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) gm[c + b] = kNegInf;
         }
-    tmax[tid] = order_key(m) >> 16;
+    gmax[tid] = order_key(m0) >> 16;
+    gmax[tid + kThreads] = order_key(m1) >> 16;
     wave_join(rs);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     __syncthreads();
 
     // wave 0: the k-th largest of the maxima, to the top 16 bits of its key
     if (wave == 0) {
-        uint32_t mk[kRowWaves];
+        uint32_t mk[2 * kNW];
 #pragma unroll
-        for (int w = 0; w < kRowWaves; ++w) mk[w] = tmax[w * 64 + tid];
+        for (int w = 0; w < 2 * kNW; ++w) mk[w] = gmax[w * 64 + tid];
         uint32_t t = 0;
         for (int b = 15; b >= 0; --b) {
             const uint32_t x = t | (1u << b);
             uint32_t count = 0;
 #pragma unroll
-            for (int w = 0; w < kRowWaves; ++w) count += (uint32_t)__popcll(wave_ballot(mk[w] >= x));
+            for (int w = 0; w < 2 * kNW; ++w) count += (uint32_t)__popcll(wave_ballot(mk[w] >= x));
             if (count >= (uint32_t)k) t = x;
         }
         if (tid == 0) s_tau = t;
+    } else if (wave == kNW - 1) {
+        RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
+        join_waves<kNW>(r);
+        if (tid == kThreads - 1) {
+            if (a.splits > 1)
+                a.part[row * a.splits + sp] = make_float2(r.ref, r.sum);
+            else if (a.lse)
+                a.lse[row] = lse_of(r.ref, (double)r.sum);
+        }
     }
     __syncthreads();
 
@@ -186,14 +198,14 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
             const uint32_t at = atomicAdd(&s_hits, 1u);
             if (at < kTopkHits) {
                 hit[at] = g[c];
-                hit_at[at] = first + (tid + c * kRowThreads) * T::kN;
+                hit_at[at] = first + (tid + c * kThreads) * T::kN;
             }
         }
     __syncthreads();
     const uint32_t hits = s_hits;
     if (hits <= kTopkHits) {
         const raw* elems = reinterpret_cast<const raw*>(hit);
-        for (uint32_t i = (uint32_t)tid; i < hits * T::kN; i += kRowThreads)
+        for (uint32_t i = (uint32_t)tid; i < hits * T::kN; i += kThreads)
             take(T::up1(elems[i]), hit_at[i / T::kN] + (int32_t)(i % T::kN));
         __syncthreads();
     }
@@ -202,9 +214,9 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
         // radix selection over 8-bit digits of the composite, largest first;
         // every part of the row by its granules, then the lone elements
         auto each = [&](auto f) {
-            for (int32_t i0 = 0; i0 < cnt; i0 += kRowThreads) {
+            for (int32_t i0 = 0; i0 < cnt; i0 += kThreads) {
                 const int32_t i = i0 + tid;
-                const gran x = i < cnt ? body[i] : no_entries<T>();
+                const gran x = i < cnt ? granule_at(body, i) : no_entries<T>();
 #pragma unroll
                 for (int j = 0; j < T::kN; ++j) f(T::up(x, j), first + i * T::kN + j);
             }
@@ -219,7 +231,7 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
                 prefix = (prefix << 8) | 0xFFu;
                 continue;
             }
-            for (int32_t i = tid; i < 256; i += kRowThreads) hist[i] = 0;
+            for (int32_t i = tid; i < 256; i += kThreads) hist[i] = 0;
             __syncthreads();
             each([&](float f, int32_t col) {
                 const uint64_t comp = ((uint64_t)order_key(f) << 32) | (uint32_t)~(uint32_t)col;
@@ -265,28 +277,19 @@ __global__ __launch_bounds__(kRowThreads, row_waves(kGran)) void k_topk_rows(Top
     }
 
     if (a.splits == 1) {
-        emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
+        emit_sorted<kThreads>(list, found, k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
     } else {
         uint64_t* out = a.cand + (row * a.splits + sp) * k;
-        emit_sorted(list, found, k, [&](int32_t r, uint64_t comp) { out[r] = comp; });
-    }
-    if (wave == kRowWaves - 1) {
-        RunningSum r{wsum[tid & 7].x, wsum[tid & 7].y};
-        join8(r);
-        if (tid == kRowThreads - 1) {
-            if (a.splits > 1)
-                a.part[row * a.splits + sp] = make_float2(r.ref, r.sum);
-            else if (a.lse)
-                a.lse[row] = lse_of(r.ref, (double)r.sum);
-        }
+        emit_sorted<kThreads>(list, found, k, [&](int32_t r, uint64_t comp) { out[r] = comp; });
     }
 }
 
 // Joins a row's parts.  Each part's candidates are sorted, so of the first
 // ceil(k / splits) of every part at least k are in the row: only entries that
 // reach the smallest of those can be among the row's k largest.
+constexpr int kMergeThreads = 512;
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
+__global__ __launch_bounds__(kMergeThreads) void k_topk_merge(TopkArgs a) {
     __shared__ uint64_t list[kTopkList];
     __shared__ uint64_t s_low;
     __shared__ uint32_t s_n;
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
     }
     __syncthreads();
     const uint64_t low = s_low;
-    for (uint32_t i = (uint32_t)tid; i < all; i += kRowThreads) {
+    for (uint32_t i = (uint32_t)tid; i < all; i += kMergeThreads) {
         const uint64_t x = cand[i];
         if (x >= low && x != 0) {
             const uint32_t at = atomicAdd(&s_n, 1u);
@@ -328,12 +331,12 @@ __global__ __launch_bounds__(kRowThreads) void k_topk_merge(TopkArgs a) {
     __syncthreads();
     const uint32_t found = s_n;
     if (found <= kTopkList) {
-        emit_sorted(list, found, a.k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
+        emit_sorted<kMergeThreads>(list, found, a.k, [&](int32_t r, uint64_t comp) { write_entry<T>(a, row, r, comp); });
         return;
     }
     // too many (one part holds most of them): an entry's rank is its place in
     // its own part plus, by binary search, the entries above it in the others
-    for (uint32_t i = (uint32_t)tid; i < all; i += kRowThreads) {
+    for (uint32_t i = (uint32_t)tid; i < all; i += kMergeThreads) {
         const uint64_t x = cand[i];
         if (x == 0) continue;
         const uint32_t own = i / k;
@@ -447,13 +450,13 @@ static hipError_t topk_typed(hipStream_t s, const TopkArgs& a) {
         return hipGetLastError();
     }
     const dim3 grid((uint32_t)(a.in.rows * a.splits));
-    const int32_t each = (a.per + kRowThreads - 1) / kRowThreads;
-    if (each <= 4) hipLaunchKernelGGL((k_topk_rows<T, 4>), grid, dim3(kRowThreads), 0, s, a);
-    else if (each <= 8) hipLaunchKernelGGL((k_topk_rows<T, 8>), grid, dim3(kRowThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_topk_rows<T, kRowGranules>), grid, dim3(kRowThreads), 0, s, a);
+    if (a.per <= 256 * 4) hipLaunchKernelGGL((k_topk_rows<T, 256, 4>), grid, dim3(256), 0, s, a);
+    else if (a.per <= 256 * 8) hipLaunchKernelGGL((k_topk_rows<T, 256, 8>), grid, dim3(256), 0, s, a);
+    else if (a.per <= 256 * 16) hipLaunchKernelGGL((k_topk_rows<T, 256, 16>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_topk_rows<T, 512, 16>), grid, dim3(512), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((k_topk_merge<T>), dim3((uint32_t)a.in.rows), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((k_topk_merge<T>), dim3((uint32_t)a.in.rows), dim3(kMergeThreads), 0, s, a);
     return hipGetLastError();
 }
 

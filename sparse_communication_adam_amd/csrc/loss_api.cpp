@@ -12,18 +12,18 @@ namespace scape {
 
 // A row is split where a kernel must hold it and it does not fit a workgroup's
 // registers, and where there are fewer rows than it takes to fill the 256 CUs:
-// up to kFill workgroups in all, none with less than a granule for every
-// thread.
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool resident) {
+// up to kFill workgroups in all, none with less than kPartUnit granules.
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool held) {
     constexpr int64_t kFill = 512;
-    const int64_t g = row_granules(dtype, cols);
-    const int64_t need = resident ? (g + kRowCapacity - 1) / kRowCapacity : 1;
+    const int64_t units = (row_granules(dtype, cols) + kPartUnit - 1) / kPartUnit;
+    const int64_t most = kRowCapacity / kPartUnit;
+    const int64_t need = held ? (units + most - 1) / most : 1;
     int64_t want = rows > 0 ? kFill / rows : 1;
-    if (want > g / kRowThreads) want = g / kRowThreads;
+    if (want > units) want = units;
     if (want > kMaxSplits) want = kMaxSplits;
     const int64_t n = want > need ? want : need;
-    const int64_t per = (g + n - 1) / n;
-    return RowSplit{(int32_t)((g + per - 1) / per), (int32_t)per};
+    const int64_t per = (units + n - 1) / n;
+    return RowSplit{(int32_t)((units + per - 1) / per), (int32_t)(per * kPartUnit)};
 }
 
 }  // namespace scape
@@ -32,7 +32,7 @@ namespace {
 
 constexpr size_t kWorkspaceAlign = 16;
 // A launch's threads are counted in 32 bits.
-constexpr int64_t kMaxRowBlocks = (int64_t(1) << 32) / kRowThreads - 1;
+constexpr int64_t kMaxRowBlocks = (int64_t(1) << 32) / 512 - 1;
 constexpr int64_t kMaxSmallRows = int64_t(1) << 25;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxSegments = int64_t(1) << 22;

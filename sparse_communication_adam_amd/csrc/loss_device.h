@@ -98,6 +98,11 @@ __device__ __forceinline__ RowShape row_shape(const void* row, int32_t n) {
     r.tail = n - r.head - r.granules * T::kN;
     return r;
 }
+// Granule i of a run, and 16 bytes at it: a uniform base and a 32-bit offset.
+__device__ __forceinline__ gran granule_at(const void* body, int32_t i) {
+    return *reinterpret_cast<const gran*>(static_cast<const char*>(body) + (size_t)((uint32_t)i * 16u));
+}
+
 // The element a thread takes beside its granules in the first or the last
 // part of a row, or -1.
 __device__ __forceinline__ int32_t lone_element(const RowShape& r, int32_t n, bool first, bool last) {
@@ -107,10 +112,12 @@ __device__ __forceinline__ int32_t lone_element(const RowShape& r, int32_t n, bo
     return -1;
 }
 
-// 16 bytes to an address of any alignment: one store (the target's memory
-// mode takes them; the compiler picks the instruction).
+// 16 bytes to granule i of a run of any alignment: one store (the target's
+// memory mode takes them; the compiler picks the instruction).
 typedef uint32_t loose_gran __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ void store_loose(void* p, const gran& g) { *static_cast<loose_gran*>(p) = g; }
+__device__ __forceinline__ void store_loose(void* run, int32_t i, const gran& g) {
+    *reinterpret_cast<loose_gran*>(static_cast<char*>(run) + (size_t)((uint32_t)i * 16u)) = g;
+}
 
 template <class T>
 __device__ __forceinline__ gran no_entries() {  // a granule of -inf
@@ -225,17 +232,19 @@ __device__ __forceinline__ double dpp64(double x) {
     return __builtin_bit_cast(double, (uint64_t)dpp32<kCtrl>((uint32_t)u) | (uint64_t)dpp32<kCtrl>((uint32_t)(u >> 32)) << 32);
 }
 
-// Sum over eight values that each group of eight lanes holds alike: the
-// workgroup's waves' partial sums, read by lane % 8.
-__device__ __forceinline__ double sum8_f64(double x) {
+// Sum over the kWaves (4 or 8) values that each group of as many lanes holds
+// alike: the workgroup's waves' partial sums, read by lane % kWaves.
+template <int kWaves>
+__device__ __forceinline__ double sum_waves_f64(double x) {
+    static_assert(kWaves == 4 || kWaves == 8, "quads or half rows");
     x += dpp64<0xB1>(x);
     x += dpp64<0x4E>(x);
-    x += dpp64<0x141>(x);
+    if constexpr (kWaves == 8) x += dpp64<0x141>(x);
     return x;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double x) {
-    x = sum8_f64(x);
+    x = sum_waves_f64<8>(x);
     x += dpp64<0x140>(x);
     {
         const uint64_t u = __builtin_bit_cast(uint64_t, x);
@@ -268,15 +277,12 @@ __device__ __forceinline__ void wave_join(RunningSum& r) {
     r.sum = group_reduce<OpSumF, 64>(r.sum * fast_exp2(r.ref - ref));
     r.ref = ref;
 }
-// Joins the sums of eight waves, that of wave l in the lanes l, l + 8, ...
-__device__ __forceinline__ void join8(RunningSum& r) {
-    const float ref = group_reduce<OpMaxNum, 8>(r.ref);
-    r.sum = group_reduce<OpSumF, 8>(r.sum * fast_exp2(r.ref - ref));
+// Joins the waves' sums, that of wave w in the lanes w, w + kWaves, ...
+template <int kWaves>
+__device__ __forceinline__ void join_waves(RunningSum& r) {
+    const float ref = group_reduce<OpMaxNum, kWaves>(r.ref);
+    r.sum = group_reduce<OpSumF, kWaves>(r.sum * fast_exp2(r.ref - ref));
     r.ref = ref;
 }
-
-// Registers a row kernel may use, as waves per SIMD: two or three workgroups
-// of kRowThreads on a CU, so that one's loads run under another's arithmetic.
-constexpr int row_waves(int granules) { return granules <= 4 ? 8 : granules <= 8 ? 6 : 4; }
 
 }  // namespace scape

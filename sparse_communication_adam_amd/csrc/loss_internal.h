@@ -23,15 +23,19 @@ struct Logits {
 inline int dtype_size(int32_t dtype) { return dtype == SCAPE_DTYPE_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------------------
-// Row kernels: a workgroup of kRowThreads threads takes a row, or a part of
-// one.  A kernel that holds it in registers holds at most kRowGranules
-// granules a thread.
-constexpr int kRowThreads = 512;
-constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kRowGranules = 16;
-constexpr int64_t kRowCapacity = (int64_t)kRowThreads * kRowGranules;
+// Row kernels.  A workgroup takes a row, or a part of one.  A kernel that holds
+// it in registers has 16 granules a thread (64 registers, which leaves as many
+// for the arithmetic at 4 waves per SIMD): 4096 with 256 threads (32768
+// elements of 16 bits), 8192 with 512.  Fewer, fuller threads beat more: the
+// work that each wave does once a row (reductions, the entries' terms) is
+// about as much as 64 elements a lane cost.
+constexpr int kHeldGranules = 16;
+constexpr int kStreamThreads = 256;  // of the kernels that hold no row
+constexpr int64_t kRowCapacity = 512 * kHeldGranules;
 constexpr int kMaxSplits = 64;  // a lane of the joining wave for each part
 static_assert((SCAPE_ROW_MAX_COLS / 4 + 2) / kRowCapacity < kMaxSplits, "the longest row fits");
+// Parts are cut at multiples of this many granules.
+constexpr int kPartUnit = 4 * kStreamThreads;
 
 // Granules a row of `cols` elements can touch, whatever its alignment.
 inline int64_t row_granules(int32_t dtype, int64_t cols) {
@@ -42,9 +46,9 @@ inline int64_t row_granules(int32_t dtype, int64_t cols) {
 // Workgroups a row is split over.
 struct RowSplit {
     int32_t splits;
-    int32_t per;  // granules of each split (the last one may have fewer)
+    int32_t per;  // granules of each part, a multiple of kPartUnit (the last one may have fewer)
 };
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool resident);
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool held);
 
 // ---- k_topk.hip
 constexpr int kTopkList = 2048;       // candidates a workgroup sorts in LDS (>= SCAPE_TOPK_MAX_K)
