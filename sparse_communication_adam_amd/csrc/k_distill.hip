@@ -8,10 +8,11 @@
 //   d/dz = s (Q p_v - q_T p_v / p_T)      outside the entries, Q = sum q_j + q_T
 //        = s (Q p_{i_j} - q_j)            at an entry
 //
-// The logits are read once.  The entries' columns are marked in an LDS bitmap
-// and struck out of the granules as they arrive (-inf), so the sums that
-// follow are the tail's own, never a difference of two large ones; the k
-// entries are gathered and their terms summed in 64 bits meanwhile.
+// The logits are read once.
+// The entries' columns are marked in an LDS bitmap and struck out of the
+// granules as they go by (-inf), so that the running sum is the tail's own,
+// never a difference of two large ones.  The entries' terms are summed in 64
+// bits.
 //  - k_distill_loss: streams a row, or a part of one, through a workgroup.
 //  - k_distill_fused: loss and gradient; the row stays in the registers of
 //    its workgroup, so it is read once for both.
@@ -30,120 +31,141 @@
 
 namespace scape {
 
-// LDS of a workgroup: a bitmap of the row's columns, then the row's k slots:
-// column (-1: no entry), teacher's value and student's logit.
+// LDS of a workgroup: a bitmap of the row's columns, then the k slots: col
+// (-1: no entry), t (the teacher's value, then q), z (the student's logit,
+// then p).
 //
 // The bitmap lies as a thread's granules do, four of them (tid, tid + threads,
-// ...) in one cell: whether a thread's next four granules hold an entry is one
-// read and one test.  The lone elements beside the granules have 16 bits of
-// their own behind the cells.
+// ...) in one cell: whether its next four granules hold an entry is one read
+// and one test.  Some lane of a wave nearly always has one, so what counts is
+// the striking: of 16-bit types a cell's low half has the bits of the even
+// elements and its high half those of the odd ones, so that two packed shifts
+// make the mask of two elements (1.5 instructions an element; testing bit by
+// bit took 5.6, as much as all the rest).  The elements beside the granules
+// have 16 bits of their own behind the cells.
 template <class T, int kThreads>
-struct Bitmap {
+struct Lds {
     using Cell = std::conditional_t<T::kN == 8, uint32_t, uint16_t>;
     static constexpr int kCellBits = 4 * T::kN, kCellGranules = 4 * kThreads;
     Cell* cells;
+    int32_t* col;
+    float* t;
+    float* z;
     RowShape sh;
-    int32_t n;
+    int32_t n, k;
+
     static __host__ __device__ int32_t cell_count(int32_t granules) {
         return (granules + kCellGranules - 1) / kCellGranules * kThreads;
     }
-    // for rows of at most this many granules
-    static __host__ __device__ int32_t bytes(int32_t granules) {
-        return (cell_count(granules) * (int32_t)sizeof(Cell) + 4 + 15) / 16 * 16;
+    static __host__ __device__ int32_t cell_bytes(int32_t granules) {
+        return cell_count(granules) * (int32_t)sizeof(Cell) + 4;
     }
-    __device__ __forceinline__ uint32_t bit_of(int32_t col) const {
-        const int32_t e = col - sh.head, i = e / T::kN;
-        if (e >= 0 && i < sh.granules) {
-            const int32_t cell = i / kCellGranules * kThreads + i % kThreads;
-            return (uint32_t)(cell * kCellBits + (i / kThreads & 3) * T::kN + e % T::kN);
-        }
-        return (uint32_t)(cell_count(sh.granules) * kCellBits + (e < 0 ? col : 8 + col - (n - sh.tail)));
+    static int32_t bytes(int32_t granules, int32_t k) { return cell_bytes(granules) + 12 * k; }
+    __device__ __forceinline__ Lds(uint8_t* at, const RowShape& shape, int32_t cols, int32_t slots) {
+        sh = shape;
+        n = cols;
+        k = slots;
+        col = reinterpret_cast<int32_t*>(at);
+        t = reinterpret_cast<float*>(col + k);
+        z = t + k;
+        cells = reinterpret_cast<Cell*>(z + k);
     }
+    __device__ __forceinline__ uint32_t* words() const { return reinterpret_cast<uint32_t*>(cells); }
     __device__ __forceinline__ void clear() const {
-        const int32_t words = bytes(sh.granules) / 4;
-        uint32_t* w = reinterpret_cast<uint32_t*>(cells);
-        for (int32_t i = (int32_t)threadIdx.x; i < words; i += kThreads) w[i] = 0;
+        const int32_t m = cell_bytes(sh.granules) / 4;
+        for (int32_t i = (int32_t)threadIdx.x; i < m; i += kThreads) words()[i] = 0;
     }
-    // whether it was set before
-    __device__ __forceinline__ bool set(int32_t col) const {
-        const uint32_t at = bit_of(col), bit = 1u << (at & 31u);
-        return (atomicOr(reinterpret_cast<uint32_t*>(cells) + (at >> 5), bit) & bit) != 0;
+    __device__ __forceinline__ uint32_t bit_of(int32_t c) const {
+        const int32_t e = c - sh.head, i = e / T::kN, j = e % T::kN;
+        if (e >= 0 && i < sh.granules) {
+            const int32_t cell = i / kCellGranules * kThreads + i % kThreads, b = i / kThreads & 3;
+            return (uint32_t)(cell * kCellBits + (T::kN == 8 ? b * 4 + j / 2 + 16 * (j & 1) : b * 4 + j));
+        }
+        return (uint32_t)(cell_count(sh.granules) * kCellBits + (e < 0 ? c : 8 + c - (n - sh.tail)));
     }
-    __device__ __forceinline__ bool has(int32_t col) const {
-        const uint32_t at = bit_of(col);
-        return (reinterpret_cast<const uint32_t*>(cells)[at >> 5] >> (at & 31u)) & 1u;
+    // Marks a column; whether it was marked before.
+    __device__ __forceinline__ bool mark(int32_t c) const {
+        const uint32_t at = bit_of(c), bit = 1u << (at & 31u);
+        return (atomicOr(words() + (at >> 5), bit) & bit) != 0;
     }
-    // Strikes the entries out of the thread's granules tid + (b + 4 c) kThreads, b < 4, c = cell_row.
+    __device__ __forceinline__ bool marked(int32_t c) const {
+        const uint32_t at = bit_of(c);
+        return (words()[at >> 5] >> (at & 31u)) & 1u;
+    }
+    // Strikes the entries out of the thread's granules
+    // tid + (b + 4 cell_row) kThreads, b < 4.
     __device__ __forceinline__ void strike(int32_t cell_row, gran (&g)[4]) const {
         const uint32_t bits = cells[cell_row * kThreads + (int32_t)threadIdx.x];
         if (bits) {
 #pragma unroll
             for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int j = 0; j < T::kN; ++j)
-                    if (bits & (1u << (b * T::kN + j))) T::set(g[b], j, (typename T::raw)T::kNegInfBits);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t m;
+                    if constexpr (T::kN == 8) {
+                        typedef int16_t pair __attribute__((ext_vector_type(2)));
+                        pair up = __builtin_bit_cast(pair, bits) << (int16_t)(15 - 4 * b - q);
+                        asm volatile("" : "+v"(up));  // else each half becomes a test and a select
+                        m = __builtin_bit_cast(uint32_t, (pair)(up >> (int16_t)15));
+                    } else {
+                        int32_t up = (int32_t)(bits << (31 - 4 * b - q));
+                        asm volatile("" : "+v"(up));
+                        m = (uint32_t)(up >> 31);
+                    }
+                    g[b][q] = (g[b][q] & ~m) | (no_entries<T>()[q] & m);
+                }
         }
     }
 };
 
-// The k slots of a row.  Slot tid's values wait in registers until the row's
-// logits have gone by; t and z hold the entry's terms q and p afterwards.
-struct Slots {
-    int32_t* col;
-    float* t;
-    float* z;
-    float t0, z0;
+// A slot's column and teacher's value as they are read; a column outside the
+// row is no entry.
+struct Slot {
+    int32_t c;
+    uint32_t t;  // bits
 };
-inline int32_t slot_bytes(int32_t k) { return 12 * k; }
-
-// Column of a slot; one outside the row is no entry.
-__device__ __forceinline__ int32_t slot_column(const DistillArgs& a, int64_t row, int32_t slot) {
-    const int32_t c = slot < a.k ? a.t_idx[row * a.k + slot] : -1;
-    return c >= 0 && c < (int32_t)a.in.cols ? c : -1;
+__device__ __forceinline__ Slot read_slot(const DistillArgs& a, int64_t row, int32_t slot) {
+    const int64_t at = row * a.k + (slot < a.k ? slot : a.k - 1);
+    Slot s{a.t_idx[at], load_bits(a.t_val, a.t_dtype, at)};
+    if (slot >= a.k) s.c = -1;
+    return s;
 }
 
-// Reads the slots' values, logits for columns in [lo, hi) only (hi = 0: no
-// values at all), and marks the columns.  c0 is slot tid's column.  An entry
-// whose column a lower slot has is dropped.  The bitmap has been cleared, by
-// this workgroup, without a barrier since; it is complete afterwards.  Returns
-// whether the row has any entry.
+// Marks the row's entries; s0 is slot tid.  An entry whose column a lower slot
+// has is dropped.  The bitmap has been cleared by this workgroup, s_flags too,
+// without a barrier since; both are complete afterwards.  Returns whether the
+// row has any entry.
 template <class T, int kThreads>
-__device__ __forceinline__ bool read_slots(const DistillArgs& a, int64_t row, const typename T::raw* z, int32_t lo,
-                                           int32_t hi, int32_t c0, const Bitmap<T, kThreads>& bitmap, Slots& s) {
+__device__ __forceinline__ bool mark_entries(const DistillArgs& a, int64_t row, Slot s0, const Lds<T, kThreads>& lds,
+                                             uint32_t* s_flags) {
     const int32_t tid = (int32_t)threadIdx.x;
     __syncthreads();
     uint32_t seen = 0;  // bit 0: some entry; bit 1: some column twice
-    s.t0 = s.z0 = 0.0f;
     for (int32_t slot = tid; slot < a.k; slot += kThreads) {
-        const int32_t c = slot == tid ? c0 : slot_column(a, row, slot);
-        s.col[slot] = c;
-        if (c < 0) continue;
-        float t = 0.0f, x = 0.0f;
-        if (hi > 0) t = load_any(a.t_val, a.t_dtype, row * a.k + slot);
-        if (c >= lo && c < hi) x = T::up1(z[c]);
-        if (slot == tid) {
-            s.t0 = t;
-            s.z0 = x;
-        } else {
-            s.t[slot] = t;
-            s.z[slot] = x;
-        }
-        seen |= bitmap.set(c) ? 3u : 1u;
+        const Slot s = slot == tid ? s0 : read_slot(a, row, slot);
+        const bool there = s.c >= 0 && s.c < lds.n;
+        lds.col[slot] = there ? s.c : -1;
+        lds.t[slot] = value_of(s.t, a.t_dtype);
+        if (!there) continue;
+        seen |= 1u;
+        if (lds.mark(s.c)) seen |= 2u;
     }
-    if (!__syncthreads_or((int)seen)) return false;
-    if (__syncthreads_or((int)(seen & 2u))) {
+    if (seen) atomicOr(s_flags, seen);
+    __syncthreads();
+    seen = *s_flags;
+    if (seen & 2u) {
         // which of two threads came first is chance, so every entry looks for
         // its column in the slots below its own
         for (int32_t slot = tid; slot < a.k; slot += kThreads) {
-            const int32_t c = s.col[slot];
+            const int32_t c = lds.col[slot];
             for (int32_t j = 0; j < slot && c >= 0; ++j)
                 if (a.t_idx[row * a.k + j] == c) {
-                    s.col[slot] = -1;
+                    lds.col[slot] = -1;
                     break;
                 }
         }
     }
-    return true;
+    return seen != 0;
 }
 
 // s t_j, minus the teacher's lse where it is given.
@@ -166,32 +188,28 @@ constexpr float kLowest = -3.402823466e38f;
 // kStudent: also the student's terms.  Slots' t and z become q and p, for the
 // gradient, in float32: each is rounded once more, a step of a float32
 // gradient (the sums are over float64).
-template <int kThreads, bool kStudent>
-__device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse, Slots& sl) {
+template <class T, int kThreads, bool kStudent>
+__device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse, const Lds<T, kThreads>& l) {
     const int32_t tid = (int32_t)threadIdx.x;
     WaveSums s{0.0, 0.0, 0.0, 0.0, kLowest, a.t_lse ? 0.0f : kLowest};
-    if (tid < a.k) {
-        sl.t[tid] = sl.t0;
-        sl.z[tid] = sl.z0;
-    }
     bool some = false;
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
-        if (sl.col[slot] >= 0) {
+        if (l.col[slot] >= 0) {
             some = true;
-            if (kStudent) s.mt = fmaxf(s.mt, sl.z[slot] * a.c2);
-            if (!a.t_lse) s.mq = fmaxf(s.mq, sl.t[slot] * a.scale);
+            if (kStudent) s.mt = fmaxf(s.mt, l.z[slot] * a.c2);
+            if (!a.t_lse) s.mq = fmaxf(s.mq, l.t[slot] * a.scale);
         }
     if (wave_ballot(some) == 0) return s;
     if (kStudent) s.mt = group_reduce<OpMaxNum, 64>(s.mt);
     if (!a.t_lse) s.mq = group_reduce<OpMaxNum, 64>(s.mq);
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
-        if (sl.col[slot] >= 0) {
-            const double lq = log_q(a, lse, sl.t[slot]) - (double)s.mq, q = exp(lq);
-            sl.t[slot] = (float)q;
+        if (l.col[slot] >= 0) {
+            const double lq = log_q(a, lse, l.t[slot]) - (double)s.mq, q = exp(lq);
+            l.t[slot] = (float)q;
             s.q += q;
             if (kStudent) {
-                const double x = (double)sl.z[slot] * (double)a.c2, p = exp2(x - (double)s.mt);
-                sl.z[slot] = (float)p;
+                const double x = (double)l.z[slot] * (double)a.c2, p = exp2(x - (double)s.mt);
+                l.z[slot] = (float)p;
                 s.top += p;
                 if (q != 0.0) {
                     s.qt += q * lq;
@@ -218,27 +236,25 @@ struct RowResult {
 };
 
 // A whole wave calls it; lane l brings the entries' sums of wave l % kWaves
-// and the tail's running sum of the row.  The four logarithms of the row are
-// one, on four lanes.
+// and the tail's running sum of the row.  The row's powers, its logarithms and
+// its divisions are one each, on as many lanes.
 template <int kWaves>
 __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const RunningSum& tail, const WaveSums& w) {
     RowResult r;
-    const double t = (double)tail.sum;
+    const uint32_t lane = lane_id();
+    const double t = (double)tail.sum, tref = (double)tail.ref;
     const bool has_tail = !(t == 0.0);
-    const double tref = (double)tail.ref;
     const double ref = fmax(has_tail ? tref : (double)kLowest, (double)group_reduce<OpMaxNum, kWaves>(w.mt));
-    const double fp = exp2((double)w.mt - ref);
+    const double dq = a.t_lse ? 0.0 : (double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq);
+    // lanes 0..: the waves' references against the row's; 16..: the teacher's
+    // likewise; 32: the tail's (0 too where the tail is out of range)
+    const double powers = exp2(lane < 16 ? (double)w.mt - ref : lane < 32 ? dq * kLog2e64 : tref - ref);
+    const double fp = from_lane_of<kWaves>(powers, 0), fq = from_lane_of<kWaves>(powers, 16);
+    const double far = has_tail ? from_lane(powers, 32) : 0.0;
     const double top = sum_waves_f64<kWaves>(w.top * fp);
-    double fq = 1.0, qt = w.qt;
-    if (!a.t_lse) {
-        const double d = (double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq);
-        fq = exp(d);
-        qt += w.q != 0.0 ? w.q * d : 0.0;
-    }
     const double q = sum_waves_f64<kWaves>(w.q * fq);
-    qt = sum_waves_f64<kWaves>(qt * fq);
+    const double qt = sum_waves_f64<kWaves>((w.qt + (w.q != 0.0 ? w.q * dq : 0.0)) * fq);
     const double qx = sum_waves_f64<kWaves>(w.qx * fq);
-    const double far = has_tail ? exp2(tref - ref) : 0.0;  // 0 too where the tail is out of range
     const double sum = t * far + top;
     double qsum, rest = 0.0;
     if (a.t_lse) {
@@ -247,11 +263,12 @@ __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const Runn
     } else {
         qsum = q == 0.0 ? 0.0 : 1.0;  // 0: every entry's value is -inf
     }
-    const uint32_t lane = lane_id();
-    const double logs = log(lane == 0 ? sum : lane == 1 ? t : lane == 2 ? q : rest);
+    const double of = lane == 0 ? sum : lane == 1 ? t : lane == 2 ? q : rest;
+    const double logs = log(of), inverses = 1.0 / of;
     const double log_sum = from_lane(logs, 0), log_t = from_lane(logs, 1), log_q = from_lane(logs, 2),
                  log_rest = from_lane(logs, 3);
-    const double qnorm = qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q;
+    const double inv = from_lane(inverses, 0);
+    const double qnorm = qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : from_lane(inverses, 2);
     const double lpt = has_tail ? log_t + (tref - ref) * kLn2 - log_sum : -__builtin_inf();
     const double lse = ref * kLn2 + log_sum;
     double kl = 0.0;
@@ -260,13 +277,12 @@ __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const Runn
         if (!a.t_lse) kl -= log_q;
     }
     if (rest > 0.0) kl += rest * (log_rest - lpt);
-    const double inv = 1.0 / sum;
     r.loss = (float)kl;
     r.stat0 = (float)lse;
     r.stat1 = (float)lpt;
     r.vref = tail.ref;
     // (Q - q_T / p_T) p_v with q_T / p_T = q_T + q_T top / (t far)
-    r.tail = has_tail ? (float)(inv * (qsum * far - rest * top / t)) : 0.0f;
+    r.tail = has_tail ? (float)(inv * (qsum * far - rest * top * from_lane(inverses, 1))) : 0.0f;
     r.p = fp * inv * (qsum + rest);
     r.q = fq * qnorm;
     r.dead = sum == 0.0;
@@ -306,22 +322,63 @@ struct Part {
         cnt = max(min(a.per, sh.granules - g0), 0);
         const bool last = sp == a.splits - 1;
         first = sh.head + g0 * T::kN;
-        body = reinterpret_cast<const gran*>(z + sh.head) + g0;
+        body = cnt > 0 ? reinterpret_cast<const gran*>(z + sh.head) + g0 : &g_no_granule;
         lone = lone_element(sh, n, sp == 0, last);
         col0 = sp == 0 ? 0 : first;
         col1 = last ? n : first + cnt * T::kN;
     }
-    // four granules of a thread, from number base + tid on
+    // Four granules of a thread, from number base + tid on; past the last one
+    // the last one again (trim takes it out).  A load under a condition, were
+    // it one that is always true, would cost the prefetch: the compiler then
+    // cannot count the loads in flight and waits for all of them.
     template <int kThreads>
     __device__ __forceinline__ void load(int32_t base, gran (&g)[4]) const {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int32_t i = base + (int32_t)threadIdx.x + b * kThreads;
-            g[b] = no_entries<T>();
-            if (i < cnt) g[b] = granule_at(body, i);
-        }
+        for (int b = 0; b < 4; ++b)
+            g[b] = granule_at(body, max(min(base + (int32_t)threadIdx.x + b * kThreads, cnt - 1), 0));
+    }
+    template <int kThreads>
+    __device__ __forceinline__ void trim(int32_t base, gran (&g)[4]) const {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (base + (int32_t)threadIdx.x + b * kThreads >= cnt) g[b] = no_entries<T>();
+    }
+    // The lone element, -inf if there is none, and an entry's logit, 0 outside
+    // the part's columns: loads without a condition too.
+    __device__ __forceinline__ float lone_logit() const {
+        const float x = T::up1(z[lone >= 0 ? lone : col0]);
+        return lone >= 0 ? x : kNegInf;
+    }
+    __device__ __forceinline__ float entry_logit(int32_t c) const {
+        const bool here = c >= col0 && c < col1;
+        const float x = T::up1(z[here ? c : col0]);
+        return here ? x : 0.0f;
     }
 };
+
+// Streams the part through two sets of four granules a thread: one is on its
+// way while the other is worked on.  `first` is loaded already.  whole(base,
+// x) takes granules base + tid + b threads that are all there, last(base, x)
+// the ones of which some are past the end.
+template <class T, int kThreads, class Whole, class Last>
+__device__ __forceinline__ void stream_row(const Part<T>& p, gran (&first)[4], Whole whole, Last last) {
+    constexpr int kStep = 4 * kThreads;
+    gran second[4];
+    int32_t base = 0;
+    for (; base + 2 * kStep <= p.cnt; base += 2 * kStep) {
+        p.template load<kThreads>(base + kStep, second);
+        whole(base, first);
+        p.template load<kThreads>(base + 2 * kStep, first);
+        whole(base + kStep, second);
+    }
+    if (base + kStep <= p.cnt) {
+        p.template load<kThreads>(base + kStep, second);
+        whole(base, first);
+        if (base + kStep < p.cnt) last(base + kStep, second);
+    } else if (base < p.cnt) {
+        last(base, first);
+    }
+}
 
 // A row that is not read: zeros.
 template <class T, int kThreads>
@@ -331,44 +388,38 @@ __device__ __forceinline__ void zero_part(const Part<T>& p, typename T::raw* dz)
     if (p.lone >= 0) dz[p.lone] = 0;
 }
 
+// The entries' logits: slot tid's comes in a register (it was asked for when
+// its column was known, and is not waited for before the row has gone by), the
+// others are read here.
 template <class T, int kThreads>
-__device__ __forceinline__ void lds_layout(const DistillArgs& a, const RowShape& sh, uint8_t* lds,
-                                           Bitmap<T, kThreads>& bitmap, Slots& s) {
-    bitmap.cells = reinterpret_cast<typename Bitmap<T, kThreads>::Cell*>(lds);
-    bitmap.sh = sh;
-    bitmap.n = (int32_t)a.in.cols;
-    s.col = reinterpret_cast<int32_t*>(lds + Bitmap<T, kThreads>::bytes(sh.granules));
-    s.t = reinterpret_cast<float*>(s.col + a.k);
-    s.z = s.t + a.k;
+__device__ __forceinline__ void take_logits(const DistillArgs& a, const Part<T>& p, float z0,
+                                            const Lds<T, kThreads>& l) {
+    for (int32_t slot = (int32_t)threadIdx.x; slot < a.k; slot += kThreads)
+        l.z[slot] = slot == (int32_t)threadIdx.x ? z0 : p.entry_logit(l.col[slot]);
 }
 
 // kPart: only the part's running sum of the tail, for k_distill_join.
 // Four granules a thread are worked on while the next four are on their way.
 template <class T, bool kPart>
-__global__ __launch_bounds__(kStreamThreads, 8) void k_distill_loss(DistillArgs a) {
+__global__ __launch_bounds__(kStreamThreads, 6) void k_distill_loss(DistillArgs a) {
     constexpr int kThreads = kStreamThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
-    extern __shared__ __align__(16) uint8_t lds[];
+    extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ float2 wsum[kNW];
     __shared__ WaveSums wrec[kNW];
+    __shared__ uint32_t s_flags;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
+    const Lds<T, kThreads> l(lds_bytes, p.sh, p.n, a.k);
     const float w = a.weight ? a.weight[p.row] : 1.0f;
-    Bitmap<T, kThreads> bitmap;
-    Slots slots;
-    lds_layout(a, p.sh, lds, bitmap, slots);
-    gran g[4], next[4];
-    float lx = kNegInf;
-    double t_lse = 0.0;
-    bool alive = false;
-    if (w != 0.0f) {
-        const int32_t c0 = slot_column(a, p.row, tid);
-        p.template load<kThreads>(0, g);
-        if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
-        if (!kPart && a.t_lse) t_lse = (double)a.t_lse[p.row];
-        bitmap.clear();
-        alive = read_slots<T, kThreads>(a, p.row, p.z, 0, kPart ? 0 : p.n, c0, bitmap, slots);
-    }
-    if (!alive) {  // the same for the whole workgroup
+    const double t_lse = !kPart && a.t_lse ? (double)a.t_lse[p.row] : 0.0;
+    const Slot s0 = read_slot(a, p.row, tid);
+    gran g[4];
+    p.template load<kThreads>(0, g);
+    const float lx = p.lone_logit();
+    const float z0 = kPart ? 0.0f : p.entry_logit(s0.c);
+    if (tid == 0) s_flags = 0;
+    l.clear();
+    if (!mark_entries(a, p.row, s0, l, &s_flags) || w == 0.0f) {
         if (tid == 0) {
             if (kPart)
                 a.part[p.row * a.splits + p.sp] = make_float2(0.0f, 0.0f);
@@ -378,21 +429,23 @@ __global__ __launch_bounds__(kStreamThreads, 8) void k_distill_loss(DistillArgs 
         return;
     }
     RunningSum rs = RunningSum::none();
-    if (p.lone >= 0 && !bitmap.has(p.lone)) rs.add1(lx, a.c2);
-    for (int32_t base = 0; base < p.cnt; base += kStep) {
-        if (base + kStep < p.cnt) p.template load<kThreads>(base + kStep, next);
-        bitmap.strike((p.g0 + base) / kStep, g);
-        float m = granule_max<T>(g[0]);
+    if (p.lone >= 0 && !l.marked(p.lone)) rs.add1(lx, a.c2);
+    auto take = [&](int32_t base, gran (&x)[4]) {
+        l.strike((p.g0 + base) / kStep, x);
+        float m = granule_max<T>(x[0]);
 #pragma unroll
-        for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(g[b]));
-        rs.template add<T, 4>(g, m, a.c2);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) g[b] = next[b];
-    }
+        for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(x[b]));
+        rs.template add<T, 4>(x, m, a.c2);
+    };
+    stream_row<T, kThreads>(p, g, take, [&](int32_t base, gran (&x)[4]) {
+        p.template trim<kThreads>(base, x);
+        take(base, x);
+    });
     wave_join(rs);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     if constexpr (!kPart) {
-        const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
+        take_logits<T, kThreads>(a, p, z0, l);
+        const WaveSums ws = entry_sums<T, kThreads, true>(a, t_lse, l);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
     __syncthreads();
@@ -410,12 +463,12 @@ __global__ __launch_bounds__(kStreamThreads, 8) void k_distill_loss(DistillArgs 
 
 // Writes the entries' columns: d_j = gs (fp p_j - fq q_j).
 template <class T, int kThreads>
-__device__ __forceinline__ void write_entries(const DistillArgs& a, const Part<T>& p, const Slots& s, float gs,
-                                              double fp, double fq, typename T::raw* dz) {
+__device__ __forceinline__ void write_entries(const DistillArgs& a, const Part<T>& p, const Lds<T, kThreads>& l,
+                                              float gs, double fp, double fq, typename T::raw* dz) {
     for (int32_t slot = (int32_t)threadIdx.x; slot < a.k; slot += kThreads) {
-        const int32_t c = s.col[slot];
+        const int32_t c = l.col[slot];
         if (c < 0 || c < p.col0 || c >= p.col1) continue;
-        const double d = (double)gs * (fp * (double)s.z[slot] - fq * (double)s.t[slot]);
+        const double d = (double)gs * (fp * (double)l.z[slot] - fq * (double)l.t[slot]);
         dz[c] = gs == 0.0f ? (typename T::raw)0 : T::down1((float)d);
     }
 }
@@ -424,43 +477,42 @@ __device__ __forceinline__ void write_entries(const DistillArgs& a, const Part<T
 template <class T, int kThreads, int kGran>
 __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
     constexpr int kNW = kThreads / 64;
-    extern __shared__ __align__(16) uint8_t lds[];
+    extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ float2 wsum[kNW];
     __shared__ WaveSums wrec[kNW];
     __shared__ double s_p[kNW], s_q[kNW];
     __shared__ float s_vref, s_tail, s_gs;
+    __shared__ uint32_t s_flags;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
+    const Lds<T, kThreads> l(lds_bytes, p.sh, p.n, a.k);
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     const float w = a.weight ? a.weight[p.row] : 1.0f;
-    Bitmap<T, kThreads> bitmap;
-    Slots slots;
-    lds_layout(a, p.sh, lds, bitmap, slots);
+    const double t_lse = a.t_lse ? (double)a.t_lse[p.row] : 0.0;
+    const Slot s0 = read_slot(a, p.row, tid);
     gran g[kGran / 4][4];
-    float lx = kNegInf;
-    double t_lse = 0.0;
-    bool alive = false;
+    p.template load<kThreads>(0, g[0]);
+    const float lx = p.lone_logit();
+    const float z0 = p.entry_logit(s0.c);
     if (w != 0.0f) {
-        const int32_t c0 = slot_column(a, p.row, tid);
 #pragma unroll
-        for (int c = 0; c < kGran / 4; ++c) p.template load<kThreads>(c * 4 * kThreads, g[c]);
-        if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
-        if (a.t_lse) t_lse = (double)a.t_lse[p.row];
-        bitmap.clear();
-        alive = read_slots<T, kThreads>(a, p.row, p.z, 0, p.n, c0, bitmap, slots);
+        for (int c = 1; c < kGran / 4; ++c) p.template load<kThreads>(c * 4 * kThreads, g[c]);
     }
-    if (!alive) {  // the same for the whole workgroup
+    if (tid == 0) s_flags = 0;
+    l.clear();
+    if (!mark_entries(a, p.row, s0, l, &s_flags) || w == 0.0f) {
         if (tid == 0) write_no_row(a, p.row);
         zero_part<T, kThreads>(p, dz);
         return;
     }
     RunningSum rs = RunningSum::none();
-    if (p.lone >= 0 && !bitmap.has(p.lone)) rs.add1(lx, a.c2);
+    if (p.lone >= 0 && !l.marked(p.lone)) rs.add1(lx, a.c2);
 #pragma unroll
     for (int c = 0; c < kGran / 4; ++c)
         if (c * 4 * kThreads < p.cnt) {
-            bitmap.strike(c, g[c]);
+            if ((c + 1) * 4 * kThreads > p.cnt) p.template trim<kThreads>(c * 4 * kThreads, g[c]);
+            l.strike(c, g[c]);
             float m = granule_max<T>(g[c][0]);
 #pragma unroll
             for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(g[c][b]));
@@ -469,7 +521,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
     wave_join(rs);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     {
-        const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
+        take_logits<T, kThreads>(a, p, z0, l);
+        const WaveSums ws = entry_sums<T, kThreads, true>(a, t_lse, l);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
     __syncthreads();
@@ -505,52 +558,49 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
         }
     }
     if (p.lone >= 0) dz[p.lone] = T::down1(f * fast_exp2(__builtin_fmaf(lx, a.c2, -vref)));
-    __syncthreads();  // the entries' columns are written over the tail's values
-    write_entries<T, kThreads>(a, p, slots, s_gs, s_p[wave], s_q[wave], dz);
+    __syncthreads();  // the entries' columns are written over what is there
+    write_entries(a, p, l, s_gs, s_p[wave], s_q[wave], dz);
 }
 
 // The gradient of a row or a part of one, from the statistics.
 template <class T>
-__global__ __launch_bounds__(kStreamThreads, 8) void k_distill_grad(DistillArgs a) {
-    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
-    extern __shared__ __align__(16) uint8_t lds[];
+__global__ __launch_bounds__(kStreamThreads, 6) void k_distill_grad(DistillArgs a) {
+    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64;
+    extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ WaveSums wrec[kNW];
     __shared__ double s_p, s_q[kNW];
     __shared__ float s_vref, s_tail, s_gs;
+    __shared__ uint32_t s_flags;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const Part<T> p(a);
+    const Lds<T, kThreads> l(lds_bytes, p.sh, p.n, a.k);
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     float w = a.weight ? a.weight[p.row] : 1.0f;
-    if (a.dloss) w = w == 0.0f ? 0.0f : w * a.dloss[p.row];
-    Bitmap<T, kThreads> bitmap;
-    Slots slots;
-    lds_layout(a, p.sh, lds, bitmap, slots);
-    gran g[4], next[4];
-    float lx = kNegInf;
-    double t_lse = 0.0;
-    bool alive = false;
-    if (w != 0.0f) {
-        const int32_t c0 = slot_column(a, p.row, tid);
-        p.template load<kThreads>(0, g);
-        if (p.lone >= 0) lx = T::up1(p.z[p.lone]);
-        if (a.t_lse) t_lse = (double)a.t_lse[p.row];
-        bitmap.clear();
-        // dz may be z, and other workgroups write their parts of it: only
-        // this part's logits are read
-        alive = read_slots<T, kThreads>(a, p.row, p.z, p.col0, p.col1, c0, bitmap, slots);
-    }
-    if (!alive) {  // the same for the whole workgroup
+    const float up = a.dloss ? a.dloss[p.row] : 1.0f;
+    const double t_lse = a.t_lse ? (double)a.t_lse[p.row] : 0.0;
+    const float lse = a.stats[2 * p.row], lpt = a.stats[2 * p.row + 1];
+    const Slot s0 = read_slot(a, p.row, tid);
+    gran g[4];
+    p.template load<kThreads>(0, g);
+    // dz may be z, and other workgroups write their parts of it: only this
+    // part's logits are read
+    const float lx = p.lone_logit();
+    const float z0 = p.entry_logit(s0.c);
+    w = w == 0.0f ? 0.0f : w * up;
+    if (tid == 0) s_flags = 0;
+    l.clear();
+    if (!mark_entries(a, p.row, s0, l, &s_flags) || w == 0.0f) {
         zero_part<T, kThreads>(p, dz);
         return;
     }
-    const float l = a.stats[2 * p.row], lpt = a.stats[2 * p.row + 1];
+    // before any other thread may write over z
+    for (int32_t slot = tid + kThreads; slot < a.k; slot += kThreads)
+        l.z[slot] = p.entry_logit(l.col[slot]);
     {
-        const WaveSums ws = entry_sums<kThreads, false>(a, t_lse, slots);
+        const WaveSums ws = entry_sums<T, kThreads, false>(a, t_lse, l);
         if ((tid & 63) == 0) wrec[wave] = ws;
     }
-    for (int32_t slot = tid; slot < a.k; slot += kThreads)
-        slots.z[slot] = (float)exp((double)slots.z[slot] * (double)a.scale - (double)l);
     __syncthreads();
     if (wave == 0) {
         const WaveSums r = wrec[tid & (kNW - 1)];
@@ -560,16 +610,16 @@ __global__ __launch_bounds__(kStreamThreads, 8) void k_distill_grad(DistillArgs 
         const double rest = a.t_lse && 1.0 - q > 0.0 && lpt != kNegInf ? 1.0 - q : 0.0;
         // (Q - q_T / p_T) p_v, against L, or where 1 / p_T could leave the
         // range against the tail's own log-sum-exp
-        float v = l, tail = (float)qsum;
+        float v = lse, tail = (float)qsum;
         if (rest > 0.0) {
             const double pt = exp((double)lpt), c = qsum * pt + rest * (pt - 1.0);
             const bool near = lpt > -30.0f;
             tail = (float)(near ? c / pt : c);
-            if (!near) v = (float)((double)l + (double)lpt);
+            if (!near) v = (float)((double)lse + (double)lpt);
         }
         if (tid < kNW) s_q[tid] = fq * (qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q);
         if (tid == 0) {
-            const float gs = l == kNegInf ? 0.0f : w * a.scale;
+            const float gs = lse == kNegInf ? 0.0f : w * a.scale;
             s_p = qsum + rest;
             s_gs = gs;
             s_tail = gs == 0.0f ? 0.0f : gs * tail;
@@ -585,58 +635,59 @@ __global__ __launch_bounds__(kStreamThreads, 8) void k_distill_grad(DistillArgs 
         const float e = T::kN == 4 ? __builtin_fmaf(x, a.scale, -vref) * kLog2e : __builtin_fmaf(x, a.c2, -vref2);
         return f * fast_exp2(e);
     };
-    for (int32_t base = 0; base < p.cnt; base += kStep) {
-        if (base + kStep < p.cnt) p.template load<kThreads>(base + kStep, next);
+    auto write = [&](int32_t i, const gran& x) {
+        float d[T::kN];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int32_t i = base + tid + b * kThreads;
-            if (i < p.cnt) {
-                float d[T::kN];
+        for (int j = 0; j < T::kN; ++j) d[j] = grad(T::up(x, j));
+        store_loose(dz + p.first, i, T::down(d));
+    };
+    stream_row<T, kThreads>(
+        p, g,
+        [&](int32_t base, const gran (&x)[4]) {
 #pragma unroll
-                for (int j = 0; j < T::kN; ++j) d[j] = grad(T::up(g[b], j));
-                store_loose(dz + p.first, i, T::down(d));
-            }
-        }
+            for (int b = 0; b < 4; ++b) write(base + tid + b * kThreads, x[b]);
+        },
+        [&](int32_t base, const gran (&x)[4]) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) g[b] = next[b];
-    }
+            for (int b = 0; b < 4; ++b)
+                if (base + tid + b * kThreads < p.cnt) write(base + tid + b * kThreads, x[b]);
+        });
     if (p.lone >= 0) dz[p.lone] = T::down1(grad(lx));
+    if (tid < a.k) l.z[tid] = z0;
+    for (int32_t slot = tid; slot < a.k; slot += kThreads)
+        l.z[slot] = (float)exp((double)l.z[slot] * (double)a.scale - (double)lse);
     __syncthreads();  // the entries' columns are written over the tail's values
-    write_entries<T, kThreads>(a, p, slots, s_gs, s_p, s_q[wave], dz);
+    write_entries(a, p, l, s_gs, s_p, s_q[wave], dz);
 }
 
 // Joins the parts of a split row: the loss and the statistics.
 template <class T>
 __global__ __launch_bounds__(kStreamThreads) void k_distill_join(DistillArgs a) {
     constexpr int kThreads = kStreamThreads, kNW = kThreads / 64;
-    extern __shared__ __align__(16) uint8_t lds[];
+    extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ WaveSums wrec[kNW];
-    using raw = typename T::raw;
-    const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
+    __shared__ uint32_t s_flags;
+    const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64, n = (int32_t)a.in.cols;
     const int64_t row = blockIdx.x;
-    const raw* z = static_cast<const raw*>(a.in.z) + row * a.in.ld;
+    const typename T::raw* z = static_cast<const typename T::raw*>(a.in.z) + row * a.in.ld;
+    const Lds<T, kThreads> l(lds_bytes, row_shape<T>(z, n), n, a.k);
     const float w = a.weight ? a.weight[row] : 1.0f;
-    Bitmap<T, kThreads> bitmap;
-    Slots slots;
-    lds_layout(a, row_shape<T>(z, (int32_t)a.in.cols), lds, bitmap, slots);
-    double t_lse = 0.0;
-    bool alive = false;
+    const double t_lse = a.t_lse ? (double)a.t_lse[row] : 0.0;
+    const Slot s0 = read_slot(a, row, tid);
     RunningSum r = RunningSum::none();  // of lane s: part s
-    if (w != 0.0f) {
-        const int32_t c0 = slot_column(a, row, tid);
-        if (a.t_lse) t_lse = (double)a.t_lse[row];
-        if ((tid & 63) < a.splits) {
-            const float2 p = a.part[row * a.splits + (tid & 63)];
-            r = RunningSum{p.x, p.y};
-        }
-        bitmap.clear();
-        alive = read_slots<T, kThreads>(a, row, z, 0, (int32_t)a.in.cols, c0, bitmap, slots);
+    if ((tid & 63) < a.splits) {
+        const float2 p = a.part[row * a.splits + (tid & 63)];
+        r = RunningSum{p.x, p.y};
     }
-    if (!alive) {
+    if (tid == 0) s_flags = 0;
+    l.clear();
+    if (!mark_entries(a, row, s0, l, &s_flags) || w == 0.0f) {
         if (tid == 0) write_no_row(a, row);
         return;
     }
-    const WaveSums ws = entry_sums<kThreads, true>(a, t_lse, slots);
+    for (int32_t slot = tid; slot < a.k; slot += kThreads)
+        if (l.col[slot] >= 0) l.z[slot] = T::up1(z[l.col[slot]]);
+    const WaveSums ws = entry_sums<T, kThreads, true>(a, t_lse, l);
     if ((tid & 63) == 0) wrec[wave] = ws;
     __syncthreads();
     if (wave == 0) {
@@ -646,27 +697,28 @@ __global__ __launch_bounds__(kStreamThreads) void k_distill_join(DistillArgs a) 
     }
 }
 
+// At most 34 KB of bitmap (2^18 columns) and 12 KB of slots (k = 1024).
 template <class T, int kThreads>
-static size_t lds_bytes(const DistillArgs& a) {
-    return (size_t)(Bitmap<T, kThreads>::bytes((int32_t)row_granules(a.in.dtype, a.in.cols)) + slot_bytes(a.k));
+static size_t lds_size(const DistillArgs& a) {
+    return (size_t)Lds<T, kThreads>::bytes((int32_t)row_granules(a.in.dtype, a.in.cols), a.k);
 }
 static dim3 parts(const DistillArgs& a) { return dim3((uint32_t)(a.in.rows * a.splits)); }
 
 template <class T>
 static hipError_t backward_typed(hipStream_t s, const DistillArgs& a) {
-    hipLaunchKernelGGL((k_distill_grad<T>), parts(a), dim3(kStreamThreads), (lds_bytes<T, kStreamThreads>(a)), s, a);
+    hipLaunchKernelGGL((k_distill_grad<T>), parts(a), dim3(kStreamThreads), (lds_size<T, kStreamThreads>(a)), s, a);
     return hipGetLastError();
 }
 
 template <class T, int kThreads, int kGran>
 static void fused(hipStream_t s, const DistillArgs& a) {
-    hipLaunchKernelGGL((k_distill_fused<T, kThreads, kGran>), parts(a), dim3(kThreads), (lds_bytes<T, kThreads>(a)), s,
+    hipLaunchKernelGGL((k_distill_fused<T, kThreads, kGran>), parts(a), dim3(kThreads), (lds_size<T, kThreads>(a)), s,
                        a);
 }
 
 template <class T>
 static hipError_t forward_typed(hipStream_t s, const DistillArgs& a) {
-    const size_t lds = lds_bytes<T, kStreamThreads>(a);
+    const size_t lds = lds_size<T, kStreamThreads>(a);
     if (a.splits > 1) {
         hipLaunchKernelGGL((k_distill_loss<T, true>), parts(a), dim3(kStreamThreads), lds, s, a);
         hipLaunchKernelGGL((k_distill_join<T>), dim3((uint32_t)a.in.rows), dim3(kStreamThreads), lds, s, a);

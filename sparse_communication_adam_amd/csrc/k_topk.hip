@@ -115,24 +115,23 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
     const RowShape sh = row_shape<T>(z, n);
     const int32_t g0 = sp * a.per;
     const int32_t cnt = min(a.per, sh.granules - g0);  // may be <= 0 in the last split
-    const gran* body = reinterpret_cast<const gran*>(z + sh.head) + g0;
+    const gran* body = cnt > 0 ? reinterpret_cast<const gran*>(z + sh.head) + g0 : &g_no_granule;
     const int32_t first = sh.head + g0 * T::kN;  // column of granule 0's first element
 
+    // loads under no condition, so that the first are worked on while the
+    // last are on their way; past the end the last granule again, taken out
+    // below
     gran g[kGran];
 #pragma unroll
-    for (int c = 0; c < kGran; ++c) {
-        const int32_t i = tid + c * kThreads;
-        g[c] = no_entries<T>();
-        if (i < cnt) g[c] = granule_at(body, i);
-    }
+    for (int c = 0; c < kGran; ++c) g[c] = granule_at(body, max(min(tid + c * kThreads, cnt - 1), 0));
     const int32_t lone = lone_element(sh, n, sp == 0, sp == a.splits - 1);
-    const float lx = lone >= 0 ? T::up1(z[lone]) : kNegInf;
+    float lx = T::up1(z[lone >= 0 ? lone : 0]);
+    if (lone < 0) lx = kNegInf;
     if (tid == 0) s_n = s_hits = 0;
 
     constexpr int kBatch = 2;
-    float gm[kGran], m0 = lx, m1 = kNegInf;
+    float gm[kGran], m0 = kNegInf, m1 = kNegInf;
     RunningSum rs = RunningSum::none();
-    rs.add1(lx, a.c2);
 #pragma unroll
     for (int c = 0; c < kGran; c += kBatch)
         if (c * kThreads < cnt || c == 0) {
@@ -140,6 +139,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
             float bm = kNegInf;
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
+                if (tid + (c + b) * kThreads >= cnt) g[c + b] = no_entries<T>();
                 x[b] = g[c + b];
                 gm[c + b] = granule_max<T>(x[b]);
                 bm = max_nan(bm, gm[c + b]);
@@ -150,6 +150,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) gm[c + b] = kNegInf;
         }
+    rs.add1(lx, a.c2);
+    m0 = max_nan(m0, lx);
     gmax[tid] = order_key(m0) >> 16;
     gmax[tid + kThreads] = order_key(m1) >> 16;
     wave_join(rs);

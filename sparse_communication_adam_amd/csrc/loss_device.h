@@ -12,7 +12,7 @@ typedef uint32_t gran __attribute__((ext_vector_type(4)));  // 16 bytes of a row
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr double kLn2 = 0.693147180559945309417;
+constexpr double kLn2 = 0.693147180559945309417, kLog2e64 = 1.44269504088896340736;
 
 // A logit type: its storage, its elements per granule, and the conversions
 // of element j (a compile-time constant after unrolling) of a granule.
@@ -74,11 +74,15 @@ struct F16 {
 };
 
 // One element of an array whose type is known at run time (the teacher's
-// values, k of them a row).
-__device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t i) {
-    if (dtype == SCAPE_DTYPE_F32) return static_cast<const float*>(p)[i];
-    const uint16_t r = static_cast<const uint16_t*>(p)[i];
-    return dtype == SCAPE_DTYPE_BF16 ? BF16::up1(r) : F16::up1(r);
+// values, k of them a row): the bits, which take no instruction that would
+// wait for the load, and what they are.
+__device__ __forceinline__ uint32_t load_bits(const void* p, int32_t dtype, int64_t i) {
+    if (dtype == SCAPE_DTYPE_F32) return static_cast<const uint32_t*>(p)[i];
+    return static_cast<const uint16_t*>(p)[i];
+}
+__device__ __forceinline__ float value_of(uint32_t bits, int32_t dtype) {
+    if (dtype == SCAPE_DTYPE_F32) return __uint_as_float(bits);
+    return dtype == SCAPE_DTYPE_BF16 ? BF16::up1((uint16_t)bits) : F16::up1((uint16_t)bits);
 }
 
 // A row starts anywhere; its granules lie on 16-byte boundaries.  The `head`
@@ -98,6 +102,10 @@ __device__ __forceinline__ RowShape row_shape(const void* row, int32_t n) {
     r.tail = n - r.head - r.granules * T::kN;
     return r;
 }
+// What a row without a whole granule reads instead, so that the loads of a
+// kernel's first granules stand under no condition.
+__device__ gran g_no_granule = {0u, 0u, 0u, 0u};
+
 // Granule i of a run, and 16 bytes at it: a uniform base and a 32-bit offset.
 __device__ __forceinline__ gran granule_at(const void* body, int32_t i) {
     return *reinterpret_cast<const gran*>(static_cast<const char*>(body) + (size_t)((uint32_t)i * 16u));
@@ -269,6 +277,12 @@ __device__ __forceinline__ double from_lane(double x, int lane) {
     return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane) |
                                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane)
                                               << 32);
+}
+
+// x of lane base + lane % kWaves (a power of two).
+template <int kWaves>
+__device__ __forceinline__ double from_lane_of(double x, int base) {
+    return __shfl(x, base + (int)(lane_id() & (kWaves - 1)), 64);
 }
 
 // Joins the lanes' running sums: every lane gets the wave's.
