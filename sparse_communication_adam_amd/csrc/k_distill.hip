@@ -104,14 +104,13 @@ struct Lds {
                     uint32_t m;
                     if constexpr (T::kN == 8) {
                         typedef int16_t pair __attribute__((ext_vector_type(2)));
-                        pair up = __builtin_bit_cast(pair, bits) << (int16_t)(15 - 4 * b - q);
-                        asm volatile("" : "+v"(up));  // else each half becomes a test and a select
-                        m = __builtin_bit_cast(uint32_t, (pair)(up >> (int16_t)15));
+                        m = __builtin_bit_cast(uint32_t, (pair)(__builtin_bit_cast(pair, bits) << (int16_t)(15 - 4 * b - q)));
+                        asm("" : "+v"(m));
+                        m = __builtin_bit_cast(uint32_t, (pair)(__builtin_bit_cast(pair, m) >> (int16_t)15));
                     } else {
-                        int32_t up = (int32_t)(bits << (31 - 4 * b - q));
-                        asm volatile("" : "+v"(up));
-                        m = (uint32_t)(up >> 31);
+                        m = (uint32_t)((int32_t)(bits << (31 - 4 * b - q)) >> 31);
                     }
+                    asm("" : "+v"(m));  // a mask: else each element becomes a test and a select
                     g[b][q] = (g[b][q] & ~m) | (no_entries<T>()[q] & m);
                 }
         }
