@@ -489,18 +489,20 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     const float w = a.weight ? a.weight[p.row] : 1.0f;
     const double t_lse = a.t_lse ? (double)a.t_lse[p.row] : 0.0;
+    if (w == 0.0f) {
+        if (tid == 0) write_no_row(a, p.row);
+        zero_part<T, kThreads>(p, dz);
+        return;
+    }
     const Slot s0 = read_slot(a, p.row, tid);
     gran g[kGran / 4][4];
-    p.template load<kThreads>(0, g[0]);
+#pragma unroll
+    for (int c = 0; c < kGran / 4; ++c) p.template load<kThreads>(c * 4 * kThreads, g[c]);
     const float lx = p.lone_logit();
     const float z0 = p.entry_logit(s0.c);
-    if (w != 0.0f) {
-#pragma unroll
-        for (int c = 1; c < kGran / 4; ++c) p.template load<kThreads>(c * 4 * kThreads, g[c]);
-    }
     if (tid == 0) s_flags = 0;
     l.clear();
-    if (!mark_entries(a, p.row, s0, l, &s_flags) || w == 0.0f) {
+    if (!mark_entries(a, p.row, s0, l, &s_flags)) {
         if (tid == 0) write_no_row(a, p.row);
         zero_part<T, kThreads>(p, dz);
         return;

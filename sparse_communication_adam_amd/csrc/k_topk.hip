@@ -95,7 +95,7 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
 // than the lists hold (ties, or k near the number of groups), the exact
 // threshold comes from a radix selection that reads the row again, from the
 // caches, for each 8-bit digit.
-constexpr int kTopkHits = 768;  // granules
+constexpr int kTopkHits = 768;  // granules, an equal share for each wave
 template <class T, int kThreads, int kGran>
 __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
     constexpr int kNW = kThreads / 64;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
     __shared__ uint32_t hist[256];
     __shared__ uint32_t gmax[2 * kThreads];
     __shared__ float2 wsum[kNW];
-    __shared__ uint32_t s_n, s_hits, s_bin, s_need, s_tau;
+    __shared__ uint32_t s_n, s_over, s_bin, s_need, s_tau;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
     const int64_t row = blockIdx.x / (uint32_t)a.splits;
@@ -127,19 +127,23 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
     const int32_t lone = lone_element(sh, n, sp == 0, sp == a.splits - 1);
     float lx = T::up1(z[lone >= 0 ? lone : 0]);
     if (lone < 0) lx = kNegInf;
-    if (tid == 0) s_n = s_hits = 0;
+    if (tid == 0) s_n = s_over = 0;
 
-    constexpr int kBatch = 2;
+    constexpr int kBatch = kGran / 2 < 4 ? kGran / 2 : 4;
     float gm[kGran], m0 = kNegInf, m1 = kNegInf;
     RunningSum rs = RunningSum::none();
 #pragma unroll
     for (int c = 0; c < kGran; c += kBatch)
         if (c * kThreads < cnt || c == 0) {
+            if ((c + kBatch) * kThreads > cnt) {
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (tid + (c + b) * kThreads >= cnt) g[c + b] = no_entries<T>();
+            }
             gran x[kBatch];
             float bm = kNegInf;
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                if (tid + (c + b) * kThreads >= cnt) g[c + b] = no_entries<T>();
                 x[b] = g[c + b];
                 gm[c + b] = granule_max<T>(x[b]);
                 bm = max_nan(bm, gm[c + b]);
@@ -194,25 +198,34 @@ __global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
         }
     };
     take(lx, lone);
+    constexpr uint32_t kShare = kTopkHits / kNW;
+    const uint32_t share = (uint32_t)wave * kShare;
+    uint32_t hits = 0;  // of the wave
 #pragma unroll
-    for (int c = 0; c < kGran; ++c)
-        if (!(gm[c] < tau)) {
-            const uint32_t at = atomicAdd(&s_hits, 1u);
-            if (at < kTopkHits) {
-                hit[at] = g[c];
-                hit_at[at] = first + (tid + c * kThreads) * T::kN;
+    for (int c = 0; c < kGran; ++c) {
+        const bool reaches = !(gm[c] < tau);
+        const uint64_t lanes = wave_ballot(reaches);
+        if (lanes) {
+            const uint32_t at = hits + lanes_below(lanes);
+            if (reaches && at < kShare) {
+                hit[share + at] = g[c];
+                hit_at[share + at] = first + (tid + c * kThreads) * T::kN;
             }
+            hits += (uint32_t)__popcll(lanes);
         }
-    __syncthreads();
-    const uint32_t hits = s_hits;
-    if (hits <= kTopkHits) {
-        const raw* elems = reinterpret_cast<const raw*>(hit);
-        for (uint32_t i = (uint32_t)tid; i < hits * T::kN; i += kThreads)
-            take(T::up1(elems[i]), hit_at[i / T::kN] + (int32_t)(i % T::kN));
-        __syncthreads();
     }
+    if (hits <= kShare) {
+        // the wave's own hits: its LDS writes are done before it reads
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const raw* elems = reinterpret_cast<const raw*>(hit + share);
+        for (uint32_t i = (uint32_t)tid & 63u; i < hits * T::kN; i += 64)
+            take(T::up1(elems[i]), hit_at[share + i / T::kN] + (int32_t)(i % T::kN));
+    } else if ((tid & 63) == 0) {
+        s_over = 1;
+    }
+    __syncthreads();
     uint32_t found = s_n;
-    if (hits > kTopkHits || found > kTopkList) {
+    if (s_over || found > kTopkList) {
         // radix selection over 8-bit digits of the composite, largest first;
         // every part of the row by its granules, then the lone elements
         auto each = [&](auto f) {
