@@ -400,8 +400,8 @@ __device__ __forceinline__ void take_logits(const DistillArgs& a, const Part<T>&
 // kPart: only the part's running sum of the tail, for k_distill_join.
 // Four granules a thread are worked on while the next four are on their way.
 template <class T, bool kPart>
-__global__ __launch_bounds__(kStreamThreads, 6) void k_distill_loss(DistillArgs a) {
-    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
+__global__ __launch_bounds__(kRowThreads, 6) void k_distill_loss(DistillArgs a) {
+    constexpr int kThreads = kRowThreads, kNW = kThreads / 64, kStep = 4 * kThreads;
     extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ float2 wsum[kNW];
     __shared__ WaveSums wrec[kNW];
@@ -565,8 +565,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
 
 // The gradient of a row or a part of one, from the statistics.
 template <class T>
-__global__ __launch_bounds__(kStreamThreads, 6) void k_distill_grad(DistillArgs a) {
-    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64;
+__global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) {
+    constexpr int kThreads = kRowThreads, kNW = kThreads / 64;
     extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ WaveSums wrec[kNW];
     __shared__ double s_p, s_q[kNW];
@@ -663,8 +663,8 @@ __global__ __launch_bounds__(kStreamThreads, 6) void k_distill_grad(DistillArgs 
 
 // Joins the parts of a split row: the loss and the statistics.
 template <class T>
-__global__ __launch_bounds__(kStreamThreads) void k_distill_join(DistillArgs a) {
-    constexpr int kThreads = kStreamThreads, kNW = kThreads / 64;
+__global__ __launch_bounds__(kRowThreads) void k_distill_join(DistillArgs a) {
+    constexpr int kThreads = kRowThreads, kNW = kThreads / 64;
     extern __shared__ __align__(16) uint8_t lds_bytes[];
     __shared__ WaveSums wrec[kNW];
     __shared__ uint32_t s_flags;
@@ -707,7 +707,10 @@ static dim3 parts(const DistillArgs& a) { return dim3((uint32_t)(a.in.rows * a.s
 
 template <class T>
 static hipError_t backward_typed(hipStream_t s, const DistillArgs& a) {
-    hipLaunchKernelGGL((k_distill_grad<T>), parts(a), dim3(kStreamThreads), (lds_size<T, kStreamThreads>(a)), s, a);
+    DistillArgs b = a;
+    b.splits = a.grad_splits;
+    b.per = a.grad_per;
+    hipLaunchKernelGGL((k_distill_grad<T>), parts(b), dim3(kRowThreads), (lds_size<T, kRowThreads>(b)), s, b);
     return hipGetLastError();
 }
 
@@ -719,18 +722,18 @@ static void fused(hipStream_t s, const DistillArgs& a) {
 
 template <class T>
 static hipError_t forward_typed(hipStream_t s, const DistillArgs& a) {
-    const size_t lds = lds_size<T, kStreamThreads>(a);
+    const size_t lds = lds_size<T, kRowThreads>(a);
     if (a.splits > 1) {
-        hipLaunchKernelGGL((k_distill_loss<T, true>), parts(a), dim3(kStreamThreads), lds, s, a);
-        hipLaunchKernelGGL((k_distill_join<T>), dim3((uint32_t)a.in.rows), dim3(kStreamThreads), lds, s, a);
-    } else if (a.dz && a.per <= kRowCapacity) {
+        hipLaunchKernelGGL((k_distill_loss<T, true>), parts(a), dim3(kRowThreads), lds, s, a);
+        hipLaunchKernelGGL((k_distill_join<T>), dim3((uint32_t)a.in.rows), dim3(kRowThreads), lds, s, a);
+    } else if (a.dz && a.per <= kFusedCapacity) {
         if (a.per <= 256 * 4) fused<T, 256, 4>(s, a);
         else if (a.per <= 256 * 8) fused<T, 256, 8>(s, a);
         else if (a.per <= 256 * 16) fused<T, 256, 16>(s, a);
         else fused<T, 512, 16>(s, a);
         return hipGetLastError();
     } else {
-        hipLaunchKernelGGL((k_distill_loss<T, false>), parts(a), dim3(kStreamThreads), lds, s, a);
+        hipLaunchKernelGGL((k_distill_loss<T, false>), parts(a), dim3(kRowThreads), lds, s, a);
     }
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !a.dz ? e : backward_typed<T>(s, a);

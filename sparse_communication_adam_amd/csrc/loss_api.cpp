@@ -10,20 +10,15 @@ using namespace scape;
 
 namespace scape {
 
-// A row is split where a kernel must hold it and it does not fit a workgroup's
-// registers, and where there are fewer rows than it takes to fill the 256 CUs:
-// up to kFill workgroups in all, none with less than kPartUnit granules.
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool held) {
-    constexpr int64_t kFill = 512;
-    const int64_t units = (row_granules(dtype, cols) + kPartUnit - 1) / kPartUnit;
-    const int64_t most = kRowCapacity / kPartUnit;
-    const int64_t need = held ? (units + most - 1) / most : 1;
-    int64_t want = rows > 0 ? kFill / rows : 1;
-    if (want > units) want = units;
-    if (want > kMaxSplits) want = kMaxSplits;
-    const int64_t n = want > need ? want : need;
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, int32_t unit, int64_t most, int64_t fill) {
+    const int64_t g = row_granules(dtype, cols);
+    const int64_t units = (g + unit - 1) / unit, need = (g + most - 1) / most;
+    int64_t n = rows > 0 ? fill / rows : 1;
+    if (n > g / kCellUnit) n = g / kCellUnit;  // smaller parts cost more to join than they gain
+    if (n > kMaxSplits) n = kMaxSplits;
+    if (n < need) n = need;
     const int64_t per = (units + n - 1) / n;
-    return RowSplit{(int32_t)((units + per - 1) / per), (int32_t)(per * kPartUnit)};
+    return RowSplit{(int32_t)((units + per - 1) / per), (int32_t)(per * unit)};
 }
 
 }  // namespace scape
@@ -103,18 +98,21 @@ int topk_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* s
         if (rows > kMaxSmallRows) return fail(SCAPE_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
         return SCAPE_OK;
     }
-    *sp = row_split(dtype, rows, cols, true);
+    *sp = row_split(dtype, rows, cols, kRowThreads, kTopkCapacity, 512);
     return check_blocks(rows, *sp);
 }
 int64_t topk_bytes(int64_t rows, int32_t k, const RowSplit& sp) {
     return sp.splits > 1 ? rows * sp.splits * ((int64_t)k * 8 + 8) : 0;
 }
 
-int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* sp) {
+// The loss splits a row to fill the 256 CUs and pays for it by joining the
+// parts; the gradient from the statistics has nothing to join and takes enough
+// parts to keep every CU's waves busy to the end (1024x50304 f32: GRADTIME).
+int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, bool loss, RowSplit* sp) {
     int rc;
     if ((rc = check_dtype(dtype, "z"))) return rc;
     if ((rc = check_rows(rows, cols, k, SCAPE_DISTILL_MAX_K))) return rc;
-    *sp = row_split(dtype, rows, cols, false);
+    *sp = row_split(dtype, rows, cols, kCellUnit, int64_t(1) << 40, loss ? 512 : 4096);
     return check_blocks(rows, *sp);
 }
 int64_t distill_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }
@@ -217,7 +215,7 @@ int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, in
 int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
     if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
     RowSplit sp;
-    if (int rc = distill_shape(dtype, rows, cols, k, &sp)) return rc;
+    if (int rc = distill_shape(dtype, rows, cols, k, true, &sp)) return rc;
     *bytes = distill_bytes(rows, sp);
     return SCAPE_OK;
 }
@@ -228,7 +226,7 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     RowSplit sp;
     int rc;
     if ((rc = check_teacher(teacher, rows))) return rc;
-    if ((rc = distill_shape(dtype, rows, cols, teacher->k, &sp))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, true, &sp))) return rc;
     if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
     if ((rc = check_scale(scale))) return rc;
     if (dz && (rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;
@@ -255,6 +253,11 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     a.part = static_cast<float2*>(workspace);
     a.splits = sp.splits;
     a.per = sp.per;
+    if (dz && sp.splits > 1) {  // the gradient's own parts
+        if ((rc = distill_shape(dtype, rows, cols, teacher->k, false, &sp))) return rc;
+    }
+    a.grad_splits = sp.splits;
+    a.grad_per = sp.per;
     const hipError_t e = launch_distill_forward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "distillation loss");
 }
@@ -265,7 +268,7 @@ int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t c
     RowSplit sp;
     int rc;
     if ((rc = check_teacher(teacher, rows))) return rc;
-    if ((rc = distill_shape(dtype, rows, cols, teacher->k, &sp))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, false, &sp))) return rc;
     if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
     if ((rc = check_scale(scale))) return rc;
     if ((rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;
@@ -288,8 +291,8 @@ int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t c
     a.stats = const_cast<float*>(stats);  // read only in this launch
     a.dz = dz;
     a.ld_dz = ld_dz;
-    a.splits = sp.splits;
-    a.per = sp.per;
+    a.grad_splits = sp.splits;
+    a.grad_per = sp.per;
     const hipError_t e = launch_distill_backward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "distillation gradient");
 }

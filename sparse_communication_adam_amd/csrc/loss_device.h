@@ -107,8 +107,11 @@ __device__ __forceinline__ RowShape row_shape(const void* row, int32_t n) {
 __device__ gran g_no_granule = {0u, 0u, 0u, 0u};
 
 // Granule i of a run, and 16 bytes at it: a uniform base and a 32-bit offset.
+// Read once, written once: non-temporal both ways (loss and gradient of
+// 4096x32000 bf16 109 -> 101 us, gradient of 1024x50304 f32 90 -> 81 us).
 __device__ __forceinline__ gran granule_at(const void* body, int32_t i) {
-    return *reinterpret_cast<const gran*>(static_cast<const char*>(body) + (size_t)((uint32_t)i * 16u));
+    return __builtin_nontemporal_load(
+        reinterpret_cast<const gran*>(static_cast<const char*>(body) + (size_t)((uint32_t)i * 16u)));
 }
 
 // The element a thread takes beside its granules in the first or the last
@@ -124,7 +127,8 @@ __device__ __forceinline__ int32_t lone_element(const RowShape& r, int32_t n, bo
 // memory mode takes them; the compiler picks the instruction).
 typedef uint32_t loose_gran __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void store_loose(void* run, int32_t i, const gran& g) {
-    *reinterpret_cast<loose_gran*>(static_cast<char*>(run) + (size_t)((uint32_t)i * 16u)) = g;
+    __builtin_nontemporal_store((loose_gran)g, reinterpret_cast<loose_gran*>(static_cast<char*>(run) +
+                                                                             (size_t)((uint32_t)i * 16u)));
 }
 
 template <class T>

@@ -23,19 +23,18 @@ struct Logits {
 inline int dtype_size(int32_t dtype) { return dtype == SCAPE_DTYPE_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------------------
-// Row kernels.  A workgroup takes a row, or a part of one.  A kernel that holds
-// it in registers has 16 granules a thread (64 registers, which leaves as many
-// for the arithmetic at 4 waves per SIMD): 4096 with 256 threads (32768
-// elements of 16 bits), 8192 with 512.  Fewer, fuller threads beat more: the
-// work that each wave does once a row (reductions, the entries' terms) is
-// about as much as 64 elements a lane cost.
+// Row kernels: workgroups of 256 threads take a row, or a part of one.  Fewer,
+// fuller threads beat more: the work that each wave does once a row
+// (reductions, the entries' terms) is about as much as 64 elements a lane cost.
+constexpr int kRowThreads = 256;
+// A kernel that holds the row in registers has at most 16 granules a thread (64
+// registers, which leaves as many for the arithmetic at 4 waves per SIMD; the
+// fused loss and gradient has a form with 512 threads for twice the row).
 constexpr int kHeldGranules = 16;
-constexpr int kStreamThreads = 256;  // of the kernels that hold no row
-constexpr int64_t kRowCapacity = 512 * kHeldGranules;
+constexpr int kTopkCapacity = kRowThreads * kHeldGranules;
+constexpr int kFusedCapacity = 2 * kTopkCapacity;
 constexpr int kMaxSplits = 64;  // a lane of the joining wave for each part
-static_assert((SCAPE_ROW_MAX_COLS / 4 + 2) / kRowCapacity < kMaxSplits, "the longest row fits");
-// Parts are cut at multiples of this many granules.
-constexpr int kPartUnit = 4 * kStreamThreads;
+static_assert((SCAPE_ROW_MAX_COLS / 4 + 2) / kTopkCapacity < kMaxSplits, "the longest row fits");
 
 // Granules a row of `cols` elements can touch, whatever its alignment.
 inline int64_t row_granules(int32_t dtype, int64_t cols) {
@@ -46,9 +45,13 @@ inline int64_t row_granules(int32_t dtype, int64_t cols) {
 // Workgroups a row is split over.
 struct RowSplit {
     int32_t splits;
-    int32_t per;  // granules of each part, a multiple of kPartUnit (the last one may have fewer)
+    int32_t per;  // granules of each part, a multiple of the unit asked for (the last one may have fewer)
 };
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, bool held);
+// Parts of at most `most` granules, and more of them, of `unit` granules at
+// least, while all rows' parts are fewer than `fill`.
+RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, int32_t unit, int64_t most, int64_t fill);
+// The distillation kernels' parts are cut at whole cells of their bitmap.
+constexpr int kCellUnit = 4 * kRowThreads;
 
 // ---- k_topk.hip
 constexpr int kTopkList = 2048;       // candidates a workgroup sorts in LDS (>= SCAPE_TOPK_MAX_K)
@@ -85,6 +88,7 @@ struct DistillArgs {
     int64_t ld_dz;
     float2* part;        // splits > 1: [rows][splits] (reference, sum)
     int32_t splits, per;
+    int32_t grad_splits, grad_per;  // of k_distill_grad
 };
 hipError_t launch_distill_forward(hipStream_t s, const DistillArgs& a);
 hipError_t launch_distill_backward(hipStream_t s, const DistillArgs& a);
