@@ -10,15 +10,41 @@ using namespace scape;
 
 namespace scape {
 
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, int32_t unit, int64_t most, int64_t fill) {
-    const int64_t g = row_granules(dtype, cols);
-    const int64_t units = (g + unit - 1) / unit, need = (g + most - 1) / most;
-    int64_t n = rows > 0 ? fill / rows : 1;
-    if (n > g / kCellUnit) n = g / kCellUnit;  // smaller parts cost more to join than they gain
-    if (n > kMaxSplits) n = kMaxSplits;
-    if (n < need) n = need;
-    const int64_t per = (units + n - 1) / n;
+namespace {
+RowSplit split_evenly(int64_t granules, int64_t parts, int32_t unit) {
+    const int64_t units = (granules + unit - 1) / unit, per = (units + parts - 1) / parts;
     return RowSplit{(int32_t)((units + per - 1) / per), (int32_t)(per * unit)};
+}
+// Parts of at least `least` granules while there are fewer than `fill` in all.
+RowSplit split_to_fill(int64_t granules, int64_t rows, int64_t fill, int64_t least) {
+    int64_t n = rows > 0 ? fill / rows : 1;
+    if (n > granules / least) n = granules / least;
+    if (n > kMaxSplits) n = kMaxSplits;
+    return split_evenly(granules, n > 1 ? n : 1, kCellUnit);
+}
+}  // namespace
+
+// The top-k holds a row in registers, so a longer row is cut into parts that
+// fit; more parts than that never paid, not even for one row (1x32000 f32: 17
+// us in two parts, 23 us in eight, both with the graph replay they were timed
+// in).
+RowSplit topk_split(int32_t dtype, int64_t cols) {
+    const int64_t g = row_granules(dtype, cols);
+    return split_evenly(g, (g + kTopkCapacity - 1) / kTopkCapacity, kRowThreads);
+}
+
+// The distillation streams a row of any length.  Cutting it costs the loss a
+// join, so only the longest rows are cut, and only where there are fewer than
+// the 256 CUs (replayed graphs, us, whole and cut: 7x131072 bf16, 16384
+// granules, 19 and 20, 256 rows of them 22 and 28; 7x262144 f32 30 and 20).
+RowSplit distill_split(int32_t dtype, int64_t rows, int64_t cols) {
+    return split_to_fill(row_granules(dtype, cols), rows, 256, 16384);
+}
+// The gradient from the statistics has nothing to join; its parts reload the
+// entries instead (64x131072 bf16 26 and 18; 16x262144 f32 60 and 18;
+// 512x50304 f32, 12576 granules, 48 and 44, 1024 rows of them 85 and 85).
+RowSplit distill_grad_split(int32_t dtype, int64_t rows, int64_t cols) {
+    return split_to_fill(row_granules(dtype, cols), rows, 2048, 4096);
 }
 
 }  // namespace scape
@@ -98,21 +124,19 @@ int topk_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* s
         if (rows > kMaxSmallRows) return fail(SCAPE_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
         return SCAPE_OK;
     }
-    *sp = row_split(dtype, rows, cols, kRowThreads, kTopkCapacity, 512);
+    *sp = topk_split(dtype, cols);
     return check_blocks(rows, *sp);
 }
 int64_t topk_bytes(int64_t rows, int32_t k, const RowSplit& sp) {
     return sp.splits > 1 ? rows * sp.splits * ((int64_t)k * 8 + 8) : 0;
 }
 
-// The loss splits a row to fill the 256 CUs and pays for it by joining the
-// parts; the gradient from the statistics has nothing to join and takes enough
-// parts to keep every CU's waves busy to the end (1024x50304 f32: GRADTIME).
-int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, bool loss, RowSplit* sp) {
+int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit (*split)(int32_t, int64_t, int64_t),
+                  RowSplit* sp) {
     int rc;
     if ((rc = check_dtype(dtype, "z"))) return rc;
     if ((rc = check_rows(rows, cols, k, SCAPE_DISTILL_MAX_K))) return rc;
-    *sp = row_split(dtype, rows, cols, kCellUnit, int64_t(1) << 40, loss ? 512 : 4096);
+    *sp = split(dtype, rows, cols);
     return check_blocks(rows, *sp);
 }
 int64_t distill_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }
@@ -215,7 +239,7 @@ int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, in
 int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
     if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
     RowSplit sp;
-    if (int rc = distill_shape(dtype, rows, cols, k, true, &sp)) return rc;
+    if (int rc = distill_shape(dtype, rows, cols, k, distill_split, &sp)) return rc;
     *bytes = distill_bytes(rows, sp);
     return SCAPE_OK;
 }
@@ -226,7 +250,7 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     RowSplit sp;
     int rc;
     if ((rc = check_teacher(teacher, rows))) return rc;
-    if ((rc = distill_shape(dtype, rows, cols, teacher->k, true, &sp))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, distill_split, &sp))) return rc;
     if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
     if ((rc = check_scale(scale))) return rc;
     if (dz && (rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;
@@ -253,11 +277,11 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     a.part = static_cast<float2*>(workspace);
     a.splits = sp.splits;
     a.per = sp.per;
-    if (dz && sp.splits > 1) {  // the gradient's own parts
-        if ((rc = distill_shape(dtype, rows, cols, teacher->k, false, &sp))) return rc;
+    if (dz) {
+        if ((rc = distill_shape(dtype, rows, cols, teacher->k, distill_grad_split, &sp))) return rc;
+        a.grad_splits = sp.splits;
+        a.grad_per = sp.per;
     }
-    a.grad_splits = sp.splits;
-    a.grad_per = sp.per;
     const hipError_t e = launch_distill_forward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "distillation loss");
 }
@@ -268,7 +292,7 @@ int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t c
     RowSplit sp;
     int rc;
     if ((rc = check_teacher(teacher, rows))) return rc;
-    if ((rc = distill_shape(dtype, rows, cols, teacher->k, false, &sp))) return rc;
+    if ((rc = distill_shape(dtype, rows, cols, teacher->k, distill_grad_split, &sp))) return rc;
     if ((rc = check_matrix(z, dtype, rows, cols, ld, "z"))) return rc;
     if ((rc = check_scale(scale))) return rc;
     if ((rc = check_matrix(dz, dtype, rows, cols, ld_dz, "dz"))) return rc;

@@ -47,11 +47,11 @@ struct RowSplit {
     int32_t splits;
     int32_t per;  // granules of each part, a multiple of the unit asked for (the last one may have fewer)
 };
-// Parts of at most `most` granules, and more of them, of `unit` granules at
-// least, while all rows' parts are fewer than `fill`.
-RowSplit row_split(int32_t dtype, int64_t rows, int64_t cols, int32_t unit, int64_t most, int64_t fill);
 // The distillation kernels' parts are cut at whole cells of their bitmap.
 constexpr int kCellUnit = 4 * kRowThreads;
+RowSplit topk_split(int32_t dtype, int64_t cols);
+RowSplit distill_split(int32_t dtype, int64_t rows, int64_t cols);  // of the loss
+RowSplit distill_grad_split(int32_t dtype, int64_t rows, int64_t cols);
 
 // ---- k_topk.hip
 constexpr int kTopkList = 2048;       // candidates a workgroup sorts in LDS (>= SCAPE_TOPK_MAX_K)

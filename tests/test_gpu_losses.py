@@ -235,10 +235,12 @@ class Case:
     def bounds(self, factor):
         """What float32 arithmetic may be off by, per row: of p relative, and
         of the loss absolute.  Exponents go up to the row's spread X; a
-        thread adds at most 128 terms, then a tree of 9 steps."""
+        thread adds at most 32 terms and the row's 256th part (a row is cut
+        only into more), then a tree of 9 steps."""
         x = (self.h * self.scale).masked_fill(~self.h.isfinite(), 0)
         X = 2 * x.abs().amax(1) + 1
-        rel = (128 + 9 + 2 + 6) * U + 6 * U * X
+        terms = max(128, 32 + self.h.shape[1] // 256)
+        rel = (terms + 9 + 2 + 6) * U + 6 * U * X
         return rel, rel * 2 + U * (1 + X)
 
 
@@ -294,7 +296,8 @@ def test_distill(sc, rows, cols, k, pad, shift, dtype, tail):
     assert bool((out[:, 0].float() == 3).all()) and bool((out[:, cols + 1:].float() == 3).all())
 
 
-@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304)], ids=["whole rows", "split rows"])
+@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304), (2, 262144)],
+                         ids=["whole rows", "few rows", "split rows"])
 @pytest.mark.parametrize("tail", [True, False], ids=["tail", "renormalised"])
 def test_distill_odd_rows(sc, rows, cols, tail):
     """Rows that hold little: no entry, entries outside the row, a column
@@ -338,7 +341,8 @@ def test_distill_odd_rows(sc, rows, cols, tail):
         assert float(loss[6]) == INF
 
 
-@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304)], ids=["whole rows", "split rows"])
+@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304), (2, 262144)],
+                         ids=["whole rows", "few rows", "split rows"])
 def test_distill_nan_stays_in_its_row(sc, rows, cols):
     c = Case(rows, cols, 5, torch.bfloat16, True, key="nan")
     c.x[0, 17] = NAN
@@ -348,11 +352,12 @@ def test_distill_nan_stays_in_its_row(sc, rows, cols):
     assert not bool(loss[1:].isnan().any()) and not bool(dz[1:].isnan().any())
 
 
-@pytest.mark.parametrize("rows", [600, 2], ids=["whole rows", "split rows"])
-def test_distill_far_tail(sc, rows):
+@pytest.mark.parametrize("rows,cols", [(600, 20000), (2, 20000), (2, 262144)],
+                         ids=["whole rows", "few rows", "split rows"])
+def test_distill_far_tail(sc, rows, cols):
     """A tail hundreds of e-folds below the entries keeps its terms: its sum
     is held against its own maximum."""
-    cols, k = 20000, 6
+    k = 6
     c = Case(rows, cols, k, torch.float32, True, scale=4.0, key="far")
     c.x -= 30.0
     c.x[torch.arange(rows)[:, None], c.idx.long()] = torch.rand(rows, k, generator=_rng("far")) * 2 + 40
@@ -372,7 +377,7 @@ def test_distill_far_tail(sc, rows):
     assert bool(((back.cpu().double() - ref).abs() <= tol).all())
 
 
-@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304), (3, 131072)], ids=str)
+@pytest.mark.parametrize("rows,cols", [(600, 2000), (2, 50304), (3, 262144)], ids=str)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
 def test_distill_gradient_over_the_logits(sc, rows, cols, dtype):
     """dz may be z: the same bits as in a tensor of its own."""
@@ -386,6 +391,35 @@ def test_distill_gradient_over_the_logits(sc, rows, cols, dtype):
     sc.scape_distill_backward(keep, c.dev[0], c.dev[1], stats, keep, t_lse=c.dev[2], weight=c.dev[3])
     torch.cuda.synchronize()
     assert torch.equal(keep, back)
+
+
+@pytest.mark.parametrize("cols", [262144, 262143, 131075, 65537])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_distill_at_the_cuts(sc, cols, dtype, shift):
+    """Entries at both ends of long rows and around every cut between parts,
+    in a matrix that ends with its allocation (12 MiB and more of float32 are
+    one of their own) or, shifted, begins inside a granule."""
+    rows, n = 12, 16 // torch.empty(0, dtype=dtype).element_size()
+    c = Case(rows, cols, 300, dtype, True, key="cuts", shift=shift)
+    at = [0, 1, 2, cols - 1, cols - 2, cols - 3, cols - n, cols - n - 1]
+    for cut in range(1024 * n, cols, 1024 * n):
+        at += [cut - 1, cut, cut + 1, cut - n, cut + n]
+    at = sorted({a for a in at if 0 <= a < cols})[-300:]
+    c.idx[:, :len(at)] = torch.tensor(at, dtype=torch.int32)
+    c.val[:, :len(at)] = c.x[:, at]
+    if shift == 0:
+        c.z = torch.empty(rows, cols, dtype=dtype, device="cuda").copy_(c.x)
+        c.h = c.z.cpu().double()
+    else:
+        c.put()
+    w = c.weight.double()
+    loss, stats, dz = c.call(sc)
+    _check_distill(c, w, loss, stats, dz)
+    back = torch.full_like(c.z, 5.0)
+    sc.scape_distill_backward(c.z, c.dev[0], c.dev[1], stats, back, t_lse=c.dev[2], weight=c.dev[3])
+    torch.cuda.synchronize()
+    _check_distill(c, w, dz=back)
 
 
 @pytest.mark.parametrize("tail", [True, False], ids=["tail", "renormalised"])
@@ -683,7 +717,7 @@ def _together_buffers(sc, rows, cols, experts, key):
 OUTPUTS = ("val", "idx", "lse", "loss", "stats", "dz", "dz2", "rval", "ridx", "counts", "psum", "n_tok", "bloss", "dr")
 
 
-@pytest.mark.parametrize("rows,cols", [(3, 50304), (640, 2000)], ids=["split rows", "whole rows"])
+@pytest.mark.parametrize("rows,cols", [(3, 50304), (640, 2000), (3, 262144)], ids=["few rows", "whole rows", "split rows"])
 def test_captured_and_replayed(sc, rows, cols):
     """The micro-step captured into a graph, replayed with new inputs and with
     eager calls of the same program between the replays: every replay gives
@@ -707,9 +741,10 @@ def test_captured_and_replayed(sc, rows, cols):
             assert torch.equal(cap[name], eager[name]), (n, name)
 
 
-def test_two_streams_at_once(sc):
+@pytest.mark.parametrize("cols", [50304, 262144])
+def test_two_streams_at_once(sc, cols):
     """Calls on two streams with workspaces of their own do not disturb each other."""
-    a, b = (_together_buffers(sc, 5, 50304, 16, k) for k in "xy")
+    a, b = (_together_buffers(sc, 5, cols, 16, k) for k in "xy")
     want = []
     for s in (a, b):
         _together(sc, s)

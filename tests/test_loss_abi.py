@@ -77,7 +77,7 @@ CASES = (
         (dict(teacher=dict(lse=66)), -3), (dict(teacher=dict(k=0)), -2), (dict(teacher=dict(k=1025)), -2),
         (dict(weight=66), -3), (dict(loss=0), -1), (dict(loss=66), -3), (dict(stats=0), -1), (dict(stats=66), -3),
         (dict(dz=129), -3), (dict(ld_dz=99), -2), (dict(dz=64, ld_dz=101), -2),
-        (dict(rows=1, cols=50304, ld=50304, ld_dz=50304), -1)]]
+        (dict(rows=1, cols=262144, ld=262144, ld_dz=262144), -1)]]  # a split row: no workspace
     + [("scape_distill_backward", BACKWARD, c, e) for c, e in ROWS + [
         (dict(teacher=None), -1), (dict(teacher=dict(k=1025)), -2), (dict(dz=0), -1), (dict(dz=129), -3),
         (dict(ld_dz=99), -2), (dict(dz=64, ld_dz=101), -2), (dict(stats=0), -1), (dict(dloss=66), -3),
@@ -121,12 +121,13 @@ def test_workspace_queries(sc, lib):
     assert lib.scape_topk_rows_workspace(1, 1, 50304, 32, ctypes.byref(b)) == 0 and b.value > 0
     assert lib.scape_topk_rows_workspace(0, 4096, 262144, 64, ctypes.byref(b)) == 0 and b.value > 0  # too long for one
     assert lib.scape_distill_workspace(1, 4096, 32000, 64, ctypes.byref(b)) == 0 and b.value == 0
-    assert lib.scape_distill_workspace(1, 1, 50304, 64, ctypes.byref(b)) == 0 and b.value > 0
+    assert lib.scape_distill_workspace(1, 1, 50304, 64, ctypes.byref(b)) == 0 and b.value == 0
+    assert lib.scape_distill_workspace(1, 1, 262144, 64, ctypes.byref(b)) == 0 and b.value > 0
     assert lib.scape_balance_workspace(131072, 64, 1, ctypes.byref(b)) == 0 and b.value > 0
     assert lib.scape_topk_rows_workspace(1, 1, 50304, 32, None) == -1
     assert lib.scape_distill_workspace(1, 1, 50304, 0, ctypes.byref(b)) == -2
     assert lib.scape_balance_workspace(1, 0, 1, ctypes.byref(b)) == -2
-    z = torch.zeros(1, 50304, dtype=torch.bfloat16)
+    z = torch.zeros(1, 262144, dtype=torch.bfloat16)
     assert sc.scape_topk_rows_workspace_bytes(z, 32) > 0 and sc.scape_distill_workspace_bytes(z, 32, grad=True) > 0
     assert sc.scape_balance_workspace_bytes(torch.zeros(7, 8), 2) > 0
 
@@ -172,7 +173,6 @@ def test_binding_refuses_before_the_library(sc):
     for i, (kind, call) in enumerate(cases):
         with pytest.raises(kind):
             call()
-            print("case", i)
     with pytest.raises(sc.ScapeError) as e:
         sc.scape_topk_rows(z, 101, torch.zeros(4, 101), torch.zeros(4, 101, dtype=torch.int32))
     assert e.value.code == -2
