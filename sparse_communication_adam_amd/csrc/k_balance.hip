@@ -19,7 +19,6 @@
 
 namespace scape {
 
-constexpr int kBalanceWaves = kBalanceThreads / 64;
 static_assert(SCAPE_BALANCE_MAX_EXPERTS <= 1024, "a thread for each expert in k_balance_finish");
 
 struct Run {
@@ -57,25 +56,68 @@ __device__ __forceinline__ Run run_of(const BalanceArgs& a, int32_t slot) {
     return Run{lo, (int32_t)t0, (int32_t)(t1 < end ? t1 : end)};
 }
 
-// A token's logits in a group of lanes: lane l has granules l, l + kLanes,
-// ...; past the last expert, and of tokens that do not count, -inf.
-template <class T, int kLanes, int kGran, bool kVec>
-__device__ __forceinline__ void load_token(const BalanceArgs& a, int64_t t, bool live, uint32_t l, gran (&g)[kGran]) {
+// A token's logits lie in a group of lanes, lane l with the granules l, l +
+// kLanes, ...  The last granule of a row whose length is no multiple of one is
+// the row's last 16 bytes, so it overlaps the one before: what it repeats, and
+// all of a lane past the row's end, does not count (`keep` has 0 there).  Rows
+// and granules may begin anywhere.  kTiny: a row shorter than a granule, one
+// lane's, element by element.
+template <class T, int kLanes, int kGran, bool kTiny>
+struct Lane {
     using raw = typename T::raw;
-    const raw* z = static_cast<const raw*>(a.in.z) + (live ? t : 0) * a.in.ld;
-    const int32_t n = live ? (int32_t)a.in.cols : 0;
+    int32_t at[kGran], skip[kGran];  // column of element 0, elements that do not count
+    gran keep[kGran];
+    __device__ __forceinline__ Lane(uint32_t l, int32_t E) {
 #pragma unroll
-    for (int c = 0; c < kGran; ++c) {
-        const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
-        g[c] = no_entries<T>();
-        if (kVec && e0 + T::kN <= n) {
-            g[c] = *reinterpret_cast<const gran*>(z + e0);
-        } else {
+        for (int c = 0; c < kGran; ++c) {
+            const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
+            at[c] = kTiny ? 0 : min(e0, E - T::kN);
+            skip[c] = kTiny ? 0 : min(e0 - at[c], T::kN);
+            keep[c] = gran{0u, 0u, 0u, 0u};
 #pragma unroll
             for (int j = 0; j < T::kN; ++j)
-                if (e0 + j < n) T::set(g[c], j, z[e0 + j]);
+                if (kTiny ? j < E : j >= skip[c]) T::set(keep[c], j, (raw)~raw(0));
         }
     }
+    __device__ __forceinline__ bool has(int c, int j, int32_t E) const { return kTiny ? j < E : j >= skip[c]; }
+    __device__ __forceinline__ void load(const BalanceArgs& a, int32_t t, gran (&g)[kGran]) const {
+        const raw* z = static_cast<const raw*>(a.in.z) + (int64_t)t * a.in.ld;
+        if constexpr (kTiny) {
+#pragma unroll
+            for (int j = 0; j < T::kN; ++j) T::set(g[0], j, z[min(j, (int32_t)a.in.cols - 1)]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kGran; ++c) g[c] = *reinterpret_cast<const loose_gran*>(z + at[c]);
+        }
+    }
+    // -inf where nothing counts; a token that does not count has nothing.
+    __device__ __forceinline__ void settle(bool live, gran (&g)[kGran]) const {
+#pragma unroll
+        for (int c = 0; c < kGran; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t m = live ? keep[c][q] : 0u;
+                g[c][q] = (g[c][q] & m) | (no_entries<T>()[q] & ~m);
+            }
+    }
+};
+
+// Tokens t of a run that a group takes together, their loads all on the way
+// before the first is worked on and under no condition: past the run's end
+// its last token, which then does not count.
+template <int kBatch, class L, int kGran>
+__device__ __forceinline__ void load_batch(const BalanceArgs& a, const Run& r, const L& lane, int32_t t, int32_t step,
+                                           gran (&g)[kBatch][kGran], bool (&live)[kBatch]) {
+    const uint8_t* mask = a.mask ? a.mask : static_cast<const uint8_t*>(a.in.z);  // any byte there is
+    uint8_t m[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        const int32_t at = min(t + i * step, r.t1 - 1);
+        m[i] = mask[a.mask ? at : 0];
+        lane.load(a, at, g[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) live[i] = t + i * step < r.t1 && (!a.mask || m[i] != 0);
 }
 
 // A token's scores, not yet divided by their sum: w[i], and 1 / sum.  A token
@@ -113,81 +155,114 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
     return sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 }
 
-template <class T, int kLanes, int kGran, bool kVec>
-__global__ __launch_bounds__(kBalanceThreads) void k_balance_runs(BalanceArgs a) {
-    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBalanceWaves * kTokens;
-    __shared__ float part[kBalanceWaves][SCAPE_BALANCE_MAX_EXPERTS];
+__device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t E, int32_t k, float alpha) {
+    if (n <= 0) return 0.0f;
+    return (float)((double)alpha * E / ((double)k * n * n) * dot);
+}
+
+// The sums over a run of tokens.  kWhole: a run is a segment, and what is left
+// to do for it is done here.
+template <class T, int kLanes, int kGran, bool kTiny, bool kWhole>
+__global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a) {
+    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kNW = kForwardThreads / 64, kStep = kNW * kTokens;
+    constexpr int kBatch = kGran == 1 ? 8 : kV == 8 ? 4 : 2;
+    __shared__ float part[kNW / 2][SCAPE_BALANCE_MAX_EXPERTS];
     __shared__ int32_t hist[SCAPE_BALANCE_MAX_EXPERTS];
     __shared__ int32_t s_tok;
+    __shared__ double wd[kNW];
     const uint32_t tid = threadIdx.x, lane = lane_id(), wave = tid / 64, l = lane % kLanes;
     const int32_t E = (int32_t)a.in.cols;
-    const Run r = run_of(a, (int32_t)blockIdx.x);
-    if (r.t0 >= r.t1) return;
-    for (int32_t e = (int32_t)tid; e < E; e += kBalanceThreads) hist[e] = 0;
+    Run r;
+    if constexpr (kWhole)
+        r = Run{(int32_t)blockIdx.x, offset_at(a, (int32_t)blockIdx.x), offset_at(a, (int32_t)blockIdx.x + 1)};
+    else
+        r = run_of(a, (int32_t)blockIdx.x);
+    if (r.t0 >= r.t1 && !kWhole) return;
+    for (int32_t e = (int32_t)tid; e < E; e += kForwardThreads) hist[e] = 0;
     if (tid == 0) s_tok = 0;
     __syncthreads();
 
     float acc[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+    const Lane<T, kLanes, kGran, kTiny> mine(l, E);
     uint32_t tokens = 0;
-    // the next token's logits are on their way while this one's are worked on
-    const int32_t mine = (int32_t)(wave * kTokens + lane / kLanes);
-    auto counts = [&](int32_t t) { return t < r.t1 && (!a.mask || a.mask[t] != 0); };
-    bool live = counts(r.t0 + mine);
-    gran g[kGran], next[kGran];
-    load_token<T, kLanes, kGran, kVec>(a, r.t0 + mine, live, l, g);
-    for (int32_t b = r.t0; b < r.t1; b += kStep) {
-        const bool live1 = counts(b + kStep + mine);
-        load_token<T, kLanes, kGran, kVec>(a, b + kStep + mine, live1, l, next);
-        float w[kV], none[kV];
-        const float inv = scores<T, kLanes, kGran, false>(a.score, g, w, none);  // a token that does not count: 0
+    for (int32_t b = r.t0 + (int32_t)(wave * kTokens + lane / kLanes); b < r.t1; b += kStep * kBatch) {
+        gran g[kBatch][kGran];
+        bool live[kBatch];
+        load_batch<kBatch>(a, r, mine, b, kStep, g, live);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] = __builtin_fmaf(w[i], inv, acc[i]);
-        tokens += live && l == 0 ? 1u : 0u;
-        live = live1;
+        for (int i = 0; i < kBatch; ++i) {
+            mine.settle(live[i], g[i]);
+            float w[kV], none[kV];
+            const float inv = scores<T, kLanes, kGran, false>(a.score, g[i], w, none);  // a token that does not count: 0
 #pragma unroll
-        for (int c = 0; c < kGran; ++c) g[c] = next[c];
+            for (int v = 0; v < kV; ++v) acc[v] = __builtin_fmaf(w[v], inv, acc[v]);
+            tokens += live[i] && l == 0 ? 1u : 0u;
+        }
     }
-    // the wave's groups, then the waves
+    const int64_t c0 = (int64_t)r.t0 * a.k;
+    const uint32_t choices = r.t1 > r.t0 ? (uint32_t)((int64_t)(r.t1 - r.t0) * a.k) : 0u;
+    for (uint32_t f0 = tid; f0 < choices; f0 += kForwardThreads * 4) {
+        int32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = a.idx[c0 + min(f0 + i * kForwardThreads, choices - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f = f0 + i * kForwardThreads;
+            if (f < choices && e[i] >= 0 && e[i] < E && (!a.mask || a.mask[r.t0 + (int32_t)(f / (uint32_t)a.k)] != 0))
+                atomicAdd(&hist[e[i]], 1);
+        }
+    }
+    // the wave's groups, then the waves, one half of them onto the other first
 #pragma unroll
     for (int i = 0; i < kV; ++i)
 #pragma unroll
         for (int d = kLanes; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d, 64);
-    if (lane < kLanes) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int32_t e = (int32_t)(l + (i / T::kN) * kLanes) * T::kN + i % T::kN;
-            if (e < E) part[wave][e] = acc[i];
-        }
-    }
     tokens = wave_sum(tokens);
-    if (lane == 0) atomicAdd(&s_tok, (int32_t)tokens);
-    const int64_t c0 = (int64_t)r.t0 * a.k;
-    const uint32_t choices = (uint32_t)((int64_t)(r.t1 - r.t0) * a.k);
-    for (uint32_t f = tid; f < choices; f += kBalanceThreads) {
-        const int32_t e = a.idx[c0 + f];
-        if (e >= 0 && e < E && (!a.mask || a.mask[r.t0 + (int32_t)(f / (uint32_t)a.k)] != 0)) atomicAdd(&hist[e], 1);
-    }
+    if (lane == 0 && tokens) atomicAdd(&s_tok, (int32_t)tokens);
+    auto columns = [&](auto f) {
+        if (lane < kLanes) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (mine.has(i / T::kN, i % T::kN, E)) f(mine.at[i / T::kN] + i % T::kN, acc[i]);
+        }
+    };
+    if (wave >= kNW / 2) columns([&](int32_t e, float x) { part[wave - kNW / 2][e] = x; });
+    __syncthreads();
+    if (wave < kNW / 2) columns([&](int32_t e, float x) { part[wave][e] += x; });
     __syncthreads();
     const int64_t o = (int64_t)blockIdx.x * E;
-    for (int32_t e = (int32_t)tid; e < E; e += kBalanceThreads) {
+    double dot = 0.0;
+    for (int32_t e = (int32_t)tid; e < E; e += kForwardThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kBalanceWaves; ++w) s += part[w][e];
-        a.part_psum[o + e] = s;
-        a.part_counts[o + e] = hist[e];
+        for (int w = 0; w < kNW / 2; ++w) s += part[w][e];
+        if constexpr (kWhole) {
+            a.counts[o + e] = hist[e];
+            a.psum[o + e] = s;
+            dot = (double)hist[e] * (double)s;
+        } else {
+            a.part[o + e] = make_float2(s, __int_as_float(hist[e]));
+        }
     }
-    if (tid == 0) a.part_tok[blockIdx.x] = s_tok;
-}
-
-__device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t E, int32_t k, float alpha) {
-    if (n <= 0) return 0.0f;
-    return (float)((double)alpha * E / ((double)k * n * n) * dot);
+    if constexpr (kWhole) {
+        dot = wave_sum_f64(dot);
+        if (lane == 0) wd[wave] = dot;
+        __syncthreads();
+        if (tid == 0) {
+            a.n_tok[blockIdx.x] = s_tok;
+            double t = 0.0;
+            for (int w = 0; w < kNW; ++w) t += wd[w];
+            if (a.loss) a.loss[blockIdx.x] = balance_loss_of(t, s_tok, E, a.k, a.alpha);
+        }
+    } else if (tid == 0) {
+        a.part_tok[blockIdx.x] = s_tok;
+    }
 }
 
 // One workgroup a segment: the sums over its runs, and the loss.  A column's
-// runs are dealt out over as many threads as there are columns to spare, eight
+// runs are dealt out over as many threads as there are columns to spare, sixteen
 // loads of each in flight, and joined in order.
 constexpr int kFinishThreads = 1024;
 __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a) {
@@ -210,22 +285,19 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a
     double p = 0.0, dot = 0.0;
     int32_t n = 0;
     if (d < deep) {
-        constexpr int kBatch = 8;
+        constexpr int kBatch = 16;
         for (int32_t c0 = d; c0 < runs; c0 += deep * kBatch) {
-            float x[kBatch];
-            int32_t y[kBatch];
+            float2 x[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int32_t c = c0 + i * deep;
-                const int64_t o = (int64_t)(base + (c < runs ? c : c0)) * E + e;
-                x[i] = a.part_psum[o];
-                y[i] = a.part_counts[o];
+                x[i] = a.part[(int64_t)(base + (c < runs ? c : c0)) * E + e];
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 if (c0 + i * deep < runs) {
-                    p += (double)x[i];
-                    n += y[i];
+                    p += (double)x[i].x;
+                    n += __float_as_int(x[i].y);
                 }
         }
     }
@@ -269,95 +341,89 @@ __global__ __launch_bounds__(kBlock) void k_balance_loss(const int32_t* counts, 
     }
 }
 
-template <class T, int kLanes, int kGran, bool kVec>
-__global__ __launch_bounds__(kBalanceThreads) void k_balance_grad(BalanceArgs a) {
+template <class T, int kLanes, int kGran, bool kTiny>
+__global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a) {
     using raw = typename T::raw;
-    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBalanceWaves * kTokens;
+    constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBackwardThreads / 64 * kTokens;
+    constexpr int kBatch = kGran == 1 ? kBackwardBatch : kGran == 2 ? kBackwardBatch / 2 : 1;
     const uint32_t lane = lane_id(), wave = threadIdx.x / 64, l = lane % kLanes;
     const int32_t E = (int32_t)a.in.cols;
     const Run r = run_of(a, (int32_t)blockIdx.x);
     if (r.t0 >= r.t1) return;
+    const Lane<T, kLanes, kGran, kTiny> mine(l, E);
     float c[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const int32_t e = (int32_t)(l + (i / T::kN) * kLanes) * T::kN + i % T::kN;
-        c[i] = e < E ? (float)a.counts[(int64_t)r.seg * E + e] : 0.0f;
+        const int32_t e = min(mine.at[i / T::kN] + i % T::kN, E - 1);
+        c[i] = (float)a.counts[(int64_t)r.seg * E + e];
     }
     const int32_t n = a.n_tok[r.seg];
     const float up = a.dloss ? a.dloss[r.seg] : 1.0f;
     const float G = n > 0 ? (float)((double)up * (double)a.alpha * E / ((double)a.k * n * n)) : 0.0f;
-    const int32_t mine = (int32_t)(wave * kTokens + lane / kLanes);
-    auto counts = [&](int32_t t) { return t < r.t1 && (!a.mask || a.mask[t] != 0); };
-    bool live = counts(r.t0 + mine);
-    gran g[kGran], next[kGran];
-    load_token<T, kLanes, kGran, kVec>(a, r.t0 + mine, live, l, g);
-    for (int32_t b = r.t0; b < r.t1; b += kStep) {
-        const int32_t t = b + mine;
-        const bool live1 = counts(t + kStep);
-        load_token<T, kLanes, kGran, kVec>(a, t + kStep, live1, l, next);
-        float w[kV], grad[kV];
-        const float inv = scores<T, kLanes, kGran, true>(a.score, g, w, grad);
-        float dot = 0.0f;
+    for (int32_t b = r.t0 + (int32_t)(wave * kTokens + lane / kLanes); b < r.t1; b += kStep * kBatch) {
+        gran g[kBatch][kGran];
+        bool live[kBatch];
+        load_batch<kBatch>(a, r, mine, b, kStep, g, live);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) dot = __builtin_fmaf(w[i], c[i], dot);
-        dot = group_reduce<OpSumF, kLanes>(dot) * inv;
-        const float up1 = G * inv;
-        if (t < r.t1) {
-            raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
+        for (int i = 0; i < kBatch; ++i) {
+            const int32_t t = b + i * kStep;
+            mine.settle(live[i], g[i]);
+            float w[kV], grad[kV];
+            const float inv = scores<T, kLanes, kGran, true>(a.score, g[i], w, grad);
+            float dot = 0.0f;
 #pragma unroll
-            for (int q = 0; q < kGran; ++q) {
-                const int32_t e0 = (int32_t)(l + q * kLanes) * T::kN;
-                float v[T::kN];
+            for (int v = 0; v < kV; ++v) dot = __builtin_fmaf(w[v], c[v], dot);
+            dot = group_reduce<OpSumF, kLanes>(dot) * inv;
+            const float up1 = G * inv;
+            if (t < r.t1) {
+                raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
 #pragma unroll
-                for (int j = 0; j < T::kN; ++j) {
-                    const int i = q * T::kN + j;
-                    v[j] = live ? up1 * grad[i] * (c[i] - dot) : 0.0f;
-                }
-                if (kVec && e0 + T::kN <= E) {
-                    *reinterpret_cast<gran*>(dz + e0) = T::down(v);
-                } else {
+                for (int q = 0; q < kGran; ++q) {
+                    float v[T::kN];
 #pragma unroll
-                    for (int j = 0; j < T::kN; ++j)
-                        if (e0 + j < E) dz[e0 + j] = T::down1(v[j]);
+                    for (int j = 0; j < T::kN; ++j) {
+                        const int x = q * T::kN + j;
+                        v[j] = live[i] ? up1 * grad[x] * (c[x] - dot) : 0.0f;
+                    }
+                    if (!kTiny && mine.skip[q] == 0) {
+                        *reinterpret_cast<loose_gran*>(dz + mine.at[q]) = (loose_gran)T::down(v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < T::kN; ++j)
+                            if (mine.has(q, j, E)) dz[mine.at[q] + j] = T::down1(v[j]);
+                    }
                 }
             }
         }
-        live = live1;
-#pragma unroll
-        for (int q = 0; q < kGran; ++q) g[q] = next[q];
     }
 }
 
-template <class T, int kLanes, int kGran, bool kVec>
+template <class T, int kLanes, int kGran, bool kTiny>
 static void runs_or_grad(hipStream_t s, const BalanceArgs& a) {
+    const dim3 grid((uint32_t)a.slots);
     if (a.dz)
-        hipLaunchKernelGGL((k_balance_grad<T, kLanes, kGran, kVec>), dim3((uint32_t)a.slots), dim3(kBalanceThreads), 0,
-                           s, a);
+        hipLaunchKernelGGL((k_balance_grad<T, kLanes, kGran, kTiny>), grid, dim3(kBackwardThreads), 0, s, a);
+    else if (a.whole)
+        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, true>), grid, dim3(kForwardThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kVec>), dim3((uint32_t)a.slots), dim3(kBalanceThreads), 0,
-                           s, a);
-}
-
-template <class T, bool kVec>
-static void balance_lanes(hipStream_t s, const BalanceArgs& a) {
-    const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a token
-    if (g <= 4) runs_or_grad<T, 4, 1, kVec>(s, a);
-    else if (g <= 16) runs_or_grad<T, 16, 1, kVec>(s, a);
-    else if (g <= 32) runs_or_grad<T, 32, 1, kVec>(s, a);
-    else if (g <= 64) runs_or_grad<T, 64, 1, kVec>(s, a);
-    else if (T::kN == 8 || g <= 128) runs_or_grad<T, 64, 2, kVec>(s, a);
-    else if constexpr (T::kN == 4) runs_or_grad<T, 64, 4, kVec>(s, a);
+        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, false>), grid, dim3(kForwardThreads), 0, s, a);
 }
 
 template <class T>
 static hipError_t balance_typed(hipStream_t s, const BalanceArgs& a) {
-    const size_t b = sizeof(typename T::raw);
-    bool vec = (uintptr_t)a.in.z % 16 == 0 && a.in.ld * b % 16 == 0;
-    if (a.dz) vec = vec && (uintptr_t)a.dz % 16 == 0 && a.ld_dz * b % 16 == 0;
-    if (vec)
-        balance_lanes<T, true>(s, a);
-    else
-        balance_lanes<T, false>(s, a);
+    const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a token
+    if (a.in.cols < T::kN) runs_or_grad<T, 1, 1, true>(s, a);
+    else switch (balance_lanes(g)) {
+        case 1: runs_or_grad<T, 1, 1, false>(s, a); break;
+        case 4: runs_or_grad<T, 4, 1, false>(s, a); break;
+        case 8: runs_or_grad<T, 8, 1, false>(s, a); break;
+        case 16: runs_or_grad<T, 16, 1, false>(s, a); break;
+        case 32: runs_or_grad<T, 32, 1, false>(s, a); break;
+        default:
+            if (g <= 64) runs_or_grad<T, 64, 1, false>(s, a);
+            else if (T::kN == 8 || g <= 128) runs_or_grad<T, 64, 2, false>(s, a);
+            else if constexpr (T::kN == 4) runs_or_grad<T, 64, 4, false>(s, a);
+    }
     return hipGetLastError();
 }
 
@@ -370,7 +436,7 @@ static hipError_t balance_any(hipStream_t s, const BalanceArgs& a) {
 hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a) {
     if (a.in.rows > 0) {
         const hipError_t e = balance_any(s, a);
-        if (e != hipSuccess) return e;
+        if (e != hipSuccess || a.whole) return e;
     }
     hipLaunchKernelGGL(k_balance_finish, dim3((uint32_t)a.segments), dim3(kFinishThreads), 0, s, a);
     return hipGetLastError();

@@ -14,6 +14,8 @@
 //  - k_topk_merge: joins the parts of a split row.
 #include <float.h>
 
+#include <type_traits>
+
 #include "loss_device.h"
 
 namespace scape {
@@ -375,8 +377,82 @@ __global__ __launch_bounds__(kMergeThreads) void k_topk_merge(TopkArgs a) {
 // ---------------------------------------------------------------------------
 // Short rows: kLanes lanes a row, kGran granules a lane; lane l holds the
 // granules l, l + kLanes, ...  (vec: rows on 16-byte boundaries; otherwise
-// element by element).  k rounds take the largest key of the group, and of
-// equal keys the lowest column, out of the lane that holds it.
+// element by element).  A lane sorts its entries; in each of k rounds the
+// largest head of the group leaves its lane's list, and lane r keeps the r-th
+// until a whole group's worth is written at once.  What bounds it is the
+// instructions: 65536x64 f32, k = 6, takes LANETIME us (the 17 MB alone 3).
+
+// An entry: value and column as one number, larger for an earlier rank.  A
+// 16-bit value and its column share a word; 0 is no entry.
+template <class T>
+struct Ranked {
+    static constexpr uint32_t kNan = std::is_same<T, BF16>::value ? 0x7FC0u : 0x7E00u;
+    static constexpr uint32_t kKeyNegInf = 0x8000u - (T::kNegInfBits & 0x7FFFu);
+    uint32_t w;
+    static __device__ __forceinline__ Ranked of(const gran& g, int j, uint32_t col) {
+        const uint32_t b = (g[j >> 1] >> (16 * (j & 1))) & 0xFFFFu, mag = b & 0x7FFFu;
+        uint32_t key = (b & 0x8000u) ? 0x8000u - mag : 0x8000u + mag;  // -0 is +0
+        key = mag > (T::kNegInfBits & 0x7FFFu) ? 0xFFFFu : key;
+        return Ranked{(key << 16) | (0xFFFFu - col)};
+    }
+    static __device__ __forceinline__ void order(Ranked& a, Ranked& b) {
+        const uint32_t hi = a.w > b.w ? a.w : b.w;
+        b.w = a.w > b.w ? b.w : a.w;
+        a.w = hi;
+    }
+    template <int kLanes>
+    __device__ __forceinline__ Ranked best() const { return Ranked{group_reduce<OpMaxU, kLanes>(w)}; }
+    __device__ __forceinline__ bool is(const Ranked& o) const { return w == o.w; }
+    __device__ __forceinline__ bool none() const { return (w >> 16) <= kKeyNegInf; }
+    __device__ __forceinline__ typename T::raw value() const {
+        const uint32_t key = w >> 16;
+        if (none()) return (typename T::raw)T::kNegInfBits;
+        return (typename T::raw)(key == 0xFFFFu ? kNan : key >= 0x8000u ? key - 0x8000u : 0x10000u - key);
+    }
+    __device__ __forceinline__ int32_t column() const { return none() ? -1 : (int32_t)(0xFFFFu - (w & 0xFFFFu)); }
+    static __device__ __forceinline__ Ranked empty() { return Ranked{0u}; }
+    __device__ __forceinline__ void take(bool which, const Ranked& o) { w = which ? o.w : w; }
+};
+template <>
+struct Ranked<F32> {
+    uint32_t key, ncol;  // ncol = ~column
+    static __device__ __forceinline__ Ranked of(const gran& g, int j, uint32_t col) {
+        return Ranked{order_key(F32::up(g, j)), ~col};
+    }
+    static __device__ __forceinline__ void order(Ranked& a, Ranked& b) {
+        const bool up = (((uint64_t)b.key << 32) | b.ncol) > (((uint64_t)a.key << 32) | a.ncol);
+        const Ranked x = a;
+        a.take(up, b);
+        b.take(up, x);
+    }
+    template <int kLanes>
+    __device__ __forceinline__ Ranked best() const {
+        const uint32_t top = group_reduce<OpMaxU, kLanes>(key);
+        return Ranked{top, group_reduce<OpMaxU, kLanes>(key == top ? ncol : 0u)};
+    }
+    __device__ __forceinline__ bool is(const Ranked& o) const { return key == o.key && ncol == o.ncol; }
+    __device__ __forceinline__ bool none() const { return key <= kKeyNegInf; }
+    __device__ __forceinline__ uint32_t value() const { return none() ? F32::kNegInfBits : __float_as_uint(key_value(key)); }
+    __device__ __forceinline__ int32_t column() const { return none() ? -1 : (int32_t)~ncol; }
+    static __device__ __forceinline__ Ranked empty() { return Ranked{0u, 0u}; }
+    __device__ __forceinline__ void take(bool which, const Ranked& o) {
+        key = which ? o.key : key;
+        ncol = which ? o.ncol : ncol;
+    }
+};
+
+// Batcher's merge exchange over a lane's kV entries, largest first.
+template <int kV, class E>
+__device__ __forceinline__ void sort_lane(E (&e)[kV]) {
+#pragma unroll
+    for (int p = 1; p < kV; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int i = 0; i + q < kV; ++i)
+                if (i >= q % p && (i - q % p) % (2 * q) < q && i / (2 * p) == (i + q) / (2 * p)) E::order(e[i], e[i + q]);
+}
+
 template <class T, int kLanes, int kGran, bool kVec>
 __global__ __launch_bounds__(kBlock) void k_topk_small(TopkArgs a) {
     using raw = typename T::raw;
@@ -386,58 +462,52 @@ __global__ __launch_bounds__(kBlock) void k_topk_small(TopkArgs a) {
     const bool live = row < a.in.rows;
     const raw* z = static_cast<const raw*>(a.in.z) + (live ? row : 0) * a.in.ld;
     const int32_t n = live ? (int32_t)a.in.cols : 0;
-    uint32_t key[kV];
-    float x[kV];
+    gran g[kGran];
 #pragma unroll
     for (int c = 0; c < kGran; ++c) {
         const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
-        gran g = {0u, 0u, 0u, 0u};
+        g[c] = no_entries<T>();
         if (kVec && e0 + T::kN <= n) {
-            g = *reinterpret_cast<const gran*>(z + e0);
+            g[c] = *reinterpret_cast<const gran*>(z + e0);
         } else {
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) T::set(g, j, e0 + j < n ? z[e0 + j] : (raw)T::kNegInfBits);
-        }
-#pragma unroll
-        for (int j = 0; j < T::kN; ++j) {
-            x[c * T::kN + j] = T::up(g, j);
-            key[c * T::kN + j] = order_key(x[c * T::kN + j]);
+            for (int j = 0; j < T::kN; ++j)
+                if (e0 + j < n) T::set(g[c], j, z[e0 + j]);
         }
     }
     if (a.lse) {
-        float m = x[0];
+        float m = granule_max<T>(g[0]);
 #pragma unroll
-        for (int i = 1; i < kV; ++i) m = fmaxf(m, x[i]);
+        for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(g[c]));
         m = group_reduce<OpMaxF, kLanes>(m);
         const float ref = m == kNegInf ? 0.0f : m * a.c2;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum += fast_exp2(__builtin_fmaf(x[i], a.c2, -ref));
+        for (int i = 0; i < kV; ++i) sum += fast_exp2(__builtin_fmaf(T::up(g[i / T::kN], i % T::kN), a.c2, -ref));
         sum = group_reduce<OpSumF, kLanes>(sum);
-        if (l == 0 && live) a.lse[row] = lse_of(ref, (double)sum);
+        // v_log_f32: the sum is 1 to 1024, so a step of it is less than what the sum is off by
+        if (l == 0 && live) a.lse[row] = (float)(((double)ref + (double)__builtin_amdgcn_logf(sum)) * kLn2);
     }
+    Ranked<T> e[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+        e[i] = Ranked<T>::of(g[i / T::kN], i % T::kN, (l + (uint32_t)(i / T::kN) * kLanes) * T::kN + (uint32_t)(i % T::kN));
+    sort_lane<kV>(e);
+    Ranked<T> kept = Ranked<T>::empty();
     for (int32_t r = 0; r < a.k; ++r) {
-        uint32_t m = key[0];
+        const Ranked<T> top = e[0].template best<kLanes>();
+        const bool mine = e[0].is(top);
 #pragma unroll
-        for (int i = 1; i < kV; ++i) m = key[i] > m ? key[i] : m;
-        const uint32_t top = group_reduce<OpMaxU, kLanes>(m);
-        // the lowest column of those that hold it: granules lie in turn over
-        // the lanes, so by granule first, then by lane
-        uint32_t col = 0xFFFFFFFFu;
-        int slot = 0;
-#pragma unroll
-        for (int i = kV - 1; i >= 0; --i)
-            if (key[i] == top) {
-                col = (l + (uint32_t)(i / T::kN) * kLanes) * T::kN + (uint32_t)(i % T::kN);
-                slot = i;
+        for (int i = 0; i + 1 < kV; ++i) e[i].take(mine, e[i + 1]);
+        e[kV - 1].take(mine, Ranked<T>::empty());
+        const int32_t at = r % kLanes;
+        kept.take((int32_t)l == at, top);
+        if (at == kLanes - 1 || r == a.k - 1) {
+            if (live && (int32_t)l <= at) {
+                const int64_t o = row * a.k + (r - at) + (int32_t)l;
+                static_cast<raw*>(a.val)[o] = kept.value();
+                a.idx[o] = kept.column();
             }
-        const uint32_t first = ~group_reduce<OpMaxU, kLanes>(~col);
-        if (col == first) {
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (i == slot) key[i] = 0;
-            // 0 and -inf: no entry is left
-            if (live) write_entry<T>(a, row, r, top <= kKeyNegInf ? 0ull : ((uint64_t)top << 32) | (uint32_t)~first);
         }
     }
 }
@@ -458,6 +528,7 @@ static hipError_t topk_typed(hipStream_t s, const TopkArgs& a) {
         const bool vec = (uintptr_t)a.in.z % 16 == 0 && a.in.ld * sizeof(typename T::raw) % 16 == 0;
         const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a row
         if (g <= 4) topk_small<T, 4, 1>(s, a, vec);
+        else if (g <= 8) topk_small<T, 8, 1>(s, a, vec);
         else if (g <= 16) topk_small<T, 16, 1>(s, a, vec);
         else if (g <= 64) topk_small<T, 64, 1>(s, a, vec);
         else if (T::kN == 8 || g <= 128) topk_small<T, 64, 2>(s, a, vec);

@@ -56,7 +56,7 @@ constexpr size_t kWorkspaceAlign = 16;
 constexpr int64_t kMaxRowBlocks = (int64_t(1) << 32) / 512 - 1;
 constexpr int64_t kMaxSmallRows = int64_t(1) << 25;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
-constexpr int64_t kMaxSegments = int64_t(1) << 22;
+constexpr int64_t kMaxSegments = int64_t(1) << 21;
 constexpr int64_t kMaxElements = int64_t(1) << 46;  // rows * ld: far beyond memory, far below 2^63
 
 bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -157,16 +157,23 @@ int check_optional(const void* p, const char* name) {
     return SCAPE_OK;
 }
 
-// Tokens of a run: whole steps of a workgroup, and about kRuns runs in all.
-// The forward pass joins its runs in one workgroup a segment, so it takes
-// fewer.
-int32_t balance_run(int64_t tokens, int64_t runs) {
-    constexpr int64_t kStep = 128;
-    int64_t r = (tokens + runs - 1) / runs;
-    r = (r + kStep - 1) / kStep * kStep;
-    return (int32_t)(r < kStep ? kStep : r);
+// Tokens of a run.  The forward pass joins a segment's runs in one workgroup,
+// so it takes about a run for each CU.
+int32_t forward_run(int64_t tokens) {
+    constexpr int64_t kRuns = 256, kStep = 128;
+    const int64_t r = (tokens + kRuns - 1) / kRuns;
+    return (int32_t)(r <= kStep ? kStep : (r + kStep - 1) / kStep * kStep);
 }
-constexpr int64_t kForwardRuns = 512, kBackwardRuns = 2048;
+// The gradient has nothing to join: a run is one batch of a workgroup's groups
+// (2^16 of them at most, then several).
+int32_t backward_run(int32_t dtype, int64_t tokens, int32_t experts) {
+    const int64_t per = 16 / dtype_size(dtype), lanes = balance_lanes((experts + per - 1) / per);
+    const int64_t batch = kBackwardThreads / lanes * kBackwardBatch, n = tokens / (batch << 16) + 1;
+    return (int32_t)(batch * n);
+}
+// Few logits: a workgroup a segment makes its sums and its loss in one launch
+// (WHOLETIME).
+bool whole_segments(int64_t tokens, int32_t experts) { return tokens * experts <= 65536; }
 
 int balance_shape(int32_t dtype, int64_t tokens, int32_t experts, int32_t segments) {
     int rc;
@@ -174,7 +181,7 @@ int balance_shape(int32_t dtype, int64_t tokens, int32_t experts, int32_t segmen
     if (tokens < 0 || tokens > kMaxTokens) return fail(SCAPE_ERR_SHAPE, "tokens must be in 0..2^30");
     if (experts < 1 || experts > SCAPE_BALANCE_MAX_EXPERTS)
         return fail(SCAPE_ERR_SHAPE, "experts must be in 1..%d (got %d)", SCAPE_BALANCE_MAX_EXPERTS, experts);
-    if (segments < 1 || segments > kMaxSegments) return fail(SCAPE_ERR_SHAPE, "segments must be in 1..2^22");
+    if (segments < 1 || segments > kMaxSegments) return fail(SCAPE_ERR_SHAPE, "segments must be in 1..2^21");
     return SCAPE_OK;
 }
 int check_choices(int64_t tokens, int32_t experts, int32_t k) {
@@ -193,7 +200,7 @@ int check_router(int32_t score, const int32_t* offsets, int32_t segments) {
     return check_optional(offsets, "offsets");
 }
 int64_t balance_bytes(int64_t tokens, int32_t experts, int32_t segments) {
-    const int64_t slots = tokens / balance_run(tokens, kForwardRuns) + segments;
+    const int64_t slots = tokens / forward_run(tokens) + segments;
     return slots * (8 * (int64_t)experts + 4);
 }
 
@@ -357,12 +364,12 @@ int scape_balance_forward(const void* logits, int32_t dtype, int64_t tokens, int
     a.psum = psum;
     a.n_tok = n_tok;
     a.loss = loss;
-    a.run = balance_run(tokens, kForwardRuns);
-    a.slots = (int32_t)(tokens / a.run + segments);
-    const int64_t cells = (int64_t)a.slots * experts;
-    a.part_psum = static_cast<float*>(workspace);
-    a.part_counts = static_cast<int32_t*>(workspace) + cells;
-    a.part_tok = static_cast<int32_t*>(workspace) + 2 * cells;
+    a.whole = tokens > 0 && whole_segments(tokens, experts);
+    a.run = forward_run(tokens);
+    a.part = static_cast<float2*>(workspace);
+    const int64_t slots = tokens / a.run + segments;
+    a.part_tok = reinterpret_cast<int32_t*>(a.part + slots * experts);
+    a.slots = (int32_t)(a.whole ? segments : slots);
     const hipError_t e = launch_balance_forward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance loss");
 }
@@ -411,7 +418,7 @@ int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, in
     a.dloss = dloss;
     a.dz = dlogits;
     a.ld_dz = ld_d;
-    a.run = balance_run(tokens, kBackwardRuns);
+    a.run = backward_run(dtype, tokens, experts);
     a.slots = (int32_t)(tokens / a.run + segments);
     const hipError_t e = launch_balance_backward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance gradient");

@@ -94,7 +94,10 @@ hipError_t launch_distill_forward(hipStream_t s, const DistillArgs& a);
 hipError_t launch_distill_backward(hipStream_t s, const DistillArgs& a);
 
 // ---- k_balance.hip
-constexpr int kBalanceThreads = 512;
+constexpr int kForwardThreads = 1024, kBackwardThreads = 256;
+constexpr int kBackwardBatch = 4;  // tokens a group has on their way
+// Lanes that hold a token of g granules (more than 64: several each).
+inline int balance_lanes(int64_t g) { return g <= 1 ? 1 : g <= 4 ? 4 : g <= 8 ? 8 : g <= 16 ? 16 : g <= 32 ? 32 : 64; }
 // The tokens of a segment are cut into runs of `run` tokens, one workgroup
 // each.  Segment s's runs start at slot offsets[s] / run + s: no two segments
 // share a slot, and tokens / run + segments slots hold them all.
@@ -115,8 +118,8 @@ struct BalanceArgs {
     void* dz;
     int64_t ld_dz;
     int32_t run, slots;
-    float* part_psum;      // [slots][experts]
-    int32_t* part_counts;  // [slots][experts]
+    bool whole;            // forward: a workgroup a segment, no runs
+    float2* part;          // [slots][experts]: a run's sum of scores, and its count's bits
     int32_t* part_tok;     // [slots]
 };
 hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a);

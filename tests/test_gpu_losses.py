@@ -548,14 +548,16 @@ def _check_balance(sc, x, idx, mask, edges, dtype, score, pad=0, shift=0, alpha=
     assert counts.cpu().tolist() == [c.tolist() for c in ref["counts"]]
     assert n_tok.cpu().tolist() == ref["n_tok"]
     # a score: the exponent's rounding (|x| <= X), a sum over at most 16 experts a lane and 6 steps, two divisions;
-    # a sum of scores: at most ceil(tokens / 512 / 8) + 128 / 8 of them one after another, a tree of 6 + 3 steps
+    # a sum of scores: a 256th of the tokens by 16 waves, or 65536 logits at once by 16 waves of up to 64 tokens, one
+    # after another, then 6 steps over a wave and 1 + 8 over the waves
     X = float(h.masked_fill(~h.isfinite(), 0).abs().max()) * 2 + 1 if tokens else 1.0
     rel = U * (2 * X + 16 + 6 + 8)
     total = torch.stack(ref["psum"])
-    tol = total * (rel + U * (tokens / 4096 + 16 + 9)) + 1e-37
+    seq = max(tokens / 4096 + 8, 64) + 15
+    tol = total * (rel + U * seq) + 1e-37
     assert bool(((psum.cpu().double() - total).abs() <= tol).all())
     l = torch.tensor(ref["loss"], dtype=torch.float64)
-    ltol = l.abs() * (rel + U * (tokens / 4096 + 26)) + 1e-37
+    ltol = l.abs() * (rel + U * (seq + 1)) + 1e-37
     assert bool(((loss.cpu().double() - l).abs() <= ltol).all())
     assert bool(((again.cpu().double() - l).abs() <= ltol + 2 * U * l.abs()).all())
     d, rd = dz.cpu().double(), ref["dz"]
@@ -571,6 +573,10 @@ def _check_balance(sc, x, idx, mask, edges, dtype, score, pad=0, shift=0, alpha=
     tol = (G[:, None] * p * (c + (p * c).sum(1, keepdim=True))) * (3 * rel + U * 32)
     tol = tol + HALF[dtype] * rd.abs() * 1.001 + TINY[dtype]
     assert bool(((d - rd).abs()[inside] <= tol[inside]).all())
+    over = _place(x, dtype, pad, shift)
+    sc.scape_balance_backward(over, counts, n_tok, up.cuda(), over, k=k, alpha=alpha, offsets=off, mask=m, score=score)
+    torch.cuda.synchronize()
+    assert torch.equal(over.cpu()[inside], dz.cpu()[inside])  # over the logits
     return counts, psum, n_tok, loss, dz
 
 
@@ -580,6 +586,8 @@ def _check_balance(sc, x, idx, mask, edges, dtype, score, pad=0, shift=0, alpha=
     (1, 1, 1, 1, 0, 0), (1, 8, 2, 1, 0, 0), (7, 3, 2, 2, 0, 1), (129, 8, 2, 5, 0, 0), (1000, 60, 4, 3, 0, 0),
     (513, 64, 6, 1, 8, 0), (300, 100, 7, 40, 0, 3), (4097, 128, 8, 9, 0, 0), (700, 256, 16, 2, 0, 0),
     (257, 500, 3, 4, 0, 0), (90, 1024, 8, 2, 0, 0), (70000, 16, 2, 3, 0, 0),
+    (1000, 61, 5, 3, 0, 1), (6000, 61, 5, 3, 3, 0), (30000, 2, 1, 6, 0, 0), (60000, 7, 2, 6, 1, 0), (9000, 9, 4, 7, 0, 0),
+    (65536, 1, 1, 1, 0, 0), (300, 1001, 2, 1, 0, 1),
 ])
 def test_balance(sc, tokens, experts, k, segments, pad, shift, dtype, score):
     x, idx, mask = _router(tokens, experts, k, dtype, score)
