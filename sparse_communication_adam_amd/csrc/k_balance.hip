@@ -15,6 +15,8 @@
 // logits (and the write of the gradient).  Sums over tokens are held in
 // float32 inside a workgroup's run and in float64 across runs, in a fixed
 // order.
+#include <float.h>
+
 #include "loss_device.h"
 
 namespace scape {
@@ -67,12 +69,15 @@ struct Lane {
     using raw = typename T::raw;
     int32_t at[kGran], skip[kGran];  // column of element 0, elements that do not count
     gran keep[kGran];
+    bool whole;  // all of them do
     __device__ __forceinline__ Lane(uint32_t l, int32_t E) {
+        whole = !kTiny;
 #pragma unroll
         for (int c = 0; c < kGran; ++c) {
             const int32_t e0 = (int32_t)(l + c * kLanes) * T::kN;
             at[c] = kTiny ? 0 : min(e0, E - T::kN);
             skip[c] = kTiny ? 0 : min(e0 - at[c], T::kN);
+            whole = whole && skip[c] == 0;
             keep[c] = gran{0u, 0u, 0u, 0u};
 #pragma unroll
             for (int j = 0; j < T::kN; ++j)
@@ -92,6 +97,7 @@ struct Lane {
     }
     // -inf where nothing counts; a token that does not count has nothing.
     __device__ __forceinline__ void settle(bool live, gran (&g)[kGran]) const {
+        if (!wave_ballot(!live || !whole)) return;
 #pragma unroll
         for (int c = 0; c < kGran; ++c)
 #pragma unroll
@@ -147,7 +153,7 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
         for (int i = 0; i < kGran * T::kN; ++i) {
             const float e = fast_exp2(T::up(g[i / T::kN], i % T::kN) * -kLog2e);  // inf for -inf: a score of 0
             w[i] = __builtin_amdgcn_rcpf(1.0f + e);
-            if constexpr (kGrad) grad[i] = e < 1e30f ? w[i] * (e * w[i]) : w[i];
+            if constexpr (kGrad) grad[i] = w[i] * (fminf(e, FLT_MAX) * w[i]);  // 0 for -inf, not inf times 0
             sum += w[i];
         }
     }
@@ -182,6 +188,22 @@ __global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a)
     if (tid == 0) s_tok = 0;
     __syncthreads();
 
+    // the choices, four a thread at a time; the first four are on their way
+    // before the logits are
+    const int64_t c0 = (int64_t)r.t0 * a.k;
+    const uint32_t choices = r.t1 > r.t0 ? (uint32_t)((int64_t)(r.t1 - r.t0) * a.k) : 0u;
+    int32_t chosen[4];
+    uint8_t counted[4];
+    auto load_choices = [&](uint32_t f0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f = min(f0 + i * kForwardThreads, choices - 1);
+            chosen[i] = a.idx[c0 + f];
+            counted[i] = a.mask ? a.mask[r.t0 + (int32_t)(f / (uint32_t)a.k)] : 1;
+        }
+    };
+    if (choices > 0) load_choices(tid);
+
     float acc[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
@@ -201,18 +223,13 @@ __global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a)
             tokens += live[i] && l == 0 ? 1u : 0u;
         }
     }
-    const int64_t c0 = (int64_t)r.t0 * a.k;
-    const uint32_t choices = r.t1 > r.t0 ? (uint32_t)((int64_t)(r.t1 - r.t0) * a.k) : 0u;
-    for (uint32_t f0 = tid; f0 < choices; f0 += kForwardThreads * 4) {
-        int32_t e[4];
+    for (uint32_t f0 = tid; f0 < choices;) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = a.idx[c0 + min(f0 + i * kForwardThreads, choices - 1)];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t f = f0 + i * kForwardThreads;
-            if (f < choices && e[i] >= 0 && e[i] < E && (!a.mask || a.mask[r.t0 + (int32_t)(f / (uint32_t)a.k)] != 0))
-                atomicAdd(&hist[e[i]], 1);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (f0 + i * kForwardThreads < choices && chosen[i] >= 0 && chosen[i] < E && counted[i] != 0)
+                atomicAdd(&hist[chosen[i]], 1);
+        f0 += kForwardThreads * 4;
+        if (f0 < choices) load_choices(f0);
     }
     // the wave's groups, then the waves, one half of them onto the other first
 #pragma unroll
@@ -374,7 +391,7 @@ __global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a
 #pragma unroll
             for (int v = 0; v < kV; ++v) dot = __builtin_fmaf(w[v], c[v], dot);
             dot = group_reduce<OpSumF, kLanes>(dot) * inv;
-            const float up1 = G * inv;
+            const float up1 = live[i] ? G * inv : 0.0f, less = up1 * dot;
             if (t < r.t1) {
                 raw* dz = static_cast<raw*>(a.dz) + (int64_t)t * a.ld_dz;
 #pragma unroll
@@ -383,7 +400,7 @@ __global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a
 #pragma unroll
                     for (int j = 0; j < T::kN; ++j) {
                         const int x = q * T::kN + j;
-                        v[j] = live[i] ? up1 * grad[x] * (c[x] - dot) : 0.0f;
+                        v[j] = grad[x] * __builtin_fmaf(c[x], up1, -less);
                     }
                     if (!kTiny && mine.skip[q] == 0) {
                         *reinterpret_cast<loose_gran*>(dz + mine.at[q]) = (loose_gran)T::down(v);
@@ -412,17 +429,17 @@ static void runs_or_grad(hipStream_t s, const BalanceArgs& a) {
 template <class T>
 static hipError_t balance_typed(hipStream_t s, const BalanceArgs& a) {
     const int64_t g = (a.in.cols + T::kN - 1) / T::kN;  // granules a token
+    constexpr int kTwo = T::kN == 4 ? 2 : 1;  // eight elements a lane, where there are as many
     if (a.in.cols < T::kN) runs_or_grad<T, 1, 1, true>(s, a);
-    else switch (balance_lanes(g)) {
+    else switch (balance_lanes(a.in.dtype, a.in.cols)) {
         case 1: runs_or_grad<T, 1, 1, false>(s, a); break;
         case 4: runs_or_grad<T, 4, 1, false>(s, a); break;
-        case 8: runs_or_grad<T, 8, 1, false>(s, a); break;
-        case 16: runs_or_grad<T, 16, 1, false>(s, a); break;
-        case 32: runs_or_grad<T, 32, 1, false>(s, a); break;
+        case 8: runs_or_grad<T, 8, kTwo, false>(s, a); break;
+        case 16: runs_or_grad<T, 16, kTwo, false>(s, a); break;
+        case 32: runs_or_grad<T, 32, kTwo, false>(s, a); break;
         default:
-            if (g <= 64) runs_or_grad<T, 64, 1, false>(s, a);
-            else if (T::kN == 8 || g <= 128) runs_or_grad<T, 64, 2, false>(s, a);
-            else if constexpr (T::kN == 4) runs_or_grad<T, 64, 4, false>(s, a);
+            if (g <= 64 * kTwo) runs_or_grad<T, 64, kTwo, false>(s, a);
+            else runs_or_grad<T, 64, 2 * kTwo, false>(s, a);
     }
     return hipGetLastError();
 }

@@ -96,8 +96,13 @@ hipError_t launch_distill_backward(hipStream_t s, const DistillArgs& a);
 // ---- k_balance.hip
 constexpr int kForwardThreads = 1024, kBackwardThreads = 256;
 constexpr int kBackwardBatch = 4;  // tokens a group has on their way
-// Lanes that hold a token of g granules (more than 64: several each).
-inline int balance_lanes(int64_t g) { return g <= 1 ? 1 : g <= 4 ? 4 : g <= 8 ? 8 : g <= 16 ? 16 : g <= 32 ? 32 : 64; }
+// Lanes that hold a token: with one granule each for up to four, then with
+// eight elements each, so that a reduction over the lanes serves more of them;
+// 64 may hold 16.
+inline int balance_lanes(int32_t dtype, int64_t experts) {
+    const int64_t n = 16 / dtype_size(dtype), g = (experts + n - 1) / n, e = (experts + 7) / 8;
+    return g <= 1 ? 1 : g <= 4 ? 4 : e <= 8 ? 8 : e <= 16 ? 16 : e <= 32 ? 32 : 64;
+}
 // The tokens of a segment are cut into runs of `run` tokens, one workgroup
 // each.  Segment s's runs start at slot offsets[s] / run + s: no two segments
 // share a slot, and tokens / run + segments slots hold them all.
