@@ -450,7 +450,8 @@ int scape_profile_read(scape_ctx* ctx, double* ms, int64_t* steps);
  * that lie `ld` >= cols elements apart.  A matrix needs no more than its
  * element's alignment; rows on 16-byte boundaries, and a gradient with the
  * logits' own alignment, are read and written fastest.  Sums are held in fp32
- * or more, and each output is rounded once, to its own type.
+ * or more, and each output is rounded once, to its own type.  A scaled logit,
+ * scale * z, has to be in fp32's range; a mask of the type's lowest value is.
  */
 #define SCAPE_DTYPE_F32 0
 #define SCAPE_DTYPE_BF16 1
@@ -472,7 +473,7 @@ int scape_profile_read(scape_ctx* ctx, double* ms, int64_t* steps);
  *   counts as larger than every number (val is then NaN).  lse is -inf for a
  *   row of -inf, and NaN where the row holds NaN or +inf.
  * 1 <= k <= min(cols, SCAPE_TOPK_MAX_K); scale > 0; rows = 0 enqueues nothing.
- * The workspace is 0 bytes unless few or long rows are split.
+ * The workspace is 0 bytes unless a row is too long for one workgroup.
  * Errors: INVALID_ARG, ALIGN, SHAPE (limits, ld < cols, workspace too small),
  * HIP.
  */
@@ -507,11 +508,11 @@ typedef struct scape_teacher {
  *   dz            = d(sum of loss)/dz, where dz is not NULL: the gradient of
  *     this call's own loss, in the same pass, for a program whose weights
  *     already hold every factor (1/tokens, loss scale).
- * A row with weight 0, or without entries, is not read: loss, stats and
- * gradient are 0.  So are loss and gradient of a row whose logits are all
+ * A row with weight 0, or without entries, does not count, whatever it holds:
+ * loss, stats and gradient are 0.  So are loss and gradient of a row whose logits are all
  * -inf.  Where the student holds nothing outside the entries the q_T term is
  * left out.  An entry with q_j > 0 at a column of -inf makes the loss +inf.  A
- * row that is read and holds NaN or +inf gives NaN.
+ * row that counts and holds NaN or +inf gives NaN.
  * Arguments: z as above, read only; loss fp32 [rows]; stats fp32 [2*rows],
  * needed also where no backward call follows; dz of z's type, rows ld_dz >=
  * cols elements apart, columns past cols untouched, may be z itself (then
@@ -526,7 +527,9 @@ int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k
 
 /* The gradient alone, from the statistics of a forward call on the same z,
  * teacher and scale: dz = dloss[r] * weight[r] * dKL/dz (either NULL: 1).  A
- * row whose factor is 0 is not read and gets 0.  Needs no workspace.
+ * row whose factor is 0 gets 0, whatever it holds.  p is good to the rounding
+ * of the statistics, 2^-24 |stats[2r]|, where the forward call's own gradient
+ * depends on differences of logits only.  Needs no workspace.
  * Errors: as scape_topk_rows. */
 int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                            const scape_teacher* teacher, float scale, const float* weight, const float* stats,

@@ -139,12 +139,10 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
 #pragma unroll
         for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(g[c]));
         m = group_reduce<OpMaxF, kLanes>(m);
-        // the reference is a float that all exponents are taken against
-        // exactly, and it cancels in the division
-        const float ref = m == kNegInf ? 0.0f : m * kLog2e;
+        const float ref = m == kNegInf ? 0.0f : m;
 #pragma unroll
         for (int i = 0; i < kGran * T::kN; ++i) {
-            w[i] = fast_exp2(__builtin_fmaf(T::up(g[i / T::kN], i % T::kN), kLog2e, -ref));
+            w[i] = fast_exp2((T::up(g[i / T::kN], i % T::kN) - ref) * kLog2e);
             if constexpr (kGrad) grad[i] = w[i];
             sum += w[i];
         }

@@ -167,22 +167,22 @@ __device__ __forceinline__ bool mark_entries(const DistillArgs& a, int64_t row, 
     return seen != 0;
 }
 
-// s t_j, minus the teacher's lse where it is given.
-__device__ __forceinline__ double log_q(const DistillArgs& a, double lse, float t) {
-    return t == kNegInf ? (double)t : (double)t * (double)a.scale - lse;
+// log q_j: s t_j minus the teacher's lse where it is given, else against mq.
+__device__ __forceinline__ double log_q(const DistillArgs& a, double lse, float t, float mq) {
+    if (t == kNegInf) return (double)t;
+    return a.t_lse ? (double)t * (double)a.scale - lse : ((double)t - (double)mq) * (double)a.scale;
 }
 
 // A wave's entries summed, against the wave's own references; the row's are
 // put together in finish_row.
 struct WaveSums {
-    double top;  // sum 2^(x_j - mt)
-    double q;    // sum q_j, q_j = exp(lq_j), lq_j the teacher's log-probability less mq
+    double top;  // sum 2^(c2 (x_j - mt))
+    double q;    // sum q_j, q_j = exp(lq_j), lq_j the teacher's log-probability (against mq)
     double qt;   // sum q_j lq_j
-    double qx;   // sum q_j x_j
+    double qx;   // sum q_j c2 (x_j - mt)
     float mt;    // the largest x_j
-    float mq;    // 0 where the teacher's lse is given, else the largest s t_j
+    float mq;    // 0 where the teacher's lse is given, else the largest t_j
 };
-constexpr float kLowest = -3.402823466e38f;
 
 // kStudent: also the student's terms.  Slots' t and z become q and p, for the
 // gradient, in float32: each is rounded once more, a step of a float32
@@ -195,19 +195,19 @@ __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse,
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
         if (l.col[slot] >= 0) {
             some = true;
-            if (kStudent) s.mt = fmaxf(s.mt, l.z[slot] * a.c2);
-            if (!a.t_lse) s.mq = fmaxf(s.mq, l.t[slot] * a.scale);
+            if (kStudent) s.mt = fmaxf(s.mt, l.z[slot]);
+            if (!a.t_lse) s.mq = fmaxf(s.mq, l.t[slot]);
         }
     if (wave_ballot(some) == 0) return s;
     if (kStudent) s.mt = group_reduce<OpMaxNum, 64>(s.mt);
     if (!a.t_lse) s.mq = group_reduce<OpMaxNum, 64>(s.mq);
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
         if (l.col[slot] >= 0) {
-            const double lq = log_q(a, lse, l.t[slot]) - (double)s.mq, q = exp(lq);
+            const double lq = log_q(a, lse, l.t[slot], s.mq), q = exp(lq);
             l.t[slot] = (float)q;
             s.q += q;
             if (kStudent) {
-                const double x = (double)l.z[slot] * (double)a.c2, p = exp2(x - (double)s.mt);
+                const double x = ((double)l.z[slot] - (double)s.mt) * (double)a.c2, p = exp2(x);
                 l.z[slot] = (float)p;
                 s.top += p;
                 if (q != 0.0) {
@@ -229,7 +229,8 @@ __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse,
 struct RowResult {
     float loss;          // KL
     float stat0, stat1;  // L, log p_T
-    float vref, tail;    // the tail's gradient is tail 2^(x_v - vref)
+    float2 anchor;       // L = scale * x + y
+    float vref, tail;    // the tail's gradient is tail 2^(c2 (x_v - vref))
     double p, q;         // an entry's gradient is p p_j - q q_j, for the entries of this lane's wave (lane % kWaves)
     bool dead;           // no student mass at all: nothing to learn
 };
@@ -241,19 +242,19 @@ template <int kWaves>
 __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const RunningSum& tail, const WaveSums& w) {
     RowResult r;
     const uint32_t lane = lane_id();
-    const double t = (double)tail.sum, tref = (double)tail.ref;
+    const double t = (double)tail.sum, tref = (double)tail.ref, c2 = (double)a.c2;
     const bool has_tail = !(t == 0.0);
     const double ref = fmax(has_tail ? tref : (double)kLowest, (double)group_reduce<OpMaxNum, kWaves>(w.mt));
-    const double dq = a.t_lse ? 0.0 : (double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq);
+    const double dq = a.t_lse ? 0.0 : ((double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq)) * (double)a.scale;
     // lanes 0..: the waves' references against the row's; 16..: the teacher's
     // likewise; 32: the tail's (0 too where the tail is out of range)
-    const double powers = exp2(lane < 16 ? (double)w.mt - ref : lane < 32 ? dq * kLog2e64 : tref - ref);
+    const double powers = exp2(lane < 16 ? ((double)w.mt - ref) * c2 : lane < 32 ? dq * kLog2e64 : (tref - ref) * c2);
     const double fp = from_lane_of<kWaves>(powers, 0), fq = from_lane_of<kWaves>(powers, 16);
     const double far = has_tail ? from_lane(powers, 32) : 0.0;
     const double top = sum_waves_f64<kWaves>(w.top * fp);
     const double q = sum_waves_f64<kWaves>(w.q * fq);
     const double qt = sum_waves_f64<kWaves>((w.qt + (w.q != 0.0 ? w.q * dq : 0.0)) * fq);
-    const double qx = sum_waves_f64<kWaves>(w.qx * fq);
+    const double qx = sum_waves_f64<kWaves>((w.qx + (w.q != 0.0 ? w.q * (((double)w.mt - ref) * c2) : 0.0)) * fq);
     const double sum = t * far + top;
     double qsum, rest = 0.0;
     if (a.t_lse) {
@@ -268,16 +269,17 @@ __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const Runn
                  log_rest = from_lane(logs, 3);
     const double inv = from_lane(inverses, 0);
     const double qnorm = qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : from_lane(inverses, 2);
-    const double lpt = has_tail ? log_t + (tref - ref) * kLn2 - log_sum : -__builtin_inf();
-    const double lse = ref * kLn2 + log_sum;
+    const double lpt = has_tail ? log_t + (tref - ref) * (c2 * kLn2) - log_sum : -__builtin_inf();
+    const double lse = ref * (double)a.scale + log_sum;
     double kl = 0.0;
     if (qsum != 0.0) {
-        kl = (qt - qx * kLn2) * qnorm + qsum * lse;
+        kl = (qt - qx * kLn2) * qnorm + qsum * log_sum;  // against ref, which cancels
         if (!a.t_lse) kl -= log_q;
     }
     if (rest > 0.0) kl += rest * (log_rest - lpt);
     r.loss = (float)kl;
     r.stat0 = (float)lse;
+    r.anchor = make_float2((float)ref, (float)log_sum);  // ref is a logit
     r.stat1 = (float)lpt;
     r.vref = tail.ref;
     // (Q - q_T / p_T) p_v with q_T / p_T = q_T + q_T top / (t far)
@@ -292,6 +294,7 @@ __device__ __forceinline__ void write_row(const DistillArgs& a, int64_t row, flo
     a.loss[row] = r.dead ? 0.0f : w * r.loss;
     a.stats[2 * row] = r.stat0;
     a.stats[2 * row + 1] = r.stat1;
+    if (a.anchor) a.anchor[row] = r.anchor;
 }
 __device__ __forceinline__ void write_no_row(const DistillArgs& a, int64_t row) {
     a.loss[row] = 0.0f;
@@ -439,7 +442,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_distill_loss(DistillArgs a) {
         p.template trim<kThreads>(base, x);
         take(base, x);
     });
-    wave_join(rs);
+    wave_join(rs, a.c2);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     if constexpr (!kPart) {
         take_logits<T, kThreads>(a, p, z0, l);
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_distill_loss(DistillArgs a) {
     __syncthreads();
     if (wave == 0) {
         RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
-        join_waves<kNW>(r);
+        join_waves<kNW>(r, a.c2);
         if constexpr (kPart) {
             if (tid == 0) a.part[p.row * a.splits + p.sp] = make_float2(r.ref, r.sum);
         } else {
@@ -518,7 +521,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
             for (int b = 1; b < 4; ++b) m = max_nan(m, granule_max<T>(g[c][b]));
             rs.template add<T, 4>(g[c], m, a.c2);
         }
-    wave_join(rs);
+    wave_join(rs, a.c2);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     {
         take_logits<T, kThreads>(a, p, z0, l);
@@ -528,7 +531,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
     __syncthreads();
     if (wave == 0) {
         RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
-        join_waves<kNW>(r);
+        join_waves<kNW>(r, a.c2);
         const RowResult res = finish_row<kNW>(a, r, wrec[tid & (kNW - 1)]);
         if (tid < kNW) {
             s_p[tid] = res.p;
@@ -553,11 +556,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
         if (i < p.cnt) {
             float d[T::kN];
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2(__builtin_fmaf(T::up(x, j), a.c2, -vref));
+            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2((T::up(x, j) - vref) * a.c2);
             store_loose(dz + p.first, i, T::down(d));
         }
     }
-    if (p.lone >= 0) dz[p.lone] = T::down1(f * fast_exp2(__builtin_fmaf(lx, a.c2, -vref)));
+    if (p.lone >= 0) dz[p.lone] = T::down1(f * fast_exp2((lx - vref) * a.c2));
     __syncthreads();  // the entries' columns are written over what is there
     write_entries(a, p, l, s_gs, s_p[wave], s_q[wave], dz);
 }
@@ -580,6 +583,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
     const float up = a.dloss ? a.dloss[p.row] : 1.0f;
     const double t_lse = a.t_lse ? (double)a.t_lse[p.row] : 0.0;
     const float lse = a.stats[2 * p.row], lpt = a.stats[2 * p.row + 1];
+    const float2 at = a.anchor ? a.anchor[p.row] : make_float2(0.0f, lse);  // L = scale * at.x + at.y
     const Slot s0 = read_slot(a, p.row, tid);
     gran g[4];
     p.template load<kThreads>(0, g);
@@ -604,18 +608,18 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
     __syncthreads();
     if (wave == 0) {
         const WaveSums r = wrec[tid & (kNW - 1)];
-        const double fq = a.t_lse ? 1.0 : exp((double)r.mq - (double)group_reduce<OpMaxNum, kNW>(r.mq));
+        const double fq = a.t_lse ? 1.0 : exp(((double)r.mq - (double)group_reduce<OpMaxNum, kNW>(r.mq)) * (double)a.scale);
         const double q = sum_waves_f64<kNW>(r.q * fq);
         const double qsum = a.t_lse ? q : q == 0.0 ? 0.0 : 1.0;
         const double rest = a.t_lse && 1.0 - q > 0.0 && lpt != kNegInf ? 1.0 - q : 0.0;
         // (Q - q_T / p_T) p_v, against L, or where 1 / p_T could leave the
         // range against the tail's own log-sum-exp
-        float v = lse, tail = (float)qsum;
+        float v = at.y, tail = (float)qsum;
         if (rest > 0.0) {
             const double pt = exp((double)lpt), c = qsum * pt + rest * (pt - 1.0);
             const bool near = lpt > -30.0f;
             tail = (float)(near ? c / pt : c);
-            if (!near) v = (float)((double)lse + (double)lpt);
+            if (!near) v = (float)((double)at.y + (double)lpt);
         }
         if (tid < kNW) s_q[tid] = fq * (qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q);
         if (tid == 0) {
@@ -628,13 +632,8 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
     }
     __syncthreads();
     const float f = s_tail, vref = s_vref;
-    // A float32 gradient takes the difference from L first: it would see the
-    // rounding of L log2(e), which a 16-bit one does not.
-    const float vref2 = vref * kLog2e;
-    auto grad = [&](float x) {
-        const float e = T::kN == 4 ? __builtin_fmaf(x, a.scale, -vref) * kLog2e : __builtin_fmaf(x, a.c2, -vref2);
-        return f * fast_exp2(e);
-    };
+    // the difference from L first: neither rounds L log2(e) nor leaves the range
+    auto grad = [&](float x) { return f * fast_exp2(__builtin_fmaf(x - at.x, a.scale, -vref) * kLog2e); };
     auto write = [&](int32_t i, const gran& x) {
         float d[T::kN];
 #pragma unroll
@@ -655,7 +654,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
     if (p.lone >= 0) dz[p.lone] = T::down1(grad(lx));
     if (tid < a.k) l.z[tid] = z0;
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
-        l.z[slot] = (float)exp((double)l.z[slot] * (double)a.scale - (double)lse);
+        l.z[slot] = (float)exp(((double)l.z[slot] - (double)at.x) * (double)a.scale - (double)at.y);
     __syncthreads();  // the entries' columns are written over the tail's values
     write_entries(a, p, l, s_gs, s_p, s_q[wave], dz);
 }
@@ -691,7 +690,7 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_join(DistillArgs a) {
     if ((tid & 63) == 0) wrec[wave] = ws;
     __syncthreads();
     if (wave == 0) {
-        wave_join(r);
+        wave_join(r, a.c2);
         const RowResult res = finish_row<kNW>(a, r, wrec[tid & (kNW - 1)]);
         if (tid == 0) write_row(a, row, w, res);
     }

@@ -42,10 +42,10 @@ __device__ __forceinline__ void write_entry(const TopkArgs& a, int64_t row, int3
     a.idx[o] = none ? -1 : (int32_t)~(uint32_t)comp;
 }
 
-// log-sum-exp from sum = sum 2^(x - ref) in the base-2 domain.  The
-// reference is a float that the exponents were taken against exactly, so it
-// adds no error; only the last step rounds.
-__device__ __forceinline__ float lse_of(float ref, double sum) { return (float)(((double)ref + log2(sum)) * kLn2); }
+// log-sum-exp from sum = sum 2^(c2 (x - ref)); only the last step rounds.
+__device__ __forceinline__ float lse_of(const TopkArgs& a, float ref, double sum) {
+    return (float)((double)ref * a.scale + kLn2 * log2(sum));
+}
 
 // ---------------------------------------------------------------------------
 // Long rows
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_topk_rows(TopkArgs a) {
     m0 = max_nan(m0, lx);
     gmax[tid] = order_key(m0) >> 16;
     gmax[tid + kThreads] = order_key(m1) >> 16;
-    wave_join(rs);
+    wave_join(rs, a.c2);
     if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
     __syncthreads();
 
@@ -190,12 +190,12 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_topk_rows(TopkArgs a) {
         if (tid == 0) s_tau = t;
     } else if (wave == kNW - 1) {
         RunningSum r{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
-        join_waves<kNW>(r);
+        join_waves<kNW>(r, a.c2);
         if (tid == kThreads - 1) {
             if (a.splits > 1)
                 a.part[row * a.splits + sp] = make_float2(r.ref, r.sum);
             else if (a.lse)
-                a.lse[row] = lse_of(r.ref, (double)r.sum);
+                a.lse[row] = lse_of(a, r.ref, (double)r.sum);
         }
     }
     __syncthreads();
@@ -343,8 +343,8 @@ __global__ __launch_bounds__(kMergeThreads) void k_topk_merge(TopkArgs a) {
             const float2 p = a.part[row * a.splits + (tid - 64)];
             r = RunningSum{p.x, p.y};
         }
-        wave_join(r);
-        if (tid == 64) a.lse[row] = lse_of(r.ref, (double)r.sum);
+        wave_join(r, a.c2);
+        if (tid == 64) a.lse[row] = lse_of(a, r.ref, (double)r.sum);
     }
     __syncthreads();
     const uint64_t low = s_low;
@@ -491,13 +491,13 @@ __global__ __launch_bounds__(kBlock) void k_topk_small(TopkArgs a) {
 #pragma unroll
         for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(g[c]));
         m = group_reduce<OpMaxF, kLanes>(m);
-        const float ref = m == kNegInf ? 0.0f : m * a.c2;
+        const float ref = m == kNegInf ? 0.0f : m;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum += fast_exp2(__builtin_fmaf(T::up(g[i / T::kN], i % T::kN), a.c2, -ref));
+        for (int i = 0; i < kV; ++i) sum += fast_exp2((T::up(g[i / T::kN], i % T::kN) - ref) * a.c2);
         sum = group_reduce<OpSumF, kLanes>(sum);
         // v_log_f32: the sum is 1 to 1024, so a step of it is less than what the sum is off by
-        if (l == 0 && live) a.lse[row] = (float)(((double)ref + (double)__builtin_amdgcn_logf(sum)) * kLn2);
+        if (l == 0 && live) a.lse[row] = (float)((double)ref * a.scale + kLn2 * (double)__builtin_amdgcn_logf(sum));
     }
     Ranked<T> e[kV];
 #pragma unroll

@@ -93,8 +93,10 @@ int check_workspace(const void* ws, int64_t have, int64_t need) {
     return SCAPE_OK;
 }
 
+float base2(float scale) { return (float)((double)scale * 1.44269504088896340736); }
+
 int check_scale(float scale) {
-    if (!(scale > 0.0f) || !std::isfinite(scale))
+    if (!(scale > 0.0f) || !std::isfinite(base2(scale)))
         return fail(SCAPE_ERR_INVALID_ARG, "scale must be positive and finite");
     return SCAPE_OK;
 }
@@ -112,7 +114,6 @@ int check_blocks(int64_t rows, const RowSplit& sp) {
     return SCAPE_OK;
 }
 
-float base2(float scale) { return (float)((double)scale * 1.44269504088896340736); }
 
 int topk_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit* sp) {
     int rc;
@@ -139,7 +140,11 @@ int distill_shape(int32_t dtype, int64_t rows, int64_t cols, int32_t k, RowSplit
     *sp = split(dtype, rows, cols);
     return check_blocks(rows, *sp);
 }
-int64_t distill_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }
+// The parts' sums, and the anchors where the gradient is a launch of its own.
+int64_t parts_bytes(int64_t rows, const RowSplit& sp) { return sp.splits > 1 ? rows * sp.splits * 8 : 0; }
+int64_t distill_bytes(int64_t rows, const RowSplit& sp, bool grad) {
+    return parts_bytes(rows, sp) + (grad && (sp.splits > 1 || sp.per > kFusedCapacity) ? rows * 8 : 0);
+}
 
 int check_teacher(const scape_teacher* t, int64_t rows) {
     if (!t) return fail(SCAPE_ERR_INVALID_ARG, "teacher is NULL");
@@ -231,6 +236,7 @@ int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, in
     TopkArgs a{};
     a.in = Logits{z, dtype, rows, cols, ld};
     a.k = k;
+    a.scale = scale;
     a.c2 = base2(scale);
     a.val = val;
     a.idx = idx;
@@ -247,7 +253,7 @@ int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k
     if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
     RowSplit sp;
     if (int rc = distill_shape(dtype, rows, cols, k, distill_split, &sp)) return rc;
-    *bytes = distill_bytes(rows, sp);
+    *bytes = distill_bytes(rows, sp, true);
     return SCAPE_OK;
 }
 
@@ -266,7 +272,7 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     if ((rc = check_optional(weight, "weight"))) return rc;
     if ((rc = check_array(loss, 4, "loss"))) return rc;
     if ((rc = check_array(stats, 4, "stats"))) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, distill_bytes(rows, sp)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, distill_bytes(rows, sp, dz != nullptr)))) return rc;
     DistillArgs a{};
     a.in = Logits{z, dtype, rows, cols, ld};
     a.t_val = teacher->val;
@@ -285,6 +291,7 @@ int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t co
     a.splits = sp.splits;
     a.per = sp.per;
     if (dz) {
+        if (distill_bytes(rows, sp, true) > parts_bytes(rows, sp)) a.anchor = a.part + parts_bytes(rows, sp) / 8;
         if ((rc = distill_shape(dtype, rows, cols, teacher->k, distill_grad_split, &sp))) return rc;
         a.grad_splits = sp.splits;
         a.grad_per = sp.per;

@@ -160,31 +160,34 @@ __device__ __forceinline__ float granule_max(const gran& g) {
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
 
-// A running sum of 2^(c2 x) held as sum * 2^ref, ref the largest c2 x so far
-// (as a float that the exponents are then taken against exactly, so it adds
-// no error).  It follows the loads as they arrive: no pass for the maximum
-// first.  -inf adds nothing; NaN and +inf make the sum NaN.
+// A running sum of 2^(c2 (x - ref)), ref the largest x so far.  The difference
+// is taken before the product: a product's rounding against a reference that
+// was rounded as well is off by as much as the logits are large, and a row of
+// the type's lowest value would leave the range.  It follows the loads as they
+// arrive: no pass for the maximum first.  -inf adds nothing; NaN and +inf make
+// the sum NaN.
+constexpr float kLowest = -3.402823466e38f;
 struct RunningSum {
     float ref, sum;
-    static __device__ __forceinline__ RunningSum none() { return RunningSum{-3.402823466e38f, 0.0f}; }
+    static __device__ __forceinline__ RunningSum none() { return RunningSum{kLowest, 0.0f}; }
     // B granules whose largest element is m
     template <class T, int B>
     __device__ __forceinline__ void add(const gran (&g)[B], float m, float c2) {
-        const float r = fmaxf(ref, m * c2);
-        float s0 = sum * fast_exp2(ref - r), s1 = 0.0f;  // two chains, for the adders
+        const float r = fmaxf(ref, m);
+        float s0 = sum * fast_exp2((ref - r) * c2), s1 = 0.0f;  // two chains, for the adders
         ref = r;
 #pragma unroll
         for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int j = 0; j < T::kN; j += 2) {
-                s0 += fast_exp2(__builtin_fmaf(T::up(g[b], j), c2, -r));
-                s1 += fast_exp2(__builtin_fmaf(T::up(g[b], j + 1), c2, -r));
+                s0 += fast_exp2((T::up(g[b], j) - r) * c2);
+                s1 += fast_exp2((T::up(g[b], j + 1) - r) * c2);
             }
         sum = s0 + s1;
     }
     __device__ __forceinline__ void add1(float x, float c2) {
-        const float r = fmaxf(ref, x * c2);
-        sum = sum * fast_exp2(ref - r) + fast_exp2(__builtin_fmaf(x, c2, -r));
+        const float r = fmaxf(ref, x);
+        sum = sum * fast_exp2((ref - r) * c2) + fast_exp2((x - r) * c2);
         ref = r;
     }
 };
@@ -290,16 +293,16 @@ __device__ __forceinline__ double from_lane_of(double x, int base) {
 }
 
 // Joins the lanes' running sums: every lane gets the wave's.
-__device__ __forceinline__ void wave_join(RunningSum& r) {
+__device__ __forceinline__ void wave_join(RunningSum& r, float c2) {
     const float ref = group_reduce<OpMaxNum, 64>(r.ref);
-    r.sum = group_reduce<OpSumF, 64>(r.sum * fast_exp2(r.ref - ref));
+    r.sum = group_reduce<OpSumF, 64>(r.sum * fast_exp2((r.ref - ref) * c2));
     r.ref = ref;
 }
 // Joins the waves' sums, that of wave w in the lanes w, w + kWaves, ...
 template <int kWaves>
-__device__ __forceinline__ void join_waves(RunningSum& r) {
+__device__ __forceinline__ void join_waves(RunningSum& r, float c2) {
     const float ref = group_reduce<OpMaxNum, kWaves>(r.ref);
-    r.sum = group_reduce<OpSumF, kWaves>(r.sum * fast_exp2(r.ref - ref));
+    r.sum = group_reduce<OpSumF, kWaves>(r.sum * fast_exp2((r.ref - ref) * c2));
     r.ref = ref;
 }
 

@@ -61,7 +61,7 @@ inline bool topk_small(int64_t cols, int32_t k) { return cols <= kTopkSmallCols 
 struct TopkArgs {
     Logits in;
     int32_t k;
-    float c2;  // scale * log2(e)
+    float scale, c2;  // c2 = scale * log2(e)
     void* val;
     int32_t* idx;
     float* lse;       // or NULL
@@ -87,6 +87,8 @@ struct DistillArgs {
     void* dz;            // or NULL
     int64_t ld_dz;
     float2* part;        // splits > 1: [rows][splits] (reference, sum)
+    float2* anchor;      // [rows] the row's L as scale * x + y: for the gradient of the same call, which then
+                         // depends on differences of logits only; NULL: from stats
     int32_t splits, per;
     int32_t grad_splits, grad_per;  // of k_distill_grad
 };

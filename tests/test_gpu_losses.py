@@ -113,7 +113,7 @@ def test_topk(sc, dtype, rows, cols, k, pad, shift):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("cols,k", [(64, 8), (1000, 32), (3000 + 1, 50), (20000, 1000), (60000, 64)])
-@pytest.mark.parametrize("kind", ["constant", "three values", "few left", "all masked", "specials", "zeros"])
+@pytest.mark.parametrize("kind", ["constant", "three values", "few left", "all masked", "specials", "zeros", "lowest"])
 def test_topk_ties_and_specials(sc, dtype, cols, k, kind):
     rows = 3
     g = _rng("ties", dtype, cols, kind)
@@ -133,6 +133,10 @@ def test_topk_ties_and_specials(sc, dtype, cols, k, kind):
         x[1, torch.randperm(cols, generator=g)[:3]] = INF
         x[1, torch.randperm(cols, generator=g)[:3]] = -INF
         x[2, 5], x[2, 7] = INF, NAN
+    elif kind == "lowest":  # a mask of the type's lowest value
+        x = torch.full((rows, cols), torch.finfo(dtype).min)
+        x[1, ::3] = torch.randn(len(range(0, cols, 3)), generator=g)
+        x[2] = 2.0 ** 15 if dtype == torch.float16 else 2.0 ** 127
     else:
         x = torch.where(torch.rand(rows, cols, generator=g) < 0.5, 0.0, -0.0)
     _check_topk(sc, _place(x, dtype, 0, 1), k)
@@ -350,6 +354,47 @@ def test_distill_nan_stays_in_its_row(sc, rows, cols):
     loss, stats, dz = c.call(sc)
     assert bool(loss[0].isnan()) and bool(dz[0].isnan().all())
     assert not bool(loss[1:].isnan().any()) and not bool(dz[1:].isnan().any())
+
+
+@pytest.mark.parametrize("tail", [True, False], ids=["tail", "renormalised"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,cols", [(600, 2000), (3, 50304), (3, 262144)],
+                         ids=["whole rows", "few rows", "split rows"])
+def test_distill_lowest_values(sc, rows, cols, dtype, tail):
+    """Logits masked with the type's lowest value: a row of nothing else is a
+    uniform one, and one with other logits left has no mass under the mask.
+    The uniform row is the same as a row of zeros, bit for bit: only
+    differences of its logits enter the loss and the forward gradient."""
+    c = Case(rows, cols, 9, dtype, tail, key="lowest")
+    low = torch.finfo(dtype).min
+    c.x[0] = low
+    c.x[1, 50:] = low
+    c.x[1, c.idx[1, :4].long()] = low                          # entries under the mask, without teacher's mass
+    c.val[1, :4] = -INF
+    c.x[1, c.idx[1, 4:].long()] = 1.0
+    c.x[2, :cols - 1] = low                                     # two logits left
+    c.x[2, c.idx[2, 0].long()] = 0.0
+    c.val[2, 1:] = -INF
+    if tail:
+        c.lse[2] = c.val[2, 0]
+    c.put()
+    loss, stats, dz = c.call(sc)
+    assert bool(loss[:3].isfinite().all()) and bool(dz[:3].isfinite().all()) and bool(stats[:3, 0].isfinite().all())
+    shown = [r for r in range(min(rows, 9)) if r != 0]
+    w = c.weight.double()
+    rl, _, rd = c.reference(w)
+    rel = (max(128, 32 + cols // 256) + 9 + 2 + 6) * U + 6 * U * 40  # the masked terms are 0, the others within 20
+    for r in shown[:2]:
+        assert abs(float(loss[r]) - float(rl[r])) <= w[r] * (2 * rel + 41 * U) + U * abs(float(rl[r]))
+        p = torch.softmax(c.h[r] * c.scale, 0)
+        part = (p + (rd[r] / w[r]).abs()) * 2
+        tol = (rel * 2 * part + 4 * U * part) * w[r] + HALF[dtype] * rd[r].abs() * 1.001 + TINY[dtype]
+        assert bool(((dz[r].cpu().double() - rd[r]).abs() <= tol).all())
+    c.x[0] = 0
+    c.put()
+    loss0, stats0, dz0 = c.call(sc)
+    assert torch.equal(loss0, loss) and torch.equal(dz0, dz)
+    assert float(stats[0, 1]) == float(stats0[0, 1]) and float(stats[0, 0]) < -6e4
 
 
 @pytest.mark.parametrize("rows,cols", [(600, 20000), (2, 20000), (2, 262144)],
@@ -593,6 +638,30 @@ def test_balance(sc, tokens, experts, k, segments, pad, shift, dtype, score):
     x, idx, mask = _router(tokens, experts, k, dtype, score)
     edges = _offsets(tokens, segments, _rng("cuts", tokens, segments))
     _check_balance(sc, x, idx, mask if tokens > 1 else None, edges, dtype, score, pad, shift)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("tokens,experts", [(400, 24), (9000, 24)])
+def test_balance_lowest_values(sc, tokens, experts, dtype):
+    """Tokens of the type's lowest value have uniform scores; experts masked
+    with it have none."""
+    x, idx, mask = _router(tokens, experts, 2, dtype, "lowest")
+    x[::7] = torch.finfo(dtype).min
+    x[1::7, ::2] = torch.finfo(dtype).min
+    z = _place(x, dtype)
+    counts = torch.zeros(1, experts, dtype=torch.int32, device="cuda")
+    psum, n_tok, loss = torch.zeros(1, experts, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), None
+    outs = []
+    for low in (z, _place(torch.where((x == x[0, 0]).all(1, keepdim=True), 0.0, x), dtype)):
+        ws = _bytes(sc.scape_balance_workspace_bytes(low, 1))
+        dz = torch.full_like(low, 5.0)
+        sc.scape_balance_forward(low, idx.cuda(), counts, psum, n_tok, loss, mask=mask.cuda(), workspace=ws, alpha=0.01)
+        sc.scape_balance_backward(low, counts, n_tok, None, dz, k=2, mask=mask.cuda(), alpha=0.01)
+        torch.cuda.synchronize()
+        outs.append((counts.clone(), psum.clone(), dz))
+    assert bool(outs[0][1].isfinite().all()) and bool((outs[0][1] > 0).all())
+    for a, b in zip(*outs):  # as if those tokens' logits were 0
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
