@@ -142,7 +142,7 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
         const float ref = m == kNegInf ? 0.0f : m;
 #pragma unroll
         for (int i = 0; i < kGran * T::kN; ++i) {
-            w[i] = fast_exp2((T::up(g[i / T::kN], i % T::kN) - ref) * kLog2e);
+            w[i] = fast_exp2(less<T>(g[i / T::kN], i % T::kN, ref) * kLog2e);
             if constexpr (kGrad) grad[i] = w[i];
             sum += w[i];
         }

@@ -556,7 +556,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
         if (i < p.cnt) {
             float d[T::kN];
 #pragma unroll
-            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2((T::up(x, j) - vref) * a.c2);
+            for (int j = 0; j < T::kN; ++j) d[j] = f * fast_exp2(less<T>(x, j, vref) * a.c2);
             store_loose(dz + p.first, i, T::down(d));
         }
     }

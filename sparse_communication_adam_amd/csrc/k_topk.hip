@@ -494,7 +494,7 @@ __global__ __launch_bounds__(kBlock) void k_topk_small(TopkArgs a) {
         const float ref = m == kNegInf ? 0.0f : m;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum += fast_exp2((T::up(g[i / T::kN], i % T::kN) - ref) * a.c2);
+        for (int i = 0; i < kV; ++i) sum += fast_exp2(less<T>(g[i / T::kN], i % T::kN, ref) * a.c2);
         sum = group_reduce<OpSumF, kLanes>(sum);
         // v_log_f32: the sum is 1 to 1024, so a step of it is less than what the sum is off by
         if (l == 0 && live) a.lse[row] = (float)((double)ref * a.scale + kLn2 * (double)__builtin_amdgcn_logf(sum));

@@ -3,6 +3,8 @@
 // and reductions over a wave and a workgroup.
 #pragma once
 
+#include <type_traits>
+
 #include "loss_internal.h"
 #include "scape_device.h"
 
@@ -152,6 +154,14 @@ __device__ __forceinline__ int32_t again(int32_t tid) {
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 template <class T>
 __device__ __forceinline__ float granule_max(const gran& g) {
+    if constexpr (std::is_same<T, F16>::value) {  // two at once, unpacked at the end
+        typedef _Float16 pair __attribute__((ext_vector_type(2)));
+        const uint32_t w0 = g[0], w1 = g[1], w2 = g[2], w3 = g[3];
+        const pair m = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(__builtin_bit_cast(pair, w0), __builtin_bit_cast(pair, w1)),
+            __builtin_elementwise_maximum(__builtin_bit_cast(pair, w2), __builtin_bit_cast(pair, w3)));
+        return max_nan((float)m[0], (float)m[1]);
+    }
     float m = T::up(g, 0);
 #pragma unroll
     for (int j = 1; j < T::kN; ++j) m = max_nan(m, T::up(g, j));
@@ -159,6 +169,19 @@ __device__ __forceinline__ float granule_max(const gran& g) {
 }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
+
+// Element j minus r.  fp16: as a multiply-add by a one that the compiler does
+// not see, which takes the element unpacked and converted in the same
+// instruction (v_fma_mix_f32).
+template <class T>
+__device__ __forceinline__ float less(const gran& g, int j, float r) {
+    if constexpr (std::is_same<T, F16>::value) {
+        float one = 1.0f;
+        asm("" : "+v"(one));
+        return __builtin_fmaf(T::up(g, j), one, -r);
+    }
+    return T::up(g, j) - r;
+}
 
 // A running sum of 2^(c2 (x - ref)), ref the largest x so far.  The difference
 // is taken before the product: a product's rounding against a reference that
@@ -180,8 +203,8 @@ struct RunningSum {
         for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int j = 0; j < T::kN; j += 2) {
-                s0 += fast_exp2((T::up(g[b], j) - r) * c2);
-                s1 += fast_exp2((T::up(g[b], j + 1) - r) * c2);
+                s0 += fast_exp2(less<T>(g[b], j, r) * c2);
+                s1 += fast_exp2(less<T>(g[b], j + 1, r) * c2);
             }
         sum = s0 + s1;
     }
