@@ -6,7 +6,8 @@
 // ~column, so no two entries of a row are equal and the result does not
 // depend on the order in which candidates are found.
 //
-// Each kernel reads a row once, so what bounds it is the read of the logits.
+// Each kernel reads a row once, so what bounds the long rows is the read of the
+// logits.
 //  - k_topk_small: rows of up to 1024 columns (a router's experts), a group
 //    of lanes per row.
 //  - k_topk_rows: longer rows, a workgroup per row or part of one, the row in
@@ -97,7 +98,11 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
 }
 
 // A workgroup takes `per` granules of a row into registers and makes the
-// row's k largest, or its part's, from them.
+// row's k largest, or its part's, from them.  4096x32000 bf16, k = 64: 50 us,
+// 5.2 TB/s (a plain read of as much 38 us): four workgroups of a CU load while
+// others choose, and the choice alone, from the threshold on, costs the 9 us
+// that this does not hide.  1021x50257 f32, k = 100, in four parts: 44 us, 4.7
+// TB/s, and 6 for the merge.
 //
 // Candidates: of disjoint groups of entries, two a thread, the k-th largest of
 // the groups' maxima is at most the k-th largest entry, and for k well below
@@ -179,8 +184,19 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_topk_rows(TopkArgs a) {
         uint32_t mk[2 * kNW];
 #pragma unroll
         for (int w = 0; w < 2 * kNW; ++w) mk[w] = gmax[w * 64 + tid];
-        uint32_t t = 0;
-        for (int b = 15; b >= 0; --b) {
+        // the bits that all maxima share are the threshold's too (where there
+        // are k of them), so the search begins at the first that differs
+        uint32_t hi = mk[0], lo = mk[0], t = 0;
+#pragma unroll
+        for (int w = 1; w < 2 * kNW; ++w) {
+            hi = mk[w] > hi ? mk[w] : hi;
+            lo = mk[w] < lo ? mk[w] : lo;
+        }
+        hi = group_reduce<OpMaxU, 64>(hi);
+        lo = ~group_reduce<OpMaxU, 64>(~lo);
+        const int top = k <= 2 * kThreads ? 31 - (int)__builtin_clz((hi ^ lo) | 1u) : 15;
+        if (k <= 2 * kThreads) t = hi & ~((2u << top) - 1u);
+        for (int b = __builtin_amdgcn_readfirstlane(top); b >= 0; --b) {
             const uint32_t x = t | (1u << b);
             uint32_t count = 0;
 #pragma unroll
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(kMergeThreads) void k_topk_merge(TopkArgs a) {
 // largest head of the group leaves its lane's list, and lane r keeps the r-th
 // until a whole group's worth is written at once.  What bounds it is the
 // instructions: 65536x64 f32, k = 6, takes 10.5 us, 5.5 of them the vector
-// units' and 3 the memory's; one row at a time without a sort took 15.
+// units' and 3 the memory's; a scan of each lane's entries in every round took 15.
 
 // An entry: value and column as one number, larger for an earlier rank.  A
 // 16-bit value and its column share a word; 0 is no entry.
