@@ -104,6 +104,8 @@ struct Lds {
     // tid + (b + 4 cell_row) kThreads, b < 4.
     __device__ __forceinline__ void strike(int32_t cell_row, gran (&g)[4]) const {
         const uint32_t bits = cells[cell_row * kThreads + (int32_t)threadIdx.x];
+        uint32_t none = no_entries<T>()[0];
+        asm("" : "+s"(none));  // in a register: one v_bfi_b32 a word, where a literal takes two instructions
         if (bits) {
 #pragma unroll
             for (int b = 0; b < 4; ++b)
@@ -119,7 +121,7 @@ struct Lds {
                         m = (uint32_t)((int32_t)(bits << (31 - 4 * b - q)) >> 31);
                     }
                     asm("" : "+v"(m));  // a mask: else each element becomes a test and a select
-                    g[b][q] = (g[b][q] & ~m) | (no_entries<T>()[q] & m);
+                    g[b][q] = (g[b][q] & ~m) | (none & m);
                 }
         }
     }
