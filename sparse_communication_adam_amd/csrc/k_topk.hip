@@ -113,9 +113,9 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
 // threshold comes from a radix selection that reads the row again, from the
 // caches, for each 8-bit digit.
 constexpr int kTopkHits = 768;  // granules, an equal share for each wave
-template <class T, int kGran>
-__global__ __launch_bounds__(kRowThreads, 4) void k_topk_rows(TopkArgs a) {
-    constexpr int kThreads = kRowThreads, kNW = kThreads / 64;
+template <class T, int kThreads, int kGran>
+__global__ __launch_bounds__(kThreads, 4) void k_topk_rows(TopkArgs a) {
+    constexpr int kNW = kThreads / 64;
     __shared__ __align__(16) uint64_t list[kTopkList];
     __shared__ gran hit[kTopkHits];
     __shared__ int32_t hit_at[kTopkHits];
@@ -565,9 +565,10 @@ static hipError_t topk_typed(hipStream_t s, const TopkArgs& a) {
         return hipGetLastError();
     }
     const dim3 grid((uint32_t)(a.in.rows * a.splits));
-    if (a.per <= kRowThreads * 4) hipLaunchKernelGGL((k_topk_rows<T, 4>), grid, dim3(kRowThreads), 0, s, a);
-    else if (a.per <= kRowThreads * 8) hipLaunchKernelGGL((k_topk_rows<T, 8>), grid, dim3(kRowThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_topk_rows<T, kHeldGranules>), grid, dim3(kRowThreads), 0, s, a);
+    if (a.per <= 256 * 4) hipLaunchKernelGGL((k_topk_rows<T, 256, 4>), grid, dim3(256), 0, s, a);
+    else if (a.per <= 256 * 8) hipLaunchKernelGGL((k_topk_rows<T, 256, 8>), grid, dim3(256), 0, s, a);
+    else if (a.per <= 256 * 16) hipLaunchKernelGGL((k_topk_rows<T, 256, 16>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_topk_rows<T, 512, 16>), grid, dim3(512), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL((k_topk_merge<T>), dim3((uint32_t)a.in.rows), dim3(kMergeThreads), 0, s, a);

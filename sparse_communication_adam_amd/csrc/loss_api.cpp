@@ -24,13 +24,15 @@ RowSplit split_to_fill(int64_t granules, int64_t rows, int64_t fill, int64_t lea
 }
 }  // namespace
 
-// The top-k holds a row in registers, so a longer row is cut into parts that
-// fit; more parts than that never paid, not even for one row (1x32000 f32: 17
-// us in two parts, 23 us in eight, both with the graph replay they were timed
-// in).
+// The top-k holds a row in registers: up to 8192 granules in a workgroup of 512
+// threads, a longer one in parts of up to 4096, each a workgroup of 256, and a
+// merge (replayed, us, k = 64: 50304 bf16 in two parts and whole, 512 rows 24
+// and 22, 4096 rows 91 and 95; 32000 f32 25 and 22, 98 and 92; 50257 f32 in
+// parts of 4096 and of 8192, 512 rows 32 and 36, 4096 rows 157 and 180).  More
+// parts than that never paid, not even for one row.
 RowSplit topk_split(int32_t dtype, int64_t cols) {
     const int64_t g = row_granules(dtype, cols);
-    return split_evenly(g, (g + kTopkCapacity - 1) / kTopkCapacity, kRowThreads);
+    return split_evenly(g, g <= kFusedCapacity ? 1 : (g + kTopkCapacity - 1) / kTopkCapacity, kRowThreads);
 }
 
 // The distillation streams a row of any length.  Cutting it costs the loss a

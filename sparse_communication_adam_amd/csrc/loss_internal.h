@@ -28,8 +28,8 @@ inline int dtype_size(int32_t dtype) { return dtype == SCAPE_DTYPE_F32 ? 4 : 2; 
 // (reductions, the entries' terms) is about as much as 64 elements a lane cost.
 constexpr int kRowThreads = 256;
 // A kernel that holds the row in registers has at most 16 granules a thread (64
-// registers, which leaves as many for the arithmetic at 4 waves per SIMD; the
-// fused loss and gradient has a form with 512 threads for twice the row).
+// registers, which leaves as many for the arithmetic at 4 waves per SIMD), and a
+// form with 512 threads for twice the row.
 constexpr int kHeldGranules = 16;
 constexpr int kTopkCapacity = kRowThreads * kHeldGranules;
 constexpr int kFusedCapacity = 2 * kTopkCapacity;

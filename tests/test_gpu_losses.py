@@ -103,7 +103,8 @@ def _check_topk(sc, z, k, scale=1.0, lse=True, stream=None):
     (9, 1024, 32, 0, 0),                                   # short rows
     (2, 64, 40, 0, 0), (9, 1024, 33, 8, 0), (3, 1025, 5, 0, 0), (600, 2500, 17, 7, 5), (2, 4096, 1024, 0, 0),
     (520, 4097, 300, 0, 1),                                # a workgroup a row
-    (1, 50304, 32, 0, 0), (2, 50257, 100, 47, 0), (1, 32000, 1024, 0, 1), (5, 131072, 64, 0, 0), (1, 262144, 257, 0, 3),
+    (1, 50304, 32, 0, 0), (2, 50257, 100, 47, 0), (1, 32000, 1024, 0, 1), (3, 16385, 1000, 0, 0), (2, 32769, 600, 0, 3),
+    (2, 65535, 80, 0, 1), (5, 131072, 64, 0, 0), (1, 262144, 257, 0, 3),
 ])
 def test_topk(sc, dtype, rows, cols, k, pad, shift):
     g = _rng("topk", dtype, rows, cols, k)
@@ -112,7 +113,7 @@ def test_topk(sc, dtype, rows, cols, k, pad, shift):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
-@pytest.mark.parametrize("cols,k", [(64, 8), (1000, 32), (3000 + 1, 50), (20000, 1000), (60000, 64)])
+@pytest.mark.parametrize("cols,k", [(64, 8), (1000, 32), (3000 + 1, 50), (20000, 1000), (60000, 64), (90000, 900)])
 @pytest.mark.parametrize("kind", ["constant", "three values", "few left", "all masked", "specials", "zeros", "lowest"])
 def test_topk_ties_and_specials(sc, dtype, cols, k, kind):
     rows = 3

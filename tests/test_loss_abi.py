@@ -68,9 +68,9 @@ CASES = (
     [("scape_topk_rows", TOPK, c, e) for c, e in ROWS + [
         (dict(k=0), -2), (dict(k=101), -2), (dict(k=1025, cols=5000, ld=5000), -2), (dict(val=0), -1), (dict(val=65), -3),
         (dict(idx=0), -1), (dict(idx=66), -3), (dict(lse=66), -3),
-        (dict(rows=1, cols=50304, ld=50304), -1),                                    # a split row: no workspace
-        (dict(rows=1, cols=50304, ld=50304, ws=64, ws_bytes=8), -2),                 # too small
-        (dict(rows=1, cols=50304, ld=50304, ws=72, ws_bytes=1 << 20), -3)]]          # misaligned
+        (dict(rows=1, cols=131072, ld=131072), -1),                                    # a split row: no workspace
+        (dict(rows=1, cols=131072, ld=131072, ws=64, ws_bytes=8), -2),                 # too small
+        (dict(rows=1, cols=131072, ld=131072, ws=72, ws_bytes=1 << 20), -3)]]          # misaligned
     + [("scape_distill_forward", FORWARD, c, e) for c, e in ROWS + [
         (dict(teacher=None), -1), (dict(teacher=dict(val=0)), -1), (dict(teacher=dict(val=65)), -3),
         (dict(teacher=dict(dtype=7)), -1), (dict(teacher=dict(idx=0)), -1), (dict(teacher=dict(idx=66)), -3),
@@ -118,7 +118,8 @@ def test_workspace_queries(sc, lib):
     b = ctypes.c_int64(-1)
     assert lib.scape_topk_rows_workspace(1, 4096, 32000, 64, ctypes.byref(b)) == 0 and b.value == 0
     assert lib.scape_topk_rows_workspace(1, 1 << 20, 64, 8, ctypes.byref(b)) == 0 and b.value == 0
-    assert lib.scape_topk_rows_workspace(1, 1, 50304, 32, ctypes.byref(b)) == 0 and b.value > 0
+    assert lib.scape_topk_rows_workspace(1, 1, 50304, 32, ctypes.byref(b)) == 0 and b.value == 0
+    assert lib.scape_topk_rows_workspace(1, 1, 131072, 32, ctypes.byref(b)) == 0 and b.value > 0
     assert lib.scape_topk_rows_workspace(0, 4096, 262144, 64, ctypes.byref(b)) == 0 and b.value > 0  # too long for one
     assert lib.scape_distill_workspace(1, 4096, 32000, 64, ctypes.byref(b)) == 0 and b.value == 0
     assert lib.scape_distill_workspace(1, 1, 50304, 64, ctypes.byref(b)) == 0 and b.value == 0
