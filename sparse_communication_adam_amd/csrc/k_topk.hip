@@ -98,8 +98,8 @@ __device__ void emit_sorted(uint64_t* list, uint32_t n, int32_t k, Emit emit) {
 }
 
 // A workgroup takes `per` granules of a row into registers and makes the
-// row's k largest, or its part's, from them.  4096x32000 bf16, k = 64: 50 us,
-// 5.2 TB/s (a plain read of as much 38 us): four workgroups of a CU load while
+// row's k largest, or its part's, from them.  4096x32000 bf16, k = 64: 49 us,
+// 5.3 TB/s (a plain read of as much 38 us): four workgroups of a CU load while
 // others choose, and the choice alone, from the threshold on, costs the 9 us
 // that this does not hide.  1021x50257 f32, k = 100, in four parts: 44 us, 4.7
 // TB/s, and 6 for the merge.
