@@ -472,7 +472,9 @@ int scape_profile_read(scape_ctx* ctx, double* ms, int64_t* steps);
  *   -inf is none: the slots that no entry is left for hold -inf and -1.  NaN
  *   counts as larger than every number (val is then NaN).  lse is -inf for a
  *   row of -inf, and NaN where the row holds NaN or +inf.
- * 1 <= k <= min(cols, SCAPE_TOPK_MAX_K); scale > 0; rows = 0 enqueues nothing.
+ * 1 <= k <= min(cols, SCAPE_TOPK_MAX_K); scale > 0; rows = 0 enqueues nothing;
+ * a launch holds 2^23 - 1 workgroups of long rows (one each, more where a row
+ * is too long for one), or 2^25 rows where cols <= 1024 and k <= 32.
  * The workspace is 0 bytes unless a row is too long for one workgroup.
  * Errors: INVALID_ARG, ALIGN, SHAPE (limits, ld < cols, workspace too small),
  * HIP.
@@ -550,6 +552,7 @@ int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t c
  *   n_tok[i]        valid tokens
  *   loss[i]         alpha * E / (k * n^2) * sum_e counts_e * psum_e, which is
  *                   alpha * sum_e (E * counts_e / (k n)) * (psum_e / n); 0 if n = 0
+ * tokens <= 2^30, tokens * k < 2^31, segments <= 2^21.
  * loss may be NULL: a data-parallel program adds counts, psum and n_tok over
  * its workers and then calls scape_balance_loss for the loss of them all.
  * Errors: as scape_topk_rows.
