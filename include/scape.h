@@ -513,8 +513,9 @@ typedef struct scape_teacher {
  * A row with weight 0, or without entries, does not count, whatever it holds:
  * loss, stats and gradient are 0.  So are loss and gradient of a row whose logits are all
  * -inf.  Where the student holds nothing outside the entries the q_T term is
- * left out.  An entry with q_j > 0 at a column of -inf makes the loss +inf.  A
- * row that counts and holds NaN or +inf gives NaN.
+ * left out.  An entry with q_j > 0 (in float64: a q_j below about exp(-745) is
+ * 0) at a column of -inf makes the loss +inf.  A row that counts and holds NaN
+ * or +inf gives NaN.
  * Arguments: z as above, read only; loss fp32 [rows]; stats fp32 [2*rows],
  * needed also where no backward call follows; dz of z's type, rows ld_dz >=
  * cols elements apart, columns past cols untouched, may be z itself (then

@@ -189,9 +189,10 @@ struct WaveSums {
     double top;  // sum 2^(c2 (x_j - mt))
     double q;    // sum q_j, q_j = exp(lq_j), lq_j the teacher's log-probability (against mq)
     double qt;   // sum q_j lq_j
-    double qx;   // sum q_j c2 (x_j - mt)
+    double qx;   // sum q_j c2 (x_j - mt), entries at a column of -inf left out
     float mt;    // the largest x_j
     float mq;    // 0 where the teacher's lse is given, else the largest t_j
+    float mi;    // the largest t_j with q_j > 0 at a column of -inf; -inf: none
 };
 
 // kStudent: also the student's terms.  Slots' t and z become q and p, for the
@@ -200,7 +201,7 @@ struct WaveSums {
 template <class T, int kThreads, bool kStudent>
 __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse, const Lds<T, kThreads>& l) {
     const int32_t tid = (int32_t)threadIdx.x;
-    WaveSums s{0.0, 0.0, 0.0, 0.0, kLowest, a.t_lse ? 0.0f : kLowest};
+    WaveSums s{0.0, 0.0, 0.0, 0.0, kLowest, a.t_lse ? 0.0f : kLowest, kNegInf};
     bool some = false;
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
         if (l.col[slot] >= 0) {
@@ -213,7 +214,8 @@ __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse,
     if (!a.t_lse) s.mq = group_reduce<OpMaxNum, 64>(s.mq);
     for (int32_t slot = tid; slot < a.k; slot += kThreads)
         if (l.col[slot] >= 0) {
-            const double lq = log_q(a, lse, l.t[slot], s.mq), q = exp(lq);
+            const float t = l.t[slot];
+            const double lq = log_q(a, lse, t, s.mq), q = exp(lq);
             l.t[slot] = (float)q;
             s.q += q;
             if (kStudent) {
@@ -222,7 +224,10 @@ __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse,
                 s.top += p;
                 if (q != 0.0) {
                     s.qt += q * lq;
-                    s.qx += q * x;
+                    if (x == -__builtin_inf())
+                        s.mi = fmaxf(s.mi, t);
+                    else
+                        s.qx += q * x;
                 }
             }
         }
@@ -231,6 +236,7 @@ __device__ __forceinline__ WaveSums entry_sums(const DistillArgs& a, double lse,
         s.top = wave_sum_f64(s.top);
         s.qt = wave_sum_f64(s.qt);
         s.qx = wave_sum_f64(s.qx);
+        s.mi = group_reduce<OpMaxNum, 64>(s.mi);
     }
     return s;
 }
@@ -255,10 +261,15 @@ __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const Runn
     const double t = (double)tail.sum, tref = (double)tail.ref, c2 = (double)a.c2;
     const bool has_tail = !(t == 0.0);
     const double ref = fmax(has_tail ? tref : (double)kLowest, (double)group_reduce<OpMaxNum, kWaves>(w.mt));
-    const double dq = a.t_lse ? 0.0 : ((double)w.mq - (double)group_reduce<OpMaxNum, kWaves>(w.mq)) * (double)a.scale;
+    const double mq = (double)group_reduce<OpMaxNum, kWaves>(w.mq), mi = (double)group_reduce<OpMaxNum, kWaves>(w.mi);
+    const double dq = a.t_lse ? 0.0 : ((double)w.mq - mq) * (double)a.scale;
     // lanes 0..: the waves' references against the row's; 16..: the teacher's
-    // likewise; 32: the tail's (0 too where the tail is out of range)
-    const double powers = exp2(lane < 16 ? ((double)w.mt - ref) * c2 : lane < 32 ? dq * kLog2e64 : (tref - ref) * c2);
+    // likewise; 32: the tail's (0 too where the tail is out of range); 48: the
+    // entry of most mass at a column of -inf against the teacher's reference
+    const double powers = exp2(lane < 16   ? ((double)w.mt - ref) * c2
+                               : lane < 32 ? dq * kLog2e64
+                               : lane < 48 ? (tref - ref) * c2
+                                           : (mi - mq) * (double)a.scale * kLog2e64);
     const double fp = from_lane_of<kWaves>(powers, 0), fq = from_lane_of<kWaves>(powers, 16);
     const double far = has_tail ? from_lane(powers, 32) : 0.0;
     const double top = sum_waves_f64<kWaves>(w.top * fp);
@@ -287,6 +298,10 @@ __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, const Runn
         if (!a.t_lse) kl -= log_q;
     }
     if (rest > 0.0) kl += rest * (log_rest - lpt);
+    // mass where the student has none: judged by the entry's probability in the
+    // row, as a wave whose entries are all faint has it too large against its own
+    // reference.  With the teacher's lse the two are the same.
+    if (a.t_lse ? mi > -__builtin_inf() : from_lane(powers, 48) > 0.0) kl += __builtin_inf();
     r.loss = (float)kl;
     r.stat0 = (float)lse;
     r.anchor = make_float2((float)ref, (float)log_sum);  // ref is a logit
