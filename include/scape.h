@@ -532,7 +532,9 @@ int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k
  * teacher and scale: dz = dloss[r] * weight[r] * dKL/dz (either NULL: 1).  A
  * row whose factor is 0 gets 0, whatever it holds.  p is good to the rounding
  * of the statistics, 2^-24 |stats[2r]|, where the forward call's own gradient
- * depends on differences of logits only.  Needs no workspace.
+ * depends on differences of logits only.  log p_T, whose rounding would show in
+ * the tail, is used down to -30; below, the row's tail is read and summed once
+ * more.  Needs no workspace.
  * Errors: as scape_topk_rows. */
 int scape_distill_backward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                            const scape_teacher* teacher, float scale, const float* weight, const float* stats,

@@ -32,7 +32,8 @@
 // Statistics kept for a later backward pass: L = log sum exp(s z) and
 // log p_T.  The latter is near 0 where the entries hold little of the
 // student's mass, and the gradient's tail factor (Q - q_T / p_T) p_T =
-// sum q_j p_T + q_T (p_T - 1) is then made of two small terms.
+// sum q_j p_T + q_T (p_T - 1) is then made of two small terms.  Where the
+// student holds almost nothing outside the entries, the tail is summed again.
 #include <type_traits>
 
 #include "loss_device.h"
@@ -345,9 +346,13 @@ struct Part {
         n = (int32_t)a.in.cols;
         z = static_cast<const raw*>(a.in.z) + row * a.in.ld;
         sh = row_shape<T>(z, n);
-        g0 = sp * a.per;
-        cnt = max(min(a.per, sh.granules - g0), 0);
-        const bool last = sp == a.splits - 1;
+        take(a.per, sp == a.splits - 1);
+    }
+    // The whole row in the place of its first part.
+    __device__ __forceinline__ void take_whole() { take(sh.granules, true); }
+    __device__ __forceinline__ void take(int32_t per, bool last) {
+        g0 = sp * per;
+        cnt = max(min(per, sh.granules - g0), 0);
         first = sh.head + g0 * T::kN;
         body = cnt > 0 ? reinterpret_cast<const gran*>(z + sh.head) + g0 : &g_no_granule;
         lone = lone_element(sh, n, sp == 0, last);
@@ -590,18 +595,24 @@ __global__ __launch_bounds__(kThreads, 4) void k_distill_fused(DistillArgs a) {
     write_entries(a, p, l, s_gs, s_p[wave], s_q[wave], dz);
 }
 
-// The gradient of a row or a part of one, from the statistics.
+// The gradient of a row or a part of one, from the statistics.  A tail of less
+// than exp(-30) of the student's mass is a faint one: log p_T has too few bits
+// for it (a step of float32 is 64 where the other columns are masked with -1e9),
+// so its sum is made again, against its own largest logit.  The row's first
+// part then takes the whole row and the other parts leave: dz may lie over z.
+constexpr float kFaint = -30.0f;
 template <class T>
 __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) {
     constexpr int kThreads = kRowThreads, kNW = kThreads / 64;
     extern __shared__ __align__(16) uint8_t lds_bytes[];
+    __shared__ float2 wsum[kNW];
     __shared__ WaveSums wrec[kNW];
     __shared__ double s_p, s_q[kNW];
-    __shared__ float s_vref, s_tail, s_gs;
+    __shared__ float s_xref, s_vref, s_tail, s_gs;
     __shared__ uint32_t s_flags;
     using raw = typename T::raw;
     const int32_t tid = (int32_t)threadIdx.x, wave = tid / 64;
-    const Part<T> p(a);
+    Part<T> p(a);
     const Lds<T, kThreads> l(lds_bytes, p.sh, p.n, a.k);
     raw* dz = static_cast<raw*>(a.dz) + p.row * a.ld_dz;
     float w = a.weight ? a.weight[p.row] : 1.0f;
@@ -614,14 +625,38 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
     p.template load<kThreads>(0, g);
     // dz may be z, and other workgroups write their parts of it: only this
     // part's logits are read
-    const float lx = p.lone_logit();
-    const float z0 = p.entry_logit(s0.c);
+    float lx = p.lone_logit();
+    float z0 = p.entry_logit(s0.c);
     w = w == 0.0f ? 0.0f : w * up;
     if (tid == 0) s_flags = 0;
     l.clear();
     if (!mark_entries(a, p.row, s0, l, &s_flags) || w == 0.0f) {
         zero_part<T, kThreads>(p, dz);
         return;
+    }
+    const bool faint = a.t_lse && lpt <= kFaint;
+    if (faint) {
+        if (p.sp != 0) return;
+        p.take_whole();
+        lx = p.lone_logit();
+        z0 = p.entry_logit(s0.c);
+        RunningSum rs = RunningSum::none();
+        if (p.lone >= 0 && !l.marked(p.lone)) rs.add1(lx, a.c2);
+        // few rows are faint ones: one set of granules, so that the others
+        // keep their registers
+        for (int32_t base = 0; base < p.cnt; base += 4 * kThreads) {
+            p.template load<kThreads>(base, g);
+            p.template trim<kThreads>(base, g);
+            l.strike(base / (4 * kThreads), g);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const gran one[1] = {g[b]};
+                rs.template add<T, 1>(one, granule_max<T>(g[b]), a.c2);
+            }
+        }
+        wave_join(rs, a.c2);
+        if ((tid & 63) == 0) wsum[wave] = make_float2(rs.ref, rs.sum);
+        p.template load<kThreads>(0, g);
     }
     // before any other thread may write over z
     for (int32_t slot = tid + kThreads; slot < a.k; slot += kThreads)
@@ -636,15 +671,21 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
         const double fq = a.t_lse ? 1.0 : exp(((double)r.mq - (double)group_reduce<OpMaxNum, kNW>(r.mq)) * (double)a.scale);
         const double q = sum_waves_f64<kNW>(r.q * fq);
         const double qsum = a.t_lse ? q : q == 0.0 ? 0.0 : 1.0;
-        const double rest = a.t_lse && 1.0 - q > 0.0 && lpt != kNegInf ? 1.0 - q : 0.0;
-        // (Q - q_T / p_T) p_v, against L, or where 1 / p_T could leave the
-        // range against the tail's own log-sum-exp
-        float v = at.y, tail = (float)qsum;
+        RunningSum own{0.0f, 1.0f};
+        if (faint) {
+            own = RunningSum{wsum[tid & (kNW - 1)].x, wsum[tid & (kNW - 1)].y};
+            join_waves<kNW>(own, a.c2);
+        }
+        const double rest = a.t_lse && 1.0 - q > 0.0 && own.sum != 0.0f ? 1.0 - q : 0.0;  // sum 0: no tail
+        // (Q - q_T / p_T) p_v, against L, or a faint tail's against its own sum
+        float xref = at.x, v = at.y, tail = (float)qsum;
         if (rest > 0.0) {
             const double pt = exp((double)lpt), c = qsum * pt + rest * (pt - 1.0);
-            const bool near = lpt > -30.0f;
-            tail = (float)(near ? c / pt : c);
-            if (!near) v = (float)((double)at.y + (double)lpt);
+            tail = (float)(c / (faint ? (double)own.sum : pt));
+            if (faint) {
+                xref = own.ref;
+                v = 0.0f;
+            }
         }
         if (tid < kNW) s_q[tid] = fq * (qsum == 0.0 ? 0.0 : a.t_lse ? 1.0 : 1.0 / q);
         if (tid == 0) {
@@ -652,13 +693,14 @@ __global__ __launch_bounds__(kRowThreads, 6) void k_distill_grad(DistillArgs a) 
             s_p = qsum + rest;
             s_gs = gs;
             s_tail = gs == 0.0f ? 0.0f : gs * tail;
+            s_xref = xref;
             s_vref = gs == 0.0f ? -kNegInf : v;  // nothing to learn: exponents of -inf
         }
     }
     __syncthreads();
-    const float f = s_tail, vref = s_vref;
+    const float f = s_tail, xref = s_xref, vref = s_vref;
     // the difference from L first: neither rounds L log2(e) nor leaves the range
-    auto grad = [&](float x) { return f * fast_exp2(__builtin_fmaf(x - at.x, a.scale, -vref) * kLog2e); };
+    auto grad = [&](float x) { return f * fast_exp2(__builtin_fmaf(x - xref, a.scale, -vref) * kLog2e); };
     auto write = [&](int32_t i, const gran& x) {
         float d[T::kN];
 #pragma unroll
