@@ -131,14 +131,20 @@ __device__ __forceinline__ void load_batch(const BalanceArgs& a, const Run& r, c
 }
 
 // A token's scores, not yet divided by their sum: w[i], and 1 / sum.  A token
-// whose logits are all -inf has 0 for both.  For sigmoids grad[i] is
-// s (1 - s), the slope of the score.  v_exp_f32 and v_rcp_f32 are good to a
-// step of float32.
-template <class T, int kLanes, int kGran, bool kGrad>
-__device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], float (&w)[kGran * T::kN],
+// whose logits are all -inf has 0 for both, and so has one that is not live.
+// For sigmoids grad[i] is s (1 - s), the slope of the score.  v_exp_f32 and
+// v_rcp_f32 are good to a step of float32.
+//
+// Sigmoids leave float32's range below about -87.  A token whose sigmoids
+// add up to less than 2^-64 has logits below -44: 1 + exp(x) is 1 there to
+// float32, so its scores are a softmax and its slopes the scores themselves.
+// Above that, what is lost is 2^-62 of the sum at most.
+constexpr float kLowSum = 0x1p-64f;
+template <class T, int kLanes, int kGran, bool kSoftmax, bool kGrad>
+__device__ __forceinline__ float scores(bool live, const gran (&g)[kGran], float (&w)[kGran * T::kN],
                                         float (&grad)[kGran * T::kN]) {
     float sum = 0.0f;
-    if (score == SCAPE_SCORE_SOFTMAX) {
+    if constexpr (kSoftmax) {
         float m = granule_max<T>(g[0]);
 #pragma unroll
         for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(g[c]));
@@ -150,6 +156,7 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
             if constexpr (kGrad) grad[i] = w[i];
             sum += w[i];
         }
+        sum = group_reduce<OpSumF, kLanes>(sum);
     } else {
 #pragma unroll
         for (int i = 0; i < kGran * T::kN; ++i) {
@@ -158,8 +165,28 @@ __device__ __forceinline__ float scores(int32_t score, const gran (&g)[kGran], f
             if constexpr (kGrad) grad[i] = w[i] * (fminf(e, FLT_MAX) * w[i]);  // 0 for -inf, not inf times 0
             sum += w[i];
         }
+        sum = group_reduce<OpSumF, kLanes>(sum);
+        if (__builtin_expect(wave_ballot(live && sum < kLowSum) != 0, 0)) {
+            const bool low = sum < kLowSum;
+            gran x[kGran];
+#pragma unroll
+            for (int c = 0; c < kGran; ++c) forget_unpacked(x[c] = g[c]);
+            float m = granule_max<T>(x[0]), of = 0.0f;
+#pragma unroll
+            for (int c = 1; c < kGran; ++c) m = max_nan(m, granule_max<T>(x[c]));
+            m = group_reduce<OpMaxF, kLanes>(m);
+            const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < kGran * T::kN; ++i) {
+                const float y = fast_exp2((T::up(x[i / T::kN], i % T::kN) - ref) * kLog2e);
+                w[i] = low ? y : w[i];
+                if constexpr (kGrad) grad[i] = low ? y : grad[i];
+                of += y;
+            }
+            of = group_reduce<OpSumF, kLanes>(of);
+            sum = low ? of : sum;
+        }
     }
-    sum = group_reduce<OpSumF, kLanes>(sum);
     return sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 }
 
@@ -172,7 +199,7 @@ __device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t 
 // to do for it is done here (2000x8 bf16 in 7 segments: 8.6 us; the two
 // launches took 11.5).  1024 threads, one workgroup a CU: with 512 and twice
 // the runs it takes as long, but the join of twice the runs 1.3 us more.
-template <class T, int kLanes, int kGran, bool kTiny, bool kWhole>
+template <class T, int kLanes, int kGran, bool kTiny, bool kSoftmax, bool kWhole>
 __global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a) {
     constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kNW = kForwardThreads / 64, kStep = kNW * kTokens;
     constexpr int kBatch = kGran == 1 ? 8 : kV == 8 ? 4 : 2;
@@ -221,7 +248,7 @@ __global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a)
         for (int i = 0; i < kBatch; ++i) {
             mine.settle(live[i], g[i]);
             float w[kV], none[kV];
-            const float inv = scores<T, kLanes, kGran, false>(a.score, g[i], w, none);  // a token that does not count: 0
+            const float inv = scores<T, kLanes, kGran, kSoftmax, false>(live[i], g[i], w, none);  // a token that does not count: 0
 #pragma unroll
             for (int v = 0; v < kV; ++v) acc[v] = __builtin_fmaf(w[v], inv, acc[v]);
             tokens += live[i] && l == 0 ? 1u : 0u;
@@ -364,7 +391,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_loss(const int32_t* counts, 
 
 // The gradient: a batch of four tokens a group, all loads first (65536x256 bf16
 // with two 17.6 us, four 17.5, eight 19.4).
-template <class T, int kLanes, int kGran, bool kTiny>
+template <class T, int kLanes, int kGran, bool kTiny, bool kSoftmax>
 __global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a) {
     using raw = typename T::raw;
     constexpr int kV = kGran * T::kN, kTokens = 64 / kLanes, kStep = kBackwardThreads / 64 * kTokens;
@@ -392,7 +419,7 @@ __global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a
             const int32_t t = b + i * kStep;
             mine.settle(live[i], g[i]);
             float w[kV], grad[kV];
-            const float inv = scores<T, kLanes, kGran, true>(a.score, g[i], w, grad);
+            const float inv = scores<T, kLanes, kGran, kSoftmax, true>(live[i], g[i], w, grad);
             float dot = 0.0f;
 #pragma unroll
             for (int v = 0; v < kV; ++v) dot = __builtin_fmaf(w[v], c[v], dot);
@@ -421,15 +448,25 @@ __global__ __launch_bounds__(kBackwardThreads) void k_balance_grad(BalanceArgs a
     }
 }
 
-template <class T, int kLanes, int kGran, bool kTiny>
-static void runs_or_grad(hipStream_t s, const BalanceArgs& a) {
+// A kernel for each score: with both in one, the sigmoids' low tokens cost the
+// softmax too (gradient of 65536x256 f16, replayed: 14.2 us before there were
+// any, 14.8 in one kernel, 13.8 in one of its own).
+template <class T, int kLanes, int kGran, bool kTiny, bool kSoftmax>
+static void runs_or_grad_of(hipStream_t s, const BalanceArgs& a) {
     const dim3 grid((uint32_t)a.slots);
     if (a.dz)
-        hipLaunchKernelGGL((k_balance_grad<T, kLanes, kGran, kTiny>), grid, dim3(kBackwardThreads), 0, s, a);
+        hipLaunchKernelGGL((k_balance_grad<T, kLanes, kGran, kTiny, kSoftmax>), grid, dim3(kBackwardThreads), 0, s, a);
     else if (a.whole)
-        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, true>), grid, dim3(kForwardThreads), 0, s, a);
+        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, kSoftmax, true>), grid, dim3(kForwardThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, false>), grid, dim3(kForwardThreads), 0, s, a);
+        hipLaunchKernelGGL((k_balance_runs<T, kLanes, kGran, kTiny, kSoftmax, false>), grid, dim3(kForwardThreads), 0, s, a);
+}
+template <class T, int kLanes, int kGran, bool kTiny>
+static void runs_or_grad(hipStream_t s, const BalanceArgs& a) {
+    if (a.score == SCAPE_SCORE_SOFTMAX)
+        runs_or_grad_of<T, kLanes, kGran, kTiny, true>(s, a);
+    else
+        runs_or_grad_of<T, kLanes, kGran, kTiny, false>(s, a);
 }
 
 template <class T>
