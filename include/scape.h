@@ -526,7 +526,10 @@ typedef struct scape_teacher {
 int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                           const scape_teacher* teacher, float scale, const float* weight, float* loss, float* stats,
                           void* dz, int64_t ld_dz, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes that serve a call with dz or without, and bytes that serve one whose
+ * dz is NULL (never more). */
 int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes);
+int scape_distill_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes);
 
 /* The gradient alone, from the statistics of a forward call on the same z,
  * teacher and scale: dz = dloss[r] * weight[r] * dKL/dz (either NULL: 1).  A

@@ -94,6 +94,7 @@ def lib() -> ctypes.CDLL:
             "scape_topk_rows_workspace": [i32, i64, i64, i32, vp],
             "scape_distill_forward": [vp, i32, i64, i64, i64, teachp, f32, vp, vp, vp, vp, i64, vp, i64, vp],
             "scape_distill_workspace": [i32, i64, i64, i32, vp],
+            "scape_distill_loss_workspace": [i32, i64, i64, i32, vp],
             "scape_distill_backward": [vp, i32, i64, i64, i64, teachp, f32, vp, vp, vp, vp, i64, vp],
             "scape_balance_forward": [vp, i32, i64, i32, i64, vp, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp, vp, i64,
                                       vp],
@@ -680,12 +681,13 @@ def _teacher(t_val, t_idx, t_lse, rows: int) -> _Teacher:
                     _array(t_lse, _TORCH.float32, rows, "t_lse"), k)
 
 
-def scape_distill_workspace_bytes(z, k: int, grad: bool = False) -> int:
-    """Bytes of workspace scape_distill_forward needs for this tensor's shape
-    (with or without the gradient)."""
+def scape_distill_workspace_bytes(z, k: int, grad: Optional[bool] = None) -> int:
+    """Bytes of workspace scape_distill_forward needs for this tensor's shape:
+    with dz (grad=True), without (False), or enough for either."""
     _, did, rows, cols, _ = _matrix(z, "z")
     b = ctypes.c_int64()
-    _check(lib().scape_distill_workspace(did, rows, cols, int(k), ctypes.byref(b)))
+    query = lib().scape_distill_loss_workspace if grad is not None and not grad else lib().scape_distill_workspace
+    _check(query(did, rows, cols, int(k), ctypes.byref(b)))
     return b.value
 
 

@@ -148,6 +148,14 @@ int64_t distill_bytes(int64_t rows, const RowSplit& sp, bool grad) {
     return parts_bytes(rows, sp) + (grad && (sp.splits > 1 || sp.per > kFusedCapacity) ? rows * 8 : 0);
 }
 
+int distill_query(int32_t dtype, int64_t rows, int64_t cols, int32_t k, bool grad, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    RowSplit sp;
+    if (int rc = distill_shape(dtype, rows, cols, k, distill_split, &sp)) return rc;
+    *bytes = distill_bytes(rows, sp, grad);
+    return SCAPE_OK;
+}
+
 int check_teacher(const scape_teacher* t, int64_t rows) {
     if (!t) return fail(SCAPE_ERR_INVALID_ARG, "teacher is NULL");
     int rc;
@@ -252,11 +260,11 @@ int scape_topk_rows(const void* z, int32_t dtype, int64_t rows, int64_t cols, in
 }
 
 int scape_distill_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
-    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
-    RowSplit sp;
-    if (int rc = distill_shape(dtype, rows, cols, k, distill_split, &sp)) return rc;
-    *bytes = distill_bytes(rows, sp, true);
-    return SCAPE_OK;
+    return distill_query(dtype, rows, cols, k, true, bytes);
+}
+
+int scape_distill_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int32_t k, int64_t* bytes) {
+    return distill_query(dtype, rows, cols, k, false, bytes);
 }
 
 int scape_distill_forward(const void* z, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
