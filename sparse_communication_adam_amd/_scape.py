@@ -565,13 +565,15 @@ def scape_profile_read(ctx: Context):
 
 _TORCH = None
 _FLOATS = None
+_WROTE = None
 
 
 def _torch():
-    global _TORCH, _FLOATS
+    global _TORCH, _FLOATS, _WROTE
     if _TORCH is None:
         import torch
         _TORCH = torch
+        _WROTE = torch.autograd.graph.increment_version
         _FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     return _TORCH
 
@@ -648,6 +650,13 @@ def _workspace(t, need):
     return t.data_ptr(), t.numel()
 
 
+def _wrote(*tensors) -> None:
+    """Tells autograd that a call changed these tensors in place, so that a
+    backward pass that needs what was there (a gradient over logits that tanh
+    or log_softmax kept) is an error instead of a wrong result."""
+    _WROTE([t for t in tensors if t is not None])
+
+
 def scape_topk_rows_workspace_bytes(z, k: int) -> int:
     """Bytes of workspace scape_topk_rows needs for this tensor's shape."""
     _, did, rows, cols, _ = _matrix(z, "z")
@@ -667,6 +676,7 @@ def scape_topk_rows(z, k: int, val, idx, lse=None, scale: float = 1.0, workspace
     wp, wb = _workspace(workspace, lambda: scape_topk_rows_workspace_bytes(z, k))
     st = _launch_on(stream, z=z, val=val, idx=idx, lse=lse, workspace=workspace)
     _check(lib().scape_topk_rows(zp, did, rows, cols, ld, k, scale, vp, ip, lp, wp, wb, st))
+    _wrote(val, idx, lse)
 
 
 def _teacher(t_val, t_idx, t_lse, rows: int) -> _Teacher:
@@ -698,7 +708,9 @@ def scape_distill_forward(z, t_val, t_idx, loss, stats, t_lse=None, scale: float
     entries is matched as one more class, without it the teacher is
     renormalised over them.  loss fp32 [rows], stats fp32 [rows, 2]; dz (z's
     dtype and shape, may be z) also takes the gradient of loss.sum().  For
-    autograd: z.backward(dz) on the logits' graph."""
+    autograd: z.backward(dz) on the logits' graph; over z itself
+    (z.backward(z.detach())) where the operation that made z does not need its
+    output again, as a matrix product does not."""
     zp, did, rows, cols, ld = _matrix(z, "z")
     t = _teacher(t_val, t_idx, t_lse, rows)
     dp, ld_dz = None, 0
@@ -712,6 +724,7 @@ def scape_distill_forward(z, t_val, t_idx, loss, stats, t_lse=None, scale: float
     st = _launch_on(stream, z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, loss=loss, stats=stats, dz=dz,
                     workspace=workspace)
     _check(lib().scape_distill_forward(zp, did, rows, cols, ld, t, scale, wt, lp, sp, dp, ld_dz, wp, wb, st))
+    _wrote(loss, stats, dz)
 
 
 def scape_distill_backward(z, t_val, t_idx, stats, dz, t_lse=None, scale: float = 1.0, weight=None, dloss=None,
@@ -727,6 +740,7 @@ def scape_distill_backward(z, t_val, t_idx, stats, dz, t_lse=None, scale: float 
     gp = _array(dloss, f32, rows, "dloss")
     st = _launch_on(stream, z=z, t_val=t_val, t_idx=t_idx, t_lse=t_lse, weight=weight, stats=stats, dloss=dloss, dz=dz)
     _check(lib().scape_distill_backward(zp, did, rows, cols, ld, t, scale, wt, sp, gp, dp, ld_dz, st))
+    _wrote(dz)
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -781,6 +795,7 @@ def scape_balance_forward(logits, idx, counts, psum, n_tok, loss=None, alpha: fl
                     loss=loss, workspace=workspace)
     _check(lib().scape_balance_forward(zp, did, tokens, experts, ld, ip, k, op, segs, mp, _score(score), alpha, cp, pp,
                                        np_, lp, wp, wb, st))
+    _wrote(counts, psum, n_tok, loss)
 
 
 def scape_balance_loss(counts, psum, n_tok, loss, k: int, alpha: float = 1.0, stream=None) -> None:
@@ -796,6 +811,7 @@ def scape_balance_loss(counts, psum, n_tok, loss, k: int, alpha: float = 1.0, st
     lp = _array(_needed(loss, "loss"), f32, segs, "loss")
     st = _launch_on(stream, counts=counts, psum=psum, n_tok=n_tok, loss=loss)
     _check(lib().scape_balance_loss(cp, pp, np_, segs, experts, k, alpha, lp, st))
+    _wrote(loss)
 
 
 def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha: float = 1.0, offsets=None, mask=None,
@@ -814,3 +830,4 @@ def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha:
                     mask=mask)
     _check(lib().scape_balance_backward(zp, did, tokens, experts, ld, k, op, segs, mp, _score(score), alpha, cp, np_,
                                         gp, dp, ld_d, st))
+    _wrote(dlogits)
