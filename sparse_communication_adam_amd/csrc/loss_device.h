@@ -237,9 +237,6 @@ struct OpSumF {
 struct OpMaxU {
     static __device__ __forceinline__ uint32_t f(uint32_t a, uint32_t b) { return a > b ? a : b; }
 };
-struct OpSumU {
-    static __device__ __forceinline__ uint32_t f(uint32_t a, uint32_t b) { return a + b; }
-};
 
 // All-reduce of a 32-bit value over groups of kLanes consecutive lanes.
 template <class Op, int kLanes, class V>
