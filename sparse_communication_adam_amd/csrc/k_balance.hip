@@ -14,11 +14,12 @@
 // experts stay inside the group.  What bounds the kernels is the read of the
 // logits (and the write of the gradient) and, as the arrays are small, what a
 // launch and a chain of dependent loads take: the loss of 131072x64 f32 (38 MB,
-// 5.6 us at the copy's rate) takes 11.4 us and 5.9 for joining the runs, 10.4
-// without any arithmetic; the gradient of 65536x256 bf16 (67 MB, 10 us) 16.4, of
-// which the vector units are busy 9; that of 4096x60 f32 5.0.  Sums over tokens are held in
-// float32 inside a workgroup's run and in float64 across runs, in a fixed
-// order.
+// 5.6 us at the copy's rate) takes 11.6 us and 5.9 for joining the runs, 10.4
+// without any arithmetic; the gradient of 65536x256 bf16 (67 MB, 10 us) 17.0 with
+// sigmoids, of which the vector units issue for 9; that of 4096x60 f32 4.8.  Sums
+// over tokens are held in float32 inside a workgroup's run (off by 4e-8 of the
+// loss at 131072x64, half a step being 6e-8) and in float64 across runs, in a
+// fixed order.
 #include <float.h>
 
 #include "loss_device.h"
@@ -196,7 +197,7 @@ __device__ __forceinline__ float balance_loss_of(double dot, int32_t n, int32_t 
 }
 
 // The sums over a run of tokens.  kWhole: a run is a segment, and what is left
-// to do for it is done here (2000x8 bf16 in 7 segments: 8.6 us; the two
+// to do for it is done here (2000x8 bf16 in 7 segments: 8.8 us; the two
 // launches took 11.5).  1024 threads, one workgroup a CU: with 512 and twice
 // the runs it takes as long, but the join of twice the runs 1.3 us more.
 template <class T, int kLanes, int kGran, bool kTiny, bool kSoftmax, bool kWhole>
@@ -248,7 +249,8 @@ __global__ __launch_bounds__(kForwardThreads) void k_balance_runs(BalanceArgs a)
         for (int i = 0; i < kBatch; ++i) {
             mine.settle(live[i], g[i]);
             float w[kV], none[kV];
-            const float inv = scores<T, kLanes, kGran, kSoftmax, false>(live[i], g[i], w, none);  // a token that does not count: 0
+            // a token that does not count: 0
+            const float inv = scores<T, kLanes, kGran, kSoftmax, false>(live[i], g[i], w, none);
 #pragma unroll
             for (int v = 0; v < kV; ++v) acc[v] = __builtin_fmaf(w[v], inv, acc[v]);
             tokens += live[i] && l == 0 ? 1u : 0u;
