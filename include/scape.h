@@ -315,6 +315,48 @@ int scape_dense_step(scape_ctx* ctx, float* x, float* m, float* v, const uint16_
 int scape_dense_step_interleaved(scape_ctx* ctx, float* x, float* m, float* v, const uint16_t* g_il, void* stream);
 
 /*
+ * Gradient norms and clipping before a step.  Each worker's gradient is local
+ * in SCAPE (no collective averages it before the mask), so each has a norm of
+ * its own; the norm of the averaged gradient, which no worker knows, is at
+ * most the root mean square of them, which one number a worker makes.
+ *   norm[i] = sqrt(sum over all layers' elements of g_i^2), i < W
+ *   norm[W] = sqrt((norm[0]^2 + ... + norm[W-1]^2) / W)
+ *   layer_norm[i*L + l]: the same of layer l alone (NULL: not wanted)
+ * Squares are summed in float64, in an order that does not depend on the run;
+ * padding elements are not read into them.  NaN and infinities show in the
+ * norms.  norm is fp32 [W+1], layer_norm fp32 [W*L], both 4-byte aligned.  The
+ * workspace is device scratch of the bytes scape_grad_norm_workspace says
+ * (16-byte aligned, contents arbitrary); nothing is allocated, and the calls
+ * can be captured.
+ * Errors: INVALID_ARG, ALIGN, SHAPE (workspace too small, more tiles than a
+ * launch holds), STATE, HIP.
+ */
+int scape_grad_norm(scape_ctx* ctx, const uint16_t* const* g, float* norm, float* layer_norm, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+int scape_grad_norm_interleaved(scape_ctx* ctx, const uint16_t* g_il, float* norm, float* layer_norm,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+int scape_grad_norm_workspace(const scape_ctx* ctx, int64_t* bytes);
+
+/*
+ * out_i = f_i * g_i, rounded to bfloat16 once, with n = norm[i], or norm[W]
+ * for every worker where shared is 1 (all keep their relative weight, and the
+ * direction of the mean does not change), and
+ *   f = max_norm / n  where n > max_norm
+ *   f = 1             where n <= max_norm
+ *   out = +0          where n is NaN or infinite: such a gradient would stay in
+ *                     the residual for good, so the worker sends none
+ * norm as scape_grad_norm writes it, or another number for each worker that
+ * the program has made of it.  out[i] may be g[i] (then nothing is read or
+ * written where f = 1); any other overlap is not allowed.  Padding elements are
+ * not written.  max_norm > 0 and finite.
+ * Errors: INVALID_ARG, ALIGN, STATE, HIP.
+ */
+int scape_grad_clip(scape_ctx* ctx, const uint16_t* const* g, const float* norm, float max_norm, int32_t shared,
+                    uint16_t* const* out, void* stream);
+int scape_grad_clip_interleaved(scape_ctx* ctx, const uint16_t* g_il, const float* norm, float max_norm,
+                                int32_t shared, uint16_t* out_il, void* stream);
+
+/*
  * Mask build alone, from first-moment statistics mtilde (fp32, n_pad): per
  * layer, the k_l positions with the largest |mtilde| (bit pattern order),
  * ties to the lower position ([TS-2] Partitioned Mask Synchronization).
@@ -586,6 +628,103 @@ int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, in
                            const int32_t* offsets, int32_t segments, const uint8_t* mask, int32_t score, float alpha,
                            const int32_t* counts, const int32_t* n_tok, const float* dloss, void* dlogits,
                            int64_t ld_d, void* stream);
+
+/*
+ * Softmax cross entropy over a vocabulary from the last hidden states and the
+ * head's weights.  The logits z = scale * h w^T are made a tile at a time and
+ * never stored.  Per row, with y = label[r]:
+ *   lse[r]  = log sum_c exp(z[r][c])
+ *   loss[r] = weight[r] * (lse[r] - z[r][y])       (weight NULL: 1)
+ * A row whose label is outside [0, cols) or whose weight is 0 does not count:
+ * its loss is 0, whatever it holds (lse[r] is of every row).  A row that counts
+ * and whose logits hold NaN or +inf gives NaN.
+ * h is [rows][dim] and w [cols][dim], both BF16 or both F16, rows ld_h and ld_w
+ * elements apart.  dim, ld_h and ld_w are multiples of 8 and h and w 16-byte
+ * aligned (the matrix instructions' operands are moved 16 bytes at a time).
+ * Products are summed in fp32.  rows <= SCAPE_VOCAB_MAX_ROWS, cols <=
+ * SCAPE_ROW_MAX_COLS, dim <= SCAPE_VOCAB_MAX_DIM, ld <= 2^21.
+ * label int32 [rows], weight, loss and lse fp32 [rows].  rows = 0 enqueues
+ * nothing.  A float32 head is not taken: the matrix instructions for it run at
+ * 1/16 of the rate, where keeping the logits costs little beside making them,
+ * and scape_distill_forward with one entry a row is the loss of stored logits.
+ * Errors: as scape_topk_rows.
+ */
+#define SCAPE_VOCAB_MAX_ROWS 1048576
+#define SCAPE_VOCAB_MAX_DIM 65536
+typedef struct scape_head {
+    const void* h;
+    int64_t ld_h;
+    const void* w;
+    int64_t ld_w;
+    int32_t dtype;
+    int64_t rows, cols, dim;
+    const int32_t* label;
+    const float* weight; /* or NULL */
+    float scale;         /* > 0 */
+} scape_head;
+int scape_vocab_loss_forward(const scape_head* head, float* loss, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+int scape_vocab_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, int64_t* bytes);
+
+/* The gradients of sum_r dloss[r] * loss[r] (dloss NULL: 1), from a forward
+ * call's lse on the same head:
+ *   P[r][c] = dloss[r] * weight[r] * scale * (exp(z[r][c] - lse[r]) - [c = y])
+ *   dh = P w, dw = P^T h
+ * in h's type, rounded once.  Either may be NULL.  The vocabulary is taken in
+ * pieces: the logits of a piece are made again and its P goes to the workspace
+ * in h's type, from where both products take it; its rounding (half a step of 8
+ * or 11 bits a term) is of the size of the gradients' own.  Rows that do not
+ * count, or whose dloss is 0, get dh = 0 and add nothing to dw, whatever h
+ * holds there.  rows = 0 writes dw = 0.  ld_dh and ld_dw are multiples of 8, dh
+ * and dw 16-byte aligned; neither may overlap an input.
+ * Errors: as scape_topk_rows. */
+int scape_vocab_loss_backward(const scape_head* head, const float* lse, const float* dloss, void* dh, int64_t ld_dh,
+                              void* dw, int64_t ld_dw, void* workspace, int64_t workspace_bytes, void* stream);
+int scape_vocab_grad_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, int64_t* bytes);
+
+/*
+ * Tokens to their experts and back.  idx [tokens*k] are a router's choices as
+ * scape_topk_rows writes them (outside [0, experts): none).
+ *   offsets[e] = choices of the experts before e; offsets[experts] = all
+ *   row[t*k + j] = the place of choice (t, j) when all are sorted by expert and
+ *     within one by (t, j); -1 for none
+ * so that expert e's tokens are rows offsets[e] .. offsets[e+1]-1 of what
+ * scape_expert_gather lays out.  1 <= experts <= SCAPE_EXPERT_MAX, k >= 1,
+ * tokens * k < 2^31; a choice may repeat.  tokens = 0 writes offsets = 0.
+ * Errors: as scape_topk_rows.
+ */
+#define SCAPE_EXPERT_MAX 1024
+int scape_expert_sort(const int32_t* idx, int64_t tokens, int32_t k, int32_t experts, int32_t* offsets, int32_t* row,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+int scape_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, int64_t* bytes);
+
+/* y[row[t*k + j]] = x[t] for every place in [0, rows); places outside it are
+ * none.  The places are distinct, as scape_expert_sort makes them.  Rows of y
+ * that no place names stay as they were.  x [tokens][dim] and y [rows][dim] of
+ * one of the three types, rows ld_x and ld_y >= dim elements apart, aligned to
+ * their element; they do not overlap.  dim >= 1; tokens <= 2^25.
+ * Its gradient is scape_expert_combine of dy without weights.
+ * Errors: as scape_topk_rows. */
+int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t dim, int64_t ld_x, const int32_t* row,
+                        int32_t k, void* y, int64_t rows, int64_t ld_y, void* stream);
+
+/* out[t] = sum_j weight[t*k + j] * y[row[t*k + j]] (weight fp32, NULL: 1), in
+ * fp32 in the order of j, rounded once.  A place outside [0, rows) and one with
+ * weight 0 add nothing, whatever is there; a token without any gets 0.
+ * Errors: as scape_topk_rows. */
+int scape_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y, const int32_t* row,
+                         const float* weight, int64_t tokens, int32_t k, void* out, int64_t ld_out, void* stream);
+
+/* Its gradients from dout [tokens][dim]:
+ *   dy[row[t*k + j]] = weight[t*k + j] * dout[t]   (+0 where the weight is 0)
+ *   dweight[t*k + j] = sum_c y[row[t*k + j]][c] * dout[t][c], fp32; 0 for none
+ * Either may be NULL (without dweight, y is not read and may be).  The places
+ * are distinct.  Rows of dy that no place names stay as they were.  dy may be y
+ * (then ld_dy = ld_y); any other overlap is not allowed.
+ * Errors: as scape_topk_rows. */
+int scape_expert_combine_backward(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y,
+                                  const int32_t* row, const float* weight, const void* dout, int64_t ld_dout,
+                                  int64_t tokens, int32_t k, void* dy, int64_t ld_dy, float* dweight, void* stream);
 
 #ifdef __cplusplus
 }

@@ -4,8 +4,9 @@ The data-parallel hot path of SCAPE ("SCAPE: Accurate and Efficient LLM
 Training with Extreme Sparse Communication") as hand-written HIP kernels
 behind a C ABI (include/scape.h, libscape.so); this package is the Python
 binding with the same entry-point names.  Beside the step: the losses whose
-gradients it takes in (distillation from a teacher's top logits, a router's
-balance loss) and the row top-k that feeds them.
+gradients it takes in (cross entropy over a vocabulary, distillation from a
+teacher's top logits, a router's balance loss), the row top-k that feeds them,
+tokens laid out by expert and back, and the gradients' norms and clipping.
 """
 from ._scape import (  # noqa: F401
     LIB_PATH, PHASES, Context, Layout, Mask, ScapeConfig, ScapeError, alloc_mask, lib, scape_dense_step, scape_destroy,
@@ -19,6 +20,11 @@ from ._scape import (  # noqa: F401
     scape_topk_rows, scape_topk_rows_workspace_bytes, scape_distill_forward, scape_distill_backward,
     scape_distill_workspace_bytes, scape_balance_forward, scape_balance_loss, scape_balance_backward,
     scape_balance_workspace_bytes,
+    scape_vocab_loss_forward, scape_vocab_loss_backward, scape_vocab_loss_workspace_bytes,
+    scape_expert_sort, scape_expert_sort_workspace_bytes, scape_expert_gather, scape_expert_combine,
+    scape_expert_combine_backward,
+    scape_grad_norm, scape_grad_norm_interleaved, scape_grad_norm_workspace_bytes, scape_grad_clip,
+    scape_grad_clip_interleaved,
     scape_version)
 
 

@@ -50,6 +50,12 @@ class _Teacher(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("k", ctypes.c_int32)]
 
 
+class _Head(ctypes.Structure):
+    _fields_ = [("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64), ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("label", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
 class _Mask(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("block_prefix", ctypes.c_void_p)]
 
@@ -63,6 +69,7 @@ def lib() -> ctypes.CDLL:
         vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         f32 = ctypes.c_float
         cfgp, maskp, teachp = ctypes.POINTER(_Config), ctypes.POINTER(_Mask), ctypes.POINTER(_Teacher)
+        headp = ctypes.POINTER(_Head)
         sig = {
             "scape_version": [vp, vp],
             "scape_layout": [cfgp, vp, vp, vp, vp, vp],
@@ -101,6 +108,20 @@ def lib() -> ctypes.CDLL:
             "scape_balance_workspace": [i64, i32, i32, vp],
             "scape_balance_loss": [vp, vp, vp, i32, i32, i32, f32, vp, vp],
             "scape_balance_backward": [vp, i32, i64, i32, i64, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp, i64, vp],
+            "scape_grad_norm": [vp, vp, vp, vp, vp, i64, vp],
+            "scape_grad_norm_interleaved": [vp, vp, vp, vp, vp, i64, vp],
+            "scape_grad_norm_workspace": [vp, vp],
+            "scape_grad_clip": [vp, vp, vp, f32, i32, vp, vp],
+            "scape_grad_clip_interleaved": [vp, vp, vp, f32, i32, vp, vp],
+            "scape_vocab_loss_forward": [headp, vp, vp, vp, i64, vp],
+            "scape_vocab_loss_workspace": [i32, i64, i64, i64, vp],
+            "scape_vocab_loss_backward": [headp, vp, vp, vp, i64, vp, i64, vp, i64, vp],
+            "scape_vocab_grad_workspace": [i32, i64, i64, i64, vp],
+            "scape_expert_sort": [vp, i64, i32, i32, vp, vp, vp, i64, vp],
+            "scape_expert_sort_workspace": [i64, i32, i32, vp],
+            "scape_expert_gather": [vp, i32, i64, i64, i64, vp, i32, vp, i64, i64, vp],
+            "scape_expert_combine": [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp],
+            "scape_expert_combine_backward": [vp, i32, i64, i64, i64, vp, vp, vp, i64, i64, i32, vp, i64, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -446,6 +467,91 @@ def scape_dense_step_interleaved(ctx: Context, x, m, v, g_il, stream=None) -> No
     vp = _dev(v, torch.float32, n, "v")
     gp = _dev(g_il, (torch.int16, torch.bfloat16, torch.uint16), n * W, "g_il")
     _check(lib().scape_dense_step_interleaved(ctx.handle, xp, mp, vp, gp, _stream(stream)))
+
+
+_BF16_BITS = None
+
+
+def _bits16():
+    """The dtypes a bfloat16 gradient's bits may have."""
+    global _BF16_BITS
+    if _BF16_BITS is None:
+        t = _torch()
+        _BF16_BITS = (t.int16, t.bfloat16, t.uint16)
+    return _BF16_BITS
+
+
+def _worker_grads(ctx: Context, g, name: str) -> ctypes.Array:
+    if isinstance(g, _torch().Tensor) or len(g) != ctx.cfg.workers:
+        raise ValueError(f"{name} needs {ctx.cfg.workers} tensors")
+    for i, t in enumerate(g):
+        _shape(t, _bits16(), ctx.layout.n_pad, f"{name}[{i}]")
+    return _ptr_array([t.data_ptr() for t in g])
+
+
+def _interleaved_grads(ctx: Context, g, name: str) -> int:
+    _shape(g, _bits16(), ctx.layout.n_pad * ctx.cfg.workers, name)
+    return g.data_ptr()
+
+
+def scape_grad_norm_workspace_bytes(ctx: Context) -> int:
+    """Bytes of workspace scape_grad_norm needs with this context."""
+    b = ctypes.c_int64()
+    _check(lib().scape_grad_norm_workspace(ctx.handle, ctypes.byref(b)))
+    return b.value
+
+
+def _grad_norm(ctx: Context, call, gp, grads: dict, norm, layer_norm, workspace, stream) -> None:
+    W, L = ctx.cfg.workers, len(ctx.layout.layer_offset)
+    np_ = _array(_needed(norm, "norm"), _TORCH.float32, W + 1, "norm")
+    lp = _array(layer_norm, _TORCH.float32, W * L, "layer_norm")
+    wp, wb = _workspace(workspace, lambda: scape_grad_norm_workspace_bytes(ctx))
+    st = _launch_on(stream, norm=norm, layer_norm=layer_norm, workspace=workspace, **grads)
+    _check(call(ctx.handle, gp, np_, lp, wp, wb, st))
+    _wrote(norm, layer_norm)
+
+
+def scape_grad_norm(ctx: Context, g: Sequence, norm, layer_norm=None, workspace=None, stream=None) -> None:
+    """norm fp32 [W+1]: the norm of each worker's gradient over all layers, and
+    the root mean square of them, an upper bound of the norm of their mean;
+    layer_norm fp32 [W, layers] where given."""
+    gp = _worker_grads(ctx, g, "g")
+    _grad_norm(ctx, lib().scape_grad_norm, gp, {f"g[{i}]": t for i, t in enumerate(g)}, norm, layer_norm, workspace,
+               stream)
+
+
+def scape_grad_norm_interleaved(ctx: Context, g_il, norm, layer_norm=None, workspace=None, stream=None) -> None:
+    """scape_grad_norm of gradients in the worker-interleaved layout."""
+    _torch()
+    gp = _interleaved_grads(ctx, g_il, "g_il")
+    _grad_norm(ctx, lib().scape_grad_norm_interleaved, gp, {"g_il": g_il}, norm, layer_norm, workspace, stream)
+
+
+def scape_grad_clip(ctx: Context, g: Sequence, norm, max_norm: float, out: Optional[Sequence] = None,
+                    shared: bool = False, stream=None) -> None:
+    """out = g scaled down to max_norm where its norm is above it (out=None: in
+    place): each worker by its own norm[i], or with shared=True all by norm[W],
+    the root mean square.  A gradient whose norm is not finite becomes 0."""
+    gp = _worker_grads(ctx, g, "g")
+    op = gp if out is None else _worker_grads(ctx, out, "out")
+    np_ = _array(_needed(norm, "norm"), _TORCH.float32, ctx.cfg.workers + 1, "norm")
+    to = g if out is None else out
+    st = _launch_on(stream, norm=norm, **{f"g[{i}]": t for i, t in enumerate(g)},
+                    **{f"out[{i}]": t for i, t in enumerate(to)})
+    _check(lib().scape_grad_clip(ctx.handle, gp, np_, max_norm, int(bool(shared)), op, st))
+    _wrote(*to)
+
+
+def scape_grad_clip_interleaved(ctx: Context, g_il, norm, max_norm: float, out=None, shared: bool = False,
+                                stream=None) -> None:
+    """scape_grad_clip of gradients in the worker-interleaved layout."""
+    _torch()
+    out = g_il if out is None else out
+    gp, op = _interleaved_grads(ctx, g_il, "g_il"), _interleaved_grads(ctx, out, "out")
+    np_ = _array(_needed(norm, "norm"), _TORCH.float32, ctx.cfg.workers + 1, "norm")
+    st = _launch_on(stream, norm=norm, g_il=g_il, out=out)
+    _check(lib().scape_grad_clip_interleaved(ctx.handle, gp, np_, max_norm, int(bool(shared)), op, st))
+    _wrote(out)
 
 
 def interleaved_view(t, W: int):
@@ -831,3 +937,155 @@ def scape_balance_backward(logits, counts, n_tok, dloss, dlogits, k: int, alpha:
     _check(lib().scape_balance_backward(zp, did, tokens, experts, ld, k, op, segs, mp, _score(score), alpha, cp, np_,
                                         gp, dp, ld_d, st))
     _wrote(dlogits)
+
+
+# ----------------------------------------------------------------------------
+# vocabulary loss: cross entropy from hidden states and head weights
+
+
+def _head(h, w, label, weight, scale) -> _Head:
+    """The C struct, after checking its tensors."""
+    hp, did, rows, dim, ld_h = _matrix(h, "h")
+    wp, wid, cols, w_dim, ld_w = _matrix(w, "w")
+    if wid != did or w_dim != dim:
+        raise ValueError(f"w must be [cols, {dim}] of {h.dtype} (got {tuple(w.shape)}, {w.dtype})")
+    lp = _array(_needed(label, "label"), _TORCH.int32, rows, "label")
+    return _Head(hp, ld_h, wp, ld_w, did, rows, cols, dim, lp, _array(weight, _TORCH.float32, rows, "weight"), scale)
+
+
+def scape_vocab_loss_workspace_bytes(h, w, grad: bool = False) -> int:
+    """Bytes of workspace scape_vocab_loss_forward (grad=False) or
+    scape_vocab_loss_backward (grad=True) needs for h [rows, dim] and w [cols,
+    dim]."""
+    _, did, rows, dim, _ = _matrix(h, "h")
+    cols = _matrix(w, "w")[2]
+    b = ctypes.c_int64()
+    query = lib().scape_vocab_grad_workspace if grad else lib().scape_vocab_loss_workspace
+    _check(query(did, rows, cols, dim, ctypes.byref(b)))
+    return b.value
+
+
+def scape_vocab_loss_forward(h, w, label, loss, lse, scale: float = 1.0, weight=None, workspace=None,
+                             stream=None) -> None:
+    """loss = weight * (lse - z[label]) per row, z = scale * h w^T never stored:
+    h [rows, dim] and w [cols, dim] bfloat16 or float16, label int32 [rows] (one
+    outside [0, cols): the row does not count), loss and lse fp32 [rows]."""
+    head = _head(h, w, label, weight, scale)
+    f32 = _TORCH.float32
+    lp = _array(_needed(loss, "loss"), f32, head.rows, "loss")
+    sp = _array(_needed(lse, "lse"), f32, head.rows, "lse")
+    wp, wb = _workspace(workspace, lambda: scape_vocab_loss_workspace_bytes(h, w))
+    st = _launch_on(stream, h=h, w=w, label=label, weight=weight, loss=loss, lse=lse, workspace=workspace)
+    _check(lib().scape_vocab_loss_forward(head, lp, sp, wp, wb, st))
+    _wrote(loss, lse)
+
+
+def scape_vocab_loss_backward(h, w, label, lse, dh=None, dw=None, scale: float = 1.0, weight=None, dloss=None,
+                              workspace=None, stream=None) -> None:
+    """dh and dw (of h's and w's dtype and shape, either may be left out): the
+    gradients of sum(dloss * loss), from the lse of a forward call on the same
+    h, w, label, scale and weight.  For autograd: hidden.backward(dh) on the
+    hidden states' graph, and dw added to the weights' gradient."""
+    head = _head(h, w, label, weight, scale)
+    hp, ld_dh, wp_, ld_dw = None, 0, None, 0
+    if dh is not None:
+        hp, _, _, _, ld_dh = _matrix(dh, "dh", like=h)
+    if dw is not None:
+        wp_, _, _, _, ld_dw = _matrix(dw, "dw", like=w)
+    f32 = _TORCH.float32
+    sp = _array(_needed(lse, "lse"), f32, head.rows, "lse")
+    gp = _array(dloss, f32, head.rows, "dloss")
+    wp, wb = _workspace(workspace, lambda: scape_vocab_loss_workspace_bytes(h, w, grad=True))
+    st = _launch_on(stream, h=h, w=w, label=label, weight=weight, lse=lse, dloss=dloss, dh=dh, dw=dw,
+                    workspace=workspace)
+    _check(lib().scape_vocab_loss_backward(head, sp, gp, hp, ld_dh, wp_, ld_dw, wp, wb, st))
+    _wrote(dh, dw)
+
+
+# ----------------------------------------------------------------------------
+# tokens to their experts and back
+
+
+def _choices(t, name: str):
+    """(pointer, tokens, k) of an int32 tensor [tokens, k]."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a tensor of [tokens, k]")
+    tokens, k = t.shape
+    return _array(t, _TORCH.int32, tokens * k, name), tokens, k
+
+
+def scape_expert_sort_workspace_bytes(idx, experts: int) -> int:
+    """Bytes of workspace scape_expert_sort needs for idx [tokens, k]."""
+    _, tokens, k = _choices(idx, "idx")
+    b = ctypes.c_int64()
+    _check(lib().scape_expert_sort_workspace(tokens, k, int(experts), ctypes.byref(b)))
+    return b.value
+
+
+def scape_expert_sort(idx, experts: int, offsets, row, workspace=None, stream=None) -> None:
+    """The places of the choices idx (int32 [tokens, k]; outside [0, experts):
+    none) in a stable sort by expert: row (int32, tokens*k; -1 for none) and
+    offsets (int32 [experts + 1]), expert e's being offsets[e]..offsets[e+1]-1."""
+    ip, tokens, k = _choices(idx, "idx")
+    i32 = _TORCH.int32
+    op = _array(_needed(offsets, "offsets"), i32, experts + 1, "offsets")
+    rp = _array(_needed(row, "row"), i32, tokens * k, "row")
+    wp, wb = _workspace(workspace, lambda: scape_expert_sort_workspace_bytes(idx, experts))
+    st = _launch_on(stream, idx=idx, offsets=offsets, row=row, workspace=workspace)
+    _check(lib().scape_expert_sort(ip, tokens, k, experts, op, rp, wp, wb, st))
+    _wrote(offsets, row)
+
+
+def _same_rows(t, name: str, like, rows=None):
+    """A matrix of `like`'s dtype and row length (and of `rows` rows)."""
+    m = _matrix(t, name)
+    if t.dtype is not like.dtype or m[3] != like.shape[1] or (rows is not None and m[2] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {like.shape[1]}] of {like.dtype} "
+                         f"(got {tuple(t.shape)}, {t.dtype})")
+    return m
+
+
+def scape_expert_gather(x, row, y, stream=None) -> None:
+    """y[row[t, j]] = x[t]: the tokens x [tokens, dim] laid out by expert, row
+    as scape_expert_sort writes it ([tokens, k], places distinct).  Rows of y
+    that no place names stay as they were."""
+    rp, tokens, k = _choices(row, "row")
+    xp, did, n, dim, ld_x = _matrix(x, "x")
+    if n != tokens:
+        raise ValueError(f"x and row must have as many rows (got {n} and {tokens})")
+    yp, _, rows, _, ld_y = _same_rows(y, "y", x)
+    st = _launch_on(stream, x=x, row=row, y=y)
+    _check(lib().scape_expert_gather(xp, did, tokens, dim, ld_x, rp, k, yp, rows, ld_y, st))
+    _wrote(y)
+
+
+def scape_expert_combine(y, row, out, weight=None, stream=None) -> None:
+    """out[t] = sum_j weight[t, j] * y[row[t, j]] (weight fp32 [tokens, k], None:
+    1): the experts' outputs back in the tokens' order, and without weights the
+    gradient of scape_expert_gather."""
+    rp, tokens, k = _choices(row, "row")
+    yp, did, rows, dim, ld_y = _matrix(y, "y")
+    op, _, _, _, ld_out = _same_rows(out, "out", y, tokens)
+    wp = _array(weight, _TORCH.float32, tokens * k, "weight")
+    st = _launch_on(stream, y=y, row=row, out=out, weight=weight)
+    _check(lib().scape_expert_combine(yp, did, rows, dim, ld_y, rp, wp, tokens, k, op, ld_out, st))
+    _wrote(out)
+
+
+def scape_expert_combine_backward(y, row, dout, dy=None, weight=None, dweight=None, stream=None) -> None:
+    """The gradients of scape_expert_combine from dout [tokens, dim]: dy (y's
+    dtype and shape, may be y; rows that no place names stay as they were) and
+    dweight (fp32 [tokens, k]).  Either may be left out."""
+    rp, tokens, k = _choices(row, "row")
+    yp, did, rows, dim, ld_y = _matrix(y, "y")
+    gp, _, _, _, ld_dout = _same_rows(dout, "dout", y, tokens)
+    dp, ld_dy = None, 0
+    if dy is not None:
+        dp, _, _, _, ld_dy = _same_rows(dy, "dy", y, rows)
+    f32 = _TORCH.float32
+    wp = _array(weight, f32, tokens * k, "weight")
+    dwp = _array(dweight, f32, tokens * k, "dweight")
+    st = _launch_on(stream, y=y, row=row, dout=dout, dy=dy, weight=weight, dweight=dweight)
+    _check(lib().scape_expert_combine_backward(yp, did, rows, dim, ld_y, rp, wp, gp, ld_dout, tokens, k, dp, ld_dy, dwp,
+                                               st))
+    _wrote(dy, dweight)

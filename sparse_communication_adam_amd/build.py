@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libscape.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["k_elementwise.hip", "k_select.hip", "k_bits.hip", "k_topk.hip", "k_distill.hip", "k_balance.hip",
-           "scape_api.cpp", "loss_api.cpp"]
+           "k_vocab.hip", "k_gradnorm.hip", "k_expert.hip", "scape_api.cpp", "loss_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,590 @@
+// k_vocab.hip - softmax cross entropy over a vocabulary from hidden states
+// h [rows][dim] and head weights w [cols][dim], without the logits: their
+// products live in registers, tile by tile.
+//
+//   z = scale * h w^T;  lse = log sum exp z;  loss = weight (lse - z[label])
+//   P = g (exp(z - lse) - onehot), g = weight * dloss * scale
+//   dh = P w;  dw = P^T h
+//
+// Three matrix products over one tile loop.  The logits' tile has the words as
+// MFMA rows and the tokens as its columns, so a lane holds words of one token
+// and the row statistics are sums in registers.  The backward pass takes the
+// vocabulary in pieces: P of a piece goes to the workspace in 16 bits, and both
+// gradients read it from there.
+#include "loss_device.h"
+
+namespace scape {
+
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char lds_t;
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <class T>
+__device__ __forceinline__ f4 mfma(const s8& a, const s8& b, const f4& c) {
+    if constexpr (std::is_same<T, BF16>::value) {
+        typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    } else {
+        typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+}
+
+constexpr int kStep = 64;                       // elements of the summed axis in a tile
+constexpr uint32_t kOutside = 0x80000000u;      // an offset that the resource's bound turns into zeros
+constexpr uint32_t kRawBuffer = 0x00027000u;
+
+// One operand of a product: rows of 16-bit elements, ld apart.  Along: the
+// summed axis lies along the rows (extent rows of them); else it runs over
+// rows of `extent` elements.
+struct Side {
+    const char* p;
+    int64_t ld, extent, depth;  // depth: elements of the summed axis
+};
+
+// Moves a tile of kR x 64 from memory to LDS, 16 bytes a lane, and reads MFMA
+// fragments of it.  The load writes LDS in lane order, so the lanes' addresses
+// are permuted instead: the 16-byte pieces of a row are exchanged by an XOR
+// that spreads what one fragment read touches over all banks.
+template <bool kAlong, int kR, int kThreads>
+struct Stage {
+    static constexpr int kBytes = kR * 2 * kStep;
+    static constexpr int kPieces = kBytes / 16;
+    static constexpr int kLoads = kPieces > kThreads ? kPieces / kThreads : 1;
+    static constexpr int kRow = kAlong ? kStep * 2 : kR * 2;  // bytes
+    static constexpr int kRowPieces = kRow / 16;
+    uint32_t off[kLoads];
+    bool on;
+
+    // what the pieces of row k are exchanged by; the same for k, k + 4 (k % 8
+    // < 4) and k + 32, which a fragment's reads are apart
+    static __device__ __forceinline__ uint32_t turn(uint32_t k) {
+        if constexpr (kAlong) return k & 7u;
+        if constexpr (kR >= 128) return ((k & 3u) | ((k >> 3) & 1u) << 2) << 1;
+        if constexpr (kR == 64) return (((k >> 1) & 1u) | ((k >> 3) & 1u) << 1) << 1;
+        if constexpr (kR == 32) return ((k >> 3) & 1u) << 1;
+        return 0;
+    }
+
+    __device__ __forceinline__ void init(uint32_t tid, int64_t ld) {
+        on = tid < (uint32_t)kPieces;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t q = (uint32_t)i * kThreads + tid, row = q / kRowPieces, pos = q % kRowPieces;
+            off[i] = row * (uint32_t)(ld * 2) + ((pos ^ turn(row)) << 4);
+        }
+    }
+
+    // The tile at row (or column) r0 and depth k.
+    __device__ __forceinline__ void load(const Side& s, int64_t r0, int64_t k, uint32_t tid, lds_t* to) const {
+        int64_t base, rows, width;
+        if constexpr (kAlong) {
+            base = r0 * s.ld + k;
+            rows = s.extent - r0 < kR ? s.extent - r0 : kR;
+            width = s.depth - k;
+        } else {
+            base = k * s.ld + r0;
+            rows = s.depth - k < kStep ? s.depth - k : kStep;
+            width = s.extent - r0;
+        }
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.p) + base * 2, 0,
+                                                            (int)(((rows - 1) * s.ld + width) * 2), kRawBuffer);
+        uint32_t kill = 0;  // pieces behind the end of the summed axis are zeros
+        if constexpr (kAlong) {
+            if (width < kStep) {
+                const uint32_t row = tid / kRowPieces, pos = tid % kRowPieces;  // alike for every i: kThreads / 8 is a multiple of 8
+                if ((int)((pos ^ turn(row)) * 8) >= (int)width) kill = kOutside;
+            }
+        }
+        if (kPieces >= kThreads || on) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                lds_t* const at = to + (i * kThreads + (int)(tid & ~63u)) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, off[i] | kill, 0, 0, 0);
+            }
+        }
+    }
+
+    // Where a lane reads fragment f of the wave's rows (from r0) in half-step h.
+    static __device__ __forceinline__ uint32_t at(uint32_t lane, uint32_t r0, int h) {
+        if constexpr (kAlong) {
+            const uint32_t row = r0 + (lane & 15u);
+            return row * kRow + ((((uint32_t)h * 4 + (lane >> 4)) ^ turn(row)) << 4);
+        } else {
+            const uint32_t k = (uint32_t)h * 32 + (lane >> 4) * 8 + ((lane & 15u) >> 2), c = lane & 3u;
+            return k * kRow + (((r0 / 8 + (c >> 1)) ^ turn(k)) << 4) + (c & 1u) * 8;
+        }
+    }
+    static __device__ __forceinline__ s8 read(const lds_t* p) {
+        if constexpr (kAlong) {
+            return *reinterpret_cast<const __attribute__((address_space(3))) s8*>(p);
+        } else {
+            typedef __attribute__((address_space(3))) s4 lds_s4;
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)const_cast<lds_t*>(p));
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)const_cast<lds_t*>(p + 4 * kRow));
+            return s8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+    }
+};
+
+// A workgroup's tile of a product: kM x kN over kWM x kWN waves.
+template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN>
+struct Tile {
+    static constexpr int kThreads = kWM * kWN * 64;
+    static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part
+    static constexpr int kFM = kTM / 16, kFN = kTN / 16;
+    using A = Stage<kAlongA, kM, kThreads>;
+    using B = Stage<kAlongB, kN, kThreads>;
+    static constexpr int kStage = A::kBytes + B::kBytes;
+    static constexpr int kLds = 2 * kStage;
+    f4 acc[kFM][kFN];
+
+    __device__ __forceinline__ void run(const Side& a, const Side& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1,
+                                        lds_t* lds) {
+        const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+        const uint32_t wm = (wave % kWM) * kTM, wn = (wave / kWM) * kTN;
+        A la;
+        B lb;
+        la.init(tid, a.ld);
+        lb.init(tid, b.ld);
+        uint32_t ra[2][kFM], rb[2][kFN];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int f = 0; f < kFM; ++f) ra[h][f] = A::at(lane, wm + f * 16, h);
+#pragma unroll
+            for (int f = 0; f < kFN; ++f) rb[h][f] = A::kBytes + B::at(lane, wn + f * 16, h);
+        }
+#pragma unroll
+        for (int i = 0; i < kFM; ++i)
+#pragma unroll
+            for (int j = 0; j < kFN; ++j) acc[i][j] = f4{0, 0, 0, 0};
+        fetch(a, b, m0, n0, k0, la, lb, lds);
+        __syncthreads();
+        for (int64_t k = k0; k < k1; k += 2 * kStep) {
+            if (k + kStep < k1) fetch(a, b, m0, n0, k + kStep, la, lb, lds + kStage);
+            multiply(ra, rb, lds);
+            __syncthreads();
+            if (k + kStep >= k1) break;
+            if (k + 2 * kStep < k1) fetch(a, b, m0, n0, k + 2 * kStep, la, lb, lds);
+            multiply(ra, rb, lds + kStage);
+            __syncthreads();
+        }
+    }
+    static __device__ __forceinline__ void fetch(const Side& a, const Side& b, int64_t m0, int64_t n0, int64_t k, const A& la,
+                                                 const B& lb, lds_t* to) {
+        la.load(a, m0, k, threadIdx.x, to);
+        lb.load(b, n0, k, threadIdx.x, to + A::kBytes);
+    }
+    __device__ __forceinline__ void multiply(const uint32_t (&ra)[2][kFM], const uint32_t (&rb)[2][kFN], const lds_t* from) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s8 fa[kFM], fb[kFN];
+#pragma unroll
+            for (int i = 0; i < kFM; ++i) fa[i] = A::read(from + ra[h][i]);
+#pragma unroll
+            for (int j = 0; j < kFN; ++j) fb[j] = B::read(from + rb[h][j]);
+#pragma unroll
+            for (int i = 0; i < kFM; ++i)
+#pragma unroll
+                for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
+        }
+    }
+    // The wave's first row and column in the tile, and the lane's of a fragment.
+    static __device__ __forceinline__ uint32_t wave_m() { return ((threadIdx.x >> 6) % kWM) * kTM; }
+    static __device__ __forceinline__ uint32_t wave_n() { return ((threadIdx.x >> 6) / kWM) * kTN; }
+    static __device__ __forceinline__ uint32_t lane_m() { return (lane_id() >> 4) * 4; }
+    static __device__ __forceinline__ uint32_t lane_n() { return lane_id() & 15u; }
+};
+
+// Block b of a grid of nm x nn tiles.  Workgroups of one XCD, which share an
+// L2, take runs of blocks; a run walks bands of kBand tiles of the n axis, all
+// of the m axis for each.
+constexpr uint32_t kBand = 8;
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, uint32_t& m, uint32_t& n) {
+    b = xcd_block(b, nm * nn);
+    const uint32_t band = b / (kBand * nm), first = band * kBand, in = b - band * kBand * nm;
+    const uint32_t wide = nn - first < kBand ? nn - first : kBand;
+    n = first + in % wide;
+    m = in / wide;
+}
+
+// ---------------------------------------------------------------------------
+// The loss: each tile's reference and sum of a token, and the label's logit.
+
+template <class T, int kM, int kN, int kWM, int kWN>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
+    using G = Tile<T, true, true, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, a.tiles_v, a.tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    G g;
+    g.run(Side{(const char*)a.w, a.ld_w, a.cols, a.dim}, Side{(const char*)a.h, a.ld_h, a.rows, a.dim}, m0, n0, 0, a.dim,
+          (lds_t*)lds);
+    // the loop's last barrier is behind every read of the tiles
+    float2* const red = reinterpret_cast<float2*>(lds);  // [kWM][kN]
+    const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
+    const int32_t left = (int32_t)(a.cols - m0) - (int32_t)lm;  // words from the lane's first on
+    const bool ragged = a.cols - m0 < kM;
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) {
+        const int64_t n = n0 + ln + j * 16;
+        const bool row = n < a.rows;
+        const int32_t label = row ? a.label[n] : -1, lab = label - (int32_t)(m0 + lm);  // of the lane's words
+        if (ragged) {
+#pragma unroll
+            for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i * 16 + e >= left) g.acc[i][j][e] = kNegInf;
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, g.acc[i][j][e]);
+        // In base 2, against a reference that is a rounded product itself: the
+        // fused multiply-add rounds each exponent once, and whatever the
+        // reference's own rounding was stands in the reference.
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float ref = top == kNegInf ? 0.0f : top * a.c2;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i) {
+            s0 += fast_exp2(__builtin_fmaf(g.acc[i][j][0], a.c2, -ref));
+            s1 += fast_exp2(__builtin_fmaf(g.acc[i][j][1], a.c2, -ref));
+            s0 += fast_exp2(__builtin_fmaf(g.acc[i][j][2], a.c2, -ref));
+            s1 += fast_exp2(__builtin_fmaf(g.acc[i][j][3], a.c2, -ref));
+        }
+        float sum = s0 + s1;
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        if (lane_id() < 16) red[(G::wave_m() / G::kTM) * kN + ln + j * 16] = float2{ref, sum};
+        if (label >= 0 && lab >= 0 && lab < G::kTM && (lab & 15) < 4 && lab < left) {
+            float at = 0.0f;
+#pragma unroll
+            for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) at = lab == i * 16 + e ? g.acc[i][j][e] : at;
+            a.at_label[n] = at;
+        }
+    }
+    __syncthreads();
+    for (uint32_t t = threadIdx.x; t < (uint32_t)kN; t += G::kThreads) {
+        float2 r = red[t];
+#pragma unroll
+        for (int w = 1; w < kWM; ++w) {
+            const float2 q = red[w * kN + t];
+            const float ref = fmaxf(r.x, q.x);
+            r.y = r.y * fast_exp2(r.x - ref) + q.y * fast_exp2(q.x - ref);
+            r.x = ref;
+        }
+        if (n0 + t < a.rows) a.part[(int64_t)tm * a.rows + n0 + t] = r;
+    }
+}
+
+// Joins a token's tiles: 16 tokens a workgroup, 64 threads each.
+constexpr int kJoinTokens = 16, kJoinParts = 64;
+__global__ __launch_bounds__(kJoinTokens* kJoinParts) void k_vocab_join(VocabArgs a) {
+    __shared__ float2 red[kJoinParts][kJoinTokens];
+    const uint32_t t = threadIdx.x % kJoinTokens, q = threadIdx.x / kJoinTokens;
+    const int64_t n = (int64_t)blockIdx.x * kJoinTokens + t;
+    float2 r = float2{kLowest, 0.0f};
+    if (n < a.rows)
+        for (uint32_t v = q; v < a.tiles_v; v += kJoinParts) {
+            const float2 p = a.part[(int64_t)v * a.rows + n];
+            const float ref = fmaxf(r.x, p.x);
+            r.y = r.y * fast_exp2(r.x - ref) + p.y * fast_exp2(p.x - ref);
+            r.x = ref;
+        }
+    red[q][t] = r;
+    __syncthreads();
+    for (int w = kJoinParts / 2; w >= 1; w >>= 1) {
+        if (q < (uint32_t)w) {
+            const float2 p = red[q + w][t];
+            r = red[q][t];
+            const float ref = fmaxf(r.x, p.x);
+            r.y = r.y * fast_exp2(r.x - ref) + p.y * fast_exp2(p.x - ref);
+            r.x = ref;
+            red[q][t] = r;
+        }
+        __syncthreads();
+    }
+    if (q != 0 || n >= a.rows) return;
+    const double lse2 = (double)r.x + log2((double)r.y);  // in base 2
+    a.lse[n] = (float)(lse2 * kLn2);
+    const int32_t lab = a.label[n];
+    const float w = a.weight ? a.weight[n] : 1.0f;
+    const bool on = lab >= 0 && lab < a.cols && w != 0.0f;
+    a.loss[n] = on ? (float)((double)w * kLn2 * (lse2 - (double)a.at_label[n] * (double)a.c2)) : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// The gradient.
+
+// Per row: the factor of its P, its log-sum-exp in base 2, and the powers of
+// two that stand beside an fp16 P.  bf16 has float32's range, so P takes the
+// whole factor; an fp16 P is (p - onehot) times a mantissa in [2^14, 2^15), so
+// that p keeps its bits down to 2^-29, and the power of two is put on dh
+// exactly and on the copy of h for dw against the largest of all rows.
+__global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
+    __shared__ int top[16];
+    const uint32_t tid = threadIdx.x;
+    const bool half = a.dtype == SCAPE_DTYPE_F16;
+    const auto factor = [&](int64_t n) {
+        const int32_t lab = a.label[n];
+        if (lab < 0 || lab >= a.cols) return 0.0f;
+        const float w = a.weight ? a.weight[n] : 1.0f, d = a.dloss ? a.dloss[n] : 1.0f;
+        return w == 0.0f || d == 0.0f ? 0.0f : (float)((double)w * (double)d * (double)a.scale);
+    };
+    int best = -10000;
+    if (half)
+        for (int64_t n = tid; n < a.rows; n += 1024) {
+            const float f = factor(n);
+            if (f != 0.0f && __builtin_isfinite(f)) {
+                int e;
+                (void)frexpf(f, &e);
+                best = e > best ? e : best;
+            }
+        }
+    for (int d = 32; d >= 1; d >>= 1) {
+        const int o = __shfl_xor(best, d, 64);
+        best = o > best ? o : best;
+    }
+    if ((tid & 63u) == 0) top[tid >> 6] = best;
+    __syncthreads();
+    for (int i = 0; i < 16; ++i) best = top[i] > best ? top[i] : best;
+    if (tid == 0) a.dw_scale[0] = half && best > -10000 ? ldexpf(1.0f, best - 15) : 1.0f;
+    for (int64_t n = tid; n < a.rows_pad; n += 1024) {
+        VocabRow r{0.0f, 0.0f, 0.0f, 0.0f};
+        const float f = n < a.rows ? factor(n) : 0.0f;
+        if (f != 0.0f) {
+            r.lse2 = a.lse[n] * kLog2e;
+            r.f = f;
+            r.dh = 1.0f;
+            r.copy = 1.0f;
+            if (half && __builtin_isfinite(f)) {
+                int e;
+                r.f = frexpf(f, &e) * 32768.0f;
+                r.dh = ldexpf(1.0f, e - 15);
+                r.copy = ldexpf(1.0f, e - best);
+            }
+        }
+        a.row[n] = r;
+    }
+}
+
+// The rows of h that dw takes: zeros where a row does not count, whatever it
+// holds, and times the row's power of two (fp16).
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
+    const int64_t n = blockIdx.x;
+    const float c = a.row[n].copy;
+    const gran* from = reinterpret_cast<const gran*>((const char*)a.h + n * a.ld_h * 2);
+    gran* to = reinterpret_cast<gran*>((char*)a.h_copy + n * a.dim * 2);
+    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) {
+        gran g = gran{0, 0, 0, 0};
+        if (c != 0.0f) {
+            g = from[i];
+            if constexpr (std::is_same<T, F16>::value) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = T::up(g, j) * c;
+                g = T::down(f);
+            }
+        }
+        to[i] = g;
+    }
+}
+
+// P of a piece of the vocabulary, rounded once to the operands' type: half a
+// step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
+template <class T, int kM, int kN, int kWM, int kWN>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int64_t v0, int64_t v1) {
+    using G = Tile<T, true, true, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, (uint32_t)((v1 - v0 + kM - 1) / kM), a.tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    G g;
+    g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, a.ld_w, v1 - v0, a.dim}, Side{(const char*)a.h, a.ld_h, a.rows, a.dim},
+          m0, n0, 0, a.dim, (lds_t*)lds);
+    const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
+    const int32_t left = (int32_t)(v1 - v0 - m0) - (int32_t)lm, first = (int32_t)(v0 + m0 + lm);
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) {
+        const int64_t n = n0 + ln + j * 16;
+        const VocabRow r = a.row[n];
+        const int32_t lab = r.f != 0.0f ? a.label[n] - first : -1;  // a row that counts has one, and is a row of the matrix
+        char* const to = (char*)a.p + (n * a.ld_p + m0 + lm) * 2;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = fast_exp2(__builtin_fmaf(g.acc[i][j][e], a.c2, -r.lse2));
+                if (lab == i * 16 + e) x -= 1.0f;
+                p[e] = r.f != 0.0f && i * 16 + e < left ? x * r.f : 0.0f;
+            }
+            *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
+        }
+    }
+}
+
+// dh of a piece: [split][rows][dim] sums in float32, split over the words.
+template <class T, int kM, int kN, int kWM, int kWN>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int64_t v0, int64_t v1, bool first) {
+    using G = Tile<T, false, true, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    uint32_t tm, tn;
+    const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
+    const uint32_t split = blockIdx.x / tiles;
+    tile_of(blockIdx.x % tiles, nm, a.tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    const int64_t k0 = (int64_t)split * a.split_words, all = v1 - v0;
+    const int64_t k1 = k0 + a.split_words < all ? k0 + a.split_words : all;
+    if (k0 >= k1 && !first) return;
+    G g;
+    if (k0 < k1) {
+        g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, a.ld_w, a.dim, all},
+              Side{(const char*)a.p, a.ld_p, a.rows_pad, a.ld_p}, m0, n0, k0, k1, (lds_t*)lds);
+    } else {
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+            for (int j = 0; j < G::kFN; ++j) g.acc[i][j] = f4{0, 0, 0, 0};
+    }
+    const int64_t m = m0 + G::wave_m() + G::lane_m(), n1 = n0 + G::wave_n() + G::lane_n();
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) {
+        const int64_t n = n1 + j * 16;
+        if (n >= a.rows) continue;
+        float* const to = a.dh_sum + ((int64_t)split * a.rows + n) * a.dim + m;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+            if (m + i * 16 < a.dim) {
+                f4* const q = reinterpret_cast<f4*>(to + i * 16);
+                *q = first ? g.acc[i][j] : *q + g.acc[i][j];
+            }
+    }
+}
+
+// dh: the splits' sums in order, times the row's power of two, rounded once.
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
+    const int64_t n = blockIdx.x;
+    const float c = a.row[n].dh;
+    gran* to = reinterpret_cast<gran*>((char*)a.dh + n * a.ld_dh * 2);
+    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) {
+        f4 lo = f4{0, 0, 0, 0}, hi = lo;
+        if (c != 0.0f)
+            for (int32_t s = 0; s < a.splits; ++s) {
+                const f4* p = reinterpret_cast<const f4*>(a.dh_sum + ((int64_t)s * a.rows + n) * a.dim) + 2 * i;
+                lo += p[0];
+                hi += p[1];
+            }
+        const float f[8] = {lo[0] * c, lo[1] * c, lo[2] * c, lo[3] * c, hi[0] * c, hi[1] * c, hi[2] * c, hi[3] * c};
+        to[i] = T::down(f);
+    }
+}
+
+// dw of a piece.
+template <class T, int kM, int kN, int kWM, int kWN>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int64_t v0, int64_t v1) {
+    using G = Tile<T, false, false, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)((v1 - v0 + kN - 1) / kN), tm, tn);
+    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    G g;
+    g.run(Side{(const char*)a.h_copy, a.dim, a.dim, a.rows}, Side{(const char*)a.p, a.ld_p, a.ld_p, a.rows_pad}, m0, n0, 0,
+          a.rows, (lds_t*)lds);
+    const float c = a.dw_scale[0];
+    const int64_t m = m0 + G::wave_m() + G::lane_m(), w1 = n0 + G::wave_n() + G::lane_n();
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) {
+        const int64_t v = v0 + w1 + j * 16;
+        if (v >= v1) continue;
+        char* const to = (char*)a.dw + (v * a.ld_dw + m) * 2;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+            if (m + i * 16 < a.dim) {
+                const f4 x = g.acc[i][j] * c;
+                *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+            }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_vocab_zero(VocabArgs a) {  // dw of no rows
+    gran* to = reinterpret_cast<gran*>((char*)a.dw + (int64_t)blockIdx.x * a.ld_dw * 2);
+    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) to[i] = gran{0, 0, 0, 0};
+}
+
+#define SCAPE_RUN(kernel, blocks, threads, ...) \
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(kernel), dim3((uint32_t)(blocks)), dim3(threads), 0, s, __VA_ARGS__)
+
+template <class T>
+hipError_t sums_of(hipStream_t s, const VocabArgs& a) {
+    const int64_t tiles = (int64_t)a.tiles_v * a.tiles_n;
+    switch (a.tile_n) {
+        case 16: SCAPE_RUN((k_vocab_sums<T, 256, 16, 4, 1>), tiles, 256, a); break;
+        case 64: SCAPE_RUN((k_vocab_sums<T, 256, 64, 4, 1>), tiles, 256, a); break;
+        case 128: SCAPE_RUN((k_vocab_sums<T, 256, 128, 4, 2>), tiles, 512, a); break;
+        default: SCAPE_RUN((k_vocab_sums<T, 256, 256, 2, 4>), tiles, 512, a); break;
+    }
+    SCAPE_RUN(k_vocab_join, (a.rows + kJoinTokens - 1) / kJoinTokens, kJoinTokens * kJoinParts, a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
+    if (a.rows == 0) {
+        if (a.dw) SCAPE_RUN(k_vocab_zero<T>, a.cols, kRowThreads, a);
+        return hipGetLastError();
+    }
+    SCAPE_RUN(k_vocab_rows, 1, 1024, a);
+    if (a.dw) SCAPE_RUN(k_vocab_copy<T>, a.rows, kRowThreads, a);
+    const int64_t dim_tiles = (a.dim + 255) / 256;
+    for (int64_t v0 = 0; v0 < a.cols; v0 += a.piece) {
+        const int64_t v1 = v0 + a.piece < a.cols ? v0 + a.piece : a.cols;
+        const int64_t words = (v1 - v0 + 255) / 256, tiles = words * a.tiles_n;
+        switch (a.tile_n) {
+            case 16: SCAPE_RUN((k_vocab_p<T, 256, 16, 4, 1>), tiles, 256, a, v0, v1); break;
+            case 64: SCAPE_RUN((k_vocab_p<T, 256, 64, 4, 1>), tiles, 256, a, v0, v1); break;
+            case 128: SCAPE_RUN((k_vocab_p<T, 256, 128, 4, 2>), tiles, 512, a, v0, v1); break;
+            default: SCAPE_RUN((k_vocab_p<T, 256, 256, 2, 4>), tiles, 512, a, v0, v1); break;
+        }
+        if (a.dh) {
+            const int64_t n = dim_tiles * a.tiles_n * a.splits;
+            const bool first = v0 == 0;
+            switch (a.tile_n) {
+                case 16: SCAPE_RUN((k_vocab_dh<T, 256, 16, 4, 1>), n, 256, a, v0, v1, first); break;
+                case 64: SCAPE_RUN((k_vocab_dh<T, 256, 64, 4, 1>), n, 256, a, v0, v1, first); break;
+                case 128: SCAPE_RUN((k_vocab_dh<T, 256, 128, 4, 2>), n, 512, a, v0, v1, first); break;
+                default: SCAPE_RUN((k_vocab_dh<T, 256, 256, 2, 4>), n, 512, a, v0, v1, first); break;
+            }
+        }
+        if (a.dw) SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4>), dim_tiles * words, 512, a, v0, v1);
+    }
+    if (a.dh) SCAPE_RUN(k_vocab_dh_join<T>, a.rows, kRowThreads, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_vocab_loss(hipStream_t s, const VocabArgs& a) {
+    return a.dtype == SCAPE_DTYPE_BF16 ? sums_of<BF16>(s, a) : sums_of<F16>(s, a);
+}
+
+hipError_t launch_vocab_grad(hipStream_t s, const VocabArgs& a) {
+    return a.dtype == SCAPE_DTYPE_BF16 ? grad_of<BF16>(s, a) : grad_of<F16>(s, a);
+}
+
+}  // namespace scape

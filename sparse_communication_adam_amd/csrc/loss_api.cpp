@@ -1,5 +1,6 @@
-// loss_api.cpp - host side of the loss operators of include/scape.h: row
-// top-k, distillation from a teacher's top logits, router balance loss.
+// loss_api.cpp - host side of the loss and routing operators of
+// include/scape.h: row top-k, distillation from a teacher's top logits, router
+// balance loss, vocabulary loss, tokens to their experts and back.
 // Arguments are validated here, before anything is launched; the operators
 // hold no state and allocate nothing.
 #include "loss_internal.h"
@@ -217,6 +218,136 @@ int check_router(int32_t score, const int32_t* offsets, int32_t segments) {
 int64_t balance_bytes(int64_t tokens, int32_t experts, int32_t segments) {
     const int64_t slots = tokens / forward_run(tokens) + segments;
     return slots * (8 * (int64_t)experts + 4);
+}
+
+// ---- vocabulary loss
+constexpr int64_t kMaxHeadLd = int64_t(1) << 21;  // a tile's offsets stay below 2^31 bytes
+constexpr int64_t kTileWordsV = 256;              // words of a tile
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Tokens of a tile.
+int32_t vocab_tile(int64_t rows) {
+    if (rows <= 16) return 16;
+    if (rows <= 64) return 64;
+    return round_up(rows, 256) * 7 <= round_up(rows, 128) * 8 ? 256 : 128;
+}
+
+int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArgs* a) {
+    if (dtype != SCAPE_DTYPE_BF16 && dtype != SCAPE_DTYPE_F16)
+        return fail(SCAPE_ERR_INVALID_ARG, "the vocabulary loss takes bfloat16 or float16 (got type %d)", dtype);
+    if (rows < 0 || rows > SCAPE_VOCAB_MAX_ROWS)
+        return fail(SCAPE_ERR_SHAPE, "rows must be in 0..%d", SCAPE_VOCAB_MAX_ROWS);
+    if (cols < 1 || cols > SCAPE_ROW_MAX_COLS) return fail(SCAPE_ERR_SHAPE, "cols must be in 1..%d", SCAPE_ROW_MAX_COLS);
+    if (dim < 8 || dim > SCAPE_VOCAB_MAX_DIM || dim % 8)
+        return fail(SCAPE_ERR_SHAPE, "dim must be a multiple of 8 in 8..%d (got %lld)", SCAPE_VOCAB_MAX_DIM, (long long)dim);
+    a->dtype = dtype;
+    a->rows = rows;
+    a->cols = cols;
+    a->dim = dim;
+    a->tile_n = vocab_tile(rows);
+    a->tiles_v = (uint32_t)((cols + kTileWordsV - 1) / kTileWordsV);
+    a->tiles_n = (uint32_t)((rows + a->tile_n - 1) / a->tile_n);
+    a->rows_pad = (int64_t)a->tiles_n * a->tile_n;
+    return SCAPE_OK;
+}
+// The pieces of the backward pass: P of one is at most 2^26 elements, which the
+// last-level cache holds, and at least 4096 words wide, so that dw has tiles
+// for the CUs.  dh's sums are split over the words until there are about two
+// workgroups for each of 256 CUs.
+void vocab_pieces(VocabArgs* a) {
+    int64_t most = a->rows_pad ? (int64_t(1) << 26) / a->rows_pad / kTileWordsV * kTileWordsV : a->cols;
+    if (most < 4096) most = 4096;
+    const int64_t pieces = (a->cols + most - 1) / most;
+    a->piece = round_up((a->cols + pieces - 1) / pieces, kTileWordsV);
+    a->ld_p = a->piece;
+    const int64_t tiles = (a->dim + 255) / 256 * (a->tiles_n ? a->tiles_n : 1);
+    int64_t n = 512 / tiles;
+    if (n > a->piece / 512) n = a->piece / 512;
+    if (n < 1) n = 1;
+    a->split_words = round_up((a->piece + n - 1) / n, 64);
+    a->splits = (int32_t)((a->piece + a->split_words - 1) / a->split_words);
+}
+int64_t vocab_loss_bytes(const VocabArgs& a) {
+    return a.rows * ((int64_t)a.tiles_v * 8 + 4);
+}
+// The workspace of the backward pass, each part a multiple of 16 bytes.
+struct VocabParts {
+    int64_t row, dw_scale, h_copy, p, dh_sum, all;
+};
+VocabParts vocab_parts(const VocabArgs& a) {
+    VocabParts w;
+    w.row = 0;
+    w.dw_scale = w.row + a.rows_pad * (int64_t)sizeof(VocabRow);
+    w.h_copy = w.dw_scale + 16;
+    w.p = w.h_copy + a.rows * a.dim * 2;
+    w.dh_sum = w.p + a.rows_pad * a.ld_p * 2;
+    w.all = a.rows ? w.dh_sum + (int64_t)a.splits * a.rows * a.dim * 4 : 0;
+    return w;
+}
+
+// A matrix that is moved 16 bytes at a time.
+int check_wide(const void* p, int64_t rows, int64_t dim, int64_t ld, const char* name) {
+    if (rows > 0 && !p) return fail(SCAPE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!is_aligned(p, 16)) return fail(SCAPE_ERR_ALIGN, "%s must be 16-byte aligned", name);
+    if (ld < dim) return fail(SCAPE_ERR_SHAPE, "%s: rows of %lld columns are %lld elements apart", name, (long long)dim,
+                              (long long)ld);
+    if (ld > kMaxHeadLd) return fail(SCAPE_ERR_SHAPE, "%s: rows are more than 2^21 elements apart", name);
+    if (ld % 8) return fail(SCAPE_ERR_ALIGN, "%s: rows must be a multiple of 8 elements apart", name);
+    return SCAPE_OK;
+}
+int vocab_head(const scape_head* h, VocabArgs* a) {
+    if (!h) return fail(SCAPE_ERR_INVALID_ARG, "head is NULL");
+    int rc;
+    if ((rc = vocab_shape(h->dtype, h->rows, h->cols, h->dim, a))) return rc;
+    if ((rc = check_wide(h->h, h->rows, h->dim, h->ld_h, "h"))) return rc;
+    if ((rc = check_wide(h->w, h->cols, h->dim, h->ld_w, "w"))) return rc;
+    if ((rc = check_scale(h->scale))) return rc;
+    if (h->rows > 0 && (rc = check_array(h->label, 4, "label"))) return rc;
+    if ((rc = check_optional(h->weight, "weight"))) return rc;
+    a->h = h->h;
+    a->w = h->w;
+    a->ld_h = h->ld_h;
+    a->ld_w = h->ld_w;
+    a->label = h->label;
+    a->weight = h->weight;
+    a->scale = h->scale;
+    a->c2 = base2(h->scale);
+    return SCAPE_OK;
+}
+
+// ---- tokens to their experts
+constexpr int64_t kMaxMoved = int64_t(1) << 25;  // tokens of a move: a wave each
+
+int sort_shape(int64_t tokens, int32_t k, int32_t experts, SortArgs* a) {
+    if (experts < 1 || experts > SCAPE_EXPERT_MAX)
+        return fail(SCAPE_ERR_SHAPE, "experts must be in 1..%d (got %d)", SCAPE_EXPERT_MAX, experts);
+    if (tokens < 0 || tokens > kMaxTokens) return fail(SCAPE_ERR_SHAPE, "tokens must be in 0..2^30");
+    if (k < 1) return fail(SCAPE_ERR_SHAPE, "k must be at least 1 (got %d)", k);
+    if (tokens * k > INT32_MAX) return fail(SCAPE_ERR_SHAPE, "more than 2^31 - 1 choices");
+    a->choices = tokens * k;
+    a->experts = experts;
+    a->bits = 0;
+    while ((1 << a->bits) < experts) ++a->bits;
+    // a block of 2048 choices; more where there would be over 512 of them
+    int64_t run = 2048;
+    if (a->choices > run * 512) run = round_up((a->choices + 511) / 512, 256);
+    a->run = (int32_t)run;
+    a->blocks = (int32_t)((a->choices + run - 1) / run);
+    return SCAPE_OK;
+}
+int64_t sort_bytes(const SortArgs& a) { return (int64_t)a.blocks * a.experts * 4; }
+
+int check_moves(int32_t dtype, int64_t tokens, int64_t dim, int64_t rows, int32_t k, const int32_t* row) {
+    int rc;
+    if ((rc = check_dtype(dtype, "the rows"))) return rc;
+    if (tokens < 0 || tokens > kMaxMoved) return fail(SCAPE_ERR_SHAPE, "tokens must be in 0..2^25");
+    if (dim < 1) return fail(SCAPE_ERR_SHAPE, "dim must be at least 1");
+    if (rows < 0) return fail(SCAPE_ERR_SHAPE, "rows must be >= 0");
+    if (k < 1) return fail(SCAPE_ERR_SHAPE, "k must be at least 1 (got %d)", k);
+    if (tokens * k > INT32_MAX) return fail(SCAPE_ERR_SHAPE, "more than 2^31 - 1 choices");
+    if (tokens > 0 && (rc = check_array(row, 4, "row"))) return rc;
+    return SCAPE_OK;
 }
 
 }  // namespace
@@ -439,6 +570,173 @@ int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, in
     a.slots = (int32_t)(tokens / a.run + segments);
     const hipError_t e = launch_balance_backward((hipStream_t)stream, a);
     return e == hipSuccess ? SCAPE_OK : hip_fail(e, "balance gradient");
+}
+
+int scape_vocab_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    VocabArgs a{};
+    if (int rc = vocab_shape(dtype, rows, cols, dim, &a)) return rc;
+    *bytes = vocab_loss_bytes(a);
+    return SCAPE_OK;
+}
+
+int scape_vocab_loss_forward(const scape_head* head, float* loss, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    VocabArgs a{};
+    int rc;
+    if ((rc = vocab_head(head, &a))) return rc;
+    if (a.rows == 0) return SCAPE_OK;
+    if ((rc = check_array(loss, 4, "loss"))) return rc;
+    if ((rc = check_array(lse, 4, "lse"))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, vocab_loss_bytes(a)))) return rc;
+    a.loss = loss;
+    a.lse = lse;
+    a.part = static_cast<float2*>(workspace);
+    a.at_label = reinterpret_cast<float*>(a.part + a.rows * a.tiles_v);
+    const hipError_t e = launch_vocab_loss((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "vocabulary loss");
+}
+
+int scape_vocab_grad_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    VocabArgs a{};
+    if (int rc = vocab_shape(dtype, rows, cols, dim, &a)) return rc;
+    vocab_pieces(&a);
+    *bytes = vocab_parts(a).all;
+    return SCAPE_OK;
+}
+
+int scape_vocab_loss_backward(const scape_head* head, const float* lse, const float* dloss, void* dh, int64_t ld_dh,
+                              void* dw, int64_t ld_dw, void* workspace, int64_t workspace_bytes, void* stream) {
+    VocabArgs a{};
+    int rc;
+    if ((rc = vocab_head(head, &a))) return rc;
+    if (dh && (rc = check_wide(dh, a.rows, a.dim, ld_dh, "dh"))) return rc;
+    if (dw && (rc = check_wide(dw, a.cols, a.dim, ld_dw, "dw"))) return rc;
+    if (a.rows > 0 && (rc = check_array(lse, 4, "lse"))) return rc;
+    if ((rc = check_optional(dloss, "dloss"))) return rc;
+    if (!dw && (!dh || a.rows == 0)) return SCAPE_OK;
+    vocab_pieces(&a);
+    const VocabParts w = vocab_parts(a);
+    if ((rc = check_workspace(workspace, workspace_bytes, w.all))) return rc;
+    char* const ws = static_cast<char*>(workspace);
+    a.lse = const_cast<float*>(lse);  // read only in these launches
+    a.dloss = dloss;
+    a.dh = dh;
+    a.dw = dw;
+    a.ld_dh = ld_dh;
+    a.ld_dw = ld_dw;
+    if (a.rows > 0) {
+        a.row = reinterpret_cast<VocabRow*>(ws + w.row);
+        a.dw_scale = reinterpret_cast<float*>(ws + w.dw_scale);
+        a.h_copy = ws + w.h_copy;
+        a.p = ws + w.p;
+        a.dh_sum = reinterpret_cast<float*>(ws + w.dh_sum);
+    }
+    const hipError_t e = launch_vocab_grad((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "vocabulary loss gradient");
+}
+
+int scape_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, int64_t* bytes) {
+    if (!bytes) return fail(SCAPE_ERR_INVALID_ARG, "bytes is NULL");
+    SortArgs a{};
+    if (int rc = sort_shape(tokens, k, experts, &a)) return rc;
+    *bytes = sort_bytes(a);
+    return SCAPE_OK;
+}
+
+int scape_expert_sort(const int32_t* idx, int64_t tokens, int32_t k, int32_t experts, int32_t* offsets, int32_t* row,
+                      void* workspace, int64_t workspace_bytes, void* stream) {
+    SortArgs a{};
+    int rc;
+    if ((rc = sort_shape(tokens, k, experts, &a))) return rc;
+    if (tokens > 0 && (rc = check_array(idx, 4, "idx"))) return rc;
+    if ((rc = check_array(offsets, 4, "offsets"))) return rc;
+    if (tokens > 0 && (rc = check_array(row, 4, "row"))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, sort_bytes(a)))) return rc;
+    a.idx = idx;
+    a.offsets = offsets;
+    a.row = row;
+    a.counts = static_cast<uint32_t*>(workspace);
+    const hipError_t e = launch_expert_sort((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "expert sort");
+}
+
+int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t dim, int64_t ld_x, const int32_t* row,
+                        int32_t k, void* y, int64_t rows, int64_t ld_y, void* stream) {
+    int rc;
+    if ((rc = check_moves(dtype, tokens, dim, rows, k, row))) return rc;
+    if ((rc = check_matrix(x, dtype, tokens, dim, ld_x, "x"))) return rc;
+    if ((rc = check_matrix(y, dtype, rows, dim, ld_y, "y"))) return rc;
+    if (tokens == 0 || rows == 0) return SCAPE_OK;
+    MoveArgs a{};
+    a.dtype = dtype;
+    a.tokens = tokens;
+    a.dim = dim;
+    a.rows = rows;
+    a.k = k;
+    a.row = row;
+    a.x = x;
+    a.ld_x = ld_x;
+    a.y = y;
+    a.ld_y = ld_y;
+    const hipError_t e = launch_expert_gather((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "expert gather");
+}
+
+int scape_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y, const int32_t* row,
+                         const float* weight, int64_t tokens, int32_t k, void* out, int64_t ld_out, void* stream) {
+    int rc;
+    if ((rc = check_moves(dtype, tokens, dim, rows, k, row))) return rc;
+    if ((rc = check_matrix(y, dtype, rows, dim, ld_y, "y"))) return rc;
+    if ((rc = check_matrix(out, dtype, tokens, dim, ld_out, "out"))) return rc;
+    if ((rc = check_optional(weight, "weight"))) return rc;
+    if (tokens == 0) return SCAPE_OK;
+    MoveArgs a{};
+    a.dtype = dtype;
+    a.tokens = tokens;
+    a.dim = dim;
+    a.rows = rows;
+    a.k = k;
+    a.row = row;
+    a.weight = weight;
+    a.y = const_cast<void*>(y);  // read only in this launch
+    a.ld_y = ld_y;
+    a.out = out;
+    a.ld_out = ld_out;
+    const hipError_t e = launch_expert_combine((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "expert combine");
+}
+
+int scape_expert_combine_backward(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y,
+                                  const int32_t* row, const float* weight, const void* dout, int64_t ld_dout,
+                                  int64_t tokens, int32_t k, void* dy, int64_t ld_dy, float* dweight, void* stream) {
+    int rc;
+    if ((rc = check_moves(dtype, tokens, dim, rows, k, row))) return rc;
+    if (dweight && (rc = check_matrix(y, dtype, rows, dim, ld_y, "y"))) return rc;
+    if ((rc = check_matrix(dout, dtype, tokens, dim, ld_dout, "dout"))) return rc;
+    if (dy && (rc = check_matrix(dy, dtype, rows, dim, ld_dy, "dy"))) return rc;
+    if (dy && dy == y && ld_dy != ld_y) return fail(SCAPE_ERR_SHAPE, "dy over y needs y's row distance");
+    if ((rc = check_optional(weight, "weight"))) return rc;
+    if ((rc = check_optional(dweight, "dweight"))) return rc;
+    if (tokens == 0 || (!dy && !dweight)) return SCAPE_OK;
+    MoveArgs a{};
+    a.dtype = dtype;
+    a.tokens = tokens;
+    a.dim = dim;
+    a.rows = rows;
+    a.k = k;
+    a.row = row;
+    a.weight = weight;
+    a.x = dout;
+    a.ld_x = ld_dout;
+    a.y = dy;
+    a.ld_y = ld_dy;
+    a.y_in = y;
+    a.ld_y_in = ld_y;
+    a.dweight = dweight;
+    const hipError_t e = launch_expert_combine_back((hipStream_t)stream, a);
+    return e == hipSuccess ? SCAPE_OK : hip_fail(e, "expert combine gradient");
 }
 
 }  // extern "C"

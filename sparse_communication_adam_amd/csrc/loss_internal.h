@@ -1,6 +1,6 @@
-// loss_internal.h - types shared by the host side of the loss operators
-// (loss_api.cpp) and their kernels (k_topk.hip, k_distill.hip,
-// k_balance.hip).  Not part of the public ABI.
+// loss_internal.h - types shared by the host side of the loss and routing
+// operators (loss_api.cpp) and their kernels (k_topk.hip, k_distill.hip,
+// k_balance.hip, k_vocab.hip, k_expert.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -133,5 +133,75 @@ hipError_t launch_balance_forward(hipStream_t s, const BalanceArgs& a);
 hipError_t launch_balance_loss(hipStream_t s, const int32_t* counts, const float* psum, const int32_t* n_tok,
                                int32_t segments, int32_t experts, int32_t k, float alpha, float* loss);
 hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a);
+
+// ---- k_vocab.hip
+struct VocabRow {
+    float f, lse2, dh, copy;  // P's factor, log-sum-exp in base 2, dh's and h's powers of two (0: does not count)
+};
+struct VocabArgs {
+    const void* h;
+    const void* w;
+    int64_t ld_h, ld_w;
+    int32_t dtype;
+    int64_t rows, cols, dim;
+    const int32_t* label;
+    const float* weight;  // or NULL
+    float scale, c2;      // c2 = scale * log2(e)
+    int32_t tile_n;       // tokens of a tile
+    uint32_t tiles_v, tiles_n;
+    // forward
+    float* loss;
+    float* lse;           // backward: read only
+    float2* part;         // [tiles_v][rows] (reference, sum), in base 2
+    float* at_label;      // [rows] the label's product
+    // backward
+    const float* dloss;   // or NULL
+    void* dh;             // or NULL
+    void* dw;             // or NULL
+    int64_t ld_dh, ld_dw;
+    int64_t rows_pad;     // whole tiles of tokens
+    int64_t piece, ld_p;  // words of a piece, and P's row
+    int64_t split_words;  // words of a split of dh's sum, a multiple of 64
+    int32_t splits;
+    VocabRow* row;        // [rows_pad]
+    float* dw_scale;      // [1]
+    void* h_copy;         // [rows][dim]
+    void* p;              // [rows_pad][ld_p]
+    float* dh_sum;        // [splits][rows][dim]
+};
+hipError_t launch_vocab_loss(hipStream_t s, const VocabArgs& a);
+hipError_t launch_vocab_grad(hipStream_t s, const VocabArgs& a);
+
+// ---- k_expert.hip
+constexpr int kMaxExperts = SCAPE_EXPERT_MAX;
+struct SortArgs {
+    const int32_t* idx;  // [choices]
+    int64_t choices;
+    int32_t experts, bits;  // bits: experts <= 2^bits
+    int32_t run, blocks;    // choices of a block (a multiple of 256), and the blocks
+    int32_t* offsets;       // [experts + 1]
+    int32_t* row;           // [choices]
+    uint32_t* counts;       // [blocks][experts]
+};
+hipError_t launch_expert_sort(hipStream_t s, const SortArgs& a);
+struct MoveArgs {
+    int32_t dtype;
+    int64_t tokens, dim, rows;  // rows: of y
+    int32_t k;
+    const int32_t* row;    // [tokens][k]
+    const void* x;         // gather: tokens' rows; gradient: dout
+    int64_t ld_x;
+    void* y;               // gather: written; combine: read; gradient: dy, or NULL
+    int64_t ld_y;
+    const void* y_in;      // gradient: y
+    int64_t ld_y_in;
+    void* out;             // combine
+    int64_t ld_out;
+    const float* weight;   // [tokens][k], or NULL
+    float* dweight;        // [tokens][k], or NULL
+};
+hipError_t launch_expert_gather(hipStream_t s, const MoveArgs& a);
+hipError_t launch_expert_combine(hipStream_t s, const MoveArgs& a);
+hipError_t launch_expert_combine_back(hipStream_t s, const MoveArgs& a);
 
 }  // namespace scape

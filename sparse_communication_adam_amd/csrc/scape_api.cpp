@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -750,6 +751,80 @@ int dense_common(scape_ctx* ctx, float* x, float* m, float* v, const uint16_t* c
     return SCAPE_OK;
 }
 
+// ---- gradient norms and clipping
+
+// The tiles' sums, the layers', and the ticket of the workgroups that join them.
+int64_t grad_norm_bytes(const scape_ctx* ctx) {
+    return (int64_t)ctx->cfg.workers * ((int64_t)ctx->tiles.size() + ctx->lay.L) * 8 + 16;
+}
+
+// A workgroup for each tile of each worker, counted with their threads in 32 bits.
+int grad_args(scape_ctx* ctx, const uint16_t* const* g, bool interleaved, GradArgs* a) {
+    if (!ctx || !g) return fail(SCAPE_ERR_INVALID_ARG, "NULL argument");
+    int rc;
+    if ((rc = check_device(ctx))) return rc;
+    const int32_t W = ctx->cfg.workers;
+    const int64_t most = (int64_t(1) << 32) / kBlock - 1;
+    if ((int64_t)ctx->tiles.size() * W > most || (int64_t)ctx->lay.L * W > most)
+        return fail(SCAPE_ERR_SHAPE, "too many tiles or layers for one launch");
+    for (int32_t i = 0; i < (interleaved ? 1 : W); ++i) {
+        if (!g[i] && ctx->n_words) return fail(SCAPE_ERR_INVALID_ARG, "g[%d] is NULL", i);
+        if (!aligned(g[i], 16)) return fail(SCAPE_ERR_ALIGN, "g[%d] must be 16-byte aligned", i);
+    }
+    for (int32_t i = 0; i < W; ++i) a->g[i] = interleaved ? g[0] + (int64_t)i * 64 : g[i];
+    a->ws = interleaved ? 64u * (uint32_t)W : 64u;
+    a->workers = (uint32_t)W;
+    a->n_tiles = (uint32_t)ctx->tiles.size();
+    a->n_layers = (uint32_t)ctx->lay.L;
+    a->tiles = ctx->d_tiles;
+    a->layers = ctx->d_layers;
+    return SCAPE_OK;
+}
+
+int norm_common(scape_ctx* ctx, const uint16_t* const* g, float* norm, float* layer_norm, void* workspace,
+                int64_t workspace_bytes, void* stream, bool interleaved) {
+    GradArgs a{};
+    int rc;
+    if ((rc = grad_args(ctx, g, interleaved, &a))) return rc;
+    if (!norm) return fail(SCAPE_ERR_INVALID_ARG, "norm is NULL");
+    if (!aligned(norm, 4) || !aligned(layer_norm, 4)) return fail(SCAPE_ERR_ALIGN, "norm and layer_norm must be 4-byte aligned");
+    if (!workspace) return fail(SCAPE_ERR_INVALID_ARG, "workspace is NULL (%lld bytes needed)", (long long)grad_norm_bytes(ctx));
+    if (workspace_bytes < grad_norm_bytes(ctx))
+        return fail(SCAPE_ERR_SHAPE, "workspace has %lld bytes, needs %lld", (long long)workspace_bytes,
+                    (long long)grad_norm_bytes(ctx));
+    if (!aligned(workspace, 16)) return fail(SCAPE_ERR_ALIGN, "workspace must be 16-byte aligned");
+    a.part = static_cast<double*>(workspace);
+    a.layer_sum = a.part + (int64_t)a.workers * a.n_tiles;
+    a.ticket = reinterpret_cast<uint32_t*>(a.layer_sum + (int64_t)a.workers * a.n_layers);
+    a.norm = norm;
+    a.layer_norm = layer_norm;
+    SCAPE_HIP(launch_grad_norm((hipStream_t)stream, a), "gradient norms");
+    return SCAPE_OK;
+}
+
+int clip_common(scape_ctx* ctx, const uint16_t* const* g, const float* norm, float max_norm, int32_t shared,
+                uint16_t* const* out, void* stream, bool interleaved) {
+    GradArgs a{};
+    int rc;
+    if ((rc = grad_args(ctx, g, interleaved, &a))) return rc;
+    if (!out) return fail(SCAPE_ERR_INVALID_ARG, "out is NULL");
+    if (!norm) return fail(SCAPE_ERR_INVALID_ARG, "norm is NULL");
+    if (!aligned(norm, 4)) return fail(SCAPE_ERR_ALIGN, "norm must be 4-byte aligned");
+    if (!(max_norm > 0.0f) || !std::isfinite(max_norm)) return fail(SCAPE_ERR_INVALID_ARG, "max_norm must be positive and finite");
+    if (shared != 0 && shared != 1) return fail(SCAPE_ERR_INVALID_ARG, "shared takes 0 or 1, not %d", shared);
+    const int32_t W = ctx->cfg.workers;
+    for (int32_t i = 0; i < (interleaved ? 1 : W); ++i) {
+        if (!out[i] && ctx->n_words) return fail(SCAPE_ERR_INVALID_ARG, "out[%d] is NULL", i);
+        if (!aligned(out[i], 16)) return fail(SCAPE_ERR_ALIGN, "out[%d] must be 16-byte aligned", i);
+    }
+    for (int32_t i = 0; i < W; ++i) a.out[i] = interleaved ? out[0] + (int64_t)i * 64 : out[i];
+    a.norm = const_cast<float*>(norm);  // read only in this launch
+    a.max_norm = max_norm;
+    a.shared = shared == 1;
+    SCAPE_HIP(launch_grad_clip((hipStream_t)stream, a), "clipping gradients");
+    return SCAPE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1016,6 +1091,35 @@ int scape_dense_step(scape_ctx* ctx, float* x, float* m, float* v, const uint16_
 int scape_dense_step_interleaved(scape_ctx* ctx, float* x, float* m, float* v, const uint16_t* g_il, void* stream) {
     const uint16_t* g[1] = {g_il};
     return dense_common(ctx, x, m, v, g, stream, true);
+}
+
+int scape_grad_norm_workspace(const scape_ctx* ctx, int64_t* bytes) {
+    if (!ctx || !bytes) return fail(SCAPE_ERR_INVALID_ARG, "NULL argument");
+    *bytes = grad_norm_bytes(ctx);
+    return SCAPE_OK;
+}
+
+int scape_grad_norm(scape_ctx* ctx, const uint16_t* const* g, float* norm, float* layer_norm, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    return norm_common(ctx, g, norm, layer_norm, workspace, workspace_bytes, stream, false);
+}
+
+int scape_grad_norm_interleaved(scape_ctx* ctx, const uint16_t* g_il, float* norm, float* layer_norm,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+    const uint16_t* g[1] = {g_il};
+    return norm_common(ctx, g, norm, layer_norm, workspace, workspace_bytes, stream, true);
+}
+
+int scape_grad_clip(scape_ctx* ctx, const uint16_t* const* g, const float* norm, float max_norm, int32_t shared,
+                    uint16_t* const* out, void* stream) {
+    return clip_common(ctx, g, norm, max_norm, shared, out, stream, false);
+}
+
+int scape_grad_clip_interleaved(scape_ctx* ctx, const uint16_t* g_il, const float* norm, float max_norm,
+                                int32_t shared, uint16_t* out_il, void* stream) {
+    const uint16_t* g[1] = {g_il};
+    uint16_t* out[1] = {out_il};
+    return clip_common(ctx, g, norm, max_norm, shared, out, stream, true);
 }
 
 int scape_mask_build(scape_ctx* ctx, const float* mtilde, int32_t num_shards, int32_t shard, const scape_mask* out,

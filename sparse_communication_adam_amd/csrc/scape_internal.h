@@ -278,4 +278,23 @@ struct StreamProbe {
 };
 hipError_t launch_stream_probe(hipStream_t s, const StreamProbe& a, uint32_t n_words);
 
+// gradient norms and clipping, in the context's layout
+constexpr float kMaxFloat = 3.402823466e38f;
+struct GradArgs {
+    const uint16_t* g[SCAPE_MAX_WORKERS];  // word stride ws, as in WorkerPtrs
+    uint16_t* out[SCAPE_MAX_WORKERS];      // clip: may be g
+    uint32_t ws, workers, n_tiles, n_layers;
+    const TileDesc* tiles;
+    const LayerDesc* layers;
+    double* part;       // [workers][n_tiles]
+    double* layer_sum;  // [workers][n_layers]
+    uint32_t* ticket;
+    float* norm;        // [workers + 1]
+    float* layer_norm;  // [workers][n_layers], or NULL
+    float max_norm;
+    bool shared;
+};
+hipError_t launch_grad_norm(hipStream_t s, const GradArgs& a);
+hipError_t launch_grad_clip(hipStream_t s, const GradArgs& a);
+
 }  // namespace scape

@@ -24,8 +24,9 @@ from __future__ import annotations
 
 from typing import Optional, Sequence
 
-from ._scape import (Context, Mask, ScapeConfig, alloc_mask, interleaved_view, scape_step, scape_step_interleaved,
-                     scape_step_offload)
+from ._scape import (Context, Mask, ScapeConfig, alloc_mask, interleaved_view, scape_grad_clip,
+                     scape_grad_clip_interleaved, scape_grad_norm, scape_grad_norm_interleaved,
+                     scape_grad_norm_workspace_bytes, scape_step, scape_step_interleaved, scape_step_offload)
 
 
 class ScapeState:
@@ -63,6 +64,8 @@ class ScapeState:
         self.sparse = [torch.zeros(max(k, 1), **f32) for _ in range(W)]
         self.key = torch.zeros(n, dtype=torch.int32, device=device)
         self.masks = [alloc_mask(self.layout, device), alloc_mask(self.layout, device)]
+        self.grad_norm = None  # fp32 [W+1], made by the first clipped step
+        self._norm_ws = None
         self._cur = 0
         self.t = 0
 
@@ -86,12 +89,34 @@ class ScapeState:
             return interleaved_view(self.r_il, self.cfg.workers)[:, i, :].reshape(-1)
         return self.r[i]
 
-    def step(self, grads, stream=None, key_out: Optional[bool] = True) -> None:
+    def clip(self, grads, max_norm: float, shared: bool = False, stream=None) -> None:
+        """The workers' gradient norms into ``self.grad_norm`` (fp32 [W+1], the
+        last their root mean square), and the gradients clipped by them in
+        place: each worker's by its own norm, or all by the last (shared).  A
+        gradient whose norm is not finite becomes 0."""
+        norm, clip = scape_grad_norm, scape_grad_clip
+        if self.interleaved:
+            norm, clip = scape_grad_norm_interleaved, scape_grad_clip_interleaved
+        self._clip_buffers()
+        norm(self.ctx, grads, self.grad_norm, workspace=self._norm_ws, stream=stream)
+        clip(self.ctx, grads, self.grad_norm, max_norm, shared=shared, stream=stream)
+
+    def _clip_buffers(self) -> None:
+        import torch
+        if self.grad_norm is None:
+            self.grad_norm = torch.zeros(self.cfg.workers + 1, dtype=torch.float32, device=self.m.device)
+            self._norm_ws = torch.empty(scape_grad_norm_workspace_bytes(self.ctx), dtype=torch.uint8,
+                                        device=self.m.device)
+
+    def step(self, grads, stream=None, key_out: Optional[bool] = True, max_norm: Optional[float] = None,
+             shared_norm: bool = False) -> None:
         """One step with the W workers' bfloat16 gradients (int16 views): a
         list of W tensors, or in the interleaved layout one tensor of
         n_pad*W.  key_out=True also writes the full statistic keys into
         ``self.key`` (4 bytes per element more); the mask does not depend on
-        it."""
+        it.  max_norm: the gradients are clipped first, in place (``clip``)."""
+        if max_norm is not None:
+            self.clip(grads, max_norm, shared_norm, stream)
         key = self.key if key_out else None
         if self.interleaved:
             scape_step_interleaved(self.ctx, self.xv, self.m, self.r_il, grads, self.cur_mask, self.next_mask,
@@ -103,20 +128,26 @@ class ScapeState:
         self._cur = 1 - self._cur
         self.t += 1
 
-    def capture(self, grads: Sequence, key_out: bool = False) -> None:
+    def capture(self, grads: Sequence, key_out: bool = False, max_norm: Optional[float] = None,
+                shared_norm: bool = False) -> None:
         """Capture the step as two HIP graphs, one for each assignment of the
         two mask slots (they swap roles every step).  The graphs read the
         gradients from `grads`, the W int16 tensors given here: before each
         ``step_graph`` the caller writes that step's gradients into them.
-        Capturing runs nothing, so the state does not change."""
+        max_norm: the graphs clip those tensors first, in place.  Capturing
+        runs nothing, so the state does not change."""
         import torch
         if self.offload:
             raise ValueError("the offloaded step copies to and from host memory and is not captured")
         self._graph_grads = grads if self.interleaved else list(grads)
+        if max_norm is not None:
+            self._clip_buffers()  # outside the graphs' own memory
         graphs = []
         for cur in (0, 1):
             g = torch.cuda.CUDAGraph()
             with torch.cuda.graph(g):
+                if max_norm is not None:
+                    self.clip(self._graph_grads, max_norm, shared_norm)
                 if self.interleaved:
                     scape_step_interleaved(self.ctx, self.xv, self.m, self.r_il, self._graph_grads,
                                            self.masks[cur], self.masks[1 - cur], self.sparse,
