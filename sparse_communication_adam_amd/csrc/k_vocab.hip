@@ -41,9 +41,10 @@ constexpr uint32_t kRawBuffer = 0x00027000u;
 // One operand of a product: rows of 16-bit elements, ld apart.  Along: the
 // summed axis lies along the rows (extent rows of them); else it runs over
 // rows of `extent` elements.
+// All sizes are below 2^21 (the call checks that), so their sums are 32-bit.
 struct Side {
-    const char* p;
-    int64_t ld, extent, depth;  // depth: elements of the summed axis
+    const void* p;
+    int32_t ld, extent, depth;  // depth: elements of the summed axis
 };
 
 // Moves a tile of kR x 64 from memory to LDS, 16 bytes a lane, and reads MFMA
@@ -57,11 +58,15 @@ struct Stage {
     static constexpr int kLoads = kPieces > kThreads ? kPieces / kThreads : 1;
     static constexpr int kRow = kAlong ? kStep * 2 : kR * 2;  // bytes
     static constexpr int kRowPieces = kRow / 16;
-    uint32_t off[kLoads];
-    bool on;
+    // Rows that one load of all threads covers.  Where the exchange is the same
+    // from one load to the next, a lane's offset is one register and a multiple
+    // of the row distance.
+    static constexpr int kRowsALoad = kThreads / kRowPieces;
+    static constexpr bool kSteady = kLoads == 1 || kRowsALoad % (kAlong ? 8 : 16) == 0;
+    uint32_t off[kSteady ? 1 : kLoads], pitch;
 
     // what the pieces of row k are exchanged by; the same for k, k + 4 (k % 8
-    // < 4) and k + 32, which a fragment's reads are apart
+    // < 4) and k + 16, which a fragment's reads and a lane's loads are apart
     static __device__ __forceinline__ uint32_t turn(uint32_t k) {
         if constexpr (kAlong) return k & 7u;
         if constexpr (kR >= 128) return ((k & 3u) | ((k >> 3) & 1u) << 2) << 1;
@@ -70,62 +75,72 @@ struct Stage {
         return 0;
     }
 
-    __device__ __forceinline__ void init(uint32_t tid, int64_t ld) {
-        on = tid < (uint32_t)kPieces;
+    __device__ __forceinline__ void init(int32_t ld) {
+        pitch = (uint32_t)(ld * 2);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t q = (uint32_t)i * kThreads + tid, row = q / kRowPieces, pos = q % kRowPieces;
-            off[i] = row * (uint32_t)(ld * 2) + ((pos ^ turn(row)) << 4);
+        for (int i = 0; i < (kSteady ? 1 : kLoads); ++i) {
+            const uint32_t q = (uint32_t)i * kThreads + threadIdx.x, row = q / kRowPieces, pos = q % kRowPieces;
+            off[i] = row * pitch + ((pos ^ turn(row)) << 4);
         }
     }
 
     // The tile at row (or column) r0 and depth k.
-    __device__ __forceinline__ void load(const Side& s, int64_t r0, int64_t k, uint32_t tid, lds_t* to) const {
-        int64_t base, rows, width;
+    __device__ __forceinline__ void load(const Side& s, int32_t r0, int32_t k, lds_t* to) {
+        const uint32_t tid = threadIdx.x;
+        int64_t base;
+        int32_t rows, width;
         if constexpr (kAlong) {
-            base = r0 * s.ld + k;
+            base = (int64_t)r0 * s.ld + k;
             rows = s.extent - r0 < kR ? s.extent - r0 : kR;
             width = s.depth - k;
         } else {
-            base = k * s.ld + r0;
+            base = (int64_t)k * s.ld + r0;
             rows = s.depth - k < kStep ? s.depth - k : kStep;
             width = s.extent - r0;
         }
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.p) + base * 2, 0,
-                                                            (int)(((rows - 1) * s.ld + width) * 2), kRawBuffer);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(s.p)) + base * 2, 0,
+                                                            ((rows - 1) * s.ld + width) * 2, kRawBuffer);
         uint32_t kill = 0;  // pieces behind the end of the summed axis are zeros
         if constexpr (kAlong) {
+            static_assert(kRowsALoad % 8 == 0, "a lane's pieces lie alike in all its rows");
             if (width < kStep) {
-                const uint32_t row = tid / kRowPieces, pos = tid % kRowPieces;  // alike for every i: kThreads / 8 is a multiple of 8
+                const uint32_t row = tid / kRowPieces, pos = tid % kRowPieces;
                 if ((int)((pos ^ turn(row)) * 8) >= (int)width) kill = kOutside;
             }
         }
-        if (kPieces >= kThreads || on) {
+        if (kPieces >= kThreads || tid < (uint32_t)kPieces) {
+            // one register, not one for each load: the sums need them
+            asm volatile("" : "+v"(off[0]));
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
+                const uint32_t o = kSteady ? off[0] + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i];
                 lds_t* const at = to + (i * kThreads + (int)(tid & ~63u)) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, off[i] | kill, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, o | kill, 0, 0, 0);
             }
         }
     }
 
-    // Where a lane reads fragment f of the wave's rows (from r0) in half-step h.
-    static __device__ __forceinline__ uint32_t at(uint32_t lane, uint32_t r0, int h) {
+    // Where a lane reads the first fragment of the wave's rows (from r0, a
+    // multiple of the wave's share) in the first half-step, and from there
+    // fragment f in half-step h: the exchange is an XOR, so they are too.
+    static __device__ __forceinline__ uint32_t first(uint32_t lane, uint32_t r0) {
         if constexpr (kAlong) {
             const uint32_t row = r0 + (lane & 15u);
-            return row * kRow + ((((uint32_t)h * 4 + (lane >> 4)) ^ turn(row)) << 4);
+            return row * kRow + (((lane >> 4) ^ turn(row)) << 4);
         } else {
-            const uint32_t k = (uint32_t)h * 32 + (lane >> 4) * 8 + ((lane & 15u) >> 2), c = lane & 3u;
+            const uint32_t k = (lane >> 4) * 8 + ((lane & 15u) >> 2), c = lane & 3u;
             return k * kRow + (((r0 / 8 + (c >> 1)) ^ turn(k)) << 4) + (c & 1u) * 8;
         }
     }
-    static __device__ __forceinline__ s8 read(const lds_t* p) {
+    static __device__ __forceinline__ s8 read(const lds_t* tile, uint32_t first, int f, int h) {
         if constexpr (kAlong) {
+            const lds_t* const p = tile + (first ^ (uint32_t)(h * 64)) + f * 16 * kRow;
             return *reinterpret_cast<const __attribute__((address_space(3))) s8*>(p);
         } else {
             typedef __attribute__((address_space(3))) s4 lds_s4;
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)const_cast<lds_t*>(p));
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)const_cast<lds_t*>(p + 4 * kRow));
+            lds_t* const p = const_cast<lds_t*>(tile) + (first ^ (uint32_t)(f * 32)) + h * 32 * kRow;
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 4 * kRow));
             return s8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
     }
@@ -135,7 +150,7 @@ struct Stage {
 template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN>
 struct Tile {
     static constexpr int kThreads = kWM * kWN * 64;
-    static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part
+    static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part, powers of two
     static constexpr int kFM = kTM / 16, kFN = kTN / 16;
     using A = Stage<kAlongA, kM, kThreads>;
     using B = Stage<kAlongB, kN, kThreads>;
@@ -143,55 +158,47 @@ struct Tile {
     static constexpr int kLds = 2 * kStage;
     f4 acc[kFM][kFN];
 
-    __device__ __forceinline__ void run(const Side& a, const Side& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1,
+    __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
                                         lds_t* lds) {
-        const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-        const uint32_t wm = (wave % kWM) * kTM, wn = (wave / kWM) * kTN;
         A la;
         B lb;
-        la.init(tid, a.ld);
-        lb.init(tid, b.ld);
-        uint32_t ra[2][kFM], rb[2][kFN];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int f = 0; f < kFM; ++f) ra[h][f] = A::at(lane, wm + f * 16, h);
-#pragma unroll
-            for (int f = 0; f < kFN; ++f) rb[h][f] = A::kBytes + B::at(lane, wn + f * 16, h);
-        }
+        la.init(a.ld);
+        lb.init(b.ld);
+        uint32_t fa = A::first(lane_id(), wave_m()), fb = B::first(lane_id(), wave_n());
 #pragma unroll
         for (int i = 0; i < kFM; ++i)
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = f4{0, 0, 0, 0};
         fetch(a, b, m0, n0, k0, la, lb, lds);
         __syncthreads();
-        for (int64_t k = k0; k < k1; k += 2 * kStep) {
-            if (k + kStep < k1) fetch(a, b, m0, n0, k + kStep, la, lb, lds + kStage);
-            multiply(ra, rb, lds);
-            __syncthreads();
-            if (k + kStep >= k1) break;
-            if (k + 2 * kStep < k1) fetch(a, b, m0, n0, k + 2 * kStep, la, lb, lds);
-            multiply(ra, rb, lds + kStage);
+        uint32_t at = 0;
+        for (int32_t k = k0 + kStep; k < k1; k += kStep, at ^= kStage) {
+            fetch(a, b, m0, n0, k, la, lb, lds + (at ^ kStage));
+            multiply(fa, fb, lds + at);
             __syncthreads();
         }
+        multiply(fa, fb, lds + at);
+        __syncthreads();
     }
-    static __device__ __forceinline__ void fetch(const Side& a, const Side& b, int64_t m0, int64_t n0, int64_t k, const A& la,
-                                                 const B& lb, lds_t* to) {
-        la.load(a, m0, k, threadIdx.x, to);
-        lb.load(b, n0, k, threadIdx.x, to + A::kBytes);
+    static __device__ __forceinline__ void fetch(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k, A& la, B& lb,
+                                                 lds_t* to) {
+        la.load(a, m0, k, to);
+        lb.load(b, n0, k, to + A::kBytes);
     }
-    __device__ __forceinline__ void multiply(const uint32_t (&ra)[2][kFM], const uint32_t (&rb)[2][kFN], const lds_t* from) {
+    __device__ __forceinline__ void multiply(uint32_t& fa, uint32_t& fb, const lds_t* from) {
+        asm volatile("" : "+v"(fa), "+v"(fb));  // addresses are made from these two here, and not kept
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            s8 fa[kFM], fb[kFN];
+            s8 x[kFM], y[kFN];
 #pragma unroll
-            for (int i = 0; i < kFM; ++i) fa[i] = A::read(from + ra[h][i]);
+            for (int i = 0; i < kFM; ++i) x[i] = A::read(from, fa, i, h);
 #pragma unroll
-            for (int j = 0; j < kFN; ++j) fb[j] = B::read(from + rb[h][j]);
+            for (int j = 0; j < kFN; ++j) y[j] = B::read(from + A::kBytes, fb, j, h);
 #pragma unroll
             for (int i = 0; i < kFM; ++i)
 #pragma unroll
-                for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
+                for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(x[i], y[j], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     // The wave's first row and column in the tile, and the lane's of a fragment.
@@ -209,8 +216,8 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, ui
     b = xcd_block(b, nm * nn);
     const uint32_t band = b / (kBand * nm), first = band * kBand, in = b - band * kBand * nm;
     const uint32_t wide = nn - first < kBand ? nn - first : kBand;
-    n = first + in % wide;
-    m = in / wide;
+    n = __builtin_amdgcn_readfirstlane(first + in % wide);  // divisions are made in vector registers
+    m = __builtin_amdgcn_readfirstlane(in / wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -222,20 +229,20 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, a.tiles_v, a.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
-    g.run(Side{(const char*)a.w, a.ld_w, a.cols, a.dim}, Side{(const char*)a.h, a.ld_h, a.rows, a.dim}, m0, n0, 0, a.dim,
-          (lds_t*)lds);
+    g.run(Side{a.w, (int32_t)a.ld_w, (int32_t)a.cols, (int32_t)a.dim}, Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0,
+          (int32_t)a.dim, (lds_t*)lds);
     // the loop's last barrier is behind every read of the tiles
     float2* const red = reinterpret_cast<float2*>(lds);  // [kWM][kN]
     const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
-    const int32_t left = (int32_t)(a.cols - m0) - (int32_t)lm;  // words from the lane's first on
+    const int32_t left = (int32_t)a.cols - m0 - (int32_t)lm;  // words from the lane's first on
     const bool ragged = a.cols - m0 < kM;
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
         const int64_t n = n0 + ln + j * 16;
         const bool row = n < a.rows;
-        const int32_t label = row ? a.label[n] : -1, lab = label - (int32_t)(m0 + lm);  // of the lane's words
+        const int32_t label = row ? a.label[n] : -1, lab = label - m0 - (int32_t)lm;  // of the lane's words
         if (ragged) {
 #pragma unroll
             for (int i = 0; i < G::kFM; ++i)
@@ -406,17 +413,17 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
 // step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
 template <class T, int kM, int kN, int kWM, int kWN>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int64_t v0, int64_t v1) {
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1) {
     using G = Tile<T, true, true, kM, kN, kWM, kWN>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, (uint32_t)((v1 - v0 + kM - 1) / kM), a.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    tile_of(blockIdx.x, (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
+    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
-    g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, a.ld_w, v1 - v0, a.dim}, Side{(const char*)a.h, a.ld_h, a.rows, a.dim},
-          m0, n0, 0, a.dim, (lds_t*)lds);
+    g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, v1 - v0, (int32_t)a.dim},
+          Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0, (int32_t)a.dim, (lds_t*)lds);
     const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
-    const int32_t left = (int32_t)(v1 - v0 - m0) - (int32_t)lm, first = (int32_t)(v0 + m0 + lm);
+    const int32_t left = v1 - v0 - m0 - (int32_t)lm, first = v0 + m0 + (int32_t)lm;
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
         const int64_t n = n0 + ln + j * 16;
@@ -433,27 +440,28 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int64_t
                 p[e] = r.f != 0.0f && i * 16 + e < left ? x * r.f : 0.0f;
             }
             *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
 template <class T, int kM, int kN, int kWM, int kWN>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int64_t v0, int64_t v1, bool first) {
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first) {
     using G = Tile<T, false, true, kM, kN, kWM, kWN>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
-    const uint32_t split = blockIdx.x / tiles;
-    tile_of(blockIdx.x % tiles, nm, a.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
-    const int64_t k0 = (int64_t)split * a.split_words, all = v1 - v0;
-    const int64_t k1 = k0 + a.split_words < all ? k0 + a.split_words : all;
+    const uint32_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
+    tile_of(blockIdx.x - split * tiles, nm, a.tiles_n, tm, tn);
+    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
+    const int32_t part = (int32_t)a.split_words, k0 = (int32_t)split * part, all = v1 - v0;
+    const int32_t k1 = k0 + part < all ? k0 + part : all;
     if (k0 >= k1 && !first) return;
     G g;
     if (k0 < k1) {
-        g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, a.ld_w, a.dim, all},
-              Side{(const char*)a.p, a.ld_p, a.rows_pad, a.ld_p}, m0, n0, k0, k1, (lds_t*)lds);
+        g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, (int32_t)a.dim, all},
+              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, (lds_t*)lds);
     } else {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
@@ -496,15 +504,15 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
 
 // dw of a piece.
 template <class T, int kM, int kN, int kWM, int kWN>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int64_t v0, int64_t v1) {
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
     using G = Tile<T, false, false, kM, kN, kWM, kWN>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)((v1 - v0 + kN - 1) / kN), tm, tn);
-    const int64_t m0 = (int64_t)tm * kM, n0 = (int64_t)tn * kN;
+    tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
+    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
-    g.run(Side{(const char*)a.h_copy, a.dim, a.dim, a.rows}, Side{(const char*)a.p, a.ld_p, a.ld_p, a.rows_pad}, m0, n0, 0,
-          a.rows, (lds_t*)lds);
+    g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
+          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, (lds_t*)lds);
     const float c = a.dw_scale[0];
     const int64_t m = m0 + G::wave_m() + G::lane_m(), w1 = n0 + G::wave_n() + G::lane_n();
 #pragma unroll
@@ -517,6 +525,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int64_
             if (m + i * 16 < a.dim) {
                 const f4 x = g.acc[i][j] * c;
                 *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+                __builtin_amdgcn_sched_barrier(0);
             }
     }
 }
@@ -552,8 +561,8 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
     SCAPE_RUN(k_vocab_rows, 1, 1024, a);
     if (a.dw) SCAPE_RUN(k_vocab_copy<T>, a.rows, kRowThreads, a);
     const int64_t dim_tiles = (a.dim + 255) / 256;
-    for (int64_t v0 = 0; v0 < a.cols; v0 += a.piece) {
-        const int64_t v1 = v0 + a.piece < a.cols ? v0 + a.piece : a.cols;
+    for (int32_t v0 = 0; v0 < a.cols; v0 += (int32_t)a.piece) {
+        const int32_t v1 = v0 + a.piece < a.cols ? v0 + (int32_t)a.piece : (int32_t)a.cols;
         const int64_t words = (v1 - v0 + 255) / 256, tiles = words * a.tiles_n;
         switch (a.tile_n) {
             case 16: SCAPE_RUN((k_vocab_p<T, 256, 16, 4, 1>), tiles, 256, a, v0, v1); break;
