@@ -34,7 +34,6 @@ __device__ __forceinline__ f4 mfma(const s8& a, const s8& b, const f4& c) {
     }
 }
 
-constexpr int kStep = 64;                       // elements of the summed axis in a tile
 constexpr uint32_t kOutside = 0x80000000u;      // an offset that the resource's bound turns into zeros
 constexpr uint32_t kRawBuffer = 0x00027000u;
 
@@ -47,28 +46,32 @@ struct Side {
     int32_t ld, extent, depth;  // depth: elements of the summed axis
 };
 
-// Moves a tile of kR x 64 from memory to LDS, 16 bytes a lane, and reads MFMA
+// Moves a tile of kR x kDepth from memory to LDS, 16 bytes a lane, and reads MFMA
 // fragments of it.  The load writes LDS in lane order, so the lanes' addresses
 // are permuted instead: the 16-byte pieces of a row are exchanged by an XOR
 // that spreads what one fragment read touches over all banks.
-template <bool kAlong, int kR, int kThreads>
+template <bool kAlong, int kR, int kThreads, int kDepth>
 struct Stage {
-    static constexpr int kBytes = kR * 2 * kStep;
+    static constexpr int kBytes = kR * 2 * kDepth;
     static constexpr int kPieces = kBytes / 16;
+    // Every wave issues as many loads, so that they can be counted: of a tile
+    // with fewer pieces than threads some are loaded twice.
     static constexpr int kLoads = kPieces > kThreads ? kPieces / kThreads : 1;
-    static constexpr int kRow = kAlong ? kStep * 2 : kR * 2;  // bytes
+    static constexpr int kLanes = kPieces < kThreads ? kPieces : kThreads;
+    static constexpr int kRow = kAlong ? kDepth * 2 : kR * 2;  // bytes
     static constexpr int kRowPieces = kRow / 16;
     // Rows that one load of all threads covers.  Where the exchange is the same
     // from one load to the next, a lane's offset is one register and a multiple
     // of the row distance.
-    static constexpr int kRowsALoad = kThreads / kRowPieces;
-    static constexpr bool kSteady = kLoads == 1 || kRowsALoad % (kAlong ? 8 : 16) == 0;
+    static constexpr int kRowsALoad = kLanes / kRowPieces;
+    static constexpr bool kSteady = kLoads == 1 || kRowsALoad % 16 == 0;
+    static_assert(kPieces % 64 == 0 && (kPieces % kThreads == 0 || kThreads % kPieces == 0), "whole waves");
     uint32_t off[kSteady ? 1 : kLoads], pitch;
 
-    // what the pieces of row k are exchanged by; the same for k, k + 4 (k % 8
-    // < 4) and k + 16, which a fragment's reads and a lane's loads are apart
+    // what the pieces of row k are exchanged by; the same for k + 4 (k % 8 < 4)
+    // and k + 16, which a fragment's reads and a lane's loads are apart
     static __device__ __forceinline__ uint32_t turn(uint32_t k) {
-        if constexpr (kAlong) return k & 7u;
+        if constexpr (kAlong) return kDepth == 32 ? (k >> 2) & 3u : k & 7u;
         if constexpr (kR >= 128) return ((k & 3u) | ((k >> 3) & 1u) << 2) << 1;
         if constexpr (kR == 64) return (((k >> 1) & 1u) | ((k >> 3) & 1u) << 1) << 1;
         if constexpr (kR == 32) return ((k >> 3) & 1u) << 1;
@@ -79,14 +82,14 @@ struct Stage {
         pitch = (uint32_t)(ld * 2);
 #pragma unroll
         for (int i = 0; i < (kSteady ? 1 : kLoads); ++i) {
-            const uint32_t q = (uint32_t)i * kThreads + threadIdx.x, row = q / kRowPieces, pos = q % kRowPieces;
+            const uint32_t q = (uint32_t)i * kThreads + threadIdx.x % kLanes, row = q / kRowPieces, pos = q % kRowPieces;
             off[i] = row * pitch + ((pos ^ turn(row)) << 4);
         }
     }
 
     // The tile at row (or column) r0 and depth k.
     __device__ __forceinline__ void load(const Side& s, int32_t r0, int32_t k, lds_t* to) {
-        const uint32_t tid = threadIdx.x;
+        const uint32_t tid = threadIdx.x % kLanes;
         int64_t base;
         int32_t rows, width;
         if constexpr (kAlong) {
@@ -95,34 +98,33 @@ struct Stage {
             width = s.depth - k;
         } else {
             base = (int64_t)k * s.ld + r0;
-            rows = s.depth - k < kStep ? s.depth - k : kStep;
+            rows = s.depth - k < kDepth ? s.depth - k : kDepth;
             width = s.extent - r0;
         }
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(s.p)) + base * 2, 0,
-                                                            ((rows - 1) * s.ld + width) * 2, kRawBuffer);
-        uint32_t kill = 0;  // pieces behind the end of the summed axis are zeros
+        // behind the end of the summed axis there is nothing: all zeros
+        const int32_t bytes = rows > 0 && width > 0 ? ((rows - 1) * s.ld + width) * 2 : 0;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(s.p)) + base * 2, 0, bytes,
+                                                            kRawBuffer);
+        uint32_t kill = 0;
         if constexpr (kAlong) {
-            static_assert(kRowsALoad % 8 == 0, "a lane's pieces lie alike in all its rows");
-            if (width < kStep) {
+            if (width < kDepth) {
                 const uint32_t row = tid / kRowPieces, pos = tid % kRowPieces;
                 if ((int)((pos ^ turn(row)) * 8) >= (int)width) kill = kOutside;
             }
         }
-        if (kPieces >= kThreads || tid < (uint32_t)kPieces) {
-            // one register, not one for each load: the sums need them
-            asm volatile("" : "+v"(off[0]));
+        // one register, not one for each load: the sums need them
+        asm volatile("" : "+v"(off[0]));
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const uint32_t o = kSteady ? off[0] + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i];
-                lds_t* const at = to + (i * kThreads + (int)(tid & ~63u)) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, o | kill, 0, 0, 0);
-            }
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t o = kSteady ? off[0] + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i];
+            lds_t* const at = to + (i * kThreads + (int)(tid & ~63u)) * 16;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, o | kill, 0, 0, 0);
         }
     }
 
     // Where a lane reads the first fragment of the wave's rows (from r0, a
-    // multiple of the wave's share) in the first half-step, and from there
-    // fragment f in half-step h: the exchange is an XOR, so they are too.
+    // multiple of the wave's share), and from there fragment f of the h-th 32
+    // of the depth.
     static __device__ __forceinline__ uint32_t first(uint32_t lane, uint32_t r0) {
         if constexpr (kAlong) {
             const uint32_t row = r0 + (lane & 15u);
@@ -134,8 +136,7 @@ struct Stage {
     }
     static __device__ __forceinline__ s8 read(const lds_t* tile, uint32_t first, int f, int h) {
         if constexpr (kAlong) {
-            const lds_t* const p = tile + (first ^ (uint32_t)(h * 64)) + f * 16 * kRow;
-            return *reinterpret_cast<const __attribute__((address_space(3))) s8*>(p);
+            return *reinterpret_cast<const __attribute__((address_space(3))) s8*>(tile + (first ^ (uint32_t)(h * 64)) + f * 16 * kRow);
         } else {
             typedef __attribute__((address_space(3))) s4 lds_s4;
             lds_t* const p = const_cast<lds_t*>(tile) + (first ^ (uint32_t)(f * 32)) + h * 32 * kRow;
@@ -146,16 +147,30 @@ struct Stage {
     }
 };
 
-// A workgroup's tile of a product: kM x kN over kWM x kWN waves.
-template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN>
+// A workgroup's tile of a product: kM x kN over kWM x kWN waves.  The operands
+// come through a ring of slots of 32 deep, loaded kSlots - 1 steps ahead; a
+// wave holds the fragments of two steps and reads the next one's between the
+// products of this one's.
+template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
 struct Tile {
     static constexpr int kThreads = kWM * kWN * 64;
     static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part, powers of two
     static constexpr int kFM = kTM / 16, kFN = kTN / 16;
-    using A = Stage<kAlongA, kM, kThreads>;
-    using B = Stage<kAlongB, kN, kThreads>;
-    static constexpr int kStage = A::kBytes + B::kBytes;
-    static constexpr int kLds = 2 * kStage;
+    using A = Stage<kAlongA, kM, kThreads, kDepth>;
+    using B = Stage<kAlongB, kN, kThreads, kDepth>;
+    static constexpr int kSlot = A::kBytes + B::kBytes, kLoads = A::kLoads + B::kLoads;
+    static constexpr int kLds = kSlots * kSlot;
+    // A step's fragments.
+    struct Step {
+        s8 a[kFM], b[kFN];
+        __device__ __forceinline__ void read(const lds_t* from, uint32_t& fa, uint32_t& fb, int h) {
+            asm volatile("" : "+v"(fa), "+v"(fb));  // addresses are made from these two here, and not kept
+#pragma unroll
+            for (int j = 0; j < kFN; ++j) b[j] = B::read(from + A::kBytes, fb, j, h);
+#pragma unroll
+            for (int i = 0; i < kFM; ++i) a[i] = A::read(from, fa, i, h);
+        }
+    };
     f4 acc[kFM][kFN];
 
     __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
@@ -169,36 +184,73 @@ struct Tile {
         for (int i = 0; i < kFM; ++i)
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = f4{0, 0, 0, 0};
-        fetch(a, b, m0, n0, k0, la, lb, lds);
-        __syncthreads();
-        uint32_t at = 0;
-        for (int32_t k = k0 + kStep; k < k1; k += kStep, at ^= kStage) {
-            fetch(a, b, m0, n0, k, la, lb, lds + (at ^ kStage));
-            multiply(fa, fb, lds + at);
-            __syncthreads();
+        Step x, y;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) fetch(a, b, m0, n0, k0 + i * kDepth, la, lb, lds + i * kSlot);
+        wait<(kSlots - 1) * kLoads>();
+        x.read(lds, fa, fb, 0);
+        uint32_t at = 0, next = kSlot;  // the slots of this step and of the next
+        for (int32_t k = k0; k < k1; k += 64) {
+            if constexpr (kDepth == 64) {
+                y.read(lds + at, fa, fb, 1);
+                multiply(x);
+                mix();
+                step(a, b, m0, n0, k, la, lb, fa, fb, lds + at, lds + next, y, x);
+            } else {
+                step(a, b, m0, n0, k, la, lb, fa, fb, lds + at, lds + next, x, y);
+                at = next;
+                next = next == kLds - kSlot ? 0 : next + kSlot;
+                step(a, b, m0, n0, k + kDepth, la, lb, fa, fb, lds + at, lds + next, y, x);
+            }
+            at = next;
+            next = next == kLds - kSlot ? 0 : next + kSlot;
         }
-        multiply(fa, fb, lds + at);
-        __syncthreads();
+        wait<0>();  // what was loaded past the end is in LDS, too
+    }
+    // One step: products of `now`, the fragments of `then` from the next slot,
+    // and loads into the slot that `now` came from.  Restricted pointers: what
+    // is loaded is not what is read, or the compiler waits for every load before
+    // a transposing read.
+    __device__ __forceinline__ void step(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k, A& la, B& lb,
+                                         uint32_t& fa, uint32_t& fb, lds_t* __restrict to, const lds_t* __restrict from,
+                                         const Step& now, Step& then) {
+        wait<(kSlots - 2) * kLoads>();
+        fetch(a, b, m0, n0, k + kSlots * kDepth, la, lb, to);
+        then.read(from, fa, fb, 0);
+        multiply(now);
+        mix();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // All but the last n loads of every wave are in LDS, and every wave has the
+    // fragments that it was reading.
+    template <int n>
+    static __device__ __forceinline__ void wait() {
+        static_assert(n < 64, "what the counter holds");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((n & 15) | 7 << 4 | 0 << 8 | (n >> 4) << 14);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
     }
     static __device__ __forceinline__ void fetch(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k, A& la, B& lb,
                                                  lds_t* to) {
         la.load(a, m0, k, to);
         lb.load(b, n0, k, to + A::kBytes);
     }
-    __device__ __forceinline__ void multiply(uint32_t& fa, uint32_t& fb, const lds_t* from) {
-        asm volatile("" : "+v"(fa), "+v"(fb));  // addresses are made from these two here, and not kept
+    __device__ __forceinline__ void multiply(const Step& f) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s8 x[kFM], y[kFN];
+        for (int i = 0; i < kFM; ++i)
 #pragma unroll
-            for (int i = 0; i < kFM; ++i) x[i] = A::read(from, fa, i, h);
-#pragma unroll
-            for (int j = 0; j < kFN; ++j) y[j] = B::read(from + A::kBytes, fb, j, h);
-#pragma unroll
-            for (int i = 0; i < kFM; ++i)
-#pragma unroll
-                for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(x[i], y[j], acc[i][j]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(f.a[i], f.b[j], acc[i][j]);
+    }
+    // The other step's reads stand between the products, not before them.
+    static constexpr int kReads = kFM * (kAlongA ? 1 : 2) + kFN * (kAlongB ? 1 : 2), kProducts = kFM * kFN;
+    template <int i = 0>
+    static __device__ __forceinline__ void mix() {
+        if constexpr (i < kReads) {
+            constexpr int n = (i + 1) * kProducts / kReads - i * kProducts / kReads;
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, n, 0);
+            mix<i + 1>();
         }
     }
     // The wave's first row and column in the tile, and the lane's of a fragment.
@@ -223,9 +275,9 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, ui
 // ---------------------------------------------------------------------------
 // The loss: each tile's reference and sum of a token, and the label's logit.
 
-template <class T, int kM, int kN, int kWM, int kWN>
+template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
-    using G = Tile<T, true, true, kM, kN, kWM, kWN>;
+    using G = Tile<T, true, true, kM, kN, kWM, kWN, kDepth, kSlots>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, a.tiles_v, a.tiles_n, tm, tn);
@@ -412,9 +464,9 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
 
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
 // step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
-template <class T, int kM, int kN, int kWM, int kWN>
+template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, true, true, kM, kN, kWM, kWN>;
+    using G = Tile<T, true, true, kM, kN, kWM, kWN, kDepth, kSlots>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
@@ -446,9 +498,10 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
 }
 
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
-template <class T, int kM, int kN, int kWM, int kWN>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first) {
-    using G = Tile<T, false, true, kM, kN, kWM, kWN>;
+// Where one split sums them all, the last piece's launch writes dh itself.
+template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last) {
+    using G = Tile<T, false, true, kM, kN, kWM, kWN, kDepth, kSlots>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
@@ -468,17 +521,26 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
 #pragma unroll
             for (int j = 0; j < G::kFN; ++j) g.acc[i][j] = f4{0, 0, 0, 0};
     }
+    const bool whole = last && a.splits == 1;
     const int64_t m = m0 + G::wave_m() + G::lane_m(), n1 = n0 + G::wave_n() + G::lane_n();
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
         const int64_t n = n1 + j * 16;
         if (n >= a.rows) continue;
         float* const to = a.dh_sum + ((int64_t)split * a.rows + n) * a.dim + m;
+        char* const out = (char*)a.dh + (n * a.ld_dh + m) * 2;
+        const float c = whole ? a.row[n].dh : 1.0f;
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
             if (m + i * 16 < a.dim) {
                 f4* const q = reinterpret_cast<f4*>(to + i * 16);
-                *q = first ? g.acc[i][j] : *q + g.acc[i][j];
+                f4 x = first ? g.acc[i][j] : *q + g.acc[i][j];
+                if (!whole) {
+                    *q = x;
+                } else {
+                    x = c != 0.0f ? x * c : f4{0, 0, 0, 0};
+                    *reinterpret_cast<uint2*>(out + i * 32) = uint2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+                }
             }
     }
 }
@@ -503,9 +565,9 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
 }
 
 // dw of a piece.
-template <class T, int kM, int kN, int kWM, int kWN>
+template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, false, false, kM, kN, kWM, kWN>;
+    using G = Tile<T, false, false, kM, kN, kWM, kWN, kDepth, kSlots>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
@@ -543,10 +605,10 @@ template <class T>
 hipError_t sums_of(hipStream_t s, const VocabArgs& a) {
     const int64_t tiles = (int64_t)a.tiles_v * a.tiles_n;
     switch (a.tile_n) {
-        case 16: SCAPE_RUN((k_vocab_sums<T, 256, 16, 4, 1>), tiles, 256, a); break;
-        case 64: SCAPE_RUN((k_vocab_sums<T, 256, 64, 4, 1>), tiles, 256, a); break;
-        case 128: SCAPE_RUN((k_vocab_sums<T, 256, 128, 4, 2>), tiles, 512, a); break;
-        default: SCAPE_RUN((k_vocab_sums<T, 256, 256, 2, 4>), tiles, 512, a); break;
+        case 16: SCAPE_RUN((k_vocab_sums<T, 256, 16, 4, 1, 64, 2>), tiles, 256, a); break;
+        case 64: SCAPE_RUN((k_vocab_sums<T, 256, 64, 4, 1, 64, 2>), tiles, 256, a); break;
+        case 128: SCAPE_RUN((k_vocab_sums<T, 256, 128, 4, 2, 64, 3>), tiles, 512, a); break;
+        default: SCAPE_RUN((k_vocab_sums<T, 256, 256, 2, 4, 64, 2>), tiles, 512, a); break;
     }
     SCAPE_RUN(k_vocab_join, (a.rows + kJoinTokens - 1) / kJoinTokens, kJoinTokens * kJoinParts, a);
     return hipGetLastError();
@@ -565,24 +627,24 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         const int32_t v1 = v0 + a.piece < a.cols ? v0 + (int32_t)a.piece : (int32_t)a.cols;
         const int64_t words = (v1 - v0 + 255) / 256, tiles = words * a.tiles_n;
         switch (a.tile_n) {
-            case 16: SCAPE_RUN((k_vocab_p<T, 256, 16, 4, 1>), tiles, 256, a, v0, v1); break;
-            case 64: SCAPE_RUN((k_vocab_p<T, 256, 64, 4, 1>), tiles, 256, a, v0, v1); break;
-            case 128: SCAPE_RUN((k_vocab_p<T, 256, 128, 4, 2>), tiles, 512, a, v0, v1); break;
-            default: SCAPE_RUN((k_vocab_p<T, 256, 256, 2, 4>), tiles, 512, a, v0, v1); break;
+            case 16: SCAPE_RUN((k_vocab_p<T, 256, 16, 4, 1, 64, 2>), tiles, 256, a, v0, v1); break;
+            case 64: SCAPE_RUN((k_vocab_p<T, 256, 64, 4, 1, 64, 2>), tiles, 256, a, v0, v1); break;
+            case 128: SCAPE_RUN((k_vocab_p<T, 256, 128, 4, 2, 64, 3>), tiles, 512, a, v0, v1); break;
+            default: SCAPE_RUN((k_vocab_p<T, 256, 256, 2, 4, 64, 2>), tiles, 512, a, v0, v1); break;
         }
         if (a.dh) {
             const int64_t n = dim_tiles * a.tiles_n * a.splits;
-            const bool first = v0 == 0;
+            const bool first = v0 == 0, last = v1 == a.cols;
             switch (a.tile_n) {
-                case 16: SCAPE_RUN((k_vocab_dh<T, 256, 16, 4, 1>), n, 256, a, v0, v1, first); break;
-                case 64: SCAPE_RUN((k_vocab_dh<T, 256, 64, 4, 1>), n, 256, a, v0, v1, first); break;
-                case 128: SCAPE_RUN((k_vocab_dh<T, 256, 128, 4, 2>), n, 512, a, v0, v1, first); break;
-                default: SCAPE_RUN((k_vocab_dh<T, 256, 256, 2, 4>), n, 512, a, v0, v1, first); break;
+                case 16: SCAPE_RUN((k_vocab_dh<T, 256, 16, 4, 1, 64, 2>), n, 256, a, v0, v1, first, last); break;
+                case 64: SCAPE_RUN((k_vocab_dh<T, 256, 64, 4, 1, 64, 2>), n, 256, a, v0, v1, first, last); break;
+                case 128: SCAPE_RUN((k_vocab_dh<T, 256, 128, 4, 2, 64, 3>), n, 512, a, v0, v1, first, last); break;
+                default: SCAPE_RUN((k_vocab_dh<T, 256, 256, 2, 4, 64, 2>), n, 512, a, v0, v1, first, last); break;
             }
         }
-        if (a.dw) SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4>), dim_tiles * words, 512, a, v0, v1);
+        if (a.dw) SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 64, 2>), dim_tiles * words, 512, a, v0, v1);
     }
-    if (a.dh) SCAPE_RUN(k_vocab_dh_join<T>, a.rows, kRowThreads, a);
+    if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows, kRowThreads, a);
     return hipGetLastError();
 }
 

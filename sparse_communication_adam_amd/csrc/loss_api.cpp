@@ -251,22 +251,32 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
     a->rows_pad = (int64_t)a->tiles_n * a->tile_n;
     return SCAPE_OK;
 }
-// The pieces of the backward pass: P of one is at most 2^26 elements, which the
-// last-level cache holds, and at least 4096 words wide, so that dw has tiles
-// for the CUs.  dh's sums are split over the words until there are about two
-// workgroups for each of 256 CUs.
+// The pieces of the backward pass: P of one is at most 2^27 elements, and at
+// least 4096 words wide, so that dw has tiles for the CUs.  P's rows lie a
+// little further apart than a piece's words, off the powers of two.
+// dh's sums are split over the words where its tiles leave CUs idle: the number
+// of splits is the one with the least rounds of tiles on 256 CUs times a split's
+// steps (and about 6 more for its start and its end), counting the splits'
+// sums, which are written and read once more, at a step for each 8 MB.
 void vocab_pieces(VocabArgs* a) {
-    int64_t most = a->rows_pad ? (int64_t(1) << 26) / a->rows_pad / kTileWordsV * kTileWordsV : a->cols;
+    int64_t most = a->rows_pad ? (int64_t(1) << 27) / a->rows_pad / kTileWordsV * kTileWordsV : a->cols;
     if (most < 4096) most = 4096;
     const int64_t pieces = (a->cols + most - 1) / most;
     a->piece = round_up((a->cols + pieces - 1) / pieces, kTileWordsV);
-    a->ld_p = a->piece;
+    a->ld_p = a->piece + 64;
     const int64_t tiles = (a->dim + 255) / 256 * (a->tiles_n ? a->tiles_n : 1);
-    int64_t n = 512 / tiles;
-    if (n > a->piece / 512) n = a->piece / 512;
-    if (n < 1) n = 1;
-    a->split_words = round_up((a->piece + n - 1) / n, 64);
-    a->splits = (int32_t)((a->piece + a->split_words - 1) / a->split_words);
+    const int64_t slots = a->tile_n <= 64 ? 512 : 256;  // two workgroups a CU where LDS holds them
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= 128 && (n == 1 || a->piece / n >= 256); ++n) {
+        const int64_t words = round_up((a->piece + n - 1) / n, 64), splits = (a->piece + words - 1) / words;
+        const int64_t cost = (tiles * splits + slots - 1) / slots * (words / 64 + 6) +
+                             (splits > 1 ? splits * a->rows * a->dim * 8 / (int64_t(8) << 20) : 0);
+        if (cost < best) {
+            best = cost;
+            a->split_words = words;
+            a->splits = (int32_t)splits;
+        }
+    }
 }
 int64_t vocab_loss_bytes(const VocabArgs& a) {
     return a.rows * ((int64_t)a.tiles_v * 8 + 4);
