@@ -702,7 +702,7 @@ int scape_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, int6
  * none.  The places are distinct, as scape_expert_sort makes them.  Rows of y
  * that no place names stay as they were.  x [tokens][dim] and y [rows][dim] of
  * one of the three types, rows ld_x and ld_y >= dim elements apart, aligned to
- * their element; they do not overlap.  dim >= 1; tokens <= 2^25.
+ * their element; they do not overlap.  1 <= dim <= 2^24; tokens <= 2^25.
  * Its gradient is scape_expert_combine of dy without weights.
  * Errors: as scape_topk_rows. */
 int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t dim, int64_t ld_x, const int32_t* row,

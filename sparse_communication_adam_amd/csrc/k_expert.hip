@@ -14,9 +14,9 @@ namespace scape {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The sort: a count, a scan over experts and blocks, and the places.  A wave
-// goes through a run of choices 64 at a time; lanes of equal expert find each
-// other by ballots over the expert's bits.
+// The sort: a count for each block, and the places.  A wave goes through a run
+// of choices 64 at a time; lanes of equal expert find each other by ballots over
+// the expert's bits.
 
 __device__ __forceinline__ uint64_t alike(int32_t e, bool on, int bits) {
     uint64_t m = wave_ballot(on);
@@ -34,197 +34,333 @@ __device__ __forceinline__ int32_t choice(const SortArgs& a, int64_t p, int64_t 
     return e >= 0 && e < a.experts ? e : -1;
 }
 
-// Counts of a wave's run, into its row of LDS.
+// Counts of a wave's run, into its row of LDS; kAhead loads are on their way.
+constexpr int kAhead = 8;
 __device__ __forceinline__ void count_run(const SortArgs& a, uint32_t* row, int64_t p0, int64_t p1) {
-    for (int64_t p = p0; p < p1; p += 64) {
-        const int32_t e = choice(a, p + lane_id(), p1);
-        if (e >= 0) atomicAdd(&row[e], 1u);
+    for (int64_t p = p0; p < p1; p += 64 * kAhead) {
+        int32_t e[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) e[i] = choice(a, p + i * 64 + lane_id(), p1);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (e[i] >= 0) atomicAdd(&row[e[i]], 1u);
     }
 }
 // The places of a wave's run; row holds each expert's next place.
 __device__ __forceinline__ void place_run(const SortArgs& a, volatile uint32_t* row, int64_t p0, int64_t p1) {
-    for (int64_t p = p0; p < p1; p += 64) {
-        const int64_t at = p + lane_id();
-        const int32_t e = choice(a, at, p1);
-        const uint64_t m = alike(e, e >= 0, a.bits);
-        const uint32_t rank = lanes_below(m);
-        // LDS serves a wave in order: all lanes have read before the first of
-        // each expert writes
-        const uint32_t base = e >= 0 ? row[e] : 0u;
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && rank == 0) row[e] = base + (uint32_t)__popcll(m);
-        __builtin_amdgcn_wave_barrier();
-        if (at < p1) a.row[at] = e >= 0 ? (int32_t)(base + rank) : -1;
+    for (int64_t p = p0; p < p1; p += 64 * kAhead) {
+        int32_t e[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) e[i] = choice(a, p + i * 64 + lane_id(), p1);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (p + i * 64 >= p1) break;
+            const int64_t at = p + i * 64 + lane_id();
+            const uint64_t m = alike(e[i], e[i] >= 0, a.bits);
+            const uint32_t rank = lanes_below(m);
+            // LDS serves a wave in order: all lanes have read before the first of
+            // each expert writes
+            const uint32_t base = e[i] >= 0 ? row[e[i]] : 0u;
+            __builtin_amdgcn_wave_barrier();
+            if (e[i] >= 0 && rank == 0) row[e[i]] = base + (uint32_t)__popcll(m);
+            __builtin_amdgcn_wave_barrier();
+            if (at < p1) a.row[at] = e[i] >= 0 ? (int32_t)(base + rank) : -1;
+        }
     }
+}
+
+// A wave's run of choices: a quarter of the block's.
+__device__ __forceinline__ void run_of(const SortArgs& a, int64_t& p0, int64_t& p1) {
+    p0 = (int64_t)blockIdx.x * a.run + (threadIdx.x >> 6) * (a.run / kWaves);
+    p1 = p0 + a.run / kWaves;
+    if (p1 > a.choices) p1 = a.choices;
 }
 
 __global__ __launch_bounds__(kBlock) void k_expert_count(SortArgs a) {
     __shared__ uint32_t hist[kMaxExperts];
     for (int32_t e = threadIdx.x; e < a.experts; e += kBlock) hist[e] = 0;
     __syncthreads();
-    const int64_t b0 = (int64_t)blockIdx.x * a.run, p0 = b0 + (threadIdx.x >> 6) * (a.run / kWaves);
-    int64_t p1 = p0 + a.run / kWaves;
-    if (p1 > a.choices) p1 = a.choices;
+    int64_t p0, p1;
+    run_of(a, p0, p1);
     count_run(a, hist, p0, p1);
     __syncthreads();
     for (int32_t e = threadIdx.x; e < a.experts; e += kBlock) a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
-// Counts become first places: of the experts before, and of the blocks before
-// within an expert.  One workgroup, a thread an expert.
-__global__ __launch_bounds__(kMaxExperts) void k_expert_scan(SortArgs a) {
-    __shared__ uint32_t scratch[kMaxExperts / 64];
-    const int32_t e = (int32_t)threadIdx.x;
-    uint32_t n = 0;
-    if (e < a.experts)
-        for (int32_t b = 0; b < a.blocks; ++b) n += a.counts[(int64_t)b * a.experts + e];
-    uint32_t total, at = block_exclusive_scan_t<kMaxExperts>(n, scratch, &total);
-    if (e < a.experts) {
-        a.offsets[e] = (int32_t)at;
-        for (int32_t b = 0; b < a.blocks; ++b) {
-            uint32_t* const c = &a.counts[(int64_t)b * a.experts + e];
-            const uint32_t k = *c;
-            *c = at;
-            at += k;
-        }
-    }
-    if (e == 0) a.offsets[a.experts] = (int32_t)total;
-}
-
+// The places.  Each block sums the counts of all blocks, and of those before
+// it, for itself: they are few (a block for 2048 choices) and in the caches,
+// and a launch between the count and this costs more (131072 choices of 64
+// experts, in a trace, us: 2.9 + 8.9 + 4.9 with a launch for the scan, 2.9 + 6.9
+// without).  One block alone needs no count before it.
 __global__ __launch_bounds__(kBlock) void k_expert_place(SortArgs a) {
-    __shared__ uint32_t next[kWaves][kMaxExperts];
-    const uint32_t wave = threadIdx.x >> 6;
-    for (int32_t e = threadIdx.x; e < a.experts; e += kBlock)
+    __shared__ uint32_t next[kWaves][kMaxExperts], before[kMaxExperts], total[kMaxExperts], scratch[kWaves];
+    const uint32_t tid = threadIdx.x, wave = tid >> 6;
+    for (int32_t e = tid; e < a.experts; e += kBlock) {
         for (int w = 0; w < kWaves; ++w) next[w][e] = 0;
+        before[e] = total[e] = 0;
+    }
     __syncthreads();
-    const int64_t p0 = (int64_t)blockIdx.x * a.run + wave * (a.run / kWaves);
-    int64_t p1 = p0 + a.run / kWaves;
-    if (p1 > a.choices) p1 = a.choices;
+    int64_t p0, p1;
+    run_of(a, p0, p1);
     count_run(a, next[wave], p0, p1);
-    __syncthreads();
-    for (int32_t e = threadIdx.x; e < a.experts; e += kBlock) {
-        uint32_t at = a.counts[(int64_t)blockIdx.x * a.experts + e];
-        for (int w = 0; w < kWaves; ++w) {
-            const uint32_t n = next[w][e];
-            next[w][e] = at;
-            at += n;
+    if (a.blocks > 1) {
+        // few experts: several threads share one's blocks
+        const int32_t parts = a.experts <= kBlock / 4 ? 4 : a.experts <= kBlock / 2 ? 2 : 1, lanes = kBlock / parts;
+        const int32_t part = (int32_t)tid / lanes;
+        for (int32_t e = (int32_t)tid % lanes; e < a.experts; e += lanes) {
+            uint32_t all = 0, here = 0;
+#pragma unroll 16
+            for (int32_t b = part; b < a.blocks; b += parts) {
+                const uint32_t n = a.counts[(int64_t)b * a.experts + e];
+                all += n;
+                here += b < (int32_t)blockIdx.x ? n : 0u;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&before[e], here);
         }
     }
+    __syncthreads();
+    // first places: a thread has kMaxExperts / kBlock experts in a row
+    constexpr int kEach = kMaxExperts / kBlock;
+    uint32_t n[kEach], sum = 0;
+    for (int i = 0; i < kEach; ++i) {
+        const int32_t e = (int32_t)tid * kEach + i;
+        n[i] = 0;
+        if (e < a.experts) {
+            n[i] = total[e];
+            if (a.blocks == 1)
+                for (int w = 0; w < kWaves; ++w) n[i] += next[w][e];
+        }
+        sum += n[i];
+    }
+    uint32_t all, at = block_exclusive_scan(sum, scratch, &all);
+    for (int i = 0; i < kEach; ++i) {
+        const int32_t e = (int32_t)tid * kEach + i;
+        if (e < a.experts) {
+            if (blockIdx.x == 0) a.offsets[e] = (int32_t)at;
+            uint32_t place = at + before[e];
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t c = next[w][e];
+                next[w][e] = place;
+                place += c;
+            }
+        }
+        at += n[i];
+    }
+    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = (int32_t)all;
     __syncthreads();
     place_run(a, next[wave], p0, p1);
 }
 
 // ---------------------------------------------------------------------------
-// The moves.  Rows lie anywhere: 16 bytes at a time from their first element,
-// at whatever alignment, and the rest one element a lane.
+// The moves.  A wave takes a token.  Its places and weights are loaded once, a
+// lane each, and handed round as scalars.  Rows lie anywhere: 16 bytes at a time
+// from their first element, at whatever alignment, and the rest one element a
+// lane.  Lanes behind a row's last granule load it again and store nothing.
 
 typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ gran read16(const char* row, int64_t i) {
-    return (gran) * reinterpret_cast<const loose*>(row + i * 16);
+__device__ __forceinline__ gran read16(const void* row, uint32_t byte) {
+    return (gran)__builtin_nontemporal_load(reinterpret_cast<const loose*>(static_cast<const char*>(row) + byte));
 }
-__device__ __forceinline__ void write16(char* row, int64_t i, const gran& g) {
-    *reinterpret_cast<loose*>(row + i * 16) = (loose)g;
+__device__ __forceinline__ gran read16_again(const void* row, uint32_t byte) {  // a row that is read more than once
+    return (gran)*reinterpret_cast<const loose*>(static_cast<const char*>(row) + byte);
 }
-
-// Where choice j of token t lies, or -1.
-__device__ __forceinline__ int64_t place(const MoveArgs& a, int64_t t, int32_t j) {
-    const int32_t r = __builtin_amdgcn_readfirstlane(a.row[t * a.k + j]);
-    return r >= 0 && r < a.rows ? r : -1;
+__device__ __forceinline__ void write16(void* row, uint32_t byte, const gran& g) {
+    __builtin_nontemporal_store((loose)g, reinterpret_cast<loose*>(static_cast<char*>(row) + byte));
 }
 
-template <class T>
+// Up to 64 choices of a token from j0 on, a lane each: the place (-1: none) and
+// the weight.
+struct Held {
+    int32_t row;
+    float weight;
+    __device__ __forceinline__ void load(const MoveArgs& a, int64_t t, int32_t j0) {
+        const int32_t j = j0 + (int32_t)lane_id();
+        row = -1;
+        weight = 1.0f;
+        if (j < a.k) {
+            row = a.row[t * a.k + j];
+            if (a.weight) weight = a.weight[t * a.k + j];
+        }
+        if (row < 0 || row >= a.rows) row = -1;
+    }
+    __device__ __forceinline__ int32_t place(int j) const { return __builtin_amdgcn_readlane(row, j); }
+    __device__ __forceinline__ float factor(int j) const {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), j));
+    }
+};
+__device__ __forceinline__ int64_t token_of_wave() {
+    return (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+// A row in granules: kB at a time for each lane.
+template <class T, int kB>
+struct Row {
+    using raw = typename T::raw;
+    static __device__ __forceinline__ uint32_t byte(int64_t whole, int64_t i) {  // of granule i, or of the last
+        return (uint32_t)(i < whole ? i : whole - 1) * 16u;
+    }
+    static __device__ __forceinline__ void load(gran (&g)[kB], const void* row, int64_t whole, int64_t i0) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b) g[b] = read16(row, byte(whole, i0 + b * 64));
+    }
+    static __device__ __forceinline__ void load_again(gran (&g)[kB], const void* row, int64_t whole, int64_t i0) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b) g[b] = read16_again(row, byte(whole, i0 + b * 64));
+    }
+    static __device__ __forceinline__ void store(const gran (&g)[kB], void* row, int64_t whole, int64_t i0) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+            if (i0 + b * 64 < whole) write16(row, (uint32_t)(i0 + b * 64) * 16u, g[b]);
+    }
+};
+
+// kB granules of the token are in registers while they go to its places.
+template <class T, int kB>
 __global__ __launch_bounds__(kBlock) void k_expert_gather(MoveArgs a) {
     using raw = typename T::raw;
     const uint32_t lane = lane_id();
-    const int64_t t = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = token_of_wave();
     if (t >= a.tokens) return;
-    const char* const x = (const char*)a.x + t * a.ld_x * sizeof(raw);
+    const raw* const x = static_cast<const raw*>(a.x) + t * a.ld_x;
+    raw* const y = static_cast<raw*>(a.y);
     const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
-    for (int64_t i = lane; i < whole; i += 64) {
-        const gran g = read16(x, i);
-        for (int32_t j = 0; j < a.k; ++j) {
-            const int64_t r = place(a, t, j);
-            if (r >= 0) write16((char*)a.y + r * a.ld_y * sizeof(raw), i, g);
+    Held h;
+    for (int32_t j0 = 0; j0 < a.k; j0 += 64) {
+        h.load(a, t, j0);
+        const int n = a.k - j0 < 64 ? a.k - j0 : 64;
+        for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+            gran g[kB];
+            Row<T, kB>::load_again(g, x, whole, i);
+            for (int j = 0; j < n; ++j) {
+                const int64_t r = h.place(j);
+                if (r >= 0) Row<T, kB>::store(g, y + r * a.ld_y, whole, i);
+            }
         }
-    }
-    if (rest < a.dim) {
-        const raw v = reinterpret_cast<const raw*>(x)[rest];
-        for (int32_t j = 0; j < a.k; ++j) {
-            const int64_t r = place(a, t, j);
-            if (r >= 0) reinterpret_cast<raw*>(a.y)[r * a.ld_y + rest] = v;
+        if (whole * T::kN < a.dim) {
+            const raw v = rest < a.dim ? x[rest] : (raw)0;
+            for (int j = 0; j < n; ++j) {
+                const int64_t r = h.place(j);
+                if (r >= 0 && rest < a.dim) y[r * a.ld_y + rest] = v;
+            }
         }
     }
 }
 
-// Sums in float32 in the order of the choices, rounded once.
-template <class T>
+// Sums in float32 in the order of the choices, rounded once.  kJ rows are on
+// their way at a time; a place that is none, or has weight 0, reads a granule of
+// zeros instead, so that no load stands under a condition.
+template <class T, int kB, int kJ>
 __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
     using raw = typename T::raw;
     const uint32_t lane = lane_id();
-    const int64_t t = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = token_of_wave();
     if (t >= a.tokens) return;
-    char* const out = (char*)a.out + t * a.ld_out * sizeof(raw);
+    raw* const out = static_cast<raw*>(a.out) + t * a.ld_out;
+    const raw* const y = static_cast<const raw*>(a.y);
     const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
-    for (int64_t i = lane; i < whole; i += 64) {
-        float s[T::kN];
+    Held h;
+    if (a.k <= 64) h.load(a, t, 0);
+    for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+        float s[kB][T::kN];
 #pragma unroll
-        for (int e = 0; e < T::kN; ++e) s[e] = 0.0f;
-        for (int32_t j = 0; j < a.k; ++j) {
-            const int64_t r = place(a, t, j);
-            const float w = a.weight ? a.weight[t * a.k + j] : 1.0f;
-            if (r < 0 || w == 0.0f) continue;
-            const gran g = read16((const char*)a.y + r * a.ld_y * sizeof(raw), i);
+        for (int b = 0; b < kB; ++b)
 #pragma unroll
-            for (int e = 0; e < T::kN; ++e) s[e] = __builtin_fmaf(w, T::up(g, e), s[e]);
+            for (int e = 0; e < T::kN; ++e) s[b][e] = 0.0f;
+        for (int32_t j0 = 0; j0 < a.k; j0 += kJ) {
+            if (a.k > 64 && (j0 & 63) == 0) h.load(a, t, j0);
+            gran g[kJ][kB];
+            float w[kJ];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {  // lanes behind the last choice hold none
+                const int64_t r = h.place((j0 + j) & 63);
+                w[j] = h.factor((j0 + j) & 63);
+                const bool on = r >= 0 && w[j] != 0.0f && j0 + j < a.k;
+                const void* const row = on ? static_cast<const void*>(y + r * a.ld_y) : &g_no_granule;
+                if (!on) w[j] = 0.0f;
+#pragma unroll
+                for (int b = 0; b < kB; ++b) g[j][b] = read16(row, on ? Row<T, kB>::byte(whole, i + b * 64) : 0u);
+            }
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                for (int b = 0; b < kB; ++b)
+#pragma unroll
+                    for (int e = 0; e < T::kN; ++e) s[b][e] = __builtin_fmaf(w[j], T::up(g[j][b], e), s[b][e]);
         }
-        write16(out, i, T::down(s));
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+            if (i + b * 64 < whole) write16(out, (uint32_t)(i + b * 64) * 16u, T::down(s[b]));
     }
-    if (rest < a.dim) {
+    if (whole * T::kN < a.dim) {
         float s = 0.0f;
         for (int32_t j = 0; j < a.k; ++j) {
-            const int64_t r = place(a, t, j);
-            const float w = a.weight ? a.weight[t * a.k + j] : 1.0f;
-            if (r < 0 || w == 0.0f) continue;
-            s = __builtin_fmaf(w, T::up1(reinterpret_cast<const raw*>(a.y)[r * a.ld_y + rest]), s);
+            if ((a.k > 64 && (j & 63) == 0)) h.load(a, t, j);
+            const int64_t r = h.place(j & 63);
+            const float w = h.factor(j & 63);
+            if (r < 0 || w == 0.0f || rest >= a.dim) continue;
+            s = __builtin_fmaf(w, T::up1(y[r * a.ld_y + rest]), s);
         }
-        reinterpret_cast<raw*>(out)[rest] = T::down1(s);
+        if (rest < a.dim) out[rest] = T::down1(s);
     }
 }
 
-template <class T>
+// A workgroup takes a token and its waves the token's choices in turn (a wave
+// for a token is slower for few tokens: 2000x1536 f16, k = 4, 12.9 us and 15.5).
+// dout is in registers where kB granules a lane hold it all, else it is read for
+// every place; the waves' reads of it meet in the L1.
+template <class T, int kB>
 __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
     using raw = typename T::raw;
     const uint32_t lane = lane_id();
-    const int64_t t = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (t >= a.tokens) return;
-    const char* const dout = (const char*)a.x + t * a.ld_x * sizeof(raw);
+    const int64_t t = blockIdx.x;
+    const raw* const dout = static_cast<const raw*>(a.x) + t * a.ld_x;
+    const raw* const y = static_cast<const raw*>(a.y_in);
+    raw* const dy = static_cast<raw*>(a.y);
     const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
-    for (int32_t j = 0; j < a.k; ++j) {
-        const int64_t r = place(a, t, j);
+    const bool held = whole <= 64 * kB, tail = whole * T::kN < a.dim;
+    gran d[kB];
+    if (held && whole) Row<T, kB>::load_again(d, dout, whole, lane);
+    const float last = tail && rest < a.dim ? T::up1(dout[rest]) : 0.0f;
+    Held h;
+    const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int32_t j = wave; j < a.k; j += kWaves) {
+        if (j == wave || (j & 63) == wave) h.load(a, t, j & ~63);
+        const int64_t r = h.place(j & 63);
         if (r < 0) {
             if (a.dweight && lane == 0) a.dweight[t * a.k + j] = 0.0f;
             continue;
         }
-        const float w = a.weight ? a.weight[t * a.k + j] : 1.0f;
-        const char* const y = (const char*)a.y_in + r * a.ld_y_in * sizeof(raw);
-        char* const dy = (char*)a.y + r * a.ld_y * sizeof(raw);
+        const float w = h.factor(j & 63);
         float dot = 0.0f;
-        for (int64_t i = lane; i < whole; i += 64) {
-            const gran d = read16(dout, i);
-            if (a.dweight) {
-                const gran g = read16(y, i);
+        for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+            gran g[kB];
+            if (a.dweight) Row<T, kB>::load(g, y + r * a.ld_y_in, whole, i);
+            if (!held) Row<T, kB>::load_again(d, dout, whole, i);
+            if (dy) {
+                gran v[kB];
 #pragma unroll
-                for (int e = 0; e < T::kN; ++e) dot = __builtin_fmaf(T::up(g, e), T::up(d, e), dot);
+                for (int b = 0; b < kB; ++b) {
+                    float f[T::kN];
+#pragma unroll
+                    for (int e = 0; e < T::kN; ++e) f[e] = w != 0.0f ? w * T::up(d[b], e) : 0.0f;
+                    v[b] = T::down(f);
+                }
+                Row<T, kB>::store(v, dy + r * a.ld_y, whole, i);
             }
-            float v[T::kN];
+            if (a.dweight) {
 #pragma unroll
-            for (int e = 0; e < T::kN; ++e) v[e] = w != 0.0f ? w * T::up(d, e) : 0.0f;
-            if (a.y) write16(dy, i, T::down(v));
+                for (int b = 0; b < kB; ++b) {
+                    float part = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < T::kN; ++e) part = __builtin_fmaf(T::up(g[b], e), T::up(d[b], e), part);
+                    dot += i + b * 64 < whole ? part : 0.0f;
+                }
+            }
         }
-        if (rest < a.dim) {
-            const float d = T::up1(reinterpret_cast<const raw*>(dout)[rest]);
-            if (a.dweight) dot = __builtin_fmaf(T::up1(reinterpret_cast<const raw*>(y)[rest]), d, dot);
-            if (a.y) reinterpret_cast<raw*>(dy)[rest] = T::down1(w != 0.0f ? w * d : 0.0f);
+        if (tail && rest < a.dim) {
+            if (a.dweight) dot = __builtin_fmaf(T::up1(y[r * a.ld_y_in + rest]), last, dot);
+            if (dy) dy[r * a.ld_y + rest] = T::down1(w != 0.0f ? w * last : 0.0f);
         }
         if (a.dweight) {
             dot = group_reduce<OpSumF, 64>(dot);
@@ -233,26 +369,58 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
     }
 }
 
-#define SCAPE_BY_TYPE(kernel)                                                                                   \
-    do {                                                                                                        \
-        const dim3 grid((uint32_t)((a.tokens + kWaves - 1) / kWaves)), block(kBlock);                           \
-        if (a.dtype == SCAPE_DTYPE_F32) hipLaunchKernelGGL(kernel<F32>, grid, block, 0, s, a);                  \
-        else if (a.dtype == SCAPE_DTYPE_BF16) hipLaunchKernelGGL(kernel<BF16>, grid, block, 0, s, a);           \
-        else hipLaunchKernelGGL(kernel<F16>, grid, block, 0, s, a);                                             \
-        return hipGetLastError();                                                                               \
-    } while (0)
+// Granules a lane: as many as a row has for it, up to four or eight.
+int granules_of(const MoveArgs& a) { return (int)((a.dim / (16 / dtype_size(a.dtype)) + 63) / 64); }
+
+#define SCAPE_RUN(...) \
+    hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)((a.tokens + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a)
+#define SCAPE_RUN_TOKEN(...) hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)a.tokens), dim3(kBlock), 0, s, a)
+
+template <class T>
+hipError_t gather_of(hipStream_t s, const MoveArgs& a) {
+    const int n = granules_of(a);
+    if (n <= 1) SCAPE_RUN(k_expert_gather<T, 1>);
+    else if (n <= 2) SCAPE_RUN(k_expert_gather<T, 2>);
+    else SCAPE_RUN(k_expert_gather<T, 4>);
+    return hipGetLastError();
+}
+template <class T>
+hipError_t combine_of(hipStream_t s, const MoveArgs& a) {
+    const int n = granules_of(a);
+    if (a.k <= 2) {
+        if (n <= 1) SCAPE_RUN(k_expert_combine<T, 1, 2>);
+        else SCAPE_RUN(k_expert_combine<T, 2, 2>);
+    } else if (a.k <= 4) {
+        if (n <= 1) SCAPE_RUN(k_expert_combine<T, 1, 4>);
+        else SCAPE_RUN(k_expert_combine<T, 2, 4>);
+    } else {
+        if (n <= 1) SCAPE_RUN(k_expert_combine<T, 1, 8>);
+        else SCAPE_RUN(k_expert_combine<T, 2, 8>);
+    }
+    return hipGetLastError();
+}
+template <class T>
+hipError_t back_of(hipStream_t s, const MoveArgs& a) {
+    const int n = granules_of(a);
+    if (n <= 1) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 1>);
+    else if (n <= 2) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 2>);
+    else if (n <= 4) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 4>);
+    else SCAPE_RUN_TOKEN(k_expert_combine_back<T, 8>);
+    return hipGetLastError();
+}
+#define SCAPE_BY_TYPE(run) \
+    return a.dtype == SCAPE_DTYPE_F32 ? run<F32>(s, a) : a.dtype == SCAPE_DTYPE_BF16 ? run<BF16>(s, a) : run<F16>(s, a)
 
 }  // namespace
 
 hipError_t launch_expert_sort(hipStream_t s, const SortArgs& a) {
-    const dim3 blocks((uint32_t)a.blocks);
-    if (a.blocks) hipLaunchKernelGGL(k_expert_count, blocks, dim3(kBlock), 0, s, a);
-    hipLaunchKernelGGL(k_expert_scan, dim3(1), dim3(kMaxExperts), 0, s, a);  // offsets are written in any case
-    if (a.blocks) hipLaunchKernelGGL(k_expert_place, blocks, dim3(kBlock), 0, s, a);
+    const dim3 blocks((uint32_t)a.blocks), threads(kBlock);
+    if (a.blocks > 1) hipLaunchKernelGGL(k_expert_count, blocks, threads, 0, s, a);
+    hipLaunchKernelGGL(k_expert_place, blocks, threads, 0, s, a);
     return hipGetLastError();
 }
-hipError_t launch_expert_gather(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(k_expert_gather); }
-hipError_t launch_expert_combine(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(k_expert_combine); }
-hipError_t launch_expert_combine_back(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(k_expert_combine_back); }
+hipError_t launch_expert_gather(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(gather_of); }
+hipError_t launch_expert_combine(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(combine_of); }
+hipError_t launch_expert_combine_back(hipStream_t s, const MoveArgs& a) { SCAPE_BY_TYPE(back_of); }
 
 }  // namespace scape

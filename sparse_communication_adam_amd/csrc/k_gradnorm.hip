@@ -36,8 +36,8 @@ constexpr int kTileGranules = kTileWords * 8, kPerThread = kTileGranules / kBloc
 
 __global__ __launch_bounds__(kBlock) void k_grad_squares(GradArgs a) {
     __shared__ double waves[kWaves];
-    const uint32_t tid = threadIdx.x, worker = blockIdx.x % a.workers, tile = blockIdx.x / a.workers;
-    if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;  // for the join, which is a launch behind
+    const uint32_t tid = threadIdx.x, b = xcd_block(blockIdx.x, gridDim.x);
+    const uint32_t worker = b % a.workers, tile = b / a.workers;
     const Share s = share_of(a, tile, worker);
     const int32_t whole = s.elements / 8;
     double sum[2] = {0.0, 0.0};
@@ -68,91 +68,87 @@ __global__ __launch_bounds__(kBlock) void k_grad_squares(GradArgs a) {
     if (tid == 0) a.part[(int64_t)worker * a.n_tiles + tile] = (waves[0] + waves[1]) + (waves[2] + waves[3]);
 }
 
-// First tile of the layers from l on.
-__device__ __forceinline__ uint32_t first_tile(const GradArgs& a, int32_t l) {
-    uint32_t lo = 0, hi = a.n_tiles;
-    while (lo < hi) {
-        const uint32_t m = (lo + hi) / 2;
-        if (a.tiles[m].layer < l) lo = m + 1;
-        else hi = m;
+// A layer's tiles, a wave each layer and worker in turn.
+__device__ __forceinline__ void join_layers(const GradArgs& a, uint32_t wave, uint32_t waves) {
+    const uint32_t lane = lane_id(), layers = a.n_layers * a.workers;
+    for (uint32_t i = wave; i < layers; i += waves) {
+        const uint32_t worker = i / a.n_layers, layer = i - worker * a.n_layers;
+        const uint32_t t0 = a.layer_tile0[layer], t1 = a.layer_tile0[layer + 1];
+        double x = 0.0;
+#pragma unroll 16
+        for (uint32_t t = t0 + lane; t < t1; t += 64) x += a.part[(int64_t)worker * a.n_tiles + t];
+        x = wave_sum_f64(x);
+        if (lane == 0) {
+            if (a.layer_norm) a.layer_norm[i] = (float)sqrt(x);
+            a.layer_sum[i] = x;
+        }
     }
-    return lo;
 }
-
-__device__ __forceinline__ double block_sum_f64(double x, double* waves) {
-    x = wave_sum_f64(x);
-    if ((threadIdx.x & 63u) == 0) waves[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = (waves[0] + waves[1]) + (waves[2] + waves[3]);
-    __syncthreads();
-    return x;
-}
-
-// A layer's tiles, one workgroup each layer and worker; the last workgroup to
-// finish sums the layers, in their order.
-__global__ __launch_bounds__(kBlock) void k_grad_join(GradArgs a) {
-    __shared__ double waves[kWaves];
-    __shared__ uint32_t turn;
-    const uint32_t tid = threadIdx.x;
-    const int32_t layer = (int32_t)(blockIdx.x % a.n_layers);
-    const uint32_t worker = blockIdx.x / a.n_layers;
-    const uint32_t t0 = first_tile(a, layer), t1 = first_tile(a, layer + 1);
-    double x = 0.0;
-    for (uint32_t t = t0 + tid; t < t1; t += kBlock) x += a.part[(int64_t)worker * a.n_tiles + t];
-    x = block_sum_f64(x, waves);
-    if (tid == 0) {
-        if (a.layer_norm) a.layer_norm[(int64_t)worker * a.n_layers + layer] = (float)sqrt(x);
-        __hip_atomic_store(&a.layer_sum[(int64_t)worker * a.n_layers + layer], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        turn = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+// The layers of a worker, in their order, by a wave each; then the workers.
+__device__ __forceinline__ void join_workers(const GradArgs& a, uint32_t wave, uint32_t waves) {
+    __shared__ double sums[SCAPE_MAX_WORKERS];
+    const uint32_t lane = lane_id();
+    for (uint32_t i = wave; i < a.workers; i += waves) {
+        double x = 0.0;
+#pragma unroll 8
+        for (uint32_t l = lane; l < a.n_layers; l += 64) x += a.layer_sum[i * a.n_layers + l];
+        x = wave_sum_f64(x);
+        if (lane == 0) {
+            a.norm[i] = (float)sqrt(x);
+            sums[i] = x;
+        }
     }
     __syncthreads();
-    if (turn != gridDim.x - 1) return;
-    double all = 0.0;
-    for (uint32_t i = 0; i < a.workers; ++i) {
-        x = 0.0;
-        for (uint32_t l = tid; l < a.n_layers; l += kBlock)
-            x += __hip_atomic_load(&a.layer_sum[(int64_t)i * a.n_layers + l], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        x = block_sum_f64(x, waves);
-        all += x;
-        if (tid == 0) a.norm[i] = (float)sqrt(x);
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+        for (uint32_t i = 0; i < a.workers; ++i) all += sums[i];
+        a.norm[a.workers] = (float)sqrt(all / (double)a.workers);
     }
-    if (tid == 0) a.norm[a.workers] = (float)sqrt(all / (double)a.workers);
+}
+// Few layers: one workgroup joins all.  Else a launch for the layers and one for
+// the workers: a ticket that the last workgroup finds would have to be ordered
+// behind the others' sums across the XCDs' caches, which takes longer than a
+// launch (2x292 layers 12-17 us, in two launches 8).
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
+__global__ __launch_bounds__(kJoinThreads) void k_grad_join(GradArgs a) {
+    join_layers(a, threadIdx.x >> 6, kJoinWaves);
+    __syncthreads();
+    join_workers(a, threadIdx.x >> 6, kJoinWaves);
+}
+__global__ __launch_bounds__(kBlock) void k_grad_layers(GradArgs a) {
+    join_layers(a, blockIdx.x * kWaves + (threadIdx.x >> 6), gridDim.x * kWaves);
+}
+__global__ __launch_bounds__(kJoinThreads) void k_grad_workers(GradArgs a) {
+    join_workers(a, threadIdx.x >> 6, kJoinWaves);
 }
 
+// 16 bytes a thread, as a plain copy does best (two workers of 355M elements:
+// 497 us with four a thread, 450 so).
+constexpr int kClipParts = kPerThread;
 __global__ __launch_bounds__(kBlock) void k_grad_clip(GradArgs a) {
-    const uint32_t tid = threadIdx.x, worker = blockIdx.x % a.workers, tile = blockIdx.x / a.workers;
+    const uint32_t tid = threadIdx.x, b = xcd_block(blockIdx.x, gridDim.x), part = b % kClipParts, c = b / kClipParts;
+    const uint32_t worker = c % a.workers, tile = c / a.workers;
     const float norm = a.norm[a.shared ? a.workers : worker];
     // One rounding of the factor, one of the product to 8 bits.
     const float f = norm > a.max_norm ? a.max_norm / norm : 1.0f;
     const bool drop = !(norm <= kMaxFloat);  // infinite or NaN
     if (f == 1.0f && !drop && a.out[worker] == a.g[worker]) return;
     const Share s = share_of(a, tile, worker);
-    char* const out = reinterpret_cast<char*>(a.out[worker]) + s.at;
-    const int32_t whole = s.elements / 8;
-    const auto scaled = [&](const gran& g) {
-        float v[8];
+    const int32_t q = (int32_t)(part * kBlock + tid), whole = s.elements / 8, rest = s.elements - q * 8;
+    if (q > whole || rest <= 0) return;
+    const int64_t at = (int64_t)(q >> 3) * s.pitch + (q & 7) * 16;
+    const gran* const from = reinterpret_cast<const gran*>(s.g + at);
+    gran* const to = reinterpret_cast<gran*>(reinterpret_cast<char*>(a.out[worker]) + s.at + at);
+    const gran g = __builtin_nontemporal_load(from);
+    float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = drop ? 0.0f : BF16::up(g, j) * f;
-        return BF16::down(v);
-    };
-    gran g[kPerThread];
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int32_t q = i * kBlock + (int32_t)tid;
-        if (q < whole)
-            g[i] = __builtin_nontemporal_load(reinterpret_cast<const gran*>(s.g + (int64_t)(q >> 3) * s.pitch + (q & 7) * 16));
-    }
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int32_t q = i * kBlock + (int32_t)tid;
-        if (q < whole)
-            __builtin_nontemporal_store(scaled(g[i]), reinterpret_cast<gran*>(out + (int64_t)(q >> 3) * s.pitch + (q & 7) * 16));
-    }
-    if (tid == 0 && (s.elements & 7)) {  // what lies behind the layer's end stays as it is
-        const int64_t at = (int64_t)(whole >> 3) * s.pitch + (whole & 7) * 16;
-        const gran last = scaled(*reinterpret_cast<const gran*>(s.g + at));
-        uint16_t* const to = reinterpret_cast<uint16_t*>(out + at);
-        for (int j = 0; j < (s.elements & 7); ++j) to[j] = (uint16_t)(last[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 8; ++j) v[j] = drop ? 0.0f : BF16::up(g, j) * f;
+    const gran r = BF16::down(v);
+    if (q < whole) {
+        __builtin_nontemporal_store(r, to);
+    } else {  // what lies behind the layer's end stays as it is
+        uint16_t* const last = reinterpret_cast<uint16_t*>(to);
+        for (int j = 0; j < rest; ++j) last[j] = (uint16_t)(r[j >> 1] >> (16 * (j & 1)));
     }
 }
 
@@ -160,14 +156,20 @@ __global__ __launch_bounds__(kBlock) void k_grad_clip(GradArgs a) {
 
 hipError_t launch_grad_norm(hipStream_t s, const GradArgs& a) {
     if (a.n_tiles) hipLaunchKernelGGL(k_grad_squares, dim3(a.n_tiles * a.workers), dim3(kBlock), 0, s, a);
-    else if (hipError_t e = launch_fill_u32(s, a.ticket, 1, 0)) return e;
-    hipLaunchKernelGGL(k_grad_join, dim3(a.n_layers * a.workers), dim3(kBlock), 0, s, a);
+    const uint32_t layers = a.n_layers * a.workers;
+    if (layers <= 4 * kJoinWaves) {
+        hipLaunchKernelGGL(k_grad_join, dim3(1), dim3(kJoinThreads), 0, s, a);
+    } else {
+        const uint32_t n = (layers + kWaves - 1) / kWaves;
+        hipLaunchKernelGGL(k_grad_layers, dim3(n < 65536 ? n : 65536), dim3(kBlock), 0, s, a);
+        hipLaunchKernelGGL(k_grad_workers, dim3(1), dim3(kJoinThreads), 0, s, a);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_grad_clip(hipStream_t s, const GradArgs& a) {
     if (!a.n_tiles) return hipSuccess;
-    hipLaunchKernelGGL(k_grad_clip, dim3(a.n_tiles * a.workers), dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL(k_grad_clip, dim3(a.n_tiles * a.workers * kClipParts), dim3(kBlock), 0, s, a);
     return hipGetLastError();
 }
 

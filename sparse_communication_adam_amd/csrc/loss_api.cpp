@@ -327,7 +327,8 @@ int vocab_head(const scape_head* h, VocabArgs* a) {
 }
 
 // ---- tokens to their experts
-constexpr int64_t kMaxMoved = int64_t(1) << 25;  // tokens of a move: a wave each
+constexpr int64_t kMaxMoved = int64_t(1) << 25;     // tokens of a move: a wave each
+constexpr int64_t kMaxMovedDim = int64_t(1) << 24;  // bytes in a row are counted in 32 bits
 
 int sort_shape(int64_t tokens, int32_t k, int32_t experts, SortArgs* a) {
     if (experts < 1 || experts > SCAPE_EXPERT_MAX)
@@ -343,16 +344,16 @@ int sort_shape(int64_t tokens, int32_t k, int32_t experts, SortArgs* a) {
     int64_t run = 2048;
     if (a->choices > run * 512) run = round_up((a->choices + 511) / 512, 256);
     a->run = (int32_t)run;
-    a->blocks = (int32_t)((a->choices + run - 1) / run);
+    a->blocks = a->choices <= run ? 1 : (int32_t)((a->choices + run - 1) / run);
     return SCAPE_OK;
 }
-int64_t sort_bytes(const SortArgs& a) { return (int64_t)a.blocks * a.experts * 4; }
+int64_t sort_bytes(const SortArgs& a) { return a.blocks > 1 ? (int64_t)a.blocks * a.experts * 4 : 0; }
 
 int check_moves(int32_t dtype, int64_t tokens, int64_t dim, int64_t rows, int32_t k, const int32_t* row) {
     int rc;
     if ((rc = check_dtype(dtype, "the rows"))) return rc;
     if (tokens < 0 || tokens > kMaxMoved) return fail(SCAPE_ERR_SHAPE, "tokens must be in 0..2^25");
-    if (dim < 1) return fail(SCAPE_ERR_SHAPE, "dim must be at least 1");
+    if (dim < 1 || dim > kMaxMovedDim) return fail(SCAPE_ERR_SHAPE, "dim must be in 1..2^24");
     if (rows < 0) return fail(SCAPE_ERR_SHAPE, "rows must be >= 0");
     if (k < 1) return fail(SCAPE_ERR_SHAPE, "k must be at least 1 (got %d)", k);
     if (tokens * k > INT32_MAX) return fail(SCAPE_ERR_SHAPE, "more than 2^31 - 1 choices");

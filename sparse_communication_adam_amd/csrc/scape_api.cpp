@@ -170,6 +170,7 @@ struct scape_ctx {
     SelState* d_sel = nullptr;
     SegDesc* d_segs = nullptr;
     uint32_t* d_layer_seg0 = nullptr;
+    uint32_t* d_layer_tile0 = nullptr;  // first tile of each layer (L+1 entries)
     uint32_t* d_seg_fill = nullptr;   // per segment: records
     uint32_t* d_seg_above = nullptr;  // per segment: keys above the window
     uint64_t* d_union_bits = nullptr;  // one worker's mask before it is OR-ed into a fill-in union
@@ -228,6 +229,7 @@ void free_ctx(scape_ctx* c) {
     hipFree(c->d_ltick);
     hipFree(c->d_dummy);
     hipFree(c->d_layer_seg0);
+    hipFree(c->d_layer_tile0);
     hipFree(c->d_seg_fill);
     hipFree(c->d_seg_above);
     hipFree(c->d_union_bits);
@@ -753,18 +755,18 @@ int dense_common(scape_ctx* ctx, float* x, float* m, float* v, const uint16_t* c
 
 // ---- gradient norms and clipping
 
-// The tiles' sums, the layers', and the ticket of the workgroups that join them.
+// The tiles' sums and the layers'.
 int64_t grad_norm_bytes(const scape_ctx* ctx) {
-    return (int64_t)ctx->cfg.workers * ((int64_t)ctx->tiles.size() + ctx->lay.L) * 8 + 16;
+    return (int64_t)ctx->cfg.workers * ((int64_t)ctx->tiles.size() + ctx->lay.L) * 8;
 }
 
-// A workgroup for each tile of each worker, counted with their threads in 32 bits.
+// Up to 16 workgroups for each tile of each worker, counted with their threads in 32 bits.
 int grad_args(scape_ctx* ctx, const uint16_t* const* g, bool interleaved, GradArgs* a) {
     if (!ctx || !g) return fail(SCAPE_ERR_INVALID_ARG, "NULL argument");
     int rc;
     if ((rc = check_device(ctx))) return rc;
     const int32_t W = ctx->cfg.workers;
-    const int64_t most = (int64_t(1) << 32) / kBlock - 1;
+    const int64_t most = (int64_t(1) << 32) / kBlock / 16 - 1;
     if ((int64_t)ctx->tiles.size() * W > most || (int64_t)ctx->lay.L * W > most)
         return fail(SCAPE_ERR_SHAPE, "too many tiles or layers for one launch");
     for (int32_t i = 0; i < (interleaved ? 1 : W); ++i) {
@@ -778,6 +780,7 @@ int grad_args(scape_ctx* ctx, const uint16_t* const* g, bool interleaved, GradAr
     a->n_layers = (uint32_t)ctx->lay.L;
     a->tiles = ctx->d_tiles;
     a->layers = ctx->d_layers;
+    a->layer_tile0 = ctx->d_layer_tile0;
     return SCAPE_OK;
 }
 
@@ -795,7 +798,6 @@ int norm_common(scape_ctx* ctx, const uint16_t* const* g, float* norm, float* la
     if (!aligned(workspace, 16)) return fail(SCAPE_ERR_ALIGN, "workspace must be 16-byte aligned");
     a.part = static_cast<double*>(workspace);
     a.layer_sum = a.part + (int64_t)a.workers * a.n_tiles;
-    a.ticket = reinterpret_cast<uint32_t*>(a.layer_sum + (int64_t)a.workers * a.n_layers);
     a.norm = norm;
     a.layer_norm = layer_norm;
     SCAPE_HIP(launch_grad_norm((hipStream_t)stream, a), "gradient norms");
@@ -956,6 +958,7 @@ int scape_init(const scape_config* cfg, scape_ctx** out) {
         (rc = dev_alloc(c, &c->d_hist, L * kHistBins, "histograms")) || (rc = dev_alloc(c, &c->d_sel, L, "selection state")) ||
         (rc = dev_alloc(c, &c->d_segs, n_segs, "segment table")) ||
         (rc = dev_alloc(c, &c->d_layer_seg0, L + 1, "layer segment table")) ||
+        (rc = dev_alloc(c, &c->d_layer_tile0, L + 1, "layer tile table")) ||
         (rc = dev_alloc(c, &c->d_seg_fill, n_segs, "segment record counters")) ||
         (rc = dev_alloc(c, &c->d_seg_above, n_segs, "segment bit counters")) ||
         (rc = dev_alloc(c, &c->d_lspace, L, "layer record spaces")) ||
@@ -997,6 +1000,8 @@ int scape_init(const scape_config* cfg, scape_ctx** out) {
     if (e == hipSuccess) e = hipMemset(c->d_dummy, 0, 4 * sizeof(float));
     if (e == hipSuccess)
         e = hipMemcpy(c->d_layer_seg0, c->layer_seg0.data(), (L + 1) * sizeof(uint32_t), hipMemcpyHostToDevice);
+    if (e == hipSuccess)
+        e = hipMemcpy(c->d_layer_tile0, c->layer_tile0.data(), (L + 1) * sizeof(uint32_t), hipMemcpyHostToDevice);
     if (e == hipSuccess && c->n_words)
         e = hipMemcpy(c->d_word_info, winfo.data(), (size_t)c->n_words * sizeof(uint16_t), hipMemcpyHostToDevice);
     if (e == hipSuccess) e = hipMemset(c->d_hist, 0, L * kHistBins * sizeof(uint32_t));

@@ -286,9 +286,9 @@ struct GradArgs {
     uint32_t ws, workers, n_tiles, n_layers;
     const TileDesc* tiles;
     const LayerDesc* layers;
+    const uint32_t* layer_tile0;  // [n_layers + 1] first tile of each layer
     double* part;       // [workers][n_tiles]
     double* layer_sum;  // [workers][n_layers]
-    uint32_t* ticket;
     float* norm;        // [workers + 1]
     float* layer_norm;  // [workers][n_layers], or NULL
     float max_norm;

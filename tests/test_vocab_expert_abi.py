@@ -66,7 +66,7 @@ HEADS = [(None, -1)] + [
         (dict(label=66), -3), (dict(weight=66), -3), (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=INF), -1),
         (dict(scale=NAN), -1)]]
 MOVES = [(dict(dtype=3), -1), (dict(tokens=-1), -2), (dict(tokens=(1 << 25) + 1), -2), (dict(dim=0), -2), (dict(rows=-1), -2),
-         (dict(k=0), -2), (dict(k=-1), -2), (dict(tokens=1 << 25, k=64), -2), (dict(row=0), -1), (dict(row=66), -3),
+         (dict(dim=1 << 25), -2), (dict(k=0), -2), (dict(k=-1), -2), (dict(tokens=1 << 25, k=64), -2), (dict(row=0), -1), (dict(row=66), -3),
          (dict(ld_y=15), -2), (dict(y=0), -1), (dict(y=129), -3), (dict(ld_y=1 << 60), -2)]
 CASES = (
     [("scape_vocab_loss_forward", FORWARD, dict(head=c), e) for c, e in HEADS]
@@ -81,7 +81,8 @@ CASES = (
     + [("scape_expert_sort", SORT, c, e) for c, e in [
         (dict(tokens=-1), -2), (dict(tokens=(1 << 30) + 1), -2), (dict(k=0), -2), (dict(experts=0), -2),
         (dict(experts=1025), -2), (dict(tokens=1 << 30), -2), (dict(idx=0), -1), (dict(idx=66), -3), (dict(offsets=0), -1),
-        (dict(offsets=66), -3), (dict(row=0), -1), (dict(row=66), -3), (dict(ws_bytes=8), -2)]]
+        (dict(offsets=66), -3), (dict(row=0), -1), (dict(row=66), -3), (dict(tokens=5000, ws_bytes=8), -2),
+        (dict(tokens=5000, ws=0), -1), (dict(tokens=5000, ws=72), -3)]]
     + [("scape_expert_gather", GATHER, c, e) for c, e in MOVES + [
         (dict(x=0), -1), (dict(x=65), -3), (dict(ld_x=15), -2)]]
     + [("scape_expert_combine", COMBINE, c, e) for c, e in MOVES + [
