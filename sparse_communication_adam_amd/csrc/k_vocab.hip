@@ -50,7 +50,8 @@ struct Side {
 // fragments of it.  The load writes LDS in lane order, so the lanes' addresses
 // are permuted instead: the 16-byte pieces of a row are exchanged by an XOR
 // that spreads what one fragment read touches over all banks.
-template <bool kAlong, int kR, int kThreads, int kDepth>
+constexpr int kDepth = 64;  // elements of the summed axis in a slot
+template <bool kAlong, int kR, int kThreads>
 struct Stage {
     static constexpr int kBytes = kR * 2 * kDepth;
     static constexpr int kPieces = kBytes / 16;
@@ -66,60 +67,57 @@ struct Stage {
     static constexpr int kRowsALoad = kLanes / kRowPieces;
     static constexpr bool kSteady = kLoads == 1 || kRowsALoad % 16 == 0;
     static_assert(kPieces % 64 == 0 && (kPieces % kThreads == 0 || kThreads % kPieces == 0), "whole waves");
-    uint32_t off[kSteady ? 1 : kLoads], pitch;
+    static_assert(kAlong || (kR & (kR - 1)) == 0, "rows of pieces that an XOR stays in");
+    uint32_t off[kSteady ? 1 : kLoads], pitch;  // a lane's
+    int32_t piece;                              // a lane's first element along the depth
+    uint32_t wave;                              // where a wave's share of a load begins in the slot
+    const char* at;                             // the next tile, and what is left of the depth there
+    int32_t left, bytes, ld;
 
     // what the pieces of row k are exchanged by; the same for k + 4 (k % 8 < 4)
     // and k + 16, which a fragment's reads and a lane's loads are apart
     static __device__ __forceinline__ uint32_t turn(uint32_t k) {
-        if constexpr (kAlong) return kDepth == 32 ? (k >> 2) & 3u : k & 7u;
+        if constexpr (kAlong) return k & 7u;
         if constexpr (kR >= 128) return ((k & 3u) | ((k >> 3) & 1u) << 2) << 1;
         if constexpr (kR == 64) return (((k >> 1) & 1u) | ((k >> 3) & 1u) << 1) << 1;
         if constexpr (kR == 32) return ((k >> 3) & 1u) << 1;
         return 0;
     }
 
-    __device__ __forceinline__ void init(int32_t ld) {
+    // The tile at row (or column) r0 and depth k is the first.
+    __device__ __forceinline__ void init(const Side& s, int32_t r0, int32_t k) {
+        const uint32_t tid = threadIdx.x % kLanes;
+        ld = s.ld;
         pitch = (uint32_t)(ld * 2);
 #pragma unroll
         for (int i = 0; i < (kSteady ? 1 : kLoads); ++i) {
-            const uint32_t q = (uint32_t)i * kThreads + threadIdx.x % kLanes, row = q / kRowPieces, pos = q % kRowPieces;
+            const uint32_t q = (uint32_t)i * kThreads + tid, row = q / kRowPieces, pos = q % kRowPieces;
             off[i] = row * pitch + ((pos ^ turn(row)) << 4);
+            if (i == 0) piece = (int32_t)((pos ^ turn(row)) * 8);
         }
+        wave = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+        left = s.depth - k;
+        const int32_t rows = s.extent - r0 < kR ? s.extent - r0 : kR;
+        bytes = kAlong ? ((rows - 1) * ld + left) * 2 : (s.extent - r0) * 2;  // all, or of a last row
+        at = static_cast<const char*>(s.p) + (kAlong ? (int64_t)r0 * ld + k : (int64_t)k * ld + r0) * 2;
     }
 
-    // The tile at row (or column) r0 and depth k.
-    __device__ __forceinline__ void load(const Side& s, int32_t r0, int32_t k, lds_t* to) {
-        const uint32_t tid = threadIdx.x % kLanes;
-        int64_t base;
-        int32_t rows, width;
-        if constexpr (kAlong) {
-            base = (int64_t)r0 * s.ld + k;
-            rows = s.extent - r0 < kR ? s.extent - r0 : kR;
-            width = s.depth - k;
-        } else {
-            base = (int64_t)k * s.ld + r0;
-            rows = s.depth - k < kDepth ? s.depth - k : kDepth;
-            width = s.extent - r0;
-        }
-        // behind the end of the summed axis there is nothing: all zeros
-        const int32_t bytes = rows > 0 && width > 0 ? ((rows - 1) * s.ld + width) * 2 : 0;
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(s.p)) + base * 2, 0, bytes,
-                                                            kRawBuffer);
-        uint32_t kill = 0;
-        if constexpr (kAlong) {
-            if (width < kDepth) {
-                const uint32_t row = tid / kRowPieces, pos = tid % kRowPieces;
-                if ((int)((pos ^ turn(row)) * 8) >= (int)width) kill = kOutside;
-            }
-        }
+    // The next tile to a slot.  Behind the end of the depth there are zeros.
+    __device__ __forceinline__ void load(lds_t* to) {
+        const int32_t rows = left < kDepth ? left : kDepth;
+        const int32_t held = kAlong ? bytes : (rows - 1) * ld * 2 + bytes, some = left > 0 ? held : 0;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, some, kRawBuffer);
         // one register, not one for each load: the sums need them
         asm volatile("" : "+v"(off[0]));
+        const uint32_t kill = kAlong && piece >= left ? kOutside : 0u;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t o = kSteady ? off[0] + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i];
-            lds_t* const at = to + (i * kThreads + (int)(tid & ~63u)) * 16;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)at, 16, o | kill, 0, 0, 0);
+            const uint32_t o = kSteady ? (off[0] | kill) + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i] | kill;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(to + wave + i * kThreads * 16), 16, o, 0, 0, 0);
         }
+        at += kAlong ? kDepth * 2 : (int64_t)kDepth * 2 * ld;
+        if (kAlong) bytes -= kDepth * 2;
+        left -= kDepth;
     }
 
     // Where a lane reads the first fragment of the wave's rows (from r0, a
@@ -148,77 +146,106 @@ struct Stage {
 };
 
 // A workgroup's tile of a product: kM x kN over kWM x kWN waves.  The operands
-// come through a ring of slots of 32 deep, loaded kSlots - 1 steps ahead; a
-// wave holds the fragments of two steps and reads the next one's between the
-// products of this one's.
-template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+// come through slots of 64 deep, kSlotsA of the one and kSlotsB of the other.  A
+// wave holds the fragments of a slot's two halves: while one half is multiplied
+// the other is read, and when both are in registers the slots are loaded anew,
+// the other slots' products ahead of their use.
+template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN, int kSlotsA = 2, int kSlotsB = 2>
 struct Tile {
     static constexpr int kThreads = kWM * kWN * 64;
     static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part, powers of two
     static constexpr int kFM = kTM / 16, kFN = kTN / 16;
-    using A = Stage<kAlongA, kM, kThreads, kDepth>;
-    using B = Stage<kAlongB, kN, kThreads, kDepth>;
-    static constexpr int kSlot = A::kBytes + B::kBytes, kLoads = A::kLoads + B::kLoads;
-    static constexpr int kLds = kSlots * kSlot;
-    // A step's fragments.
-    struct Step {
+    using A = Stage<kAlongA, kM, kThreads>;
+    using B = Stage<kAlongB, kN, kThreads>;
+    static constexpr int kLoads = A::kLoads + B::kLoads;
+    static constexpr int kLdsA = kSlotsA * A::kBytes, kLds = kLdsA + kSlotsB * B::kBytes;
+    // Loads that may be on their way when the next slots have to be there: those
+    // issued behind the last of them (of a step's loads B's are first).
+    static constexpr int kAhead = (kSlotsB - 2) * kLoads + (kSlotsA > kSlotsB ? A::kLoads : 0);
+    static_assert(kSlotsA >= kSlotsB && kSlotsB >= 2, "");
+    // A half's fragments.
+    struct Half {
         s8 a[kFM], b[kFN];
-        __device__ __forceinline__ void read(const lds_t* from, uint32_t& fa, uint32_t& fb, int h) {
+        __device__ __forceinline__ void read(const lds_t* from_a, const lds_t* from_b, uint32_t& fa, uint32_t& fb, int h) {
             asm volatile("" : "+v"(fa), "+v"(fb));  // addresses are made from these two here, and not kept
 #pragma unroll
-            for (int j = 0; j < kFN; ++j) b[j] = B::read(from + A::kBytes, fb, j, h);
+            for (int j = 0; j < kFN; ++j) b[j] = B::read(from_b, fb, j, h);
 #pragma unroll
-            for (int i = 0; i < kFM; ++i) a[i] = A::read(from, fa, i, h);
+            for (int i = 0; i < kFM; ++i) a[i] = A::read(from_a, fa, i, h);
         }
     };
     f4 acc[kFM][kFN];
+    A la;
+    B lb;
+    uint32_t fa, fb;
 
-    __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
-                                        lds_t* lds) {
-        A la;
-        B lb;
-        la.init(a.ld);
-        lb.init(b.ld);
-        uint32_t fa = A::first(lane_id(), wave_m()), fb = B::first(lane_id(), wave_n());
+    __device__ __forceinline__ void start(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0) {
+        la.init(a, m0, k0);
+        lb.init(b, n0, k0);
+        fa = A::first(lane_id(), wave_m());
+        fb = B::first(lane_id(), wave_n());
 #pragma unroll
         for (int i = 0; i < kFM; ++i)
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = f4{0, 0, 0, 0};
-        Step x, y;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) fetch(a, b, m0, n0, k0 + i * kDepth, la, lb, lds + i * kSlot);
-        wait<(kSlots - 1) * kLoads>();
-        x.read(lds, fa, fb, 0);
-        uint32_t at = 0, next = kSlot;  // the slots of this step and of the next
-        for (int32_t k = k0; k < k1; k += 64) {
-            if constexpr (kDepth == 64) {
-                y.read(lds + at, fa, fb, 1);
-                multiply(x);
-                mix();
-                step(a, b, m0, n0, k, la, lb, fa, fb, lds + at, lds + next, y, x);
-            } else {
-                step(a, b, m0, n0, k, la, lb, fa, fb, lds + at, lds + next, x, y);
-                at = next;
-                next = next == kLds - kSlot ? 0 : next + kSlot;
-                step(a, b, m0, n0, k + kDepth, la, lb, fa, fb, lds + at, lds + next, y, x);
-            }
-            at = next;
-            next = next == kLds - kSlot ? 0 : next + kSlot;
-        }
-        wait<0>();  // what was loaded past the end is in LDS, too
     }
-    // One step: products of `now`, the fragments of `then` from the next slot,
-    // and loads into the slot that `now` came from.  Restricted pointers: what
-    // is loaded is not what is read, or the compiler waits for every load before
-    // a transposing read.
-    __device__ __forceinline__ void step(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k, A& la, B& lb,
-                                         uint32_t& fa, uint32_t& fb, lds_t* __restrict to, const lds_t* __restrict from,
-                                         const Step& now, Step& then) {
-        wait<(kSlots - 2) * kLoads>();
-        fetch(a, b, m0, n0, k + kSlots * kDepth, la, lb, to);
-        then.read(from, fa, fb, 0);
-        multiply(now);
-        mix();
+
+    // Both operands along the depth from k0 to k1; what is loaded behind the end
+    // of it is zeros.
+    __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
+                                        lds_t* lds) {
+        static_assert(kAlongA && kAlongB, "the compiler waits for every load before a transposing read of the same object");
+        start(a, b, m0, n0, k0);
+#pragma unroll
+        for (int i = -kSlotsA; i < 0; ++i) {
+            if (i + kSlotsB >= 0) lb.load(lds + kLdsA + (i + kSlotsB) * B::kBytes);
+            asm volatile("" ::: "memory");
+            la.load(lds + (i + kSlotsA) * A::kBytes);
+        }
+        wait<kAhead + kLoads>();
+        Half x, y;
+        x.read(lds, lds + kLdsA, fa, fb, 0);
+        uint32_t ia = 0, ib = kLdsA, ja = A::kBytes, jb = kLdsA + B::kBytes;  // this step's slots and the next one's
+        for (int32_t k = k0; k < k1; k += kDepth) {
+            slot(lds + ia, lds + ib, lds + ja, lds + jb, x, y);
+            ia = ja;
+            ib = jb;
+            ja = ja == kLdsA - A::kBytes ? 0 : ja + A::kBytes;
+            jb = jb == kLds - B::kBytes ? kLdsA : jb + B::kBytes;
+        }
+        wait<0>();  // what was loaded behind the end is in LDS, too
+    }
+    // Any operands, the depth from k0 to k1, a multiple of 128 of it or all that
+    // there is.  The slots are two objects, so that the compiler knows a read from
+    // one to be none of what is loaded into the other.
+    __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
+                                        lds_t* even, lds_t* odd) {
+        static_assert(kSlotsA == 2 && kSlotsB == 2, "");
+        start(a, b, m0, n0, k0);
+        lb.load(even + A::kBytes);
+        la.load(even);
+        lb.load(odd + A::kBytes);
+        la.load(odd);
+        wait<kLoads>();
+        Half x, y;
+        x.read(even, even + A::kBytes, fa, fb, 0);
+        for (int32_t k = k0; k < k1; k += 2 * kDepth) {
+            slot(even, even + A::kBytes, odd, odd + A::kBytes, x, y);
+            slot(odd, odd + A::kBytes, even, even + A::kBytes, x, y);
+        }
+        wait<0>();
+    }
+    __device__ __forceinline__ void slot(lds_t* now_a, lds_t* now_b, const lds_t* next_a, const lds_t* next_b, Half& x, Half& y) {
+        y.read(now_a, now_b, fa, fb, 1);
+        multiply(x);
+        mix<false>();
+        wait<kAhead>();
+        x.read(next_a, next_b, fa, fb, 0);
+        lb.load(now_b);
+        asm volatile("" ::: "memory");  // in this order: kAhead counts on it
+        la.load(now_a);
+        multiply(y);
+        mix<true>();
         __builtin_amdgcn_sched_barrier(0);
     }
     // All but the last n loads of every wave are in LDS, and every wave has the
@@ -231,26 +258,39 @@ struct Tile {
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     }
-    static __device__ __forceinline__ void fetch(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k, A& la, B& lb,
-                                                 lds_t* to) {
-        la.load(a, m0, k, to);
-        lb.load(b, n0, k, to + A::kBytes);
-    }
-    __device__ __forceinline__ void multiply(const Step& f) {
+    __device__ __forceinline__ void multiply(const Half& f) {
 #pragma unroll
         for (int i = 0; i < kFM; ++i)
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = mfma<T>(f.a[i], f.b[j], acc[i][j]);
     }
-    // The other step's reads stand between the products, not before them.
-    static constexpr int kReads = kFM * (kAlongA ? 1 : 2) + kFN * (kAlongB ? 1 : 2), kProducts = kFM * kFN;
-    template <int i = 0>
+    // The order of a half: a product for each read (of 16 bytes a lane) first, so
+    // that the rest of the products covers the last read's way, and the loads
+    // between those.
+    static constexpr int kReadsA = kAlongA ? 1 : 2, kReadsB = kAlongB ? 1 : 2, kProducts = kFM * kFN;
+    template <bool kFetch>
     static __device__ __forceinline__ void mix() {
-        if constexpr (i < kReads) {
-            constexpr int n = (i + 1) * kProducts / kReads - i * kProducts / kReads;
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, n, 0);
-            mix<i + 1>();
+        constexpr int kPlain = kProducts - kFM - kFN;
+        static_assert(kFM + kFN <= 2 * kProducts, "");
+        mix_reads<kFN, kReadsB>();
+        mix_reads<kFM, kReadsA>();
+        if constexpr (kFetch) mix_loads<kLoads, kPlain>();
+    }
+    template <int n, int each>
+    static __device__ __forceinline__ void mix_reads() {
+        if constexpr (n > 0) {
+            __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            mix_reads<n - 1, each>();
+        }
+    }
+    template <int n, int products>
+    static __device__ __forceinline__ void mix_loads() {
+        if constexpr (n > 0) {
+            constexpr int m = products > 0 ? (products + n - 1) / n : 0;
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);
+            mix_loads<n - 1, products - m>();
         }
     }
     // The wave's first row and column in the tile, and the lane's of a fragment.
@@ -275,9 +315,9 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, ui
 // ---------------------------------------------------------------------------
 // The loss: each tile's reference and sum of a token, and the label's logit.
 
-template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
-    using G = Tile<T, true, true, kM, kN, kWM, kWN, kDepth, kSlots>;
+    using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, a.tiles_v, a.tiles_n, tm, tn);
@@ -392,20 +432,20 @@ __global__ __launch_bounds__(kJoinTokens* kJoinParts) void k_vocab_join(VocabArg
 // whole factor; an fp16 P is (p - onehot) times a mantissa in [2^14, 2^15), so
 // that p keeps its bits down to 2^-29, and the power of two is put on dh
 // exactly and on the copy of h for dw against the largest of all rows.
-__global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
-    __shared__ int top[16];
-    const uint32_t tid = threadIdx.x;
-    const bool half = a.dtype == SCAPE_DTYPE_F16;
-    const auto factor = [&](int64_t n) {
-        const int32_t lab = a.label[n];
-        if (lab < 0 || lab >= a.cols) return 0.0f;
-        const float w = a.weight ? a.weight[n] : 1.0f, d = a.dloss ? a.dloss[n] : 1.0f;
-        return w == 0.0f || d == 0.0f ? 0.0f : (float)((double)w * (double)d * (double)a.scale);
-    };
-    int best = -10000;
-    if (half)
-        for (int64_t n = tid; n < a.rows; n += 1024) {
-            const float f = factor(n);
+__device__ __forceinline__ float row_factor(const VocabArgs& a, int64_t n) {
+    const int32_t lab = a.label[n];
+    if (lab < 0 || lab >= a.cols) return 0.0f;
+    const float w = a.weight ? a.weight[n] : 1.0f, d = a.dloss ? a.dloss[n] : 1.0f;
+    return w == 0.0f || d == 0.0f ? 0.0f : (float)((double)w * (double)d * (double)a.scale);
+}
+constexpr int kNoExponent = -10000;
+// The largest exponent of the rows' factors (fp16), by a whole workgroup.
+template <int kThreads>
+__device__ __forceinline__ int top_exponent(const VocabArgs& a, int* scratch) {
+    int best = kNoExponent;
+    if (a.dtype == SCAPE_DTYPE_F16)
+        for (int64_t n = threadIdx.x; n < a.rows; n += kThreads) {
+            const float f = row_factor(a, n);
             if (f != 0.0f && __builtin_isfinite(f)) {
                 int e;
                 (void)frexpf(f, &e);
@@ -416,35 +456,42 @@ __global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
         const int o = __shfl_xor(best, d, 64);
         best = o > best ? o : best;
     }
-    if ((tid & 63u) == 0) top[tid >> 6] = best;
+    if ((threadIdx.x & 63u) == 0) scratch[threadIdx.x >> 6] = best;
     __syncthreads();
-    for (int i = 0; i < 16; ++i) best = top[i] > best ? top[i] : best;
-    if (tid == 0) a.dw_scale[0] = half && best > -10000 ? ldexpf(1.0f, best - 15) : 1.0f;
-    for (int64_t n = tid; n < a.rows_pad; n += 1024) {
-        VocabRow r{0.0f, 0.0f, 0.0f, 0.0f};
-        const float f = n < a.rows ? factor(n) : 0.0f;
-        if (f != 0.0f) {
-            r.lse2 = a.lse[n] * kLog2e;
-            r.f = f;
-            r.dh = 1.0f;
-            r.copy = 1.0f;
-            if (half && __builtin_isfinite(f)) {
-                int e;
-                r.f = frexpf(f, &e) * 32768.0f;
-                r.dh = ldexpf(1.0f, e - 15);
-                r.copy = ldexpf(1.0f, e - best);
-            }
+    for (int i = 0; i < kThreads / 64; ++i) best = scratch[i] > best ? scratch[i] : best;
+    return best;
+}
+__device__ __forceinline__ void put_dw_scale(const VocabArgs& a, int best) {
+    a.dw_scale[0] = a.dtype == SCAPE_DTYPE_F16 && best > kNoExponent ? ldexpf(1.0f, best - 15) : 1.0f;
+}
+__device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n, int best) {
+    VocabRow r{0.0f, 0.0f, 0.0f, 0.0f};
+    const float f = n < a.rows ? row_factor(a, n) : 0.0f;
+    if (f != 0.0f) {
+        r.lse2 = a.lse[n] * kLog2e;
+        r.f = f;
+        r.dh = 1.0f;
+        r.copy = 1.0f;
+        if (a.dtype == SCAPE_DTYPE_F16 && __builtin_isfinite(f)) {
+            int e;
+            r.f = frexpf(f, &e) * 32768.0f;
+            r.dh = ldexpf(1.0f, e - 15);
+            r.copy = ldexpf(1.0f, e - best);
         }
-        a.row[n] = r;
     }
+    return r;
+}
+__global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
+    __shared__ int scratch[16];
+    const int best = top_exponent<1024>(a, scratch);
+    if (threadIdx.x == 0) put_dw_scale(a, best);
+    for (int64_t n = threadIdx.x; n < a.rows_pad; n += 1024) a.row[n] = row_of(a, n, best);
 }
 
 // The rows of h that dw takes: zeros where a row does not count, whatever it
 // holds, and times the row's power of two (fp16).
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
-    const int64_t n = blockIdx.x;
-    const float c = a.row[n].copy;
+__device__ __forceinline__ void copy_row(const VocabArgs& a, int64_t n, float c) {
     const gran* from = reinterpret_cast<const gran*>((const char*)a.h + n * a.ld_h * 2);
     gran* to = reinterpret_cast<gran*>((char*)a.h_copy + n * a.dim * 2);
     for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) {
@@ -461,12 +508,31 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
         to[i] = g;
     }
 }
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
+    copy_row<T>(a, blockIdx.x, a.row[blockIdx.x].copy);
+}
+// Both for few rows, in one launch: a workgroup a row, each finds the largest
+// exponent for itself.
+constexpr int64_t kFewRows = 512;
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_vocab_rows_copy(VocabArgs a) {
+    __shared__ int scratch[kRowThreads / 64];
+    const int best = top_exponent<kRowThreads>(a, scratch);
+    const int64_t n = blockIdx.x;
+    const VocabRow r = row_of(a, n, best);
+    if (threadIdx.x == 0) {
+        a.row[n] = r;
+        if (n == 0) put_dw_scale(a, best);
+    }
+    if (a.dw && n < a.rows) copy_row<T>(a, n, r.copy);
+}
 
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
 // step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
-template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, true, true, kM, kN, kWM, kWN, kDepth, kSlots>;
+    using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
     tile_of(blockIdx.x, (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
@@ -499,10 +565,10 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
 
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
 // Where one split sums them all, the last piece's launch writes dh itself.
-template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+template <class T, int kM, int kN, int kWM, int kWN>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last) {
-    using G = Tile<T, false, true, kM, kN, kWM, kWN, kDepth, kSlots>;
-    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    using G = Tile<T, false, true, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char even[G::kLds / 2], odd[G::kLds / 2];
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
     const uint32_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
@@ -514,7 +580,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     G g;
     if (k0 < k1) {
         g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, (int32_t)a.dim, all},
-              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, (lds_t*)lds);
+              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, (lds_t*)even, (lds_t*)odd);
     } else {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
@@ -545,36 +611,49 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     }
 }
 
-// dh: the splits' sums in order, times the row's power of two, rounded once.
+// dh: the splits' sums, times the row's power of two, rounded once.  A workgroup
+// takes 512 elements of a row, each wave a quarter of the splits, in an order
+// that the sizes alone decide.
+constexpr int kJoinWidth = 512;
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
-    const int64_t n = blockIdx.x;
-    const float c = a.row[n].dh;
-    gran* to = reinterpret_cast<gran*>((char*)a.dh + n * a.ld_dh * 2);
-    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) {
-        f4 lo = f4{0, 0, 0, 0}, hi = lo;
-        if (c != 0.0f)
-            for (int32_t s = 0; s < a.splits; ++s) {
-                const f4* p = reinterpret_cast<const f4*>(a.dh_sum + ((int64_t)s * a.rows + n) * a.dim) + 2 * i;
-                lo += p[0];
-                hi += p[1];
-            }
-        const float f[8] = {lo[0] * c, lo[1] * c, lo[2] * c, lo[3] * c, hi[0] * c, hi[1] * c, hi[2] * c, hi[3] * c};
-        to[i] = T::down(f);
+    __shared__ f4 part[kWaves][2][64];
+    const uint32_t lane = lane_id(), wave = threadIdx.x >> 6, chunks = (uint32_t)((a.dim + kJoinWidth - 1) / kJoinWidth);
+    const int64_t n = blockIdx.x / chunks, at = (int64_t)(blockIdx.x % chunks) * kJoinWidth + lane * 8;
+    f4 lo = f4{0, 0, 0, 0}, hi = lo;
+    if (at < a.dim) {
+        const float* p = a.dh_sum + ((int64_t)wave * a.rows + n) * a.dim + at;
+#pragma unroll 4
+        for (int32_t s = (int32_t)wave; s < a.splits; s += kWaves, p += kWaves * a.rows * a.dim) {
+            lo += reinterpret_cast<const f4*>(p)[0];
+            hi += reinterpret_cast<const f4*>(p)[1];
+        }
     }
+    part[wave][0][lane] = lo;
+    part[wave][1][lane] = hi;
+    __syncthreads();
+    if (wave != 0 || at >= a.dim) return;
+    for (int w = 1; w < kWaves; ++w) {
+        lo += part[w][0][lane];
+        hi += part[w][1][lane];
+    }
+    const float c = a.row[n].dh;
+    if (c == 0.0f) lo = hi = f4{0, 0, 0, 0};
+    const float f[8] = {lo[0] * c, lo[1] * c, lo[2] * c, lo[3] * c, hi[0] * c, hi[1] * c, hi[2] * c, hi[3] * c};
+    *reinterpret_cast<gran*>((char*)a.dh + (n * a.ld_dh + at) * 2) = T::down(f);
 }
 
 // dw of a piece.
-template <class T, int kM, int kN, int kWM, int kWN, int kDepth, int kSlots>
+template <class T, int kM, int kN, int kWM, int kWN>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, false, false, kM, kN, kWM, kWN, kDepth, kSlots>;
-    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    using G = Tile<T, false, false, kM, kN, kWM, kWN>;
+    __shared__ __attribute__((aligned(16))) char even[G::kLds / 2], odd[G::kLds / 2];
     uint32_t tm, tn;
     tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
-          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, (lds_t*)lds);
+          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, (lds_t*)even, (lds_t*)odd);
     const float c = a.dw_scale[0];
     const int64_t m = m0 + G::wave_m() + G::lane_m(), w1 = n0 + G::wave_n() + G::lane_n();
 #pragma unroll
@@ -601,15 +680,38 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_zero(VocabArgs a) {  // d
 #define SCAPE_RUN(kernel, blocks, threads, ...) \
     hipLaunchKernelGGL(HIP_KERNEL_NAME(kernel), dim3((uint32_t)(blocks)), dim3(threads), 0, s, __VA_ARGS__)
 
+// The tiles by the tokens of one (a.tile_n): words or columns of h and w on one
+// side, tokens on the other.  Few tokens are a matter of reading w: small tiles,
+// so that a CU holds several and every CU has some.  From 129 tokens on the tile
+// is as large as two waves a SIMD hold: what a product moves through the caches
+// goes with 1 / kM + 1 / kN (8192x32000x2048 bf16: loss 840 us with 256x256, 1005
+// with 128x256 and two workgroups a CU).
+// The logits' operands are read along their rows and take as many slots as LDS
+// holds beside the other workgroups of the CU: w comes from memory, and a tile's
+// time for one slot is shorter than its way.
+#define SCAPE_LOGITS_BY_TILE(kernel, blocks, ...)                                                          \
+    switch (a.tile_n) {                                                                                    \
+        case 16: SCAPE_RUN((kernel<T, kSmallWords, 16, 4, 1, 4, 4>), blocks, 256, __VA_ARGS__); break;      \
+        case 32: SCAPE_RUN((kernel<T, kSmallWords, 32, 4, 1, 4, 4>), blocks, 256, __VA_ARGS__); break;      \
+        case 64: SCAPE_RUN((kernel<T, kSmallWords, 64, 2, 2, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
+        case 128: SCAPE_RUN((kernel<T, kSmallWords, 128, 2, 2, 3, 3>), blocks, 256, __VA_ARGS__); break;    \
+        case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;            \
+        default: SCAPE_RUN((kernel<T, 256, 256, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;             \
+    }
+#define SCAPE_DH_BY_TILE(kernel, blocks, ...)                                                       \
+    switch (a.tile_n) {                                                                             \
+        case 16: SCAPE_RUN((kernel<T, kSmallDims, 16, 4, 1>), blocks, 256, __VA_ARGS__); break;      \
+        case 32: SCAPE_RUN((kernel<T, kSmallDims, 32, 4, 1>), blocks, 256, __VA_ARGS__); break;      \
+        case 64: SCAPE_RUN((kernel<T, kSmallDims, 64, 2, 2>), blocks, 256, __VA_ARGS__); break;      \
+        case 128: SCAPE_RUN((kernel<T, kSmallDims, 128, 2, 2>), blocks, 256, __VA_ARGS__); break;    \
+        case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4>), blocks, 512, __VA_ARGS__); break;           \
+        default: SCAPE_RUN((kernel<T, 256, 256, 2, 4>), blocks, 512, __VA_ARGS__); break;            \
+    }
+
 template <class T>
 hipError_t sums_of(hipStream_t s, const VocabArgs& a) {
     const int64_t tiles = (int64_t)a.tiles_v * a.tiles_n;
-    switch (a.tile_n) {
-        case 16: SCAPE_RUN((k_vocab_sums<T, 256, 16, 4, 1, 64, 2>), tiles, 256, a); break;
-        case 64: SCAPE_RUN((k_vocab_sums<T, 256, 64, 4, 1, 64, 2>), tiles, 256, a); break;
-        case 128: SCAPE_RUN((k_vocab_sums<T, 256, 128, 4, 2, 64, 3>), tiles, 512, a); break;
-        default: SCAPE_RUN((k_vocab_sums<T, 256, 256, 2, 4, 64, 2>), tiles, 512, a); break;
-    }
+    SCAPE_LOGITS_BY_TILE(k_vocab_sums, tiles, a);
     SCAPE_RUN(k_vocab_join, (a.rows + kJoinTokens - 1) / kJoinTokens, kJoinTokens * kJoinParts, a);
     return hipGetLastError();
 }
@@ -620,31 +722,29 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         if (a.dw) SCAPE_RUN(k_vocab_zero<T>, a.cols, kRowThreads, a);
         return hipGetLastError();
     }
-    SCAPE_RUN(k_vocab_rows, 1, 1024, a);
-    if (a.dw) SCAPE_RUN(k_vocab_copy<T>, a.rows, kRowThreads, a);
-    const int64_t dim_tiles = (a.dim + 255) / 256;
-    for (int32_t v0 = 0; v0 < a.cols; v0 += (int32_t)a.piece) {
-        const int32_t v1 = v0 + a.piece < a.cols ? v0 + (int32_t)a.piece : (int32_t)a.cols;
-        const int64_t words = (v1 - v0 + 255) / 256, tiles = words * a.tiles_n;
-        switch (a.tile_n) {
-            case 16: SCAPE_RUN((k_vocab_p<T, 256, 16, 4, 1, 64, 2>), tiles, 256, a, v0, v1); break;
-            case 64: SCAPE_RUN((k_vocab_p<T, 256, 64, 4, 1, 64, 2>), tiles, 256, a, v0, v1); break;
-            case 128: SCAPE_RUN((k_vocab_p<T, 256, 128, 4, 2, 64, 3>), tiles, 512, a, v0, v1); break;
-            default: SCAPE_RUN((k_vocab_p<T, 256, 256, 2, 4, 64, 2>), tiles, 512, a, v0, v1); break;
-        }
-        if (a.dh) {
-            const int64_t n = dim_tiles * a.tiles_n * a.splits;
-            const bool first = v0 == 0, last = v1 == a.cols;
-            switch (a.tile_n) {
-                case 16: SCAPE_RUN((k_vocab_dh<T, 256, 16, 4, 1, 64, 2>), n, 256, a, v0, v1, first, last); break;
-                case 64: SCAPE_RUN((k_vocab_dh<T, 256, 64, 4, 1, 64, 2>), n, 256, a, v0, v1, first, last); break;
-                case 128: SCAPE_RUN((k_vocab_dh<T, 256, 128, 4, 2, 64, 3>), n, 512, a, v0, v1, first, last); break;
-                default: SCAPE_RUN((k_vocab_dh<T, 256, 256, 2, 4, 64, 2>), n, 512, a, v0, v1, first, last); break;
-            }
-        }
-        if (a.dw) SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 64, 2>), dim_tiles * words, 512, a, v0, v1);
+    if (a.rows <= kFewRows) {
+        SCAPE_RUN(k_vocab_rows_copy<T>, a.rows_pad, kRowThreads, a);
+    } else {
+        SCAPE_RUN(k_vocab_rows, 1, 1024, a);
+        if (a.dw) SCAPE_RUN(k_vocab_copy<T>, a.rows, kRowThreads, a);
     }
-    if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows, kRowThreads, a);
+    const int32_t piece = (int32_t)a.piece, cols = (int32_t)a.cols;
+    for (int32_t v0 = 0; v0 < cols; v0 += piece) {
+        const int32_t v1 = v0 + piece < cols ? v0 + piece : cols;
+        const bool first = v0 == 0, last = v1 == cols;
+        const int64_t tiles = (int64_t)((v1 - v0 + a.tile_m - 1) / a.tile_m) * a.tiles_n;
+        SCAPE_LOGITS_BY_TILE(k_vocab_p, tiles, a, v0, v1);
+        if (a.dh) {
+            const int64_t n = (a.dim + a.dh_tile - 1) / a.dh_tile * a.tiles_n * a.splits;
+            SCAPE_DH_BY_TILE(k_vocab_dh, n, a, v0, v1, first, last);
+        }
+        if (a.dw) {
+            const int64_t t = a.dw_tile, n = (a.dim + t - 1) / t * ((v1 - v0 + t - 1) / t);
+            if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2>), n, 256, a, v0, v1);
+            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4>), n, 512, a, v0, v1);
+        }
+    }
+    if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows * ((a.dim + kJoinWidth - 1) / kJoinWidth), kRowThreads, a);
     return hipGetLastError();
 }
 

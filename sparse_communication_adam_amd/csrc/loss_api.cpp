@@ -222,15 +222,15 @@ int64_t balance_bytes(int64_t tokens, int32_t experts, int32_t segments) {
 
 // ---- vocabulary loss
 constexpr int64_t kMaxHeadLd = int64_t(1) << 21;  // a tile's offsets stay below 2^31 bytes
-constexpr int64_t kTileWordsV = 256;              // words of a tile
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Tokens of a tile.
+// Tokens of a tile: what holds few, and of many the size that wastes least (a
+// tile of 192 takes about 4/5 of one of 256).
 int32_t vocab_tile(int64_t rows) {
-    if (rows <= 16) return 16;
-    if (rows <= 64) return 64;
-    return round_up(rows, 256) * 7 <= round_up(rows, 128) * 8 ? 256 : 128;
+    for (int32_t t = 16; t <= 128; t *= 2)
+        if (rows <= t) return t;
+    return (rows + 191) / 192 * 4 < (rows + 255) / 256 * 5 ? 192 : 256;
 }
 
 int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArgs* a) {
@@ -246,7 +246,11 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
     a->cols = cols;
     a->dim = dim;
     a->tile_n = vocab_tile(rows);
-    a->tiles_v = (uint32_t)((cols + kTileWordsV - 1) / kTileWordsV);
+    const bool small = a->tile_n <= 128;
+    a->tile_m = small ? kSmallWords : 256;
+    a->dh_tile = small ? kSmallDims : 256;
+    a->dw_tile = rows <= 512 ? 128 : 256;
+    a->tiles_v = (uint32_t)((cols + a->tile_m - 1) / a->tile_m);
     a->tiles_n = (uint32_t)((rows + a->tile_n - 1) / a->tile_n);
     a->rows_pad = (int64_t)a->tiles_n * a->tile_n;
     return SCAPE_OK;
@@ -255,20 +259,20 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
 // least 4096 words wide, so that dw has tiles for the CUs.  P's rows lie a
 // little further apart than a piece's words, off the powers of two.
 // dh's sums are split over the words where its tiles leave CUs idle: the number
-// of splits is the one with the least rounds of tiles on 256 CUs times a split's
+// of splits is the one with the least rounds of tiles on the CUs times a split's
 // steps (and about 6 more for its start and its end), counting the splits'
 // sums, which are written and read once more, at a step for each 8 MB.
 void vocab_pieces(VocabArgs* a) {
-    int64_t most = a->rows_pad ? (int64_t(1) << 27) / a->rows_pad / kTileWordsV * kTileWordsV : a->cols;
+    int64_t most = a->rows_pad ? (int64_t(1) << 27) / a->rows_pad / 256 * 256 : a->cols;
     if (most < 4096) most = 4096;
     const int64_t pieces = (a->cols + most - 1) / most;
-    a->piece = round_up((a->cols + pieces - 1) / pieces, kTileWordsV);
+    a->piece = round_up((a->cols + pieces - 1) / pieces, 256);
     a->ld_p = a->piece + 64;
-    const int64_t tiles = (a->dim + 255) / 256 * (a->tiles_n ? a->tiles_n : 1);
-    const int64_t slots = a->tile_n <= 64 ? 512 : 256;  // two workgroups a CU where LDS holds them
+    const int64_t tiles = (a->dim + a->dh_tile - 1) / a->dh_tile * (a->tiles_n ? a->tiles_n : 1);
+    const int64_t slots = a->tile_n <= 32 ? 1024 : a->tile_n <= 64 ? 768 : a->tile_n <= 128 ? 512 : 256;  // as LDS holds
     int64_t best = INT64_MAX;
     for (int64_t n = 1; n <= 128 && (n == 1 || a->piece / n >= 256); ++n) {
-        const int64_t words = round_up((a->piece + n - 1) / n, 64), splits = (a->piece + words - 1) / words;
+        const int64_t words = round_up((a->piece + n - 1) / n, 128), splits = (a->piece + words - 1) / words;
         const int64_t cost = (tiles * splits + slots - 1) / slots * (words / 64 + 6) +
                              (splits > 1 ? splits * a->rows * a->dim * 8 / (int64_t(8) << 20) : 0);
         if (cost < best) {

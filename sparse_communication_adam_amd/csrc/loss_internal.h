@@ -135,6 +135,7 @@ hipError_t launch_balance_loss(hipStream_t s, const int32_t* counts, const float
 hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a);
 
 // ---- k_vocab.hip
+constexpr int kSmallWords = 64, kSmallDims = 128;  // tiles of up to 128 tokens
 struct VocabRow {
     float f, lse2, dh, copy;  // P's factor, log-sum-exp in base 2, dh's and h's powers of two (0: does not count)
 };
@@ -147,7 +148,8 @@ struct VocabArgs {
     const int32_t* label;
     const float* weight;  // or NULL
     float scale, c2;      // c2 = scale * log2(e)
-    int32_t tile_n;       // tokens of a tile
+    int32_t tile_m, tile_n;    // words and tokens of a tile of the logits
+    int32_t dh_tile, dw_tile;  // columns of a tile of dh, columns and words of one of dw
     uint32_t tiles_v, tiles_n;
     // forward
     float* loss;
@@ -161,7 +163,7 @@ struct VocabArgs {
     int64_t ld_dh, ld_dw;
     int64_t rows_pad;     // whole tiles of tokens
     int64_t piece, ld_p;  // words of a piece, and P's row
-    int64_t split_words;  // words of a split of dh's sum, a multiple of 64
+    int64_t split_words;  // words of a split of dh's sum, a multiple of 128
     int32_t splits;
     VocabRow* row;        // [rows_pad]
     float* dw_scale;      // [1]
