@@ -18,6 +18,7 @@ namespace scape {
 namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef short s8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_t;
@@ -293,6 +294,34 @@ struct Tile {
             mix_loads<n - 1, products - m>();
         }
     }
+    // The wave's part of the tile as rows of the n axis: put(i, j) gives the four
+    // 16-bit elements of the lane's place in fragment (i, j), out(n, m, granule)
+    // takes eight of them of row n from m on, both counted within the wave's part.
+    // A lane's own four are 8 bytes of a row and 16 lanes are 16 rows; through LDS
+    // (behind the products, which are done with it) a row's 2 kTM bytes lie beside
+    // each other.  16 rows at a time, LDS serving a wave in order.
+    template <class Put, class Out>
+    static __device__ __forceinline__ void hand_out(lds_t* lds, const Put& put, const Out& out) {
+        constexpr int kPitch = kTM * 2 + 16, kRowPieces = kTM / 8;
+        lds_t* const mine = lds + (threadIdx.x >> 6) * (16 * kPitch);
+        const uint32_t lane = lane_id();
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) {
+#pragma unroll
+            for (int i = 0; i < kFM; ++i)
+                *reinterpret_cast<__attribute__((address_space(3))) u2*>(mine + lane_n() * kPitch + (i * 16 + lane_m()) * 2) =
+                    put(i, j);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int q = 0; q < (16 * kRowPieces + 63) / 64; ++q) {
+                const uint32_t at = (uint32_t)q * 64 + lane, row = at / kRowPieces, piece = at % kRowPieces;
+                if (16 * kRowPieces % 64 && at >= 16 * kRowPieces) break;
+                const gran g = *reinterpret_cast<const __attribute__((address_space(3))) gran*>(mine + row * kPitch + piece * 16);
+                out(j * 16 + row, piece * 8, g);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
     // The wave's first row and column in the tile, and the lane's of a fragment.
     static __device__ __forceinline__ uint32_t wave_m() { return ((threadIdx.x >> 6) % kWM) * kTM; }
     static __device__ __forceinline__ uint32_t wave_n() { return ((threadIdx.x >> 6) / kWM) * kTN; }
@@ -540,27 +569,32 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
     G g;
     g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, v1 - v0, (int32_t)a.dim},
           Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0, (int32_t)a.dim, (lds_t*)lds);
-    const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
-    const int32_t left = v1 - v0 - m0 - (int32_t)lm, first = v0 + m0 + (int32_t)lm;
+    const int32_t lm = m0 + (int32_t)(G::wave_m() + G::lane_m()), left = v1 - v0 - lm;
+    const int32_t n1 = n0 + (int32_t)G::wave_n();
+    VocabRow r[G::kFN];
+    int32_t lab[G::kFN];
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
-        const int64_t n = n0 + ln + j * 16;
-        const VocabRow r = a.row[n];
-        const int32_t lab = r.f != 0.0f ? a.label[n] - first : -1;  // a row that counts has one, and is a row of the matrix
-        char* const to = (char*)a.p + (n * a.ld_p + m0 + lm) * 2;
-#pragma unroll
-        for (int i = 0; i < G::kFM; ++i) {
+        const int32_t n = n1 + j * 16 + (int32_t)G::lane_n();
+        r[j] = a.row[n];
+        lab[j] = -1;  // a row that counts has one, and is a row of the matrix
+        if (r[j].f != 0.0f) lab[j] = a.label[n] - v0 - lm;
+    }
+    G::hand_out(
+        (lds_t*)lds,
+        [&](int i, int j) {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = fast_exp2(__builtin_fmaf(g.acc[i][j][e], a.c2, -r.lse2));
-                if (lab == i * 16 + e) x -= 1.0f;
-                p[e] = r.f != 0.0f && i * 16 + e < left ? x * r.f : 0.0f;
+                float x = fast_exp2(__builtin_fmaf(g.acc[i][j][e], a.c2, -r[j].lse2));
+                if (lab[j] == i * 16 + e) x -= 1.0f;
+                p[e] = r[j].f != 0.0f && i * 16 + e < left ? x * r[j].f : 0.0f;
             }
-            *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
+            return u2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
+        },
+        [&](uint32_t n, uint32_t m, const gran& q) {
+            *reinterpret_cast<gran*>((char*)a.p + ((n1 + (int64_t)n) * a.ld_p + m0 + G::wave_m() + m) * 2) = q;
+        });
 }
 
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
@@ -587,26 +621,37 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
 #pragma unroll
             for (int j = 0; j < G::kFN; ++j) g.acc[i][j] = f4{0, 0, 0, 0};
     }
-    const bool whole = last && a.splits == 1;
     const int64_t m = m0 + G::wave_m() + G::lane_m(), n1 = n0 + G::wave_n() + G::lane_n();
+    if (last && a.splits == 1) {
+        G::hand_out(
+            (lds_t*)even,
+            [&](int i, int j) {
+                const int64_t n = n1 + j * 16;
+                f4 x = g.acc[i][j];
+                float c = 0.0f;
+                if (n < a.rows && m + i * 16 < a.dim) {
+                    c = a.row[n].dh;
+                    if (!first) x += *reinterpret_cast<const f4*>(a.dh_sum + n * a.dim + m + i * 16);
+                }
+                x = c != 0.0f ? x * c : f4{0, 0, 0, 0};
+                return u2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+            },
+            [&](uint32_t n, uint32_t d, const gran& q) {
+                const int64_t row = n0 + G::wave_n() + n, col = m0 + G::wave_m() + d;
+                if (row < a.rows && col < a.dim) *reinterpret_cast<gran*>((char*)a.dh + (row * a.ld_dh + col) * 2) = q;
+            });
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
         const int64_t n = n1 + j * 16;
         if (n >= a.rows) continue;
         float* const to = a.dh_sum + ((int64_t)split * a.rows + n) * a.dim + m;
-        char* const out = (char*)a.dh + (n * a.ld_dh + m) * 2;
-        const float c = whole ? a.row[n].dh : 1.0f;
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
             if (m + i * 16 < a.dim) {
                 f4* const q = reinterpret_cast<f4*>(to + i * 16);
-                f4 x = first ? g.acc[i][j] : *q + g.acc[i][j];
-                if (!whole) {
-                    *q = x;
-                } else {
-                    x = c != 0.0f ? x * c : f4{0, 0, 0, 0};
-                    *reinterpret_cast<uint2*>(out + i * 32) = uint2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
-                }
+                *q = first ? g.acc[i][j] : *q + g.acc[i][j];
             }
     }
 }
@@ -655,20 +700,17 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_
     g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
           Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, (lds_t*)even, (lds_t*)odd);
     const float c = a.dw_scale[0];
-    const int64_t m = m0 + G::wave_m() + G::lane_m(), w1 = n0 + G::wave_n() + G::lane_n();
-#pragma unroll
-    for (int j = 0; j < G::kFN; ++j) {
-        const int64_t v = v0 + w1 + j * 16;
-        if (v >= v1) continue;
-        char* const to = (char*)a.dw + (v * a.ld_dw + m) * 2;
-#pragma unroll
-        for (int i = 0; i < G::kFM; ++i)
-            if (m + i * 16 < a.dim) {
-                const f4 x = g.acc[i][j] * c;
-                *reinterpret_cast<uint2*>(to + i * 32) = uint2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
-                __builtin_amdgcn_sched_barrier(0);
-            }
-    }
+    G::hand_out(
+        (lds_t*)even,
+        [&](int i, int j) {
+            const f4 x = g.acc[i][j] * c;
+            return u2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+        },
+        [&](uint32_t n, uint32_t d, const gran& q) {
+            const int64_t v = v0 + n0 + (int64_t)(G::wave_n() + n), col = m0 + G::wave_m() + d;
+            if (v < v1 && col < a.dim)
+                __builtin_nontemporal_store(q, reinterpret_cast<gran*>((char*)a.dw + (v * a.ld_dw + col) * 2));
+        });
 }
 
 template <class T>
