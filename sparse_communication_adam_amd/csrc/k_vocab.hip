@@ -159,6 +159,7 @@ struct Tile {
     using A = Stage<kAlongA, kM, kThreads>;
     using B = Stage<kAlongB, kN, kThreads>;
     static constexpr int kLoads = A::kLoads + B::kLoads;
+    static_assert(kWM * kWN * 16 * kTM * 2 <= A::kBytes, "hand_out's rows");
     static constexpr int kLdsA = kSlotsA * A::kBytes, kLds = kLdsA + kSlotsB * B::kBytes;
     // Loads that may be on their way when the next slots have to be there: those
     // issued behind the last of them (of a step's loads B's are first).
@@ -216,25 +217,44 @@ struct Tile {
         }
         wait<0>();  // what was loaded behind the end is in LDS, too
     }
-    // Any operands, the depth from k0 to k1, a multiple of 128 of it or all that
-    // there is.  The slots are two objects, so that the compiler knows a read from
-    // one to be none of what is loaded into the other.
+    // The same for any operands.  Every slot is an object of its own and the loop
+    // goes through them by name, so that the compiler knows what is read to be
+    // none of what is loaded meanwhile.
+    struct Slots {
+        lds_t *a[3], *b[3];
+    };
+    static constexpr int kTurn = kSlotsA == kSlotsB ? kSlotsA : kSlotsA * kSlotsB;
     __device__ __forceinline__ void run(const Side& a, const Side& b, int32_t m0, int32_t n0, int32_t k0, int32_t k1,
-                                        lds_t* even, lds_t* odd) {
-        static_assert(kSlotsA == 2 && kSlotsB == 2, "");
+                                        const Slots& s) {
         start(a, b, m0, n0, k0);
-        lb.load(even + A::kBytes);
-        la.load(even);
-        lb.load(odd + A::kBytes);
-        la.load(odd);
-        wait<kLoads>();
-        Half x, y;
-        x.read(even, even + A::kBytes, fa, fb, 0);
-        for (int32_t k = k0; k < k1; k += 2 * kDepth) {
-            slot(even, even + A::kBytes, odd, odd + A::kBytes, x, y);
-            slot(odd, odd + A::kBytes, even, even + A::kBytes, x, y);
+#pragma unroll
+        for (int i = -kSlotsA; i < 0; ++i) {
+            if (i + kSlotsB >= 0) lb.load(s.b[i + kSlotsB]);
+            asm volatile("" ::: "memory");
+            la.load(s.a[i + kSlotsA]);
         }
+        wait<kAhead + kLoads>();
+        Half x, y;
+        x.read(s.a[0], s.b[0], fa, fb, 0);
+        int32_t k = k0;
+        for (; k + (kTurn - 1) * kDepth < k1; k += kTurn * kDepth) turn<0>(s, x, y);
+        rest<0>(s, x, y, k, k1);
         wait<0>();
+    }
+    template <int i>
+    __device__ __forceinline__ void turn(const Slots& s, Half& x, Half& y) {
+        if constexpr (i < kTurn) {
+            slot(s.a[i % kSlotsA], s.b[i % kSlotsB], s.a[(i + 1) % kSlotsA], s.b[(i + 1) % kSlotsB], x, y);
+            turn<i + 1>(s, x, y);
+        }
+    }
+    template <int i>
+    __device__ __forceinline__ void rest(const Slots& s, Half& x, Half& y, int32_t k, int32_t k1) {
+        if constexpr (i < kTurn - 1)
+            if (k < k1) {
+                slot(s.a[i % kSlotsA], s.b[i % kSlotsB], s.a[(i + 1) % kSlotsA], s.b[(i + 1) % kSlotsB], x, y);
+                rest<i + 1>(s, x, y, k + kDepth, k1);
+            }
     }
     __device__ __forceinline__ void slot(lds_t* now_a, lds_t* now_b, const lds_t* next_a, const lds_t* next_b, Half& x, Half& y) {
         y.read(now_a, now_b, fa, fb, 1);
@@ -302,21 +322,24 @@ struct Tile {
     // each other.  16 rows at a time, LDS serving a wave in order.
     template <class Put, class Out>
     static __device__ __forceinline__ void hand_out(lds_t* lds, const Put& put, const Out& out) {
-        constexpr int kPitch = kTM * 2 + 16, kRowPieces = kTM / 8;
+        constexpr int kPitch = kTM * 2, kRowPieces = kTM / 8;  // pieces are exchanged as the operands' are
         lds_t* const mine = lds + (threadIdx.x >> 6) * (16 * kPitch);
         const uint32_t lane = lane_id();
 #pragma unroll
         for (int j = 0; j < kFN; ++j) {
 #pragma unroll
-            for (int i = 0; i < kFM; ++i)
-                *reinterpret_cast<__attribute__((address_space(3))) u2*>(mine + lane_n() * kPitch + (i * 16 + lane_m()) * 2) =
+            for (int i = 0; i < kFM; ++i) {
+                const uint32_t piece = ((uint32_t)i * 2 + lane_m() / 8) ^ (lane_n() % kRowPieces);
+                *reinterpret_cast<__attribute__((address_space(3))) u2*>(mine + lane_n() * kPitch + piece * 16 + lane_m() % 8 * 2) =
                     put(i, j);
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int q = 0; q < (16 * kRowPieces + 63) / 64; ++q) {
                 const uint32_t at = (uint32_t)q * 64 + lane, row = at / kRowPieces, piece = at % kRowPieces;
                 if (16 * kRowPieces % 64 && at >= 16 * kRowPieces) break;
-                const gran g = *reinterpret_cast<const __attribute__((address_space(3))) gran*>(mine + row * kPitch + piece * 16);
+                const gran g = *reinterpret_cast<const __attribute__((address_space(3))) gran*>(
+                    mine + row * kPitch + (piece ^ (row % kRowPieces)) * 16);
                 out(j * 16 + row, piece * 8, g);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -597,12 +620,19 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
         });
 }
 
+// A kernel's slots: objects of their own (the third is next to nothing where
+// there are two).  What leaves through LDS takes the first of A.
+#define SCAPE_SLOTS(G)                                                                                       \
+    __shared__ __attribute__((aligned(16))) char a0[G::A::kBytes], a1[G::A::kBytes], b0[G::B::kBytes], b1[G::B::kBytes]; \
+    __shared__ __attribute__((aligned(16))) char a2[kSlotsA > 2 ? G::A::kBytes : 16], b2[kSlotsB > 2 ? G::B::kBytes : 16]; \
+    const typename G::Slots slots{{(lds_t*)a0, (lds_t*)a1, (lds_t*)a2}, {(lds_t*)b0, (lds_t*)b1, (lds_t*)b2}}
+
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
 // Where one split sums them all, the last piece's launch writes dh itself.
-template <class T, int kM, int kN, int kWM, int kWN>
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last) {
-    using G = Tile<T, false, true, kM, kN, kWM, kWN>;
-    __shared__ __attribute__((aligned(16))) char even[G::kLds / 2], odd[G::kLds / 2];
+    using G = Tile<T, false, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
+    SCAPE_SLOTS(G);
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
     const uint32_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
@@ -614,7 +644,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     G g;
     if (k0 < k1) {
         g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, (int32_t)a.dim, all},
-              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, (lds_t*)even, (lds_t*)odd);
+              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, slots);
     } else {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
@@ -624,7 +654,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     const int64_t m = m0 + G::wave_m() + G::lane_m(), n1 = n0 + G::wave_n() + G::lane_n();
     if (last && a.splits == 1) {
         G::hand_out(
-            (lds_t*)even,
+            slots.a[0],
             [&](int i, int j) {
                 const int64_t n = n1 + j * 16;
                 f4 x = g.acc[i][j];
@@ -689,19 +719,19 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
 }
 
 // dw of a piece.
-template <class T, int kM, int kN, int kWM, int kWN>
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, false, false, kM, kN, kWM, kWN>;
-    __shared__ __attribute__((aligned(16))) char even[G::kLds / 2], odd[G::kLds / 2];
+    using G = Tile<T, false, false, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
+    SCAPE_SLOTS(G);
     uint32_t tm, tn;
     tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
-          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, (lds_t*)even, (lds_t*)odd);
+          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, slots);
     const float c = a.dw_scale[0];
     G::hand_out(
-        (lds_t*)even,
+        slots.a[0],
         [&](int i, int j) {
             const f4 x = g.acc[i][j] * c;
             return u2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
@@ -740,14 +770,14 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_zero(VocabArgs a) {  // d
         case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;            \
         default: SCAPE_RUN((kernel<T, 256, 256, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;             \
     }
-#define SCAPE_DH_BY_TILE(kernel, blocks, ...)                                                       \
-    switch (a.tile_n) {                                                                             \
-        case 16: SCAPE_RUN((kernel<T, kSmallDims, 16, 4, 1>), blocks, 256, __VA_ARGS__); break;      \
-        case 32: SCAPE_RUN((kernel<T, kSmallDims, 32, 4, 1>), blocks, 256, __VA_ARGS__); break;      \
-        case 64: SCAPE_RUN((kernel<T, kSmallDims, 64, 2, 2>), blocks, 256, __VA_ARGS__); break;      \
-        case 128: SCAPE_RUN((kernel<T, kSmallDims, 128, 2, 2>), blocks, 256, __VA_ARGS__); break;    \
-        case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4>), blocks, 512, __VA_ARGS__); break;           \
-        default: SCAPE_RUN((kernel<T, 256, 256, 2, 4>), blocks, 512, __VA_ARGS__); break;            \
+#define SCAPE_DH_BY_TILE(kernel, blocks, ...)                                                             \
+    switch (a.tile_n) {                                                                                   \
+        case 16: SCAPE_RUN((kernel<T, kSmallDims, 16, 4, 1, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
+        case 32: SCAPE_RUN((kernel<T, kSmallDims, 32, 4, 1, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
+        case 64: SCAPE_RUN((kernel<T, kSmallDims, 64, 2, 2, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
+        case 128: SCAPE_RUN((kernel<T, kSmallDims, 128, 2, 2, 2, 2>), blocks, 256, __VA_ARGS__); break;    \
+        case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;           \
+        default: SCAPE_RUN((kernel<T, 256, 256, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;            \
     }
 
 template <class T>
@@ -782,8 +812,8 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         }
         if (a.dw) {
             const int64_t t = a.dw_tile, n = (a.dim + t - 1) / t * ((v1 - v0 + t - 1) / t);
-            if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2>), n, 256, a, v0, v1);
-            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4>), n, 512, a, v0, v1);
+            if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2>), n, 256, a, v0, v1);
+            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 2, 2>), n, 512, a, v0, v1);
         }
     }
     if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows * ((a.dim + kJoinWidth - 1) / kJoinWidth), kRowThreads, a);

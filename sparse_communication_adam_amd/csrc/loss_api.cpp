@@ -272,7 +272,7 @@ void vocab_pieces(VocabArgs* a) {
     const int64_t slots = a->tile_n <= 32 ? 1024 : a->tile_n <= 64 ? 768 : a->tile_n <= 128 ? 512 : 256;  // as LDS holds
     int64_t best = INT64_MAX;
     for (int64_t n = 1; n <= 128 && (n == 1 || a->piece / n >= 256); ++n) {
-        const int64_t words = round_up((a->piece + n - 1) / n, 128), splits = (a->piece + words - 1) / words;
+        const int64_t words = round_up((a->piece + n - 1) / n, 64), splits = (a->piece + words - 1) / words;
         const int64_t cost = (tiles * splits + slots - 1) / slots * (words / 64 + 6) +
                              (splits > 1 ? splits * a->rows * a->dim * 8 / (int64_t(8) << 20) : 0);
         if (cost < best) {

@@ -163,7 +163,7 @@ struct VocabArgs {
     int64_t ld_dh, ld_dw;
     int64_t rows_pad;     // whole tiles of tokens
     int64_t piece, ld_p;  // words of a piece, and P's row
-    int64_t split_words;  // words of a split of dh's sum, a multiple of 128
+    int64_t split_words;  // words of a split of dh's sum, a multiple of 64
     int32_t splits;
     VocabRow* row;        // [rows_pad]
     float* dw_scale;      // [1]
