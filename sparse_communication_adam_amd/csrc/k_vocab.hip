@@ -440,33 +440,41 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
     }
 }
 
-// Joins a token's tiles: 16 tokens a workgroup, 64 threads each.
-constexpr int kJoinTokens = 16, kJoinParts = 64;
+// Joins a token's tiles: 16 tokens a workgroup, 64 threads each, four tiles on
+// their way to a thread.
+constexpr int kJoinTokens = 16, kJoinParts = 64, kJoinEach = 4;
+__device__ __forceinline__ void join_sums(float2& r, const float2& p) {
+    const float ref = fmaxf(r.x, p.x);
+    r.y = r.y * fast_exp2(r.x - ref) + p.y * fast_exp2(p.x - ref);
+    r.x = ref;
+}
 __global__ __launch_bounds__(kJoinTokens* kJoinParts) void k_vocab_join(VocabArgs a) {
-    __shared__ float2 red[kJoinParts][kJoinTokens];
+    __shared__ float2 red[kJoinParts / 4][kJoinTokens];
     const uint32_t t = threadIdx.x % kJoinTokens, q = threadIdx.x / kJoinTokens;
     const int64_t n = (int64_t)blockIdx.x * kJoinTokens + t;
     float2 r = float2{kLowest, 0.0f};
     if (n < a.rows)
-        for (uint32_t v = q; v < a.tiles_v; v += kJoinParts) {
-            const float2 p = a.part[(int64_t)v * a.rows + n];
-            const float ref = fmaxf(r.x, p.x);
-            r.y = r.y * fast_exp2(r.x - ref) + p.y * fast_exp2(p.x - ref);
-            r.x = ref;
+        for (uint32_t v = q; v < a.tiles_v; v += kJoinParts * kJoinEach) {
+            float2 p[kJoinEach];
+#pragma unroll
+            for (int i = 0; i < kJoinEach; ++i) {
+                const uint32_t at = v + i * kJoinParts;
+                p[i] = at < a.tiles_v ? a.part[(int64_t)at * a.rows + n] : float2{kLowest, 0.0f};
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinEach; ++i) join_sums(r, p[i]);
         }
-    red[q][t] = r;
+    // a wave holds four threads of each token
+    join_sums(r, float2{__shfl_xor(r.x, 16, 64), __shfl_xor(r.y, 16, 64)});
+    join_sums(r, float2{__shfl_xor(r.x, 32, 64), __shfl_xor(r.y, 32, 64)});
+    if (lane_id() < kJoinTokens) red[threadIdx.x >> 6][t] = r;
     __syncthreads();
-    for (int w = kJoinParts / 2; w >= 1; w >>= 1) {
-        if (q < (uint32_t)w) {
-            const float2 p = red[q + w][t];
-            r = red[q][t];
-            const float ref = fmaxf(r.x, p.x);
-            r.y = r.y * fast_exp2(r.x - ref) + p.y * fast_exp2(p.x - ref);
-            r.x = ref;
-            red[q][t] = r;
-        }
-        __syncthreads();
-    }
+    if (q >= 4) return;
+    r = red[q * 4][t];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) join_sums(r, red[q * 4 + i][t]);
+    join_sums(r, float2{__shfl_xor(r.x, 16, 64), __shfl_xor(r.y, 16, 64)});
+    join_sums(r, float2{__shfl_xor(r.x, 32, 64), __shfl_xor(r.y, 32, 64)});
     if (q != 0 || n >= a.rows) return;
     const double lse2 = (double)r.x + log2((double)r.y);  // in base 2
     a.lse[n] = (float)(lse2 * kLn2);
