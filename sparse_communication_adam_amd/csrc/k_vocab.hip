@@ -404,7 +404,8 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
         // reference's own rounding was stands in the reference.
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float ref = top == kNegInf ? 0.0f : top * a.c2;
+        // Words that are none leave the lowest reference, which no sum gives way to.
+        const float ref = top == kNegInf ? kLowest : top * a.c2;
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i) {

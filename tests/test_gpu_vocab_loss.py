@@ -197,6 +197,22 @@ def test_large_logits(sc, dtype):
     _check_backward(sc, c)
 
 
+@pytest.mark.parametrize("rows", [3, 20, 60, 100, 200, 300])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_logits_far_below_zero(sc, dtype, rows):
+    """Every logit near -400: what lies behind the last word of a tile counts for nothing there, too."""
+    c = Case(rows, 100, 64, dtype, key="low")
+    c.h[:, 0] = 20
+    c.w[:, 0] = -20
+    _check_forward(sc, c)
+    _check_backward(sc, c)
+    c = Case(rows, 5000, 24, dtype, key="low")
+    c.h[:, 0] = 20
+    c.w[:, 0] = -20
+    _check_forward(sc, c)
+    _check_backward(sc, c)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_equal_logits(sc, dtype):
     """All words alike: the loss is log(cols) exactly to the roundings, dw's columns are alike."""
