@@ -308,12 +308,15 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
 // A workgroup takes a token and its waves the token's choices in turn (a wave
 // for a token is slower for few tokens: 2000x1536 f16, k = 4, 12.9 us and 15.5).
 // dout is in registers where kB granules a lane hold it all, else it is read for
-// every place; the waves' reads of it meet in the L1.
+// every place; the waves' reads of it meet in the L1.  A grid's axis counts its
+// threads in 32 bits, so more tokens than that lie along the other axis.
+constexpr int64_t kTokensAcross = int64_t(1) << 22;
 template <class T, int kB>
 __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
     using raw = typename T::raw;
     const uint32_t lane = lane_id();
-    const int64_t t = blockIdx.x;
+    const int64_t t = (int64_t)blockIdx.y * kTokensAcross + blockIdx.x;
+    if (t >= a.tokens) return;
     const raw* const dout = static_cast<const raw*>(a.x) + t * a.ld_x;
     const raw* const y = static_cast<const raw*>(a.y_in);
     raw* const dy = static_cast<raw*>(a.y);
@@ -374,7 +377,9 @@ int granules_of(const MoveArgs& a) { return (int)((a.dim / (16 / dtype_size(a.dt
 
 #define SCAPE_RUN(...) \
     hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)((a.tokens + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a)
-#define SCAPE_RUN_TOKEN(...) hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)a.tokens), dim3(kBlock), 0, s, a)
+#define SCAPE_RUN_TOKEN(...)                                                                                            \
+    hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)(a.tokens < kTokensAcross ? a.tokens : kTokensAcross),             \
+                                           (uint32_t)((a.tokens + kTokensAcross - 1) / kTokensAcross)), dim3(kBlock), 0, s, a)
 
 template <class T>
 hipError_t gather_of(hipStream_t s, const MoveArgs& a) {

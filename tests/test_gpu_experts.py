@@ -328,6 +328,24 @@ def test_rows_beyond_32_bit_offsets(sc):
     assert int((y != 0).any(1).sum()) == tokens
 
 
+def test_the_most_tokens(sc):
+    """As many tokens as a move takes, and one more is refused."""
+    tokens = 2 ** 25
+    x = (torch.arange(tokens, device="cuda", dtype=torch.int32) % 251).to(torch.bfloat16).view(tokens, 1)
+    row = torch.arange(tokens - 1, -1, -1, device="cuda", dtype=torch.int32).view(tokens, 1)
+    y, out, dy = torch.empty_like(x), torch.empty_like(x), torch.full_like(x, NAN)
+    dw = torch.full((tokens, 1), NAN, device="cuda")
+    sc.scape_expert_gather(x, row, y)
+    assert torch.equal(y, x.flip(0))
+    sc.scape_expert_combine(y, row, out)
+    assert torch.equal(out, x)
+    sc.scape_expert_combine_backward(y, row, x, dy, dweight=dw)
+    assert torch.equal(dy, y) and torch.equal(dw, x.float() ** 2)
+    more = torch.empty(tokens + 1, 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(sc.ScapeError):
+        sc.scape_expert_gather(more, torch.zeros(tokens + 1, 1, dtype=torch.int32, device="cuda"), more)
+
+
 def test_autograd_sees_what_was_written(sc):
     c = Case(sc, 10, 2, 4, 32, torch.float32, key="versions")
     x = torch.randn(20, 32, device="cuda", requires_grad=True)
