@@ -347,8 +347,9 @@ int scape_grad_norm_workspace(const scape_ctx* ctx, int64_t* bytes);
  *                     the residual for good, so the worker sends none
  * norm as scape_grad_norm writes it, or another number for each worker that
  * the program has made of it.  out[i] may be g[i] (then nothing is read or
- * written where f = 1); any other overlap is not allowed.  Padding elements are
- * not written.  max_norm > 0 and finite.
+ * written where f = 1); any other overlap is refused, one gradient for two
+ * workers that is clipped in place among them.  Padding elements are not
+ * written.  max_norm > 0 and finite.
  * Errors: INVALID_ARG, ALIGN, STATE, HIP.
  */
 int scape_grad_clip(scape_ctx* ctx, const uint16_t* const* g, const float* norm, float max_norm, int32_t shared,

@@ -814,10 +814,21 @@ int clip_common(scape_ctx* ctx, const uint16_t* const* g, const float* norm, flo
     if (!aligned(norm, 4)) return fail(SCAPE_ERR_ALIGN, "norm must be 4-byte aligned");
     if (!(max_norm > 0.0f) || !std::isfinite(max_norm)) return fail(SCAPE_ERR_INVALID_ARG, "max_norm must be positive and finite");
     if (shared != 0 && shared != 1) return fail(SCAPE_ERR_INVALID_ARG, "shared takes 0 or 1, not %d", shared);
-    const int32_t W = ctx->cfg.workers;
-    for (int32_t i = 0; i < (interleaved ? 1 : W); ++i) {
+    const int32_t W = ctx->cfg.workers, buffers = interleaved ? 1 : W;
+    const uintptr_t bytes = (uintptr_t)ctx->n_words * 128 * (uintptr_t)(W / buffers);
+    const auto meet = [&](const void* p, const void* q) {
+        const uintptr_t x = (uintptr_t)p, y = (uintptr_t)q;
+        return (x < y ? y - x : x - y) < bytes;
+    };
+    for (int32_t i = 0; i < buffers; ++i) {
         if (!out[i] && ctx->n_words) return fail(SCAPE_ERR_INVALID_ARG, "out[%d] is NULL", i);
         if (!aligned(out[i], 16)) return fail(SCAPE_ERR_ALIGN, "out[%d] must be 16-byte aligned", i);
+        for (int32_t j = 0; j < buffers; ++j) {
+            // one buffer for two workers would be scaled by both
+            if (j != i && meet(out[i], out[j])) return fail(SCAPE_ERR_INVALID_ARG, "out[%d] and out[%d] overlap", i, j);
+            if (meet(out[i], g[j]) && (j != i || out[i] != g[j]))
+                return fail(SCAPE_ERR_INVALID_ARG, "out[%d] overlaps g[%d]", i, j);
+        }
     }
     for (int32_t i = 0; i < W; ++i) a.out[i] = interleaved ? out[0] + (int64_t)i * 64 : out[i];
     a.norm = const_cast<float*>(norm);  // read only in this launch

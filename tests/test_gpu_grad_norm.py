@@ -222,6 +222,30 @@ def test_refusals_with_a_context(sc):
     assert sc.lib().scape_grad_clip_interleaved(g.ctx.handle, il.data_ptr(), norm.data_ptr(), 1.0, 2, il.data_ptr(), None) == -1
 
 
+def test_gradients_that_overlap(sc):
+    """One buffer for two workers is read by both, and never written by both."""
+    g = Grads(sc, LAYERS["ragged"], 3)
+    t, il = g.given(False), g.given(True)
+    n = g.ctx.layout.n_pad
+    norm = torch.full((4,), 2.0, device="cuda")
+    both, wide = torch.zeros(n + 64, dtype=t[0].dtype, device="cuda"), torch.zeros(3 * n + 64, dtype=t[0].dtype, device="cuda")
+    for call in [
+        lambda: sc.scape_grad_clip(g.ctx, [t[0], t[1], t[0]], norm, 1.0),
+        lambda: sc.scape_grad_clip(g.ctx, t, norm, 1.0, out=[t[1], t[0], t[2]]),
+        lambda: sc.scape_grad_clip(g.ctx, t, norm, 1.0, out=[both[:n], both[64:], t[2]]),
+        lambda: sc.scape_grad_clip(g.ctx, [both[:n], t[1], t[2]], norm, 1.0, out=[both[64:], t[1], t[2]]),
+        lambda: sc.scape_grad_clip_interleaved(g.ctx, wide[:3 * n], norm, 1.0, out=wide[64:]),
+    ]:
+        with pytest.raises(sc.ScapeError):
+            call()
+    before = [x.clone() for x in t]
+    out = [torch.zeros_like(x) for x in t]
+    sc.scape_grad_clip(g.ctx, [t[0], t[1], t[0]], norm, 1.0, out=out)  # read twice
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[2]) and all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(t, before))
+    sc.scape_grad_clip_interleaved(g.ctx, il, norm, 1.0, out=wide[:3 * n])
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_a_clipped_step(sc, interleaved):
     """ScapeState.step(max_norm=) is the step on gradients clipped beforehand, eager and from graphs."""
