@@ -353,11 +353,10 @@ struct Tile {
 };
 
 // Block b of a grid of nm x nn tiles.  Workgroups of one XCD, which share an
-// L2, take runs of blocks; a run walks bands of kBand tiles of the n axis, all
-// of the m axis for each.
+// L2, take runs of blocks (xcd_block); a run walks bands of kBand tiles of the n
+// axis, all of the m axis for each.
 constexpr uint32_t kBand = 8;
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, uint32_t& m, uint32_t& n) {
-    b = xcd_block(b, nm * nn);
     const uint32_t band = b / (kBand * nm), first = band * kBand, in = b - band * kBand * nm;
     const uint32_t wide = nn - first < kBand ? nn - first : kBand;
     n = __builtin_amdgcn_readfirstlane(first + in % wide);  // divisions are made in vector registers
@@ -372,7 +371,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
     using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, a.tiles_v, a.tiles_n, tm, tn);
+    tile_of(xcd_block(blockIdx.x, gridDim.x), a.tiles_v, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{a.w, (int32_t)a.ld_w, (int32_t)a.cols, (int32_t)a.dim}, Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0,
@@ -596,7 +595,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
     using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
+    tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, v1 - v0, (int32_t)a.dim},
@@ -644,8 +643,9 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     SCAPE_SLOTS(G);
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
-    const uint32_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
-    tile_of(blockIdx.x - split * tiles, nm, a.tiles_n, tm, tn);
+    // a split's tiles, which share its words, on one XCD
+    const uint32_t b = xcd_block(blockIdx.x, gridDim.x), split = __builtin_amdgcn_readfirstlane(b / tiles);
+    tile_of(b - split * tiles, nm, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     const int32_t part = (int32_t)a.split_words, k0 = (int32_t)split * part, all = v1 - v0;
     const int32_t k1 = k0 + part < all ? k0 + part : all;
@@ -733,7 +733,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_
     using G = Tile<T, false, false, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     SCAPE_SLOTS(G);
     uint32_t tm, tn;
-    tile_of(blockIdx.x, (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
+    tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
