@@ -40,11 +40,13 @@ constexpr uint32_t kRawBuffer = 0x00027000u;
 
 // One operand of a product: rows of 16-bit elements, ld apart.  Along: the
 // summed axis lies along the rows (extent rows of them); else it runs over
-// rows of `extent` elements.
+// rows of `extent` elements.  A blocked one lies in blocks of 64 elements of its
+// rows, which are `block` apart; it has nothing but whole tiles.
 // All sizes are below 2^21 (the call checks that), so their sums are 32-bit.
 struct Side {
     const void* p;
     int32_t ld, extent, depth;  // depth: elements of the summed axis
+    int32_t block = 0;
 };
 
 // Moves a tile of kR x kDepth from memory to LDS, 16 bytes a lane, and reads MFMA
@@ -52,7 +54,7 @@ struct Side {
 // are permuted instead: the 16-byte pieces of a row are exchanged by an XOR
 // that spreads what one fragment read touches over all banks.
 constexpr int kDepth = 64;  // elements of the summed axis in a slot
-template <bool kAlong, int kR, int kThreads>
+template <bool kAlong, int kR, int kThreads, bool kBlocked>
 struct Stage {
     static constexpr int kBytes = kR * 2 * kDepth;
     static constexpr int kPieces = kBytes / 16;
@@ -73,7 +75,7 @@ struct Stage {
     int32_t piece;                              // a lane's first element along the depth
     uint32_t wave;                              // where a wave's share of a load begins in the slot
     const char* at;                             // the next tile, and what is left of the depth there
-    int32_t left, bytes, ld;
+    int32_t left, bytes, ld, block;
 
     // what the pieces of row k are exchanged by; the same for k + 4 (k % 8 < 4)
     // and k + 16, which a fragment's reads and a lane's loads are apart
@@ -88,19 +90,27 @@ struct Stage {
     // The tile at row (or column) r0 and depth k is the first.
     __device__ __forceinline__ void init(const Side& s, int32_t r0, int32_t k) {
         const uint32_t tid = threadIdx.x % kLanes;
-        ld = s.ld;
+        ld = kBlocked ? kDepth : s.ld;
+        block = s.block;
         pitch = (uint32_t)(ld * 2);
 #pragma unroll
         for (int i = 0; i < (kSteady ? 1 : kLoads); ++i) {
             const uint32_t q = (uint32_t)i * kThreads + tid, row = q / kRowPieces, pos = q % kRowPieces;
-            off[i] = row * pitch + ((pos ^ turn(row)) << 4);
-            if (i == 0) piece = (int32_t)((pos ^ turn(row)) * 8);
+            const uint32_t at16 = pos ^ turn(row);
+            off[i] = row * pitch + (kBlocked ? (at16 >> 3) * (uint32_t)(block * 2) + ((at16 & 7) << 4) : at16 << 4);
+            if (i == 0) piece = (int32_t)(at16 * 8);
         }
         wave = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
         left = s.depth - k;
         const int32_t rows = s.extent - r0 < kR ? s.extent - r0 : kR;
-        bytes = kAlong ? ((rows - 1) * ld + left) * 2 : (s.extent - r0) * 2;  // all, or of a last row
-        at = static_cast<const char*>(s.p) + (kAlong ? (int64_t)r0 * ld + k : (int64_t)k * ld + r0) * 2;
+        if constexpr (kBlocked) {
+            bytes = kAlong ? rows * ld * 2 : (kR / 64 - 1) * block * 2 + 128;  // of all rows, or of a last one
+            at = static_cast<const char*>(s.p) +
+                 (kAlong ? (int64_t)r0 * ld + (int64_t)(k / 64) * block : (int64_t)k * ld + (int64_t)(r0 / 64) * block) * 2;
+        } else {
+            bytes = kAlong ? ((rows - 1) * ld + left) * 2 : (s.extent - r0) * 2;  // the same
+            at = static_cast<const char*>(s.p) + (kAlong ? (int64_t)r0 * ld + k : (int64_t)k * ld + r0) * 2;
+        }
     }
 
     // The next tile to a slot.  Behind the end of the depth there are zeros.
@@ -116,8 +126,8 @@ struct Stage {
             const uint32_t o = kSteady ? (off[0] | kill) + (uint32_t)(i * kRowsALoad) * pitch : off[kSteady ? 0 : i] | kill;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(to + wave + i * kThreads * 16), 16, o, 0, 0, 0);
         }
-        at += kAlong ? kDepth * 2 : (int64_t)kDepth * 2 * ld;
-        if (kAlong) bytes -= kDepth * 2;
+        at += !kAlong ? (int64_t)kDepth * 2 * ld : kBlocked ? (int64_t)block * 2 : kDepth * 2;
+        if (kAlong && !kBlocked) bytes -= kDepth * 2;
         left -= kDepth;
     }
 
@@ -151,13 +161,13 @@ struct Stage {
 // wave holds the fragments of a slot's two halves: while one half is multiplied
 // the other is read, and when both are in registers the slots are loaded anew,
 // the other slots' products ahead of their use.
-template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN, int kSlotsA = 2, int kSlotsB = 2>
+template <class T, bool kAlongA, bool kAlongB, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB, bool kBlockedB = false>
 struct Tile {
     static constexpr int kThreads = kWM * kWN * 64;
     static constexpr int kTM = kM / kWM, kTN = kN / kWN;  // a wave's part, powers of two
     static constexpr int kFM = kTM / 16, kFN = kTN / 16;
-    using A = Stage<kAlongA, kM, kThreads>;
-    using B = Stage<kAlongB, kN, kThreads>;
+    using A = Stage<kAlongA, kM, kThreads, false>;
+    using B = Stage<kAlongB, kN, kThreads, kBlockedB>;
     static constexpr int kLoads = A::kLoads + B::kLoads;
     static_assert(kWM * kWN * 16 * kTM * 2 <= A::kBytes, "hand_out's rows");
     static constexpr int kLdsA = kSlotsA * A::kBytes, kLds = kLdsA + kSlotsB * B::kBytes;
@@ -624,7 +634,9 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
             return u2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
         },
         [&](uint32_t n, uint32_t m, const gran& q) {
-            *reinterpret_cast<gran*>((char*)a.p + ((n1 + (int64_t)n) * a.ld_p + m0 + G::wave_m() + m) * 2) = q;
+            const int64_t v = m0 + G::wave_m() + m, row = n1 + (int64_t)n;
+            const int64_t at = kN >= kDepth ? (v >> 6) * a.block_p + row * kDepth + (v & 63) : row * a.ld_p + v;
+            *reinterpret_cast<gran*>((char*)a.p + at * 2) = q;
         });
 }
 
@@ -639,7 +651,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
 // Where one split sums them all, the last piece's launch writes dh itself.
 template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last) {
-    using G = Tile<T, false, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
+    using G = Tile<T, false, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB, (kN >= kDepth)>;
     SCAPE_SLOTS(G);
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
@@ -653,7 +665,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
     G g;
     if (k0 < k1) {
         g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, (int32_t)a.dim, all},
-              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.ld_p}, m0, n0, k0, k1, slots);
+              Side{a.p, (int32_t)a.ld_p, (int32_t)a.rows_pad, (int32_t)a.piece, (int32_t)a.block_p}, m0, n0, k0, k1, slots);
     } else {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
@@ -728,16 +740,16 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
 }
 
 // dw of a piece.
-template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB, bool kBlocked>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, false, false, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
+    using G = Tile<T, false, false, kM, kN, kWM, kWN, kSlotsA, kSlotsB, kBlocked>;
     SCAPE_SLOTS(G);
     uint32_t tm, tn;
     tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     G g;
     g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
-          Side{a.p, (int32_t)a.ld_p, (int32_t)a.ld_p, (int32_t)a.rows_pad}, m0, n0, 0, (int32_t)a.rows, slots);
+          Side{a.p, (int32_t)a.ld_p, (int32_t)a.piece, (int32_t)a.rows_pad, (int32_t)a.block_p}, m0, n0, 0, (int32_t)a.rows, slots);
     const float c = a.dw_scale[0];
     G::hand_out(
         slots.a[0],
@@ -821,8 +833,9 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         }
         if (a.dw) {
             const int64_t t = a.dw_tile, n = (a.dim + t - 1) / t * ((v1 - v0 + t - 1) / t);
-            if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2>), n, 256, a, v0, v1);
-            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 2, 2>), n, 512, a, v0, v1);
+            if (a.tile_n < kDepth) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2, false>), n, 256, a, v0, v1);
+            else if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2, true>), n, 256, a, v0, v1);
+            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 2, 2, true>), n, 512, a, v0, v1);
         }
     }
     if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows * ((a.dim + kJoinWidth - 1) / kJoinWidth), kRowThreads, a);

@@ -256,8 +256,9 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
     return SCAPE_OK;
 }
 // The pieces of the backward pass: P of one is at most 2^27 elements, and at
-// least 4096 words wide, so that dw has tiles for the CUs.  P's rows lie a
-// little further apart than a piece's words, off the powers of two.
+// least 4096 words wide, so that dw has tiles for the CUs.  P lies in blocks of
+// 64 words, [words / 64][rows_pad][64], so that what a step of either product
+// takes is one run of memory or four; fewer rows than a step's lie as rows.
 // dh's sums are split over the words where its tiles leave CUs idle: the number
 // of splits is the one with the least rounds of tiles on the CUs times a split's
 // steps (and about 6 more for its start and its end), counting the splits'
@@ -267,7 +268,8 @@ void vocab_pieces(VocabArgs* a) {
     if (most < 4096) most = 4096;
     const int64_t pieces = (a->cols + most - 1) / most;
     a->piece = round_up((a->cols + pieces - 1) / pieces, 256);
-    a->ld_p = a->piece + 64;
+    a->ld_p = a->tile_n >= 64 ? 64 : a->piece;
+    a->block_p = a->rows_pad * 64;
     const int64_t tiles = (a->dim + a->dh_tile - 1) / a->dh_tile * (a->tiles_n ? a->tiles_n : 1);
     const int64_t slots = a->tile_n <= 32 ? 1024 : a->tile_n <= 64 ? 768 : a->tile_n <= 128 ? 512 : 256;  // as LDS holds
     int64_t best = INT64_MAX;
@@ -295,7 +297,7 @@ VocabParts vocab_parts(const VocabArgs& a) {
     w.dw_scale = w.row + a.rows_pad * (int64_t)sizeof(VocabRow);
     w.h_copy = w.dw_scale + 16;
     w.p = w.h_copy + a.rows * a.dim * 2;
-    w.dh_sum = w.p + a.rows_pad * a.ld_p * 2;
+    w.dh_sum = w.p + a.rows_pad * a.piece * 2;
     w.all = a.rows ? w.dh_sum + (int64_t)a.splits * a.rows * a.dim * 4 : 0;
     return w;
 }

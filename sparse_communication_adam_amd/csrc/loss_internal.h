@@ -162,13 +162,14 @@ struct VocabArgs {
     void* dw;             // or NULL
     int64_t ld_dh, ld_dw;
     int64_t rows_pad;     // whole tiles of tokens
-    int64_t piece, ld_p;  // words of a piece, and P's row
+    int64_t piece;        // words of a piece
+    int64_t ld_p, block_p;  // P: from a row to the next, and from 64 words to the next 64
     int64_t split_words;  // words of a split of dh's sum, a multiple of 64
     int32_t splits;
     VocabRow* row;        // [rows_pad]
     float* dw_scale;      // [1]
     void* h_copy;         // [rows][dim]
-    void* p;              // [rows_pad][ld_p]
+    void* p;              // rows_pad x piece
     float* dh_sum;        // [splits][rows][dim]
 };
 hipError_t launch_vocab_loss(hipStream_t s, const VocabArgs& a);
