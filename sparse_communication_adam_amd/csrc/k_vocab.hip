@@ -383,19 +383,20 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
     uint32_t tm, tn;
     tile_of(xcd_block(blockIdx.x, gridDim.x), a.tiles_v, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
+    const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
+    int32_t label[G::kFN];  // loaded ahead of the products
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) label[j] = n0 + (int32_t)ln + j * 16 < a.rows ? a.label[n0 + (int32_t)ln + j * 16] : -1;
     G g;
     g.run(Side{a.w, (int32_t)a.ld_w, (int32_t)a.cols, (int32_t)a.dim}, Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0,
           (int32_t)a.dim, (lds_t*)lds);
     // the loop's last barrier is behind every read of the tiles
     float2* const red = reinterpret_cast<float2*>(lds);  // [kWM][kN]
-    const uint32_t lm = G::wave_m() + G::lane_m(), ln = G::wave_n() + G::lane_n();
     const int32_t left = (int32_t)a.cols - m0 - (int32_t)lm;  // words from the lane's first on
     const bool ragged = a.cols - m0 < kM;
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
-        const int64_t n = n0 + ln + j * 16;
-        const bool row = n < a.rows;
-        const int32_t label = row ? a.label[n] : -1, lab = label - m0 - (int32_t)lm;  // of the lane's words
+        const int32_t lab = label[j] - m0 - (int32_t)lm;  // of the lane's words
         if (ragged) {
 #pragma unroll
             for (int i = 0; i < G::kFM; ++i)
@@ -427,13 +428,13 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_sums(VocabArgs a) {
         sum += __shfl_xor(sum, 16, 64);
         sum += __shfl_xor(sum, 32, 64);
         if (lane_id() < 16) red[(G::wave_m() / G::kTM) * kN + ln + j * 16] = float2{ref, sum};
-        if (label >= 0 && lab >= 0 && lab < G::kTM && (lab & 15) < 4 && lab < left) {
+        if (label[j] >= 0 && lab >= 0 && lab < G::kTM && (lab & 15) < 4 && lab < left) {
             float at = 0.0f;
 #pragma unroll
             for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) at = lab == i * 16 + e ? g.acc[i][j][e] : at;
-            a.at_label[n] = at;
+            a.at_label[n0 + (int64_t)ln + j * 16] = at;
         }
     }
     __syncthreads();
@@ -531,22 +532,25 @@ __device__ __forceinline__ int top_exponent(const VocabArgs& a, int* scratch) {
     for (int i = 0; i < kThreads / 64; ++i) best = scratch[i] > best ? scratch[i] : best;
     return best;
 }
-__device__ __forceinline__ void put_dw_scale(const VocabArgs& a, int best) {
-    a.dw_scale[0] = a.dtype == SCAPE_DTYPE_F16 && best > kNoExponent ? ldexpf(1.0f, best - 15) : 1.0f;
+__device__ __forceinline__ float dw_scale_of(const VocabArgs& a, int best) {
+    return a.dtype == SCAPE_DTYPE_F16 && best > kNoExponent ? ldexpf(1.0f, best - 15) : 1.0f;
 }
-__device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n, int best) {
-    VocabRow r{0.0f, 0.0f, 0.0f, 0.0f};
+// What a row of the copy of h is multiplied by; dividing powers of two is exact.
+__device__ __forceinline__ float copy_factor(const VocabRow& r, float dw_scale) {
+    return r.f == 0.0f ? 0.0f : dw_scale != 0.0f && __builtin_isfinite(r.f) ? r.dh / dw_scale : 1.0f;
+}
+__device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n) {
+    VocabRow r{0.0f, 0.0f, -1, 0.0f};
     const float f = n < a.rows ? row_factor(a, n) : 0.0f;
     if (f != 0.0f) {
         r.lse2 = a.lse[n] * kLog2e;
         r.f = f;
+        r.label = a.label[n];
         r.dh = 1.0f;
-        r.copy = 1.0f;
         if (a.dtype == SCAPE_DTYPE_F16 && __builtin_isfinite(f)) {
             int e;
             r.f = frexpf(f, &e) * 32768.0f;
             r.dh = ldexpf(1.0f, e - 15);
-            r.copy = ldexpf(1.0f, e - best);
         }
     }
     return r;
@@ -554,8 +558,8 @@ __device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n, int be
 __global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
     __shared__ int scratch[16];
     const int best = top_exponent<1024>(a, scratch);
-    if (threadIdx.x == 0) put_dw_scale(a, best);
-    for (int64_t n = threadIdx.x; n < a.rows_pad; n += 1024) a.row[n] = row_of(a, n, best);
+    if (threadIdx.x == 0) a.dw_scale[0] = dw_scale_of(a, best);
+    for (int64_t n = threadIdx.x; n < a.rows_pad; n += 1024) a.row[n] = row_of(a, n);
 }
 
 // The rows of h that dw takes: zeros where a row does not count, whatever it
@@ -580,7 +584,7 @@ __device__ __forceinline__ void copy_row(const VocabArgs& a, int64_t n, float c)
 }
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
-    copy_row<T>(a, blockIdx.x, a.row[blockIdx.x].copy);
+    copy_row<T>(a, blockIdx.x, copy_factor(a.row[blockIdx.x], a.dw_scale[0]));
 }
 // Both for few rows, in one launch: a workgroup a row, each finds the largest
 // exponent for itself.
@@ -588,14 +592,14 @@ constexpr int64_t kFewRows = 512;
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_rows_copy(VocabArgs a) {
     __shared__ int scratch[kRowThreads / 64];
-    const int best = top_exponent<kRowThreads>(a, scratch);
+    const float dw_scale = dw_scale_of(a, top_exponent<kRowThreads>(a, scratch));
     const int64_t n = blockIdx.x;
-    const VocabRow r = row_of(a, n, best);
+    const VocabRow r = row_of(a, n);
     if (threadIdx.x == 0) {
         a.row[n] = r;
-        if (n == 0) put_dw_scale(a, best);
+        if (n == 0) a.dw_scale[0] = dw_scale;
     }
-    if (a.dw && n < a.rows) copy_row<T>(a, n, r.copy);
+    if (a.dw && n < a.rows) copy_row<T>(a, n, copy_factor(r, dw_scale));
 }
 
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
@@ -607,30 +611,44 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
     uint32_t tm, tn;
     tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
+    const int32_t lm = m0 + (int32_t)(G::wave_m() + G::lane_m()), left = v1 - v0 - lm;
+    const int32_t n1 = n0 + (int32_t)G::wave_n();
+    VocabRow r[G::kFN];  // loaded ahead of the products
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) r[j] = a.row[n1 + j * 16 + (int32_t)G::lane_n()];
     G g;
     g.run(Side{(const char*)a.w + v0 * a.ld_w * 2, (int32_t)a.ld_w, v1 - v0, (int32_t)a.dim},
           Side{a.h, (int32_t)a.ld_h, (int32_t)a.rows, (int32_t)a.dim}, m0, n0, 0, (int32_t)a.dim, (lds_t*)lds);
-    const int32_t lm = m0 + (int32_t)(G::wave_m() + G::lane_m()), left = v1 - v0 - lm;
-    const int32_t n1 = n0 + (int32_t)G::wave_n();
-    VocabRow r[G::kFN];
-    int32_t lab[G::kFN];
+    const bool ragged = v1 - v0 - m0 < kM;
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
-        const int32_t n = n1 + j * 16 + (int32_t)G::lane_n();
-        r[j] = a.row[n];
-        lab[j] = -1;  // a row that counts has one, and is a row of the matrix
-        if (r[j].f != 0.0f) lab[j] = a.label[n] - v0 - lm;
+        const int32_t lab = r[j].label - v0 - lm;  // of the lane's words
+        const bool on = r[j].f != 0.0f;            // else the row may hold anything
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = fast_exp2(__builtin_fmaf(g.acc[i][j][e], a.c2, -r[j].lse2));
+                g.acc[i][j][e] = on ? x : 0.0f;
+            }
+        if (on && lab >= 0 && lab < G::kTM && (lab & 15) < 4) {
+#pragma unroll
+            for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g.acc[i][j][e] -= lab == i * 16 + e ? 1.0f : 0.0f;
+        }
+        if (ragged) {
+#pragma unroll
+            for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i * 16 + e >= left) g.acc[i][j][e] = 0.0f;
+        }
     }
     G::hand_out(
         (lds_t*)lds,
         [&](int i, int j) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = fast_exp2(__builtin_fmaf(g.acc[i][j][e], a.c2, -r[j].lse2));
-                if (lab[j] == i * 16 + e) x -= 1.0f;
-                p[e] = r[j].f != 0.0f && i * 16 + e < left ? x * r[j].f : 0.0f;
-            }
+            const f4 p = g.acc[i][j] * r[j].f;
             return u2{T::down2(p[0], p[1]), T::down2(p[2], p[3])};
         },
         [&](uint32_t n, uint32_t m, const gran& q) {

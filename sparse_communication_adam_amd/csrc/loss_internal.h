@@ -137,7 +137,9 @@ hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a);
 // ---- k_vocab.hip
 constexpr int kSmallWords = 64, kSmallDims = 128;  // tiles of up to 128 tokens
 struct VocabRow {
-    float f, lse2, dh, copy;  // P's factor, log-sum-exp in base 2, dh's and h's powers of two (0: does not count)
+    float f, lse2;  // P's factor (0: does not count), log-sum-exp in base 2
+    int32_t label;
+    float dh;       // dh's power of two
 };
 struct VocabArgs {
     const void* h;
