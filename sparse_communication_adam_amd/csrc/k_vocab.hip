@@ -658,23 +658,74 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
         });
 }
 
-// A kernel's slots: objects of their own (the third is next to nothing where
-// there are two).  What leaves through LDS takes the first of A.
-#define SCAPE_SLOTS(G)                                                                                       \
-    __shared__ __attribute__((aligned(16))) char a0[G::A::kBytes], a1[G::A::kBytes], b0[G::B::kBytes], b1[G::B::kBytes]; \
-    __shared__ __attribute__((aligned(16))) char a2[kSlotsA > 2 ? G::A::kBytes : 16], b2[kSlotsB > 2 ? G::B::kBytes : 16]; \
-    const typename G::Slots slots{{(lds_t*)a0, (lds_t*)a1, (lds_t*)a2}, {(lds_t*)b0, (lds_t*)b1, (lds_t*)b2}}
+// dw of a piece.
+template <class T, class G, int kM, int kN>
+__device__ __forceinline__ void dw_tile(const VocabArgs& a, const typename G::Slots& slots, uint32_t b, int32_t v0, int32_t v1) {
+    const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), nn = (uint32_t)(v1 - v0 + kN - 1) / kN;
+    uint32_t tm, tn;
+    tile_of(b, nm, nn, tm, tn);
+    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
+    G g;
+    g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
+          Side{a.p, (int32_t)a.ld_p, (int32_t)a.piece, (int32_t)a.rows_pad, (int32_t)a.block_p}, m0, n0, 0, (int32_t)a.rows, slots);
+    const float c = a.dw_scale[0];
+    G::hand_out(
+        slots.a[0],
+        [&](int i, int j) {
+            const f4 x = g.acc[i][j] * c;
+            return u2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
+        },
+        [&](uint32_t n, uint32_t d, const gran& q) {
+            const int64_t v = v0 + n0 + (int64_t)(G::wave_n() + n), col = m0 + G::wave_m() + d;
+            if (v < v1 && col < a.dim)
+                __builtin_nontemporal_store(q, reinterpret_cast<gran*>((char*)a.dw + (v * a.ld_dw + col) * 2));
+        });
+}
+
+// The slots are objects of their own, so that the compiler knows what is read to
+// be none of what is loaded meanwhile (one that is not there is next to nothing).
+template <class T, int kM, int kN, int kWM, int kWN>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
+    using G = Tile<T, false, false, kM, kN, kWM, kWN, 2, 2, true>;
+    __shared__ __attribute__((aligned(16))) char a0[G::A::kBytes], a1[G::A::kBytes], b0[G::B::kBytes], b1[G::B::kBytes];
+    const typename G::Slots slots{{(lds_t*)a0, (lds_t*)a1, nullptr}, {(lds_t*)b0, (lds_t*)b1, nullptr}};
+    dw_tile<T, G, kM, kN>(a, slots, xcd_block(blockIdx.x, gridDim.x), v0, v1);
+}
 
 // dh of a piece: [split][rows][dim] sums in float32, split over the words.
 // Where one split sums them all, the last piece's launch writes dh itself.
-template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last) {
+// kBoth: and dw, for few tokens, eight workgroups of the one (one an XCD) and
+// eight of the other in turn: dh reads the head's weights while dw writes as much
+// (bf16 us, in two launches and in one: 7x50304x1024 77 and 64, 24x32000x2048 100
+// and 87, 64x50304x1024 91 and 73; from 65 tokens on the two take each other's
+// caches, 512x32000x2048 212 and 236).
+template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB, bool kBoth>
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_t v0, int32_t v1, bool first, bool last, uint32_t n_dh,
+                                                             uint32_t n_dw) {
     using G = Tile<T, false, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB, (kN >= kDepth)>;
-    SCAPE_SLOTS(G);
+    __shared__ __attribute__((aligned(16))) char a0[G::A::kBytes], a1[G::A::kBytes], b0[kBoth ? G::A::kBytes : G::B::kBytes], b1[G::B::kBytes];
+    __shared__ __attribute__((aligned(16))) char a2[kSlotsA > 2 ? G::A::kBytes : 16], b2[kSlotsB > 2 ? G::B::kBytes : 16];
+    const typename G::Slots slots{{(lds_t*)a0, (lds_t*)a1, (lds_t*)a2}, {(lds_t*)b0, (lds_t*)b1, (lds_t*)b2}};
+    uint32_t at = blockIdx.x, of_them = gridDim.x;
+    if constexpr (kBoth) {
+        using W = Tile<T, false, false, kM, kM, 2, 2, 2, 2, (kN >= kDepth)>;
+        static_assert(W::kThreads == G::kThreads && W::A::kBytes == G::A::kBytes && W::B::kBytes == G::A::kBytes && kSlotsA == 3, "");
+        const uint32_t g = at / kXcds, gh = (n_dh + kXcds - 1) / kXcds, gw = (n_dw + kXcds - 1) / kXcds, both = gh < gw ? gh : gw;
+        const bool of_dh = g < 2 * both ? (g & 1) == 0 : gh > gw;
+        at = (g < 2 * both ? g / 2 : g - both) * kXcds + at % kXcds;
+        of_them = of_dh ? n_dh : n_dw;
+        if (at >= of_them) return;
+        if (!of_dh) {
+            const typename W::Slots w{{(lds_t*)a0, (lds_t*)a1, nullptr}, {(lds_t*)b0, (lds_t*)a2, nullptr}};
+            dw_tile<T, W, kM, kM>(a, w, xcd_block(at, of_them), v0, v1);
+            return;
+        }
+    }
+    // a split's tiles, which share its words, on one XCD
+    const uint32_t b = xcd_block(at, of_them);
     uint32_t tm, tn;
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), tiles = nm * a.tiles_n;
-    // a split's tiles, which share its words, on one XCD
-    const uint32_t b = xcd_block(blockIdx.x, gridDim.x), split = __builtin_amdgcn_readfirstlane(b / tiles);
+    const uint32_t split = __builtin_amdgcn_readfirstlane(b / tiles);
     tile_of(b - split * tiles, nm, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     const int32_t part = (int32_t)a.split_words, k0 = (int32_t)split * part, all = v1 - v0;
@@ -757,31 +808,6 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_dh_join(VocabArgs a) {
     *reinterpret_cast<gran*>((char*)a.dh + (n * a.ld_dh + at) * 2) = T::down(f);
 }
 
-// dw of a piece.
-template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB, bool kBlocked>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dw(VocabArgs a, int32_t v0, int32_t v1) {
-    using G = Tile<T, false, false, kM, kN, kWM, kWN, kSlotsA, kSlotsB, kBlocked>;
-    SCAPE_SLOTS(G);
-    uint32_t tm, tn;
-    tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)((a.dim + kM - 1) / kM), (uint32_t)(v1 - v0 + kN - 1) / kN, tm, tn);
-    const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
-    G g;
-    g.run(Side{a.h_copy, (int32_t)a.dim, (int32_t)a.dim, (int32_t)a.rows},
-          Side{a.p, (int32_t)a.ld_p, (int32_t)a.piece, (int32_t)a.rows_pad, (int32_t)a.block_p}, m0, n0, 0, (int32_t)a.rows, slots);
-    const float c = a.dw_scale[0];
-    G::hand_out(
-        slots.a[0],
-        [&](int i, int j) {
-            const f4 x = g.acc[i][j] * c;
-            return u2{T::down2(x[0], x[1]), T::down2(x[2], x[3])};
-        },
-        [&](uint32_t n, uint32_t d, const gran& q) {
-            const int64_t v = v0 + n0 + (int64_t)(G::wave_n() + n), col = m0 + G::wave_m() + d;
-            if (v < v1 && col < a.dim)
-                __builtin_nontemporal_store(q, reinterpret_cast<gran*>((char*)a.dw + (v * a.ld_dw + col) * 2));
-        });
-}
-
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_zero(VocabArgs a) {  // dw of no rows
     gran* to = reinterpret_cast<gran*>((char*)a.dw + (int64_t)blockIdx.x * a.ld_dw * 2);
@@ -809,15 +835,31 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_zero(VocabArgs a) {  // d
         case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;            \
         default: SCAPE_RUN((kernel<T, 256, 256, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;             \
     }
-#define SCAPE_DH_BY_TILE(kernel, blocks, ...)                                                             \
-    switch (a.tile_n) {                                                                                   \
-        case 16: SCAPE_RUN((kernel<T, kSmallDims, 16, 4, 1, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
-        case 32: SCAPE_RUN((kernel<T, kSmallDims, 32, 4, 1, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
-        case 64: SCAPE_RUN((kernel<T, kSmallDims, 64, 2, 2, 3, 3>), blocks, 256, __VA_ARGS__); break;      \
-        case 128: SCAPE_RUN((kernel<T, kSmallDims, 128, 2, 2, 2, 2>), blocks, 256, __VA_ARGS__); break;    \
-        case 192: SCAPE_RUN((kernel<T, 256, 192, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;           \
-        default: SCAPE_RUN((kernel<T, 256, 256, 2, 4, 3, 2>), blocks, 512, __VA_ARGS__); break;            \
+// Both gradients of a piece.
+template <class T>
+void back_of(hipStream_t s, const VocabArgs& a, int32_t v0, int32_t v1, bool first, bool last) {
+    const int64_t across = (a.dim + a.dh_tile - 1) / a.dh_tile;
+    const int64_t n_dh = a.dh ? across * a.tiles_n * a.splits : 0;
+    const int64_t n_dw = a.dw ? across * ((v1 - v0 + a.dh_tile - 1) / a.dh_tile) : 0;
+    const uint32_t nh = (uint32_t)n_dh, nw = (uint32_t)n_dw;
+    if (a.tile_n <= 64) {
+        const int64_t n = ((n_dh + kXcds - 1) / kXcds + (n_dw + kXcds - 1) / kXcds) * kXcds;
+        if (n == 0) return;
+        if (a.tile_n == 16) SCAPE_RUN((k_vocab_dh<T, kSmallDims, 16, 4, 1, 3, 3, true>), n, 256, a, v0, v1, first, last, nh, nw);
+        else if (a.tile_n == 32) SCAPE_RUN((k_vocab_dh<T, kSmallDims, 32, 4, 1, 3, 3, true>), n, 256, a, v0, v1, first, last, nh, nw);
+        else SCAPE_RUN((k_vocab_dh<T, kSmallDims, 64, 2, 2, 3, 3, true>), n, 256, a, v0, v1, first, last, nh, nw);
+        return;
     }
+    if (n_dh) {
+        if (a.tile_n == 128) SCAPE_RUN((k_vocab_dh<T, kSmallDims, 128, 2, 2, 2, 2, false>), n_dh, 256, a, v0, v1, first, last, nh, nw);
+        else if (a.tile_n == 192) SCAPE_RUN((k_vocab_dh<T, 256, 192, 2, 4, 3, 2, false>), n_dh, 512, a, v0, v1, first, last, nh, nw);
+        else SCAPE_RUN((k_vocab_dh<T, 256, 256, 2, 4, 3, 2, false>), n_dh, 512, a, v0, v1, first, last, nh, nw);
+    }
+    if (n_dw) {
+        if (a.tile_n == 128) SCAPE_RUN((k_vocab_dw<T, kSmallDims, kSmallDims, 2, 2>), n_dw, 256, a, v0, v1);
+        else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4>), n_dw, 512, a, v0, v1);
+    }
+}
 
 template <class T>
 hipError_t sums_of(hipStream_t s, const VocabArgs& a) {
@@ -845,16 +887,7 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         const bool first = v0 == 0, last = v1 == cols;
         const int64_t tiles = (int64_t)((v1 - v0 + a.tile_m - 1) / a.tile_m) * a.tiles_n;
         SCAPE_LOGITS_BY_TILE(k_vocab_p, tiles, a, v0, v1);
-        if (a.dh) {
-            const int64_t n = (a.dim + a.dh_tile - 1) / a.dh_tile * a.tiles_n * a.splits;
-            SCAPE_DH_BY_TILE(k_vocab_dh, n, a, v0, v1, first, last);
-        }
-        if (a.dw) {
-            const int64_t t = a.dw_tile, n = (a.dim + t - 1) / t * ((v1 - v0 + t - 1) / t);
-            if (a.tile_n < kDepth) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2, false>), n, 256, a, v0, v1);
-            else if (t == 128) SCAPE_RUN((k_vocab_dw<T, 128, 128, 2, 2, 2, 2, true>), n, 256, a, v0, v1);
-            else SCAPE_RUN((k_vocab_dw<T, 256, 256, 2, 4, 2, 2, true>), n, 512, a, v0, v1);
-        }
+        back_of<T>(s, a, v0, v1, first, last);
     }
     if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows * ((a.dim + kJoinWidth - 1) / kJoinWidth), kRowThreads, a);
     return hipGetLastError();

@@ -249,7 +249,6 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
     const bool small = a->tile_n <= 128;
     a->tile_m = small ? kSmallWords : 256;
     a->dh_tile = small ? kSmallDims : 256;
-    a->dw_tile = rows <= 192 ? 128 : 256;  // 200x32000x2048 bf16 alike, 333x50257x1536 f16 259 and 270 us
     a->tiles_v = (uint32_t)((cols + a->tile_m - 1) / a->tile_m);
     a->tiles_n = (uint32_t)((rows + a->tile_n - 1) / a->tile_n);
     a->rows_pad = (int64_t)a->tiles_n * a->tile_n;
@@ -262,7 +261,11 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
 // dh's sums are split over the words where its tiles leave CUs idle: the number
 // of splits is the one with the least rounds of tiles on the CUs times a split's
 // steps (and about 6 more for its start and its end), counting the splits'
-// sums, which are written and read once more, at a step for each 8 MB.
+// sums, which are written and read once more, at a step for each 8 MB.  Beside
+// dw, in one launch (up to 64 tokens), 128 workgroups are best where the tiles
+// divide them, and three times as many where not (gradient us with 128 and 384
+// of them: 7x50304x1024 64 and 67, 64x32000x2048 96 and 108, but 50x50257x1536
+// 129 and 121); alone as many as LDS holds.
 void vocab_pieces(VocabArgs* a) {
     int64_t most = a->rows_pad ? (int64_t(1) << 27) / a->rows_pad / 256 * 256 : a->cols;
     if (most < 4096) most = 4096;
@@ -271,7 +274,7 @@ void vocab_pieces(VocabArgs* a) {
     a->ld_p = a->tile_n >= 64 ? 64 : a->piece;
     a->block_p = a->rows_pad * 64;
     const int64_t tiles = (a->dim + a->dh_tile - 1) / a->dh_tile * (a->tiles_n ? a->tiles_n : 1);
-    const int64_t slots = a->tile_n <= 32 ? 1024 : a->tile_n <= 64 ? 768 : a->tile_n <= 128 ? 512 : 256;  // as LDS holds
+    const int64_t slots = a->tile_n <= 64 ? (128 % tiles == 0 ? 128 : 384) : a->tile_n <= 128 ? 512 : 256;
     int64_t best = INT64_MAX;
     for (int64_t n = 1; n <= 128 && (n == 1 || a->piece / n >= 256); ++n) {
         const int64_t words = round_up((a->piece + n - 1) / n, 64), splits = (a->piece + words - 1) / words;

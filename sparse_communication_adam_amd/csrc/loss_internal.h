@@ -151,7 +151,7 @@ struct VocabArgs {
     const float* weight;  // or NULL
     float scale, c2;      // c2 = scale * log2(e)
     int32_t tile_m, tile_n;    // words and tokens of a tile of the logits
-    int32_t dh_tile, dw_tile;  // columns of a tile of dh, columns and words of one of dw
+    int32_t dh_tile;           // columns of a tile of dh; columns and words of one of dw
     uint32_t tiles_v, tiles_n;
     // forward
     float* loss;
