@@ -155,8 +155,11 @@ __global__ __launch_bounds__(kBlock) void k_expert_place(SortArgs a) {
 // ---------------------------------------------------------------------------
 // The moves.  A wave takes a token.  Its places and weights are loaded once, a
 // lane each, and handed round as scalars.  Rows lie anywhere: 16 bytes at a time
-// from their first element, at whatever alignment, and the rest one element a
-// lane.  Lanes behind a row's last granule load it again and store nothing.
+// from their first element, at whatever alignment.  Of a row that is no whole
+// number of granules the last one ends with the row and repeats elements of the
+// one before it, which get the same values twice (16384x257 f16, k = 8, one
+// element a lane instead: combine 29 us).  Lanes behind a row's last granule load
+// it again and store nothing.  Rows of less than a granule go an element a lane.
 
 typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ gran read16(const void* row, uint32_t byte) {
@@ -193,27 +196,54 @@ __device__ __forceinline__ int64_t token_of_wave() {
     return (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
-// A row in granules: kB at a time for each lane.
+// A row's granules: how many, and where the last one begins.
+struct Span {
+    int64_t granules;
+    uint32_t last;
+};
+template <class T>
+__device__ __forceinline__ Span span_of(const MoveArgs& a) {
+    constexpr uint32_t kSize = 16 / T::kN;
+    return a.dim < T::kN ? Span{0, 0} : Span{(a.dim + T::kN - 1) / T::kN, (uint32_t)a.dim * kSize - 16u};
+}
+// kB granules at a time for each lane.
 template <class T, int kB>
 struct Row {
-    using raw = typename T::raw;
-    static __device__ __forceinline__ uint32_t byte(int64_t whole, int64_t i) {  // of granule i, or of the last
-        return (uint32_t)(i < whole ? i : whole - 1) * 16u;
+    static __device__ __forceinline__ uint32_t byte(const Span& s, int64_t i) {  // of granule i, or of the last
+        const uint32_t b = (uint32_t)i * 16u;
+        return b < s.last ? b : s.last;
     }
-    static __device__ __forceinline__ void load(gran (&g)[kB], const void* row, int64_t whole, int64_t i0) {
+    static __device__ __forceinline__ void load(gran (&g)[kB], const void* row, const Span& s, int64_t i0) {
 #pragma unroll
-        for (int b = 0; b < kB; ++b) g[b] = read16(row, byte(whole, i0 + b * 64));
+        for (int b = 0; b < kB; ++b) g[b] = read16(row, byte(s, i0 + b * 64));
     }
-    static __device__ __forceinline__ void load_again(gran (&g)[kB], const void* row, int64_t whole, int64_t i0) {
+    static __device__ __forceinline__ void load_again(gran (&g)[kB], const void* row, const Span& s, int64_t i0) {
 #pragma unroll
-        for (int b = 0; b < kB; ++b) g[b] = read16_again(row, byte(whole, i0 + b * 64));
+        for (int b = 0; b < kB; ++b) g[b] = read16_again(row, byte(s, i0 + b * 64));
     }
-    static __device__ __forceinline__ void store(const gran (&g)[kB], void* row, int64_t whole, int64_t i0) {
+    static __device__ __forceinline__ void store(const gran (&g)[kB], void* row, const Span& s, int64_t i0) {
 #pragma unroll
         for (int b = 0; b < kB; ++b)
-            if (i0 + b * 64 < whole) write16(row, (uint32_t)(i0 + b * 64) * 16u, g[b]);
+            if (i0 + b * 64 < s.granules) write16(row, byte(s, i0 + b * 64), g[b]);
     }
 };
+// g . d of granule i, without what the granule before the last has of it.
+template <class T>
+__device__ __forceinline__ float dot_of(const gran& g, const gran& d, const Span& s, int64_t i) {
+    float part = 0.0f;
+    if (s.last + 16u == (uint32_t)s.granules * 16u) {
+#pragma unroll
+        for (int e = 0; e < T::kN; ++e) part = __builtin_fmaf(T::up(g, e), T::up(d, e), part);
+    } else {
+        const uint32_t back = i + 1 == s.granules ? (uint32_t)i * 16u - s.last : 0u;
+#pragma unroll
+        for (int e = 0; e < T::kN; ++e) {
+            const bool first = (uint32_t)e * (16 / T::kN) >= back;
+            part = __builtin_fmaf(first ? T::up(g, e) : 0.0f, first ? T::up(d, e) : 0.0f, part);
+        }
+    }
+    return i < s.granules ? part : 0.0f;
+}
 
 // kB granules of the token are in registers while they go to its places.
 template <class T, int kB>
@@ -224,24 +254,24 @@ __global__ __launch_bounds__(kBlock) void k_expert_gather(MoveArgs a) {
     if (t >= a.tokens) return;
     const raw* const x = static_cast<const raw*>(a.x) + t * a.ld_x;
     raw* const y = static_cast<raw*>(a.y);
-    const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
+    const Span s = span_of<T>(a);
     Held h;
     for (int32_t j0 = 0; j0 < a.k; j0 += 64) {
         h.load(a, t, j0);
         const int n = a.k - j0 < 64 ? a.k - j0 : 64;
-        for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+        for (int64_t i = lane; i - lane < s.granules; i += 64 * kB) {
             gran g[kB];
-            Row<T, kB>::load_again(g, x, whole, i);
+            Row<T, kB>::load_again(g, x, s, i);
             for (int j = 0; j < n; ++j) {
                 const int64_t r = h.place(j);
-                if (r >= 0) Row<T, kB>::store(g, y + r * a.ld_y, whole, i);
+                if (r >= 0) Row<T, kB>::store(g, y + r * a.ld_y, s, i);
             }
         }
-        if (whole * T::kN < a.dim) {
-            const raw v = rest < a.dim ? x[rest] : (raw)0;
+        if (s.granules == 0 && lane < a.dim) {
+            const raw v = x[lane];
             for (int j = 0; j < n; ++j) {
                 const int64_t r = h.place(j);
-                if (r >= 0 && rest < a.dim) y[r * a.ld_y + rest] = v;
+                if (r >= 0) y[r * a.ld_y + lane] = v;
             }
         }
     }
@@ -258,10 +288,10 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
     if (t >= a.tokens) return;
     raw* const out = static_cast<raw*>(a.out) + t * a.ld_out;
     const raw* const y = static_cast<const raw*>(a.y);
-    const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
+    const Span span = span_of<T>(a);
     Held h;
     if (a.k <= 64) h.load(a, t, 0);
-    for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+    for (int64_t i = lane; i - lane < span.granules; i += 64 * kB) {
         float s[kB][T::kN];
 #pragma unroll
         for (int b = 0; b < kB; ++b)
@@ -279,7 +309,7 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
                 const void* const row = on ? static_cast<const void*>(y + r * a.ld_y) : &g_no_granule;
                 if (!on) w[j] = 0.0f;
 #pragma unroll
-                for (int b = 0; b < kB; ++b) g[j][b] = read16(row, on ? Row<T, kB>::byte(whole, i + b * 64) : 0u);
+                for (int b = 0; b < kB; ++b) g[j][b] = read16(row, on ? Row<T, kB>::byte(span, i + b * 64) : 0u);
             }
 #pragma unroll
             for (int j = 0; j < kJ; ++j)
@@ -290,18 +320,18 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b)
-            if (i + b * 64 < whole) write16(out, (uint32_t)(i + b * 64) * 16u, T::down(s[b]));
+            if (i + b * 64 < span.granules) write16(out, Row<T, kB>::byte(span, i + b * 64), T::down(s[b]));
     }
-    if (whole * T::kN < a.dim) {
+    if (span.granules == 0) {
         float s = 0.0f;
         for (int32_t j = 0; j < a.k; ++j) {
             if ((a.k > 64 && (j & 63) == 0)) h.load(a, t, j);
             const int64_t r = h.place(j & 63);
             const float w = h.factor(j & 63);
-            if (r < 0 || w == 0.0f || rest >= a.dim) continue;
-            s = __builtin_fmaf(w, T::up1(y[r * a.ld_y + rest]), s);
+            if (r < 0 || w == 0.0f || lane >= a.dim) continue;
+            s = __builtin_fmaf(w, T::up1(y[r * a.ld_y + lane]), s);
         }
-        if (rest < a.dim) out[rest] = T::down1(s);
+        if (lane < a.dim) out[lane] = T::down1(s);
     }
 }
 
@@ -320,11 +350,11 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
     const raw* const dout = static_cast<const raw*>(a.x) + t * a.ld_x;
     const raw* const y = static_cast<const raw*>(a.y_in);
     raw* const dy = static_cast<raw*>(a.y);
-    const int64_t whole = a.dim / T::kN, rest = whole * T::kN + lane;
-    const bool held = whole <= 64 * kB, tail = whole * T::kN < a.dim;
+    const Span s = span_of<T>(a);
+    const bool held = s.granules <= 64 * kB, tiny = s.granules == 0 && lane < a.dim;
     gran d[kB];
-    if (held && whole) Row<T, kB>::load_again(d, dout, whole, lane);
-    const float last = tail && rest < a.dim ? T::up1(dout[rest]) : 0.0f;
+    if (held && s.granules) Row<T, kB>::load_again(d, dout, s, lane);
+    const float last = tiny ? T::up1(dout[lane]) : 0.0f;
     Held h;
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int32_t j = wave; j < a.k; j += kWaves) {
@@ -336,10 +366,10 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
         }
         const float w = h.factor(j & 63);
         float dot = 0.0f;
-        for (int64_t i = lane; i - lane < whole; i += 64 * kB) {
+        for (int64_t i = lane; i - lane < s.granules; i += 64 * kB) {
             gran g[kB];
-            if (a.dweight) Row<T, kB>::load(g, y + r * a.ld_y_in, whole, i);
-            if (!held) Row<T, kB>::load_again(d, dout, whole, i);
+            if (a.dweight) Row<T, kB>::load(g, y + r * a.ld_y_in, s, i);
+            if (!held) Row<T, kB>::load_again(d, dout, s, i);
             if (dy) {
                 gran v[kB];
 #pragma unroll
@@ -349,21 +379,16 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
                     for (int e = 0; e < T::kN; ++e) f[e] = w != 0.0f ? w * T::up(d[b], e) : 0.0f;
                     v[b] = T::down(f);
                 }
-                Row<T, kB>::store(v, dy + r * a.ld_y, whole, i);
+                Row<T, kB>::store(v, dy + r * a.ld_y, s, i);
             }
             if (a.dweight) {
 #pragma unroll
-                for (int b = 0; b < kB; ++b) {
-                    float part = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < T::kN; ++e) part = __builtin_fmaf(T::up(g[b], e), T::up(d[b], e), part);
-                    dot += i + b * 64 < whole ? part : 0.0f;
-                }
+                for (int b = 0; b < kB; ++b) dot += dot_of<T>(g[b], d[b], s, i + b * 64);
             }
         }
-        if (tail && rest < a.dim) {
-            if (a.dweight) dot = __builtin_fmaf(T::up1(y[r * a.ld_y_in + rest]), last, dot);
-            if (dy) dy[r * a.ld_y + rest] = T::down1(w != 0.0f ? w * last : 0.0f);
+        if (tiny) {
+            if (a.dweight) dot = T::up1(y[r * a.ld_y_in + lane]) * last;
+            if (dy) dy[r * a.ld_y + lane] = T::down1(w != 0.0f ? w * last : 0.0f);
         }
         if (a.dweight) {
             dot = group_reduce<OpSumF, 64>(dot);
@@ -372,8 +397,72 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine_back(MoveArgs a) {
     }
 }
 
+// Short rows: kL lanes take a choice, so that a wave has several on their way.
+template <class T, int kL>
+struct Choice {
+    int64_t c, t, r;  // the choice, its token and its place
+    uint32_t lane, byte;
+    float weight;
+    bool in, on, mine;  // in: there is one; on: it has a place; mine: the lane has a granule of it
+    __device__ __forceinline__ Choice(const MoveArgs& a, const Span& s) {
+        lane = threadIdx.x % kL;
+        c = (int64_t)blockIdx.x * (kBlock / kL) + threadIdx.x / kL;
+        in = c < a.tokens * a.k;
+        t = in ? (uint32_t)c / (uint32_t)a.k : 0;
+        r = in ? a.row[c] : -1;
+        weight = in && a.weight ? a.weight[c] : 1.0f;
+        on = r >= 0 && r < a.rows;
+        mine = on && lane < s.granules;
+        byte = Row<T, 1>::byte(s, lane);
+    }
+};
+template <class T, int kL>
+__global__ __launch_bounds__(kBlock) void k_expert_gather_rows(MoveArgs a) {
+    using raw = typename T::raw;
+    const Span s = span_of<T>(a);
+    const Choice<T, kL> q(a, s);
+    if (!q.mine) return;
+    const gran g = read16_again(static_cast<const raw*>(a.x) + q.t * a.ld_x, q.byte);
+    write16(static_cast<raw*>(a.y) + q.r * a.ld_y, q.byte, g);
+}
+template <class T, int kL>
+__global__ __launch_bounds__(kBlock) void k_expert_back_rows(MoveArgs a) {
+    using raw = typename T::raw;
+    const Span s = span_of<T>(a);
+    const Choice<T, kL> q(a, s);
+    gran g = gran{0, 0, 0, 0}, d = g;
+    if (q.mine) {
+        d = read16_again(static_cast<const raw*>(a.x) + q.t * a.ld_x, q.byte);
+        if (a.dweight) g = read16(static_cast<const raw*>(a.y_in) + q.r * a.ld_y_in, q.byte);
+        if (a.y) {
+            float f[T::kN];
+#pragma unroll
+            for (int e = 0; e < T::kN; ++e) f[e] = q.weight != 0.0f ? q.weight * T::up(d, e) : 0.0f;
+            write16(static_cast<raw*>(a.y) + q.r * a.ld_y, q.byte, T::down(f));
+        }
+    }
+    if (!a.dweight) return;
+    const float dot = group_reduce<OpSumF, kL>(dot_of<T>(g, d, s, q.lane));
+    if (q.in && q.lane == 0) a.dweight[q.c] = dot;
+}
+
 // Granules a lane: as many as a row has for it, up to four or eight.
-int granules_of(const MoveArgs& a) { return (int)((a.dim / (16 / dtype_size(a.dtype)) + 63) / 64); }
+int granules_of(const MoveArgs& a) {
+    const int64_t n = 16 / dtype_size(a.dtype);
+    return (int)(((a.dim + n - 1) / n + 63) / 64);
+}
+// Lanes for a choice of a short row, 0 where it is none (or where the choices'
+// threads do not fit a grid's axis).  The gradient of 16384 tokens, k =
+// 8, takes a wave a choice and so: 128 bf16 38.5 and 16.7 us, 100 f16 60 and 21,
+// 256 bf16 44.7 and 30.8; with all 64 lanes no less (512 bf16 54.5 and 58.2).
+int lanes_of(const MoveArgs& a) {
+    const int64_t n = 16 / dtype_size(a.dtype), granules = a.dim < n ? 33 : (a.dim + n - 1) / n;
+    for (int lanes = 8; lanes <= 32; lanes *= 2)
+        if (granules <= lanes) return a.tokens * a.k <= (int64_t(1) << 31) / lanes ? lanes : 0;
+    return 0;
+}
+#define SCAPE_RUN_ROWS(lanes, ...)                                                                                      \
+    hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)((a.tokens * a.k * lanes + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, a)
 
 #define SCAPE_RUN(...) \
     hipLaunchKernelGGL((__VA_ARGS__), dim3((uint32_t)((a.tokens + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a)
@@ -383,8 +472,11 @@ int granules_of(const MoveArgs& a) { return (int)((a.dim / (16 / dtype_size(a.dt
 
 template <class T>
 hipError_t gather_of(hipStream_t s, const MoveArgs& a) {
-    const int n = granules_of(a);
-    if (n <= 1) SCAPE_RUN(k_expert_gather<T, 1>);
+    const int n = granules_of(a), lanes = lanes_of(a);
+    if (lanes == 8) SCAPE_RUN_ROWS(8, k_expert_gather_rows<T, 8>);
+    else if (lanes == 16) SCAPE_RUN_ROWS(16, k_expert_gather_rows<T, 16>);
+    else if (lanes == 32) SCAPE_RUN_ROWS(32, k_expert_gather_rows<T, 32>);
+    else if (n <= 1) SCAPE_RUN(k_expert_gather<T, 1>);
     else if (n <= 2) SCAPE_RUN(k_expert_gather<T, 2>);
     else SCAPE_RUN(k_expert_gather<T, 4>);
     return hipGetLastError();
@@ -406,8 +498,11 @@ hipError_t combine_of(hipStream_t s, const MoveArgs& a) {
 }
 template <class T>
 hipError_t back_of(hipStream_t s, const MoveArgs& a) {
-    const int n = granules_of(a);
-    if (n <= 1) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 1>);
+    const int n = granules_of(a), lanes = lanes_of(a);
+    if (lanes == 8) SCAPE_RUN_ROWS(8, k_expert_back_rows<T, 8>);
+    else if (lanes == 16) SCAPE_RUN_ROWS(16, k_expert_back_rows<T, 16>);
+    else if (lanes == 32) SCAPE_RUN_ROWS(32, k_expert_back_rows<T, 32>);
+    else if (n <= 1) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 1>);
     else if (n <= 2) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 2>);
     else if (n <= 4) SCAPE_RUN_TOKEN(k_expert_combine_back<T, 4>);
     else SCAPE_RUN_TOKEN(k_expert_combine_back<T, 8>);

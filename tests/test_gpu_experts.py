@@ -188,6 +188,13 @@ def test_moves(sc, tokens, k, experts, dim, pad, shift, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("dim", [4, 9, 31, 33, 64, 65, 100, 129, 249, 257, 500, 513, 1025, 2047, 4101, 8195, 512, 1536])
+def test_row_lengths(sc, dim, dtype):
+    """Rows on either side of each way they are cut: lanes for a choice, granules a lane, a last granule that reaches back."""
+    _check_moves(sc, Case(sc, 37, 5, 8, dim, dtype, dim % 3, dim % 2, key="rows"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_what_does_not_count_holds_anything(sc, dtype):
     """NaN in rows that no place or only weights of 0 name; places outside y; a token without experts."""
     c = Case(sc, 40, 3, 8, 100, dtype, key="junk")
