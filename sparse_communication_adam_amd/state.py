@@ -64,8 +64,10 @@ class ScapeState:
         self.sparse = [torch.zeros(max(k, 1), **f32) for _ in range(W)]
         self.key = torch.zeros(n, dtype=torch.int32, device=device)
         self.masks = [alloc_mask(self.layout, device), alloc_mask(self.layout, device)]
-        self.grad_norm = None  # fp32 [W+1], made by the first clipped step
-        self._norm_ws = None
+        # made here, with the rest of the state: a clipped step may run on any
+        # stream, or be captured, and fills both anew
+        self.grad_norm = torch.zeros(W + 1, **f32)
+        self._norm_ws = torch.empty(scape_grad_norm_workspace_bytes(self.ctx), dtype=torch.uint8, device=device)
         self._cur = 0
         self.t = 0
 
@@ -97,16 +99,8 @@ class ScapeState:
         norm, clip = scape_grad_norm, scape_grad_clip
         if self.interleaved:
             norm, clip = scape_grad_norm_interleaved, scape_grad_clip_interleaved
-        self._clip_buffers()
         norm(self.ctx, grads, self.grad_norm, workspace=self._norm_ws, stream=stream)
         clip(self.ctx, grads, self.grad_norm, max_norm, shared=shared, stream=stream)
-
-    def _clip_buffers(self) -> None:
-        import torch
-        if self.grad_norm is None:
-            self.grad_norm = torch.zeros(self.cfg.workers + 1, dtype=torch.float32, device=self.m.device)
-            self._norm_ws = torch.empty(scape_grad_norm_workspace_bytes(self.ctx), dtype=torch.uint8,
-                                        device=self.m.device)
 
     def step(self, grads, stream=None, key_out: Optional[bool] = True, max_norm: Optional[float] = None,
              shared_norm: bool = False) -> None:
@@ -140,8 +134,6 @@ class ScapeState:
         if self.offload:
             raise ValueError("the offloaded step copies to and from host memory and is not captured")
         self._graph_grads = grads if self.interleaved else list(grads)
-        if max_norm is not None:
-            self._clip_buffers()  # outside the graphs' own memory
         graphs = []
         for cur in (0, 1):
             g = torch.cuda.CUDAGraph()
