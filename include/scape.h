@@ -674,7 +674,11 @@ int scape_vocab_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_
  * in h's type, rounded once.  Either may be NULL.  The vocabulary is taken in
  * pieces: the logits of a piece are made again and its P goes to the workspace
  * in h's type, from where both products take it; its rounding (half a step of 8
- * or 11 bits a term) is of the size of the gradients' own.  Rows that do not
+ * or 11 bits a term) is of the size of the gradients' own.  F16 has two limits
+ * besides: a p = exp(z - lse) below 2^-28 is off by up to 2^-39, and a term of dw
+ * by up to |p - [c = y]| * 2^-38 of the batch's largest |dloss weight scale h|
+ * (rows of dw are right to their last bits where the factors of the rows lie
+ * within about 2^24 of one another).  Rows that do not
  * count, or whose dloss is 0, get dh = 0 and add nothing to dw, whatever h
  * holds there.  rows = 0 writes dw = 0.  ld_dh and ld_dw are multiples of 8, dh
  * and dw 16-byte aligned; neither may overlap an input.

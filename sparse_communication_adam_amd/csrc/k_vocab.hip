@@ -507,46 +507,22 @@ __global__ __launch_bounds__(kJoinTokens* kJoinParts) void k_vocab_join(VocabArg
 // ---------------------------------------------------------------------------
 // The gradient.
 
-// Per row: the factor of its P, its log-sum-exp in base 2, and the powers of
-// two that stand beside an fp16 P.  bf16 has float32's range, so P takes the
-// whole factor; an fp16 P is (p - onehot) times a mantissa in [2^14, 2^15), so
-// that p keeps its bits down to 2^-29, and the power of two is put on dh
-// exactly and on the copy of h for dw against the largest of all rows.
+// Per row: the factor of its P, its log-sum-exp in base 2, and the power of two
+// that stands beside an fp16 P.  bf16 has float32's range, so P takes the whole
+// factor; an fp16 P is (p - onehot) times a mantissa in [2^14, 2^15), so that p
+// keeps its bits down to 2^-28, and the power of two is put on dh exactly and on
+// the copy of h that dw takes.
 __device__ __forceinline__ float row_factor(const VocabArgs& a, int64_t n) {
     const int32_t lab = a.label[n];
     if (lab < 0 || lab >= a.cols) return 0.0f;
     const float w = a.weight ? a.weight[n] : 1.0f, d = a.dloss ? a.dloss[n] : 1.0f;
     return w == 0.0f || d == 0.0f ? 0.0f : (float)((double)w * (double)d * (double)a.scale);
 }
-constexpr int kNoExponent = -10000;
-// The largest exponent of the rows' factors (fp16), by a whole workgroup.
-template <int kThreads>
-__device__ __forceinline__ int top_exponent(const VocabArgs& a, int* scratch) {
-    int best = kNoExponent;
-    if (a.dtype == SCAPE_DTYPE_F16)
-        for (int64_t n = threadIdx.x; n < a.rows; n += kThreads) {
-            const float f = row_factor(a, n);
-            if (f != 0.0f && __builtin_isfinite(f)) {
-                int e;
-                (void)frexpf(f, &e);
-                best = e > best ? e : best;
-            }
-        }
-    for (int d = 32; d >= 1; d >>= 1) {
-        const int o = __shfl_xor(best, d, 64);
-        best = o > best ? o : best;
-    }
-    if ((threadIdx.x & 63u) == 0) scratch[threadIdx.x >> 6] = best;
-    __syncthreads();
-    for (int i = 0; i < kThreads / 64; ++i) best = scratch[i] > best ? scratch[i] : best;
-    return best;
-}
-__device__ __forceinline__ float dw_scale_of(const VocabArgs& a, int best) {
-    return a.dtype == SCAPE_DTYPE_F16 && best > kNoExponent ? ldexpf(1.0f, best - 15) : 1.0f;
-}
-// What a row of the copy of h is multiplied by; dividing powers of two is exact.
-__device__ __forceinline__ float copy_factor(const VocabRow& r, float dw_scale) {
-    return r.f == 0.0f ? 0.0f : dw_scale != 0.0f && __builtin_isfinite(r.f) ? r.dh / dw_scale : 1.0f;
+__device__ __forceinline__ bool has_exponent(float f) { return f != 0.0f && __builtin_isfinite(f); }
+__device__ __forceinline__ int exponent_of(float f) {  // |f| < 2^e
+    int e;
+    (void)frexpf(f, &e);
+    return e;
 }
 __device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n) {
     VocabRow r{0.0f, 0.0f, -1, 0.0f};
@@ -564,21 +540,68 @@ __device__ __forceinline__ VocabRow row_of(const VocabArgs& a, int64_t n) {
     }
     return r;
 }
-// One workgroup: 8192 rows take 11 us, beside 2.5 ms of products.
+// One workgroup: 8192 rows take 14 us, beside 2.5 ms of products.
 __global__ __launch_bounds__(1024) void k_vocab_rows(VocabArgs a) {
-    __shared__ int scratch[16];
-    const int best = top_exponent<1024>(a, scratch);
-    if (threadIdx.x == 0) a.dw_scale[0] = dw_scale_of(a, best);
+    if (threadIdx.x == 0) a.dw_scale[0] = 1.0f;
     for (int64_t n = threadIdx.x; n < a.rows_pad; n += 1024) a.row[n] = row_of(a, n);
 }
 
+// The same where fp16 rows go to dw.  Their sum has one power of two, so row n's
+// copy of h is h 2^(e - E + 15), e of its factor and E the largest e + x of all
+// rows, |h| < 2^x in a row: the largest element of all lies in [2^14, 2^15), and
+// every copy is exact down to 2^-14, 2^-28 of that.  Below, its rounding is 2^-25
+// at most, in dw |p - onehot| 2^(E-40) a term; 2^E is at most four times the
+// largest |factor h|.  (With h against the largest factor alone, the top half of
+// the type's range was left unused, and of a row whose factor is 2^20 below it
+// 4 of 11 bits.)  A wave a row; each workgroup leaves its largest e + x.
+// A reading of h: 8192x2048 15 us.
+constexpr int kNoExponent = -10000;
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const int o = __shfl_xor(x, d, 64);
+        x = o > x ? o : x;
+    }
+    return x;
+}
+__global__ __launch_bounds__(kRowThreads) void k_vocab_tops(VocabArgs a) {
+    __shared__ int tops[kWaves];
+    const uint32_t lane = lane_id(), wave = threadIdx.x >> 6;
+    int top = kNoExponent;
+    for (int64_t n = (int64_t)blockIdx.x * kWaves + wave; n < a.rows_pad; n += (int64_t)gridDim.x * kWaves) {
+        if (lane == 0) a.row[n] = row_of(a, n);
+        const float f = n < a.rows ? row_factor(a, n) : 0.0f;
+        if (!has_exponent(f)) continue;
+        const gran* const from = reinterpret_cast<const gran*>((const char*)a.h + n * a.ld_h * 2);
+        int most = 0;  // the bits of the largest finite magnitude
+        for (int64_t i = lane; i < a.dim / 8; i += 64) {
+            const gran g = from[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int bits = (int)(g[j >> 1] >> (16 * (j & 1)) & 0x7fffu);
+                most = bits < 0x7c00 && bits > most ? bits : most;
+            }
+        }
+        most = wave_max(most);
+        if (most == 0) continue;
+        const int x = exponent_of((float)__builtin_bit_cast(_Float16, (uint16_t)most)) + exponent_of(f);
+        top = x > top ? x : top;
+    }
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWaves; ++w) top = tops[w] > top ? tops[w] : top;
+        a.top[blockIdx.x] = top;
+    }
+}
+
 // The rows of h that dw takes: zeros where a row does not count, whatever it
-// holds, and times the row's power of two (fp16).  A copy: 8192x2048 14 us.
-template <class T>
+// holds, and times the row's power of two (fp16).  A copy: 8192x2048 14 us (fp16 17).
+template <class T, int kThreads>
 __device__ __forceinline__ void copy_row(const VocabArgs& a, int64_t n, float c) {
     const gran* from = reinterpret_cast<const gran*>((const char*)a.h + n * a.ld_h * 2);
     gran* to = reinterpret_cast<gran*>((char*)a.h_copy + n * a.dim * 2);
-    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kRowThreads) {
+    for (int64_t i = threadIdx.x; i < a.dim / 8; i += kThreads) {
         gran g = gran{0, 0, 0, 0};
         if (c != 0.0f) {
             g = from[i];
@@ -592,35 +615,61 @@ __device__ __forceinline__ void copy_row(const VocabArgs& a, int64_t n, float c)
         to[i] = g;
     }
 }
-template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_copy(VocabArgs a) {
-    copy_row<T>(a, blockIdx.x, copy_factor(a.row[blockIdx.x], a.dw_scale[0]));
+    copy_row<BF16, kRowThreads>(a, blockIdx.x, a.row[blockIdx.x].f != 0.0f ? 1.0f : 0.0f);
 }
-// Both for few rows, in one launch: a workgroup a row, each finds the largest
-// exponent for itself.
+template <int kThreads>
+__device__ __forceinline__ void copy_scaled(const VocabArgs& a, int64_t n, int32_t tops, int* scratch) {
+    int top = kNoExponent;
+    for (int32_t i = (int32_t)threadIdx.x; i < tops; i += kThreads) top = a.top[i] > top ? a.top[i] : top;
+    top = wave_max(top);
+    if ((threadIdx.x & 63u) == 0) scratch[threadIdx.x >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 64; ++w) top = scratch[w] > top ? scratch[w] : top;
+    const bool none = top == kNoExponent;  // no row has both a factor and a finite element
+    if (n == 0 && threadIdx.x == 0) a.dw_scale[0] = none ? 1.0f : ldexpf(1.0f, top - 30);
+    const float f = row_factor(a, n);
+    int shift = 0;
+    if (!none && has_exponent(f)) {
+        shift = exponent_of(f) - top + 15;
+        shift = shift < -100 ? -100 : shift;  // a number becomes 0, a NaN stays one
+    }
+    copy_row<F16, kThreads>(a, n, f != 0.0f ? ldexpf(1.0f, shift) : 0.0f);
+}
+__global__ __launch_bounds__(kRowThreads) void k_vocab_copy_scaled(VocabArgs a, int32_t tops) {
+    __shared__ int scratch[kWaves];
+    copy_scaled<kRowThreads>(a, blockIdx.x, tops, scratch);
+}
+// Few rows: they are copied without a launch for it, bf16 with the rows' factors,
+// fp16 by workgroups behind the tiles of the first piece's P (gradient with a
+// launch for it and so: 7x50304x1024 68.7 and 65.6 us, 64x32000x2048 100.3 and 98.4).
 constexpr int64_t kFewRows = 512;
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_vocab_rows_copy(VocabArgs a) {
-    __shared__ int scratch[kRowThreads / 64];
-    const float dw_scale = dw_scale_of(a, top_exponent<kRowThreads>(a, scratch));
     const int64_t n = blockIdx.x;
     const VocabRow r = row_of(a, n);
     if (threadIdx.x == 0) {
         a.row[n] = r;
-        if (n == 0) a.dw_scale[0] = dw_scale;
+        if (n == 0) a.dw_scale[0] = 1.0f;
     }
-    if (a.dw && n < a.rows) copy_row<T>(a, n, copy_factor(r, dw_scale));
+    if constexpr (std::is_same<T, BF16>::value)
+        if (a.dw && n < a.rows) copy_row<T, kRowThreads>(a, n, r.f != 0.0f ? 1.0f : 0.0f);
 }
 
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
 // step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
 // 333x50257x1536 f16 takes 77 us: 394 tiles are two rounds of 256 CUs.
 template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
-__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1) {
+__global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1, uint32_t tiles, int32_t tops) {
     using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    if constexpr (std::is_same<T, F16>::value)
+        if (blockIdx.x >= tiles) {  // a row of h for dw
+            copy_scaled<G::kThreads>(a, blockIdx.x - tiles, tops, reinterpret_cast<int*>(lds));
+            return;
+        }
     uint32_t tm, tn;
-    tile_of(xcd_block(blockIdx.x, gridDim.x), (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
+    tile_of(xcd_block(blockIdx.x, tiles), (uint32_t)(v1 - v0 + kM - 1) / kM, a.tiles_n, tm, tn);
     const int32_t m0 = (int32_t)tm * kM, n0 = (int32_t)tn * kN;
     const int32_t lm = m0 + (int32_t)(G::wave_m() + G::lane_m()), left = v1 - v0 - lm;
     const int32_t n1 = n0 + (int32_t)G::wave_n();
@@ -891,18 +940,25 @@ hipError_t grad_of(hipStream_t s, const VocabArgs& a) {
         if (a.dw) SCAPE_RUN(k_vocab_zero<T>, a.cols, kRowThreads, a);
         return hipGetLastError();
     }
-    if (a.rows <= kFewRows) {
+    const int64_t groups = (a.rows_pad + kWaves - 1) / kWaves;
+    const int32_t tops = (int32_t)(groups < kVocabTops ? groups : kVocabTops);
+    int64_t copies = 0;  // of rows beside the first piece's P
+    if (std::is_same<T, F16>::value && a.dw) {
+        SCAPE_RUN(k_vocab_tops, tops, kRowThreads, a);
+        if (a.rows <= kFewRows) copies = a.rows;
+        else SCAPE_RUN(k_vocab_copy_scaled, a.rows, kRowThreads, a, tops);
+    } else if (a.rows <= kFewRows) {
         SCAPE_RUN(k_vocab_rows_copy<T>, a.rows_pad, kRowThreads, a);
     } else {
         SCAPE_RUN(k_vocab_rows, 1, 1024, a);
-        if (a.dw) SCAPE_RUN(k_vocab_copy<T>, a.rows, kRowThreads, a);
+        if (a.dw) SCAPE_RUN(k_vocab_copy, a.rows, kRowThreads, a);
     }
     const int32_t piece = (int32_t)a.piece, cols = (int32_t)a.cols;
     for (int32_t v0 = 0; v0 < cols; v0 += piece) {
         const int32_t v1 = v0 + piece < cols ? v0 + piece : cols;
         const bool first = v0 == 0, last = v1 == cols;
         const int64_t tiles = (int64_t)((v1 - v0 + a.tile_m - 1) / a.tile_m) * a.tiles_n;
-        SCAPE_LOGITS_BY_TILE(k_vocab_p, tiles, a, v0, v1);
+        SCAPE_LOGITS_BY_TILE(k_vocab_p, tiles + (first ? copies : 0), a, v0, v1, (uint32_t)tiles, tops);
         back_of<T>(s, a, v0, v1, first, last);
     }
     if (a.dh && a.splits > 1) SCAPE_RUN(k_vocab_dh_join<T>, a.rows * ((a.dim + kJoinWidth - 1) / kJoinWidth), kRowThreads, a);

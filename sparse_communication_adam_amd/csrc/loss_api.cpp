@@ -292,13 +292,14 @@ int64_t vocab_loss_bytes(const VocabArgs& a) {
 }
 // The workspace of the backward pass, each part a multiple of 16 bytes.
 struct VocabParts {
-    int64_t row, dw_scale, h_copy, p, dh_sum, all;
+    int64_t row, dw_scale, top, h_copy, p, dh_sum, all;
 };
 VocabParts vocab_parts(const VocabArgs& a) {
     VocabParts w;
     w.row = 0;
     w.dw_scale = w.row + a.rows_pad * (int64_t)sizeof(VocabRow);
-    w.h_copy = w.dw_scale + 16;
+    w.top = w.dw_scale + 16;
+    w.h_copy = w.top + (a.dtype == SCAPE_DTYPE_F16 ? kVocabTops * 4 : 0);
     w.p = w.h_copy + a.rows * a.dim * 2;
     w.dh_sum = w.p + a.rows_pad * a.piece * 2;
     w.all = a.rows ? w.dh_sum + (int64_t)a.splits * a.rows * a.dim * 4 : 0;
@@ -649,6 +650,7 @@ int scape_vocab_loss_backward(const scape_head* head, const float* lse, const fl
     if (a.rows > 0) {
         a.row = reinterpret_cast<VocabRow*>(ws + w.row);
         a.dw_scale = reinterpret_cast<float*>(ws + w.dw_scale);
+        a.top = reinterpret_cast<int32_t*>(ws + w.top);
         a.h_copy = ws + w.h_copy;
         a.p = ws + w.p;
         a.dh_sum = reinterpret_cast<float*>(ws + w.dh_sum);

@@ -136,6 +136,7 @@ hipError_t launch_balance_backward(hipStream_t s, const BalanceArgs& a);
 
 // ---- k_vocab.hip
 constexpr int kSmallWords = 64, kSmallDims = 128;  // tiles of up to 128 tokens
+constexpr int kVocabTops = 1024;                   // workgroups that look for the largest exponent
 struct VocabRow {
     float f, lse2;  // P's factor (0: does not count), log-sum-exp in base 2
     int32_t label;
@@ -170,6 +171,7 @@ struct VocabArgs {
     int32_t splits;
     VocabRow* row;        // [rows_pad]
     float* dw_scale;      // [1]
+    int32_t* top;         // [kVocabTops] largest exponents (fp16)
     void* h_copy;         // [rows][dim]
     void* p;              // rows_pad x piece
     float* dh_sum;        // [splits][rows][dim]
