@@ -504,7 +504,7 @@ def scape_grad_norm_workspace_bytes(ctx: Context) -> int:
 def _grad_norm(ctx: Context, call, gp, grads: dict, norm, layer_norm, workspace, stream) -> None:
     W, L = ctx.cfg.workers, len(ctx.layout.layer_offset)
     np_ = _array(_needed(norm, "norm"), _TORCH.float32, W + 1, "norm")
-    lp = _array(layer_norm, _TORCH.float32, W * L, "layer_norm")
+    lp = _grid(layer_norm, _TORCH.float32, W, L, "layer_norm")
     wp, wb = _workspace(workspace, lambda: scape_grad_norm_workspace_bytes(ctx))
     st = _launch_on(stream, norm=norm, layer_norm=layer_norm, workspace=workspace, **grads)
     _check(call(ctx.handle, gp, np_, lp, wp, wb, st))
@@ -719,6 +719,20 @@ def _array(t, dtype, numel: int, name: str):
     if not isinstance(t, _TORCH.Tensor) or t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
         _shape(t, dtype, numel, name)  # says which
     return t.data_ptr()
+
+
+def _grid(t, dtype, rows: int, cols: int, name: str):
+    """_array of a tensor [rows, cols] or longer; one that is not flat must have
+    rows of `cols`, or its elements would be taken for others'."""
+    p = _array(t, dtype, rows * cols, name)
+    if t is not None and t.dim() > 1 and t.shape[-1] != cols:
+        shape = list(t.shape)
+        while len(shape) > 1 and shape[-1] == 1:
+            shape.pop()
+        flat = t.numel() == rows * cols and max(shape, default=1) == t.numel()
+        if shape[-1] != cols and len(shape) > 1 and not flat:
+            raise ValueError(f"{name} must be [{rows}, {cols}] (got {tuple(t.shape)})")
+    return p
 
 
 def _needed(t, name: str):
@@ -1029,7 +1043,7 @@ def scape_expert_sort(idx, experts: int, offsets, row, workspace=None, stream=No
     ip, tokens, k = _choices(idx, "idx")
     i32 = _TORCH.int32
     op = _array(_needed(offsets, "offsets"), i32, experts + 1, "offsets")
-    rp = _array(_needed(row, "row"), i32, tokens * k, "row")
+    rp = _grid(_needed(row, "row"), i32, tokens, k, "row")
     wp, wb = _workspace(workspace, lambda: scape_expert_sort_workspace_bytes(idx, experts))
     st = _launch_on(stream, idx=idx, offsets=offsets, row=row, workspace=workspace)
     _check(lib().scape_expert_sort(ip, tokens, k, experts, op, rp, wp, wb, st))
@@ -1066,7 +1080,7 @@ def scape_expert_combine(y, row, out, weight=None, stream=None) -> None:
     rp, tokens, k = _choices(row, "row")
     yp, did, rows, dim, ld_y = _matrix(y, "y")
     op, _, _, _, ld_out = _same_rows(out, "out", y, tokens)
-    wp = _array(weight, _TORCH.float32, tokens * k, "weight")
+    wp = _grid(weight, _TORCH.float32, tokens, k, "weight")
     st = _launch_on(stream, y=y, row=row, out=out, weight=weight)
     _check(lib().scape_expert_combine(yp, did, rows, dim, ld_y, rp, wp, tokens, k, op, ld_out, st))
     _wrote(out)
@@ -1083,8 +1097,8 @@ def scape_expert_combine_backward(y, row, dout, dy=None, weight=None, dweight=No
     if dy is not None:
         dp, _, _, _, ld_dy = _same_rows(dy, "dy", y, rows)
     f32 = _TORCH.float32
-    wp = _array(weight, f32, tokens * k, "weight")
-    dwp = _array(dweight, f32, tokens * k, "dweight")
+    wp = _grid(weight, f32, tokens, k, "weight")
+    dwp = _grid(dweight, f32, tokens, k, "dweight")
     st = _launch_on(stream, y=y, row=row, dout=dout, dy=dy, weight=weight, dweight=dweight)
     _check(lib().scape_expert_combine_backward(yp, did, rows, dim, ld_y, rp, wp, gp, ld_dout, tokens, k, dp, ld_dy, dwp,
                                                st))
