@@ -644,8 +644,9 @@ int scape_balance_backward(const void* logits, int32_t dtype, int64_t tokens, in
  * aligned (the matrix instructions' operands are moved 16 bytes at a time).
  * Products are summed in fp32.  rows <= SCAPE_VOCAB_MAX_ROWS, cols <=
  * SCAPE_ROW_MAX_COLS, dim <= SCAPE_VOCAB_MAX_DIM, ld <= 2^21.
- * label int32 [rows], weight, loss and lse fp32 [rows].  rows = 0 enqueues
- * nothing.  A float32 head is not taken: the matrix instructions for it run at
+ * label int32 [rows], weight, loss and lse fp32 [rows].  loss may be weight;
+ * any other overlap of loss, lse or the workspace with one another or an input is
+ * refused.  rows = 0 enqueues nothing.  A float32 head is not taken: the matrix instructions for it run at
  * 1/16 of the rate, where keeping the logits costs little beside making them,
  * and scape_distill_forward with one entry a row is the loss of stored logits.
  * Errors: as scape_topk_rows.
@@ -681,7 +682,8 @@ int scape_vocab_loss_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_
  * within about 2^24 of one another).  Rows that do not
  * count, or whose dloss is 0, get dh = 0 and add nothing to dw, whatever h
  * holds there.  rows = 0 writes dw = 0.  ld_dh and ld_dw are multiples of 8, dh
- * and dw 16-byte aligned; neither may overlap an input.
+ * and dw 16-byte aligned.  dh, dw or a workspace that overlaps another of them or
+ * an input is refused (rows of one between rows of another do not overlap).
  * Errors: as scape_topk_rows. */
 int scape_vocab_loss_backward(const scape_head* head, const float* lse, const float* dloss, void* dh, int64_t ld_dh,
                               void* dw, int64_t ld_dw, void* workspace, int64_t workspace_bytes, void* stream);
@@ -695,7 +697,8 @@ int scape_vocab_grad_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_
  *     within one by (t, j); -1 for none
  * so that expert e's tokens are rows offsets[e] .. offsets[e+1]-1 of what
  * scape_expert_gather lays out.  1 <= experts <= SCAPE_EXPERT_MAX, k >= 1,
- * tokens * k < 2^31; a choice may repeat.  tokens = 0 writes offsets = 0.
+ * tokens * k < 2^31; a choice may repeat.  tokens = 0 writes offsets = 0.  row
+ * may be idx; any other overlap is refused.
  * Errors: as scape_topk_rows.
  */
 #define SCAPE_EXPERT_MAX 1024
@@ -707,7 +710,7 @@ int scape_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, int6
  * none.  The places are distinct, as scape_expert_sort makes them.  Rows of y
  * that no place names stay as they were.  x [tokens][dim] and y [rows][dim] of
  * one of the three types, rows ld_x and ld_y >= dim elements apart, aligned to
- * their element; they do not overlap.  1 <= dim <= 2^24; tokens <= 2^25.
+ * their element; a y that overlaps x or row is refused.  1 <= dim <= 2^24; tokens <= 2^25.
  * Its gradient is scape_expert_combine of dy without weights.
  * Errors: as scape_topk_rows. */
 int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t dim, int64_t ld_x, const int32_t* row,
@@ -715,7 +718,8 @@ int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t di
 
 /* out[t] = sum_j weight[t*k + j] * y[row[t*k + j]] (weight fp32, NULL: 1), in
  * fp32 in the order of j, rounded once.  A place outside [0, rows) and one with
- * weight 0 add nothing, whatever is there; a token without any gets 0.
+ * weight 0 add nothing, whatever is there; a token without any gets 0.  An out
+ * that overlaps an input is refused.
  * Errors: as scape_topk_rows. */
 int scape_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y, const int32_t* row,
                          const float* weight, int64_t tokens, int32_t k, void* out, int64_t ld_out, void* stream);
@@ -725,7 +729,7 @@ int scape_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t dim
  *   dweight[t*k + j] = sum_c y[row[t*k + j]][c] * dout[t][c], fp32; 0 for none
  * Either may be NULL (without dweight, y is not read and may be).  The places
  * are distinct.  Rows of dy that no place names stay as they were.  dy may be y
- * (then ld_dy = ld_y); any other overlap is not allowed.
+ * (then ld_dy = ld_y); any other overlap of dy or dweight is refused.
  * Errors: as scape_topk_rows. */
 int scape_expert_combine_backward(const void* y, int32_t dtype, int64_t rows, int64_t dim, int64_t ld_y,
                                   const int32_t* row, const float* weight, const void* dout, int64_t ld_dout,

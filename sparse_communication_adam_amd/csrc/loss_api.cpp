@@ -6,6 +6,7 @@
 #include "loss_internal.h"
 
 #include <cmath>
+#include <initializer_list>
 
 using namespace scape;
 
@@ -93,6 +94,47 @@ int check_workspace(const void* ws, int64_t have, int64_t need) {
     if (have < need)
         return fail(SCAPE_ERR_SHAPE, "workspace has %lld bytes, needs %lld", (long long)have, (long long)need);
     if (!is_aligned(ws, kWorkspaceAlign)) return fail(SCAPE_ERR_ALIGN, "workspace must be %zu-byte aligned", kWorkspaceAlign);
+    return SCAPE_OK;
+}
+
+// What an argument takes of memory: rows of `width` bytes, `pitch` apart (an
+// array is one row).  No memory: p is NULL.
+struct Extent {
+    const void* p;
+    int64_t rows, width, pitch;
+    const char* name;
+};
+Extent matrix_of(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const char* name) {
+    const int64_t size = dtype_size(dtype);
+    return Extent{p, rows, cols * size, ld * size, name};
+}
+Extent array_of(const void* p, int64_t bytes, const char* name) { return Extent{p, 1, bytes, bytes, name}; }
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }  // b > 0
+
+// Whether two extents share a byte; columns of one buffer beside each other do not.
+bool share(const Extent& a, const Extent& b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+    const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);  // b's first byte as a counts
+    if (d >= (a.rows - 1) * a.pitch + a.width || -d >= (b.rows - 1) * b.pitch + b.width) return false;
+    if (a.rows > b.rows) return share(b, a);
+    if (a.pitch == b.pitch && a.rows > 1) {
+        // b's row t + i meets a's row i where -b.width < d + t pitch < a.width
+        int64_t t = floor_div(-b.width - d, a.pitch) + 1;
+        if (t < 1 - a.rows) t = 1 - a.rows;
+        return t < b.rows && d + t * a.pitch < a.width;
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const int64_t at = i * a.pitch - d;  // a's row as b counts
+        int64_t j = floor_div(at - b.width, b.pitch) + 1;
+        if (j < 0) j = 0;
+        if (j < b.rows && j * b.pitch < at + a.width) return true;
+    }
+    return false;
+}
+int check_apart(const Extent& out, std::initializer_list<Extent> others) {
+    for (const Extent& o : others)
+        if (share(out, o)) return fail(SCAPE_ERR_INVALID_ARG, "%s overlaps %s", out.name, o.name);
     return SCAPE_OK;
 }
 
@@ -335,6 +377,13 @@ int vocab_head(const scape_head* h, VocabArgs* a) {
     a->c2 = base2(h->scale);
     return SCAPE_OK;
 }
+
+struct HeadExtents {
+    Extent h, w, label, weight;
+    explicit HeadExtents(const VocabArgs& a)
+        : h(matrix_of(a.h, a.dtype, a.rows, a.dim, a.ld_h, "h")), w(matrix_of(a.w, a.dtype, a.cols, a.dim, a.ld_w, "w")),
+          label(array_of(a.label, a.rows * 4, "label")), weight(array_of(a.weight, a.rows * 4, "weight")) {}
+};
 
 // ---- tokens to their experts
 constexpr int64_t kMaxMoved = int64_t(1) << 25;     // tokens of a move: a wave each
@@ -610,6 +659,13 @@ int scape_vocab_loss_forward(const scape_head* head, float* loss, float* lse, vo
     if ((rc = check_array(loss, 4, "loss"))) return rc;
     if ((rc = check_array(lse, 4, "lse"))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, vocab_loss_bytes(a)))) return rc;
+    const HeadExtents in(a);
+    const Extent to = array_of(loss, a.rows * 4, "loss"), to_lse = array_of(lse, a.rows * 4, "lse");
+    const Extent ws = array_of(workspace, vocab_loss_bytes(a), "workspace");
+    if ((rc = check_apart(to, {to_lse, ws, in.h, in.w, in.label}))) return rc;
+    if (loss != a.weight && (rc = check_apart(to, {in.weight}))) return rc;
+    if ((rc = check_apart(to_lse, {ws, in.h, in.w, in.label, in.weight}))) return rc;
+    if ((rc = check_apart(ws, {in.h, in.w, in.label, in.weight}))) return rc;
     a.loss = loss;
     a.lse = lse;
     a.part = static_cast<float2*>(workspace);
@@ -640,6 +696,13 @@ int scape_vocab_loss_backward(const scape_head* head, const float* lse, const fl
     vocab_pieces(&a);
     const VocabParts w = vocab_parts(a);
     if ((rc = check_workspace(workspace, workspace_bytes, w.all))) return rc;
+    const HeadExtents in(a);
+    const Extent from_lse = array_of(lse, a.rows * 4, "lse"), from_dloss = array_of(dloss, a.rows * 4, "dloss");
+    const Extent to_h = matrix_of(dh, a.dtype, a.rows, a.dim, ld_dh, "dh"), to_w = matrix_of(dw, a.dtype, a.cols, a.dim, ld_dw, "dw");
+    const Extent scratch = array_of(workspace, w.all, "workspace");
+    if ((rc = check_apart(to_h, {to_w, scratch, in.h, in.w, in.label, in.weight, from_lse, from_dloss}))) return rc;
+    if ((rc = check_apart(to_w, {scratch, in.h, in.w, in.label, in.weight, from_lse, from_dloss}))) return rc;
+    if ((rc = check_apart(scratch, {in.h, in.w, in.label, in.weight, from_lse, from_dloss}))) return rc;
     char* const ws = static_cast<char*>(workspace);
     a.lse = const_cast<float*>(lse);  // read only in these launches
     a.dloss = dloss;
@@ -676,6 +739,11 @@ int scape_expert_sort(const int32_t* idx, int64_t tokens, int32_t k, int32_t exp
     if ((rc = check_array(offsets, 4, "offsets"))) return rc;
     if (tokens > 0 && (rc = check_array(row, 4, "row"))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, sort_bytes(a)))) return rc;
+    const Extent from = array_of(idx, a.choices * 4, "idx"), to = array_of(row, a.choices * 4, "row");
+    const Extent first = array_of(offsets, ((int64_t)experts + 1) * 4, "offsets"), ws = array_of(workspace, sort_bytes(a), "workspace");
+    if (row != idx && (rc = check_apart(to, {from}))) return rc;  // in place a wave reads its choices before their places are written
+    if ((rc = check_apart(first, {from, to, ws}))) return rc;
+    if ((rc = check_apart(ws, {from, to}))) return rc;
     a.idx = idx;
     a.offsets = offsets;
     a.row = row;
@@ -691,6 +759,9 @@ int scape_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t di
     if ((rc = check_matrix(x, dtype, tokens, dim, ld_x, "x"))) return rc;
     if ((rc = check_matrix(y, dtype, rows, dim, ld_y, "y"))) return rc;
     if (tokens == 0 || rows == 0) return SCAPE_OK;
+    if ((rc = check_apart(matrix_of(y, dtype, rows, dim, ld_y, "y"),
+                          {matrix_of(x, dtype, tokens, dim, ld_x, "x"), array_of(row, tokens * k * 4, "row")})))
+        return rc;
     MoveArgs a{};
     a.dtype = dtype;
     a.tokens = tokens;
@@ -714,6 +785,10 @@ int scape_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t dim
     if ((rc = check_matrix(out, dtype, tokens, dim, ld_out, "out"))) return rc;
     if ((rc = check_optional(weight, "weight"))) return rc;
     if (tokens == 0) return SCAPE_OK;
+    if ((rc = check_apart(matrix_of(out, dtype, tokens, dim, ld_out, "out"),
+                          {matrix_of(y, dtype, rows, dim, ld_y, "y"), array_of(row, tokens * k * 4, "row"),
+                           array_of(weight, tokens * k * 4, "weight")})))
+        return rc;
     MoveArgs a{};
     a.dtype = dtype;
     a.tokens = tokens;
@@ -742,6 +817,13 @@ int scape_expert_combine_backward(const void* y, int32_t dtype, int64_t rows, in
     if ((rc = check_optional(weight, "weight"))) return rc;
     if ((rc = check_optional(dweight, "dweight"))) return rc;
     if (tokens == 0 || (!dy && !dweight)) return SCAPE_OK;
+    const Extent from = matrix_of(dweight ? y : nullptr, dtype, rows, dim, ld_y, "y");  // else it is not read
+    const Extent from_out = matrix_of(dout, dtype, tokens, dim, ld_dout, "dout"), places = array_of(row, tokens * k * 4, "row");
+    const Extent gates = array_of(weight, tokens * k * 4, "weight"), to_gates = array_of(dweight, tokens * k * 4, "dweight");
+    const Extent to = matrix_of(dy, dtype, rows, dim, ld_dy, "dy");
+    if (dy != y && (rc = check_apart(to, {from}))) return rc;
+    if ((rc = check_apart(to, {from_out, places, gates, to_gates}))) return rc;
+    if ((rc = check_apart(to_gates, {from, from_out, places, gates}))) return rc;
     MoveArgs a{};
     a.dtype = dtype;
     a.tokens = tokens;
