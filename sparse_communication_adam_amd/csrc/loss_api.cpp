@@ -296,8 +296,9 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
     a->rows_pad = (int64_t)a->tiles_n * a->tile_n;
     return SCAPE_OK;
 }
-// The pieces of the backward pass: P of one is at most 2^27 elements, and at
-// least 4096 words wide, so that dw has tiles for the CUs.  P lies in blocks of
+// The pieces of the backward pass: P of one is at most 2^27 elements, but never
+// less than 4096 words wide, so that dw has tiles for the CUs: above 32768 rows it
+// is up to 4096 rows_pad elements (8 GB at the most rows).  P lies in blocks of
 // 64 words, [words / 64][rows_pad][64], so that what a step of either product
 // takes is one run of memory or four; fewer rows than a step's lie as rows.
 // dh's sums are split over the words where its tiles leave CUs idle: the number
@@ -344,7 +345,8 @@ VocabParts vocab_parts(const VocabArgs& a) {
     w.h_copy = w.top + (a.dtype == SCAPE_DTYPE_F16 ? kVocabTops * 4 : 0);
     w.p = w.h_copy + a.rows * a.dim * 2;
     w.dh_sum = w.p + a.rows_pad * a.piece * 2;
-    w.all = a.rows ? w.dh_sum + (int64_t)a.splits * a.rows * a.dim * 4 : 0;
+    const bool summed = a.splits > 1 || a.piece < a.cols;  // else one launch writes dh itself
+    w.all = a.rows ? w.dh_sum + (summed ? (int64_t)a.splits * a.rows * a.dim * 4 : 0) : 0;
     return w;
 }
 
