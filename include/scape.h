@@ -328,8 +328,8 @@ int scape_dense_step_interleaved(scape_ctx* ctx, float* x, float* m, float* v, c
  * workspace is device scratch of the bytes scape_grad_norm_workspace says
  * (16-byte aligned, contents arbitrary); nothing is allocated, and the calls
  * can be captured.
- * Errors: INVALID_ARG, ALIGN, SHAPE (workspace too small, more tiles than a
- * launch holds), STATE, HIP.
+ * Errors: INVALID_ARG, ALIGN, SHAPE (workspace too small; more tiles of up to
+ * 32768 elements of a layer, or layers, than 2^20 over all workers), STATE, HIP.
  */
 int scape_grad_norm(scape_ctx* ctx, const uint16_t* const* g, float* norm, float* layer_norm, void* workspace,
                     int64_t workspace_bytes, void* stream);
@@ -350,7 +350,7 @@ int scape_grad_norm_workspace(const scape_ctx* ctx, int64_t* bytes);
  * written where f = 1); any other overlap is refused, one gradient for two
  * workers that is clipped in place among them.  Padding elements are not
  * written.  max_norm > 0 and finite.
- * Errors: INVALID_ARG, ALIGN, STATE, HIP.
+ * Errors: INVALID_ARG, ALIGN, SHAPE (as scape_grad_norm), STATE, HIP.
  */
 int scape_grad_clip(scape_ctx* ctx, const uint16_t* const* g, const float* norm, float max_norm, int32_t shared,
                     uint16_t* const* out, void* stream);

@@ -21,10 +21,11 @@ def sc():
     torch.cuda.empty_cache()
 
 
-def _state(sc, interleaved):
+def _state(sc, interleaved, offload=False):
     from sparse_communication_adam_amd.state import ScapeState
     wl = synth.ragged()
-    return ScapeState(sc.ScapeConfig(layer_numel=wl.layer_sizes, workers=wl.W, keep_num=1, keep_den=5), interleaved=interleaved)
+    return ScapeState(sc.ScapeConfig(layer_numel=wl.layer_sizes, workers=wl.W, keep_num=1, keep_den=5), interleaved=interleaved,
+                      offload=offload)
 
 
 def _grads(state, interleaved, seed):
@@ -49,12 +50,12 @@ def _same(a, b):
     assert torch.equal(a.grad_norm.view(torch.int32), b.grad_norm.view(torch.int32))
     assert torch.equal(a.x, b.x) and torch.equal(a.m, b.m) and torch.equal(a.v, b.v)
     for i in range(a.cfg.workers):
-        assert torch.equal(a.residual(i), b.residual(i))
+        assert torch.equal(a.residual(i).cpu(), b.residual(i).cpu())
 
 
-@pytest.mark.parametrize("interleaved", [False, True])
-def test_first_clipped_step_on_another_stream(sc, interleaved):
-    want, got = _state(sc, interleaved), _state(sc, interleaved)
+@pytest.mark.parametrize("interleaved,offload", [(False, False), (True, False), (False, True)])
+def test_first_clipped_step_on_another_stream(sc, interleaved, offload):
+    want, got = _state(sc, interleaved), _state(sc, interleaved, offload)
     mine, theirs = _grads(want, interleaved, 3), _grads(want, interleaved, 3)
     want.step(mine, max_norm=0.5)
     a = torch.randn(4096, 4096, device="cuda")
