@@ -724,6 +724,8 @@ def _array(t, dtype, numel: int, name: str):
 def _grid(t, dtype, rows: int, cols: int, name: str):
     """_array of a tensor [rows, cols] or longer; one that is not flat must have
     rows of `cols`, or its elements would be taken for others'."""
+    if isinstance(t, _TORCH.Tensor) and t.dtype is dtype and t.shape == (rows, cols) and t.is_contiguous():
+        return t.data_ptr()
     p = _array(t, dtype, rows * cols, name)
     if t is not None and t.dim() > 1 and t.shape[-1] != cols:
         shape = list(t.shape)
