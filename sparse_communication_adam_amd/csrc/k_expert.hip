@@ -90,9 +90,11 @@ __global__ __launch_bounds__(kBlock) void k_expert_count(SortArgs a) {
 // The places.  Each block sums the counts of all blocks, and of those before
 // it, for itself: they are few (a block for 2048 choices) and in the caches,
 // and a launch between the count and this costs more.  131072 choices of 64
-// experts take 4.9 + 8.1 us in a trace: two launches, and in each a chain of the
+// experts take 5.0 + 8.3 us in a trace: two launches, and in each a chain of the
 // choices' load, LDS and the counts; the bytes (1 MB) are nothing.  One block
-// alone needs no count before it (one token: 3.2 us, a launch).
+// alone needs no count before it (one token: 3.2 us, a launch).  Of very many
+// choices and experts the counts are what takes the time: 1200000 choices of 512
+// experts 5.8 + 44 us, 469 blocks reading 469 x 512 counts each.
 __global__ __launch_bounds__(kBlock) void k_expert_place(SortArgs a) {
     __shared__ uint32_t next[kWaves][kMaxExperts], before[kMaxExperts], total[kMaxExperts], scratch[kWaves];
     const uint32_t tid = threadIdx.x, wave = tid >> 6;
@@ -247,7 +249,7 @@ __device__ __forceinline__ float dot_of(const gran& g, const gran& d, const Span
 }
 
 // kB granules of the token are in registers while they go to its places.  Bound
-// by the writes: 16384x2048 bf16, k = 8, 102 us in a trace, 5.8 TB/s of 6.7 that a
+// by the writes: 16384x2048 bf16, k = 8, 102 us in a trace, 5.9 TB/s of 6.7 that a
 // copy reaches; the workgroups' rows lie all over y.
 template <class T, int kB>
 __global__ __launch_bounds__(kBlock) void k_expert_gather(MoveArgs a) {
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(kBlock) void k_expert_combine(MoveArgs a) {
 
 // A workgroup takes a token and its waves the token's choices in turn (a wave
 // for a token is slower for few tokens: 2000x1536 f16, k = 4, 12.9 us and 15.5).
-// Bound by reading y and writing dy: 8192x4096 bf16, k = 8, 206 us in a trace, 5.5
+// Bound by reading y and writing dy: 8192x4096 bf16, k = 8, 208 us in a trace, 5.5
 // TB/s.
 // dout is in registers where kB granules a lane hold it all, else it is read for
 // every place; the waves' reads of it meet in the L1.  A grid's axis counts its

@@ -35,7 +35,7 @@ __device__ __forceinline__ Share share_of(const GradArgs& a, uint32_t tile, uint
 constexpr int kTileGranules = kTileWords * 8, kPerThread = kTileGranules / kBlock;
 
 // A workgroup a tile of a worker, 16 bytes a load, all of a thread's on their way.
-// Bound by the read: two workers of 355M elements 202 us in a trace, 7.0 TB/s.
+// Bound by the read: two workers of 355M elements 203 us in a trace, 7.0 TB/s.
 __global__ __launch_bounds__(kBlock) void k_grad_squares(GradArgs a) {
     __shared__ double waves[kWaves];
     const uint32_t tid = threadIdx.x, b = xcd_block(blockIdx.x, gridDim.x);
@@ -110,7 +110,7 @@ __device__ __forceinline__ void join_workers(const GradArgs& a, uint32_t wave, u
 // Few layers: one workgroup joins all.  Else a launch for the layers and one for
 // the workers: a ticket that the last workgroup finds would have to be ordered
 // behind the others' sums across the XCDs' caches, which takes longer than a
-// launch (2x292 layers 12-17 us, in two launches 9.5 in a trace).
+// launch (2x292 layers 12-17 us, in two launches 10.2 in a trace).
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
 __global__ __launch_bounds__(kJoinThreads) void k_grad_join(GradArgs a) {
     join_layers(a, threadIdx.x >> 6, kJoinWaves);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_grad_workers(GradArgs a) {
 }
 
 // 16 bytes a thread, as a plain copy does best (two workers of 355M elements in a
-// trace: 497 us with four a thread, 456 so, 6.2 TB/s; bound by read and write).
+// trace: 497 us with four a thread, 460 so, 6.2 TB/s; bound by read and write).
 constexpr int kClipParts = kPerThread;
 __global__ __launch_bounds__(kBlock) void k_grad_clip(GradArgs a) {
     const uint32_t tid = threadIdx.x, b = xcd_block(blockIdx.x, gridDim.x), part = b % kClipParts, c = b / kClipParts;

@@ -14,9 +14,10 @@
 //
 // What bounds it: of many tokens the matrix cores, which at this load run below
 // their top clock; of few the reading of w and the writing of dw.  8192x32000x2048
-// bf16, us in a trace, and PFLOP/s: sums 750 (1.43), P 2 x 416 (1.29), dh 2 x 396
-// (1.36), dw 2 x 446 (1.20); the library's plain products of these shapes take 732
-// to 923, 803 to 951 and 1082 to 1214.  7x50304x1024: loss 24 us, 4.2 TB/s of w.
+// bf16, us in a trace (averages of 43 passes, here and below), and PFLOP/s: sums 828
+// (1.30), P 2 x 427 (1.26), dh 2 x 398 (1.35), dw 2 x 450 (1.19); the library's plain
+// products of these shapes take 834, 856 and 1129.  7x50304x1024: sums 21 us, 4.9
+// TB/s of w.
 #include "loss_device.h"
 
 namespace scape {
@@ -381,7 +382,7 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nm, uint32_t nn, ui
 
 // ---------------------------------------------------------------------------
 // The loss: each tile's reference and sum of a token, and the label's logit.
-// 2048x50257x1024 f16 takes 190 us: 1576 tiles on 256 CUs are seven rounds where
+// 2048x50257x1024 f16 takes 218 us (198 at the least): 1576 tiles on 256 CUs are seven rounds where
 // 6.2 would do, and a tile's exponentials are not hidden behind products.
 
 template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
@@ -658,7 +659,7 @@ __global__ __launch_bounds__(kRowThreads) void k_vocab_rows_copy(VocabArgs a) {
 
 // P of a piece of the vocabulary, rounded once to the operands' type: half a
 // step of its 8 (bf16) or 11 bits, as each gradient's own rounding is.
-// 333x50257x1536 f16 takes 77 us: 394 tiles are two rounds of 256 CUs.
+// 333x50257x1536 f16 takes 82 us: 394 tiles are two rounds of 256 CUs.
 template <class T, int kM, int kN, int kWM, int kWN, int kSlotsA, int kSlotsB>
 __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t v0, int32_t v1, uint32_t tiles, int32_t tops) {
     using G = Tile<T, true, true, kM, kN, kWM, kWN, kSlotsA, kSlotsB>;
@@ -720,9 +721,9 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_p(VocabArgs a, int32_t
 
 // dw of a piece.  It is stored past the caches, 256 bytes of a row at a time: with
 // 64 or 32 at a time, exchanged between the lanes without LDS, the gradient of
-// 7x50304x1024 took 82 and 104 us instead of 78.  333x50257x1536 f16 takes 76 us, of
+// 7x50304x1024 took 82 and 104 us instead of 78.  333x50257x1536 f16 takes 86 us, of
 // which the six steps of a tile are half: all CUs multiply and then all write.
-// Loading the next tile's operands meanwhile gained nothing (75).
+// Loading the next tile's operands meanwhile gained nothing (75.4 us for 75.8 then).
 template <class T, class G, int kM, int kN>
 __device__ __forceinline__ void dw_tile(const VocabArgs& a, const typename G::Slots& slots, uint32_t b, int32_t v0, int32_t v1) {
     const uint32_t nm = (uint32_t)((a.dim + kM - 1) / kM), nn = (uint32_t)(v1 - v0 + kN - 1) / kN;
@@ -841,7 +842,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void k_vocab_dh(VocabArgs a, int32_
 }
 
 // dh: the splits' sums, times the row's power of two, rounded once (21 splits of
-// 333x1536: 8.6 us in a trace, 43 MB at 5 TB/s).  A workgroup
+// 333x1536: 8.9 us in a trace, 43 MB at 4.8 TB/s).  A workgroup
 // takes 512 elements of a row, each wave a quarter of the splits, in an order
 // that the sizes alone decide.
 constexpr int kJoinWidth = 512;

@@ -267,8 +267,12 @@ constexpr int64_t kMaxHeadLd = int64_t(1) << 21;  // a tile's offsets stay below
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Tokens of a tile: what holds few, and of many the size that wastes least (a
-// tile of 192 takes about 4/5 of one of 256).
+// Tokens of a tile: what holds few, and of many the size that wastes least.  A
+// tile of 192 takes 4/5 of one of 256 (1536 tokens in 8 and in 6 tiles, us: loss of
+// 50257x1024 bf16 159 and 147, of 131072x2048 f16 694 and 636, gradients 496 and
+// 467, 2280 and 2173; 300 tokens of 50257x1024 50 and 55, 500 of them 72 and 59).
+// How many CUs get a tile is not looked at: 129 to 256 tokens under fewer than
+// 65536 words leave some idle.
 int32_t vocab_tile(int64_t rows) {
     for (int32_t t = 16; t <= 128; t *= 2)
         if (rows <= t) return t;
@@ -305,10 +309,14 @@ int vocab_shape(int32_t dtype, int64_t rows, int64_t cols, int64_t dim, VocabArg
 // of splits is the one with the least rounds of tiles on the CUs times a split's
 // steps (and about 6 more for its start and its end), counting the splits'
 // sums, which are written and read once more, at a step for each 8 MB.  Beside
-// dw, in one launch (up to 64 tokens), 128 workgroups are best where the tiles
-// divide them, and three times as many where not (gradient us with 128 and 384
-// of them: 7x50304x1024 64 and 67, 64x32000x2048 96 and 108, but 50x50257x1536
-// 129 and 121); alone as many as LDS holds.
+// dw, in one launch (up to 64 tokens), there are 128 workgroups where the tiles
+// divide them, three times as many where not.  bf16 gradient us with 128 and 384:
+//   7 x 50257 x 256 26 and 28, 512 37 and 39, 768 50 and 53, 1024 64 and 67, 1536
+//   115 and 107, 2048 150 and 134, 4096 295 and 287, 5120 369 and 354
+//   64 x 32000 x 1024 46 and 49, 1536 68 and 75, 2048 95 and 103, 4096 178 and 190
+// so it is right up to a width of 1024 but for 768, and for wider rows as the
+// vocabulary has it; where it is not, it costs a tenth.  Alone dh takes as many
+// workgroups as LDS holds.
 void vocab_pieces(VocabArgs* a) {
     int64_t most = a->rows_pad ? (int64_t(1) << 27) / a->rows_pad / 256 * 256 : a->cols;
     if (most < 4096) most = 4096;
