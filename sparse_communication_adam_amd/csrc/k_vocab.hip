@@ -633,7 +633,9 @@ __device__ __forceinline__ void copy_scaled(const VocabArgs& a, int64_t n, int32
     int shift = 0;
     if (!none && has_exponent(f)) {
         shift = exponent_of(f) - top + 15;
-        shift = shift < -100 ? -100 : shift;  // a number becomes 0, a NaN stays one
+        // A number becomes 0 far below and a NaN stays one; only a row of zeros or
+        // of no numbers, which has no part in E, lies far above.
+        shift = shift < -100 ? -100 : shift > 100 ? 100 : shift;
     }
     copy_row<F16, kThreads>(a, n, f != 0.0f ? ldexpf(1.0f, shift) : 0.0f);
 }

@@ -130,6 +130,20 @@ def test_rows_of_zeros_and_of_no_number(sc):
         assert not bool(_dw(sc, c, lse).any())
 
 
+@pytest.mark.parametrize("rows", [20, 600])
+def test_a_row_of_zeros_with_a_huge_factor(sc, rows):
+    """Zeros have no part in the scale and stay zeros under it, whatever their factor (2^120 above the others here)."""
+    c = Spread(rows, 100, 64, 10)
+    c.h[0] = 0
+    c.factor[1:] = 2.0 ** -20
+    c.factor[0] = 2.0 ** 100
+    lse = c.exact()[0]
+    got = _dw(sc, c, lse)
+    c.label[0] = -1
+    want = _dw(sc, c, lse)
+    assert bool(want.any()) and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
 def test_a_factor_that_is_no_number(sc, bad):
     """It shows in dw, and the scale is that of the others."""
